@@ -6,7 +6,7 @@ exceptions. There is no fallback: if libdsa.so is missing, ``load()`` raises.
 
 Entry points mirror include/dsa.h: ``workspace_size``, ``indexer_scores``,
 ``indexer_frontend``, ``indexer_prefill_scores``, ``topk``, ``topk_noalloc``, ``dcp_topk_merge``, ``lse_combine``, ``sparse_mla_decode``,
-``decode``, ``get_device_error``, ``selftest_wait_timeout``, ``status_string``.
+``decode``, ``prefix_mla_decode``, ``pages_resize``, ``pages_fork``, ``pages_compact``, ``verify_draft``, ``get_device_error``, ``selftest_wait_timeout``, ``status_string``.
 """
 from __future__ import annotations
 
@@ -21,6 +21,8 @@ DSA_LAT_FP8_576, DSA_LAT_NVFP4_352 = 0, 1
 DSA_EMIT_PHYS_ROWS = 0x1
 DSA_Q_PREPARED = 0x2
 DSA_DEVERR_BLOCK_TABLE, DSA_DEVERR_CTX, DSA_DEVERR_TOPK_INDEX, DSA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DSA_DEVERR_PAGES, DSA_DEVERR_NO_PAGES, DSA_DEVERR_DRAFT, DSA_DEVERR_PROB = 0x10, 0x20, 0x40, 0x80
+DSA_PROB_F32, DSA_PROB_BF16, DSA_PROB_F16 = 0, 1, 2
 
 # Kernels one dsa_decode launches (q quantisation, indexer, top-k, sparse MLA,
 # split combine); kept in step with csrc/.
@@ -37,6 +39,11 @@ EXPORTS = (
     "dsa_lse_combine",
     "dsa_sparse_mla_decode",
     "dsa_decode",
+    "dsa_prefix_mla_decode",
+    "dsa_pages_resize",
+    "dsa_pages_fork",
+    "dsa_pages_compact",
+    "dsa_verify_draft",
     "dsa_get_device_error",
     "dsa_selftest_wait_timeout",
     "dsa_status_string",
@@ -47,6 +54,12 @@ class FrontendDims(ctypes.Structure):
     """dsa_frontend_dims_t."""
 
     _fields_ = [("d_c", ctypes.c_int32), ("d_model", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class PagePool(ctypes.Structure):
+    """dsa_page_pool_t."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
 
 
 class Params(ctypes.Structure):
@@ -117,6 +130,12 @@ def load() -> ctypes.CDLL:
         "dsa_lse_combine": [P, ctypes.c_int32, vp, vp, vp, vp, vp],
         "dsa_sparse_mla_decode": [P, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "dsa_decode": [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_prefix_mla_decode": [P, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_pages_resize": [P, vp, ctypes.POINTER(PagePool), ctypes.c_int32, vp, vp, vp, vp, sz, vp],
+        "dsa_pages_fork": [P, ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_pages_compact": [P, ctypes.POINTER(PagePool), ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_verify_draft": [P, ctypes.c_int32, ctypes.c_int32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                             vp],
         "dsa_get_device_error": [vp, vp, ctypes.POINTER(ctypes.c_int32)],
         "dsa_selftest_wait_timeout": [vp, sz, ctypes.c_uint32, vp],
         "dsa_status_string": [ctypes.c_int],
@@ -231,6 +250,74 @@ def decode(params, q_idx, w, key_pool, q, lat_pool, block_table, ctx_lens, out, 
         ctypes.byref(params), _ptr(q_idx), _ptr(w), _ptr(key_pool), _ptr(q), _ptr(lat_pool),
         _ptr(block_table), _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(topk_idx_out), _ptr(ws), _nbytes(ws),
         _stream(stream)))
+
+
+def prefix_mla_decode(params, q, lat_pool, prefix_pages, prefix_len, block_table, ctx_lens, out, lse, ws,
+                      stream=None):
+    """Dense attention of a batch whose contexts start with the same `prefix_len` tokens
+    (int32 page numbers `prefix_pages`, None without a prefix)."""
+    _check("dsa_prefix_mla_decode", load().dsa_prefix_mla_decode(
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _ptr(prefix_pages), int(prefix_len), _ptr(block_table),
+        _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def make_pools(pools):
+    """The page operations' pool list from (tensor or address, page_bytes, page_stride) triples."""
+    pools = list(pools)
+    return (PagePool * max(len(pools), 1))(*[PagePool(_ptr(b), int(n), int(s)) for b, n, s in pools]), len(pools)
+
+
+def pages_resize(params, new_lens, pools, block_table, ctx_lens, page_refs, ws, stream=None):
+    """Grow, shrink or free every request to `new_lens` (negative: as it is); `pools` from make_pools."""
+    _check("dsa_pages_resize", load().dsa_pages_resize(
+        ctypes.byref(params), _ptr(new_lens), pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def pages_fork(params, src, dst, block_table, ctx_lens, page_refs, ws, stream=None):
+    """Slots dst[i] share the pages of requests src[i] (int32 tensors of one length)."""
+    if src.numel() != dst.numel():
+        raise ValueError("pages_fork: src and dst differ in length")
+    _check("dsa_pages_fork", load().dsa_pages_fork(
+        ctypes.byref(params), src.numel(), _ptr(src), _ptr(dst), _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def pages_compact(params, pools, block_table, ctx_lens, page_refs, page_map, live, ws, stream=None):
+    """Move the pages in use to the front of the pools; `page_map` and `live` may be None."""
+    _check("dsa_pages_compact", load().dsa_pages_compact(
+        ctypes.byref(params), pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs), _ptr(page_map),
+        _ptr(live), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _prob_rows(name, t, rows):
+    """(dtype code, row stride) of a tensor of `rows` equally spaced rows of probabilities."""
+    code = {"torch.float32": DSA_PROB_F32, "torch.bfloat16": DSA_PROB_BF16, "torch.float16": DSA_PROB_F16}.get(str(t.dtype))
+    if code is None:
+        raise ValueError(f"verify_draft: {name} is {t.dtype}, not float32, bfloat16 or float16")
+    stride = t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else t.stride(0) if t.dim() == 3 else t.shape[-1]
+    even = t.dim() < 3 or t.shape[0] == 1 or t.shape[1] == 1 or t.stride(0) == t.shape[1] * t.stride(1)
+    if t.numel() != rows * t.shape[-1] or t.stride(-1) != 1 or not even:
+        raise ValueError(f"verify_draft: {name} is not {rows} equally spaced rows")
+    return code, max(stride, t.shape[-1])
+
+
+def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_lens, n_accepted, out_tokens, new_lens, ws,
+                 stream=None):
+    """Accept or reject the drafted tokens and draw the next one. `target` [B, n_q, vocab] and `draft`
+    [B, n_q - 1, vocab] (or None) are probabilities; `n_draft`, `ctx_lens`, `new_lens` may be None."""
+    code, p_stride = _prob_rows("target", target, params.batch * params.n_q)
+    q_stride = 0
+    if draft is not None and params.n_q > 1:
+        qcode, q_stride = _prob_rows("draft", draft, params.batch * (params.n_q - 1))
+        if qcode != code or draft.shape[-1] != target.shape[-1]:
+            raise ValueError("verify_draft: target and draft differ in type or vocabulary")
+    else:
+        draft = None
+    _check("dsa_verify_draft", load().dsa_verify_draft(
+        ctypes.byref(params), target.shape[-1], code, _ptr(target), p_stride, _ptr(draft), q_stride,
+        _ptr(draft_tokens) if params.n_q > 1 else None, _ptr(n_draft), _ptr(uniforms), _ptr(ctx_lens),
+        _ptr(n_accepted), _ptr(out_tokens), _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def get_device_error(ws, stream=None) -> int:

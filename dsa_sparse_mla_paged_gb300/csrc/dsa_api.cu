@@ -62,6 +62,19 @@ dsa_status_t check_mla_args(const void* q, const void* lat_pool, const int32_t* 
   return DSA_OK;
 }
 
+dsa_status_t check_pools(const dsa_page_pool_t* pools, int32_t n_pools) {
+  if (n_pools < 0 || (n_pools > 0 && !pools)) return DSA_ERR_INVALID;
+  if (n_pools > kMaxPools) return DSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_pools; ++i) {
+    const dsa_page_pool_t& q = pools[i];
+    if (!q.base || !aligned16(q.base) || q.page_bytes < 16 || (q.page_bytes & 15) || q.page_stride < q.page_bytes ||
+        (q.page_stride & 15))
+      return DSA_ERR_INVALID;
+    if (q.page_bytes > (int64_t(1) << 32)) return DSA_ERR_UNSUPPORTED;
+  }
+  return DSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,6 +224,83 @@ dsa_status_t dsa_decode(const dsa_params_t* params, const void* q_idx, const flo
     e = launch_sparse_mla(*params, L, w8, q, lat_pool, block_table, ctx_lens, topk_idx_out, out, lse,
                           stream, true);
   return cuda_status(e);
+}
+
+dsa_status_t dsa_prefix_mla_decode(const dsa_params_t* params, const void* q, const void* lat_pool,
+                                   const int32_t* prefix_pages, int32_t prefix_len, const int32_t* block_table,
+                                   const int32_t* ctx_lens, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if ((s = check_mla_args(q, lat_pool, block_table, ctx_lens, out)) != DSA_OK) return s;
+  if (prefix_len < 0 || prefix_len % params->page_size || (prefix_len > 0 && !prefix_pages)) return DSA_ERR_INVALID;
+  if (int64_t(prefix_len) + params->n_q > int64_t(params->max_pages_per_req) * params->page_size)
+    return DSA_ERR_INVALID;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_prefix_mla(*params, L, static_cast<char*>(ws), q, lat_pool, prefix_pages, prefix_len,
+                                       block_table, ctx_lens, out, lse, stream));
+}
+
+dsa_status_t dsa_pages_resize(const dsa_params_t* params, const int32_t* new_lens, const dsa_page_pool_t* pools,
+                              int32_t n_pools, int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, void* ws,
+                              size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (!new_lens || !block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  if ((s = check_pools(pools, n_pools)) != DSA_OK) return s;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_pages_resize(*params, L, static_cast<char*>(ws), new_lens, pools, n_pools, block_table,
+                                         ctx_lens, page_refs, stream));
+}
+
+dsa_status_t dsa_pages_fork(const dsa_params_t* params, int32_t n, const int32_t* src, const int32_t* dst,
+                            int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, void* ws, size_t ws_bytes,
+                            cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (n < 0 || n > params->batch || (n > 0 && (!src || !dst))) return DSA_ERR_INVALID;
+  if (!block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  if (n == 0) return DSA_OK;
+  return cuda_status(launch_pages_fork(*params, L, static_cast<char*>(ws), n, src, dst, block_table, ctx_lens,
+                                       page_refs, stream));
+}
+
+dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t* pools, int32_t n_pools,
+                               int32_t* block_table, const int32_t* ctx_lens, int32_t* page_refs, int32_t* page_map,
+                               int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (!block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  if ((s = check_pools(pools, n_pools)) != DSA_OK) return s;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_pages_compact(*params, L, static_cast<char*>(ws), pools, n_pools, block_table, ctx_lens,
+                                          page_refs, page_map, live, stream));
+}
+
+dsa_status_t dsa_verify_draft(const dsa_params_t* params, int32_t vocab, int32_t dtype, const void* p_target,
+                              int64_t p_stride, const void* p_draft, int64_t q_stride, const int32_t* draft_tokens,
+                              const int32_t* n_draft, const float* uniforms, const int32_t* ctx_lens,
+                              int32_t* n_accepted, int32_t* out_tokens, int32_t* new_lens, void* ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (vocab < 1 || dtype < DSA_PROB_F32 || dtype > DSA_PROB_F16) return DSA_ERR_INVALID;
+  if (vocab > (1 << 24)) return DSA_ERR_UNSUPPORTED;
+  const uintptr_t mis = dtype == DSA_PROB_F32 ? 3 : 1;  // elements are aligned to their size
+  if (!p_target || (reinterpret_cast<uintptr_t>(p_target) & mis) || p_stride < vocab) return DSA_ERR_INVALID;
+  if (p_draft && ((reinterpret_cast<uintptr_t>(p_draft) & mis) || q_stride < vocab)) return DSA_ERR_INVALID;
+  if (params->n_q > 1 && !draft_tokens) return DSA_ERR_INVALID;
+  if (!uniforms || !n_accepted || !out_tokens || (new_lens && !ctx_lens)) return DSA_ERR_INVALID;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  const VerifyIn in{p_target, p_draft, p_stride, q_stride, draft_tokens, n_draft, uniforms, ctx_lens,
+                    n_accepted, out_tokens, new_lens, vocab, dtype};
+  return cuda_status(launch_verify_draft(*params, L, static_cast<char*>(ws), in, stream));
 }
 
 dsa_status_t dsa_get_device_error(void* ws, cudaStream_t stream, int32_t* code) {

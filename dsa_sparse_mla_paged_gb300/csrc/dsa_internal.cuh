@@ -42,6 +42,14 @@ constexpr int kDcpMaxWorld = 16;
 constexpr int kFeMaxRows = 512;
 constexpr int kFeMaxPasses = kFeMaxRows / 4;
 
+// shared-prefix attention: at most this many CTA pairs share a call's tokens (a
+// pair per two of the GPU's 152 SMs)
+constexpr int kPfxMaxClusters = 76;
+constexpr int kPfxTileRows = 128;  // query heads (row * 96 + head) of one work tile
+
+// page operations: at most this many pools in a call
+constexpr int kMaxPools = 64;
+
 // Byte offsets of the workspace regions (all 256-B aligned).
 struct WsLayout {
   size_t err;       // int32 error word
@@ -53,7 +61,12 @@ struct WsLayout {
   size_t cand;      // uint64 [rows][kCandCap] top-k candidates (key << 32 | token)
   size_t gmax;      // uint32 [rows][gstride] order key of the largest score of each 32 tokens
   size_t gmax128;   // uint32 [rows][g128stride] the same per 128 tokens (dsa_decode; zero between calls)
-  size_t opart;     // float [rows][splits][96][512]
+  size_t opart;     // float [rows][splits][96][512]; dsa_prefix_mla_decode keeps its state (pfx_*) here
+  size_t pfx_q;     // half [rows * 96][576] the scaled query
+  size_t pfx_qs;    // float [rows * 96] its power-of-two scales
+  size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
+  size_t pfx_lse;   // float [pfx_slots][128] partial log-sum-exps
+  size_t pfx_part;  // float [pfx_slots][128][512] partial outputs
   size_t lpart;     // float [rows][splits][96]
   size_t topk;      // int32 [rows][topk] (dsa_decode without topk_idx_out)
   size_t dcp_key;   // uint32 [rows][kDcpMaxWorld][topk] shard lists: bf16 keys by position
@@ -63,9 +76,13 @@ struct WsLayout {
   size_t fe_q;      // fp32 [rows][32][128] the front end's head outputs
   size_t fe_cnt;    // int32 [33][kFeMaxPasses] the front end's arrival counters
   size_t dcp_keys16;  // uint16 [rows][W][S] shard-major score keys, W * S <= cap + 8 * kDcpMaxWorld
+  size_t pg_head;   // int32 [16] totals of a page operation
+  size_t pg_req;    // int32 [3][batch] a page operation's plan per request (or fork pair)
+  size_t pg_list;   // int32 [3][num_pages] its page lists
   size_t scores;    // float [rows][cap]
   size_t total;
   int rows, cap, max_chunks, splits, gstride, g128stride;
+  int pfx_tiles, pfx_jobs, pfx_slots;
 };
 
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -92,6 +109,18 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   L.gmax = o; o = align256(o + size_t(L.rows) * L.gstride * 4);
   L.gmax128 = o; o = align256(o + size_t(L.rows) * L.g128stride * 4);
   L.opart = o; o = align256(o + size_t(L.rows) * L.splits * kHeads * kDNope * 4);
+  // the prefix attention's partials: one slot per job (a tile of 128 query
+  // heads on the prefix, or a row on its own tokens) and cut between CTA pairs
+  L.pfx_tiles = (L.rows * kHeads + kPfxTileRows - 1) / kPfxTileRows;
+  L.pfx_jobs = L.pfx_tiles + L.rows;
+  L.pfx_slots = L.pfx_jobs + kPfxMaxClusters;
+  size_t x = L.opart;
+  L.pfx_q = x; x = align256(x + size_t(L.rows) * kHeads * kDQK * 2);
+  L.pfx_qs = x; x = align256(x + size_t(L.rows) * kHeads * 4);
+  L.pfx_plan = x; x = align256(x + size_t(L.pfx_jobs) * 2 * 4);
+  L.pfx_lse = x; x = align256(x + size_t(L.pfx_slots) * kPfxTileRows * 4);
+  L.pfx_part = x; x = align256(x + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
+  o = x > o ? x : o;
   L.lpart = o; o = align256(o + size_t(L.rows) * L.splits * kHeads * 4);
   L.topk = o; o = align256(o + size_t(L.rows) * p.topk * 4);
   L.dcp_key = o; o = align256(o + size_t(L.rows) * kDcpMaxWorld * p.topk * 4);
@@ -101,6 +130,9 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   L.fe_q = o; o = align256(o + size_t(L.rows) * kIdxHeads * kIdxDim * 4);
   L.fe_cnt = o; o = align256(o + size_t(kIdxHeads + 1) * kFeMaxPasses * 4);
   L.dcp_keys16 = o; o = align256(o + size_t(L.rows) * (size_t(L.cap) + 8 * kDcpMaxWorld) * 2);
+  L.pg_head = o; o = align256(o + 64);
+  L.pg_req = o; o = align256(o + size_t(3) * p.batch * 4);
+  L.pg_list = o; o = align256(o + size_t(3) * p.num_pages * 4);
   L.scores = o; o = align256(o + size_t(L.rows) * L.cap * 4);
   L.total = o;
   return L;
@@ -278,6 +310,32 @@ struct FrontendIn {
 };
 cudaError_t launch_idx_frontend(const dsa_params_t& p, const WsLayout& L, char* ws, const FrontendIn& in,
                                 cudaStream_t st);
+cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
+                              const int32_t* prefix_pages, int prefix_len, const int32_t* block_table,
+                              const int32_t* ctx_lens, void* out, float* lse, cudaStream_t st);
+cudaError_t launch_pages_resize(const dsa_params_t& p, const WsLayout& L, char* ws, const int32_t* new_lens,
+                                const dsa_page_pool_t* pools, int n_pools, int32_t* block_table, int32_t* ctx_lens,
+                                int32_t* page_refs, cudaStream_t st);
+cudaError_t launch_pages_fork(const dsa_params_t& p, const WsLayout& L, char* ws, int n, const int32_t* src,
+                              const int32_t* dst, int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs,
+                              cudaStream_t st);
+cudaError_t launch_pages_compact(const dsa_params_t& p, const WsLayout& L, char* ws, const dsa_page_pool_t* pools,
+                                 int n_pools, int32_t* block_table, const int32_t* ctx_lens, int32_t* page_refs,
+                                 int32_t* page_map, int32_t* live, cudaStream_t st);
+struct VerifyIn {
+  const void* p;
+  const void* q;
+  int64_t p_stride, q_stride;
+  const int32_t* tokens;
+  const int32_t* n_draft;
+  const float* uniforms;
+  const int32_t* ctx_lens;
+  int32_t* n_accepted;
+  int32_t* out_tokens;
+  int32_t* new_lens;
+  int vocab, dtype;
+};
+cudaError_t launch_verify_draft(const dsa_params_t& p, const WsLayout& L, char* ws, const VerifyIn& in, cudaStream_t st);
 // early: the call follows this library's own kernels in one chain (dsa_decode),
 // so the query and the set-up may be fetched before the wait on the top-k.
 cudaError_t launch_sparse_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q,

@@ -43,7 +43,8 @@
  *   be ordered (same stream, or synchronised by the caller).
  * - Launch failures return DSA_ERR_CUDA.
  * - Results are deterministic: the same inputs give the same bits, whatever
- *   the batch composition.
+ *   the batch composition (dsa_prefix_mla_decode: the same call gives the same
+ *   bits, but how it cuts the contexts depends on the whole batch).
  */
 #ifndef DSA_H_
 #define DSA_H_
@@ -92,6 +93,10 @@ typedef enum { DSA_LAT_FP8_576 = 0, DSA_LAT_NVFP4_352 = 1 } dsa_lat_fmt_t;
 #define DSA_DEVERR_CTX 0x2          /* ctx_b outside [n_q, max_pages_per_req * page_size] */
 #define DSA_DEVERR_TOPK_INDEX 0x4   /* a top-k index outside [-1, L_{b,t}) */
 #define DSA_DEVERR_TIMEOUT 0x8      /* a bounded in-kernel wait gave up (results unspecified) */
+#define DSA_DEVERR_PAGES 0x10       /* a refused fork pair, or a reference count below what the tables hold */
+#define DSA_DEVERR_NO_PAGES 0x20    /* dsa_pages_resize: not enough free pages */
+#define DSA_DEVERR_DRAFT 0x40       /* dsa_verify_draft: a draft token or count out of range */
+#define DSA_DEVERR_PROB 0x80        /* dsa_verify_draft: a row that is not one of probabilities */
 
 typedef struct {
   int32_t batch;              /* B >= 1 */
@@ -313,6 +318,144 @@ dsa_status_t dsa_lse_combine(const dsa_params_t* params, int32_t parts, const vo
 dsa_status_t dsa_topk_noalloc(const dsa_params_t* params, const float* scores, int64_t score_stride,
                               const int32_t* ctx_lens, const int32_t* block_table, int32_t* topk_idx,
                               int32_t* phys_rows, cudaStream_t stream);
+
+/* Dense attention of a batch whose requests share a prefix: every request's
+ * context starts with the same prefix_len tokens, whose latents are read once
+ * for all rows, and goes on with tokens of its own. No selection: row (b, t)
+ * attends to every token s < L_{b,t} (what dsa_sparse_mla_decode computes when
+ * its index list holds all of them), for a dense layer, for contexts up to K,
+ * or for many samples of one prompt. With c_s as in dsa_sparse_mla_decode:
+ *   logit_s = softmax_scale * q_h . c_s  (576 dims), 0 <= s < L_{b,t}
+ *   out[h]  = sum_s softmax(logit)_s * c_s[0:512]          (bf16, RNE)
+ *   lse[h]  = ln sum_s exp(logit_s)                        (fp32)
+ * Products of the query (each head's 576 values scaled by a power of two) and
+ * of the softmax weights are taken in fp16 with fp32 sums: the latents are
+ * exact, a query value is exact unless it is below 2^-32 of its head's largest,
+ * and a weight is rounded to 11 bits (or 2^-32 of the row's largest).
+ *   prefix_pages int32 [prefix_len / 64] physical pages of the shared tokens
+ *                (NULL if prefix_len is 0); rows of block_table need not repeat
+ *                them: their first prefix_len / 64 entries are not read
+ *   prefix_len   0 or a multiple of the page size; prefix_len + n_q at most
+ *                max_pages_per_req * page_size
+ *   block_table, ctx_lens, q, lat_pool, out, lse  as dsa_sparse_mla_decode;
+ *                ctx_b counts the prefix, and prefix_len + n_q <= ctx_b
+ * Errors: a row whose ctx_b is out of that range gets out = 0, lse = -inf and
+ * DSA_DEVERR_CTX; the tokens of a page outside [0, num_pages) are left out
+ * (DSA_DEVERR_BLOCK_TABLE). `topk` and the key fields of params are not used. */
+dsa_status_t dsa_prefix_mla_decode(const dsa_params_t* params, const void* q, const void* lat_pool,
+                                   const int32_t* prefix_pages, int32_t prefix_len, const int32_t* block_table,
+                                   const int32_t* ctx_lens, void* out, float* lse, void* ws, size_t ws_bytes,
+                                   cudaStream_t stream);
+
+/* Page operations: the bookkeeping that the calls above leave to their caller,
+ * on the device and without a host sync. The state is the caller's:
+ *   block_table int32 [batch, max_pages_per_req] and ctx_lens int32 [batch], as
+ *               above; ctx_b = 0 is an empty slot
+ *   page_refs   int32 [num_pages], how many times a page is held: once per
+ *               block-table row that uses it (its first ceil(ctx_b / 64)
+ *               entries), plus once for each hold the caller keeps himself (a
+ *               cached prefix); 0 is a free page
+ *   pools       host array of n_pools (0 .. 64) pools that the same page numbers
+ *               address: keys, latents, those of every layer. Page p of a pool
+ *               is page_bytes at base + p * page_stride (base 16-B aligned,
+ *               sizes multiples of 16, page_bytes <= page_stride)
+ * The calls change block_table, ctx_lens and page_refs in place. */
+typedef struct {
+  void* base;
+  int64_t page_bytes;
+  int64_t page_stride;
+} dsa_page_pool_t;
+
+/* Gives every request b the length new_lens[b] (int32 [batch]; a negative entry
+ * leaves the request as it is):
+ * - shorter: the pages past ceil(new / 64) lose one reference each, and their
+ *   entries become -1. A length of 0 frees the request.
+ * - longer: fresh pages are appended (references 1, contents unspecified). If
+ *   the last page is partly filled and has more than one reference, the request
+ *   gets a copy of it (in every pool) in a fresh page of its own, so that what is
+ *   appended is never seen by the other holders; the shared one loses one
+ *   reference. Every holder that grows in the call gets its copy.
+ * - fresh pages are the free pages with the lowest numbers, handed out in the
+ *   order of the requests (a copy first, then the appended pages in order).
+ *   Pages that this call frees are not handed out by it.
+ * - if the free pages do not reach, the first request that does not fit and
+ *   every later one that needs pages keep their length, and
+ *   DSA_DEVERR_NO_PAGES is set.
+ * A request with ctx_b or new_lens[b] above max_pages_per_req * 64, or with a
+ * negative ctx_b (DSA_DEVERR_CTX), or whose partly filled page is a bad entry
+ * (DSA_DEVERR_BLOCK_TABLE), keeps its length; bad entries that are released are
+ * skipped. */
+dsa_status_t dsa_pages_resize(const dsa_params_t* params, const int32_t* new_lens, const dsa_page_pool_t* pools,
+                              int32_t n_pools, int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, void* ws,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/* Forks requests: for each pair i < n (0 <= n <= batch), slot dst[i] gets the context
+ * of request src[i]: its length, its first ceil(ctx / 64) block-table entries,
+ * one more reference on each of those pages, and no copy of their contents (a later
+ * dsa_pages_resize copies the open page when one of the holders grows).
+ *   src, dst int32 [n]; the same src may stand in several pairs
+ * A pair is refused (DSA_DEVERR_PAGES, nothing changed for it) if a slot is outside
+ * [0, batch), if dst holds tokens before the call, or if an earlier pair has the
+ * same dst; ctx[src] out of range: DSA_DEVERR_CTX. Bad entries are copied, and
+ * set DSA_DEVERR_BLOCK_TABLE. */
+dsa_status_t dsa_pages_fork(const dsa_params_t* params, int32_t n, const int32_t* src, const int32_t* dst,
+                            int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, void* ws, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/* Packs the pages in use to the front of the pools: with n_live pages of
+ * page_refs > 0, the live pages numbered n_live and up move (in every pool,
+ * with their references) into the free pages below n_live, lowest to lowest, and
+ * the used entries of block_table follow. Contents of the pages left free are
+ * not changed.
+ *   page_map int32 [num_pages] or NULL: the new number of each page, -1 for a free one
+ *            (for page numbers that the caller keeps, such as prefix_pages)
+ *   live     int32 [1] or NULL: n_live
+ * A row with ctx_b out of [0, max_pages_per_req * 64] is left as it is
+ * (DSA_DEVERR_CTX), and so is an entry out of range (DSA_DEVERR_BLOCK_TABLE) or
+ * on a page without references (DSA_DEVERR_PAGES). */
+dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t* pools, int32_t n_pools,
+                               int32_t* block_table, const int32_t* ctx_lens, int32_t* page_refs, int32_t* page_map,
+                               int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Element types of dsa_verify_draft's probabilities. */
+typedef enum { DSA_PROB_F32 = 0, DSA_PROB_BF16 = 1, DSA_PROB_F16 = 2 } dsa_prob_t;
+
+/* Verifies the drafted tokens of a speculative step against the target's
+ * probabilities (the article's speculative decoding runs the last token and its
+ * drafts as the n_q rows of one step). Request b has
+ * k_b = n_draft[b] drafts x_0 .. x_{k-1} (at most n_q - 1); row i of p is the
+ * target's distribution for the place of draft i (row k_b: for the token after
+ * the last draft), row i of q the distribution that draft i was drawn from, and
+ * u the request's n_q uniform random numbers in [0, 1):
+ *   draft i passes if u_i * q_i(x_i) < p_i(x_i); a = the number of drafts
+ *   before the first that does not pass (k_b if all do);
+ *   weights over the vocabulary: w_v = max(p_a(v) - q_a(v), 0) if a < k_b
+ *   (p_a where that is 0 everywhere), else w_v = p_a(v);
+ *   the next token is the lowest v with w_0 + ... + w_v > u_{n_q - 1} * sum w.
+ * The tests are exact (products in fp64); the weights are differences and sums of
+ * 64-bit integers, the probabilities being taken as multiples of 2^-60 (rounded down).
+ * Without p_draft (drafts not drawn at random: a lookup, a greedy draft) q_i is 1
+ * at x_i and 0 elsewhere.
+ *   vocab        1 .. 2^24;  dtype  dsa_prob_t of p_target and p_draft
+ *   p_target     [B * n_q] rows of vocab values, p_stride elements apart
+ *   p_draft      [B * (n_q - 1)] rows, q_stride elements apart, or NULL
+ *   draft_tokens int32 [B, n_q - 1] (NULL allowed if n_q is 1)
+ *   n_draft      int32 [B] or NULL (n_q - 1 for all)
+ *   uniforms     fp32 [B, n_q]: column i < n_q - 1 tests draft i, the last draws the token
+ *   ctx_lens     int32 [B] or NULL, the lengths the step ran with (new tokens included)
+ *   n_accepted   int32 [B]: a
+ *   out_tokens   int32 [B, n_q]: the a accepted drafts, the next token, then -1
+ *   new_lens     int32 [B] or NULL (needs ctx_lens): ctx_b - n_q + 1 + a, what is left of the
+ *                context, as dsa_pages_resize takes it
+ * Entries outside [0, 1] (NaN among them) count as 0 and set DSA_DEVERR_PROB, and so do
+ * weights that sum to 0 or to more than 4, where the next token is -1. A draft token
+ * out of [0, vocab) does not pass; it and a count outside [0, n_q - 1] (clamped) set DSA_DEVERR_DRAFT;
+ * ctx_b < n_q gives new_lens -1 and DSA_DEVERR_CTX. A last uniform number outside [0, 1) is clamped into it. */
+dsa_status_t dsa_verify_draft(const dsa_params_t* params, int32_t vocab, int32_t dtype, const void* p_target,
+                              int64_t p_stride, const void* p_draft, int64_t q_stride, const int32_t* draft_tokens,
+                              const int32_t* n_draft, const float* uniforms, const int32_t* ctx_lens,
+                              int32_t* n_accepted, int32_t* out_tokens, int32_t* new_lens, void* ws, size_t ws_bytes,
+                              cudaStream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device error word of the
  * workspace `ws` into *code (0 = no error; DSA_DEVERR_* bits otherwise).

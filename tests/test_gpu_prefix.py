@@ -1,0 +1,322 @@
+"""dsa_prefix_mla_decode against the float64 oracle.
+
+Bounds, derived from the arithmetic that include/dsa.h states:
+- a logit is a sum of 576 products in fp32: at most 64 roundings of a partial
+  sum no larger than bulk = scale * sum |q c|, 2^-23 of it each (a factor of two
+  for accumulators that truncate), and 2^-22 for scaling: d = 66 * 2^-23 * bulk;
+- a weight exp(z) is off by a factor 1 + d, by 2^-21 in the exponential, and
+  rounded to 11 bits (2^-11); the normaliser by d + 2^-21 and the rounding of its
+  fp32 sum; splitting and merging adds a few 2^-22 on either;
+- so lse is off by d + 2^-19 + 2^-22 |lse|, and out by (2^-11 + 2 d + 2^-18) * mass with
+  mass = sum p |c|, plus the bf16 rounding, 2^-8 |out| (2^-133 among subnormals).
+Nothing here is measured first."""
+import numpy as np
+import pytest
+
+import dsa_sparse_mla_paged_gb300 as dsa
+import gen
+from oracle import serving as S
+
+from dsa_testlib import Dev, bf16_to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need(lib, cuda_ok):
+    yield
+
+
+def make(batch, n_q, prefix, tails, seed=1, **kw):
+    """Inputs whose requests share `prefix` tokens (request 0's pages; the other rows'
+    entries there are left bad, as they are not read) and add `tails` of their own."""
+    inp = gen.make_inputs(batch, n_q, [prefix + t for t in tails], seed=seed, bt_mode="permuted", **kw)
+    inp.latent_scale = 0.75
+    pages = inp.block_table[0, :prefix // 64].copy()
+    inp.block_table[:, :prefix // 64] = 10 ** 8
+    return inp, pages
+
+
+def launch(d, pages, prefix, ws=None, stream=None, lse=True):
+    import torch
+
+    out = torch.full((d.rows, 96, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ls = torch.full((d.rows, 96), float("nan"), dtype=torch.float32, device="cuda") if lse else None
+    pg = torch.from_numpy(pages).cuda() if prefix else None
+    dsa.prefix_mla_decode(d.p, d.q, d.lat_pool, pg, prefix, d.block_table, d.ctx, out, ls, d.ws if ws is None else ws, stream)
+    return out, ls
+
+
+def check_row(inp, pages, prefix, b, t, out, lse):
+    ref, ref_lse, mass, bulk = S.prefix_mla(inp, pages, prefix, b, t)
+    d = (66 * 2.0 ** -23 * bulk)[:, None]
+    bound = (2.0 ** -11 + 2 * d + 2.0 ** -18) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
+    err = np.abs(out.astype(np.float64) - ref)
+    assert np.isfinite(out).all()
+    assert (err <= bound).all(), f"({b}, {t}): {(err / bound).max():.2f} of the bound at {np.unravel_index((err / bound).argmax(), err.shape)}"
+    if lse is not None:
+        assert (np.abs(lse - ref_lse) <= d[:, 0] + 2.0 ** -19 + 2.0 ** -22 * np.abs(ref_lse)).all(), (b, t, np.abs(lse - ref_lse).max())
+
+
+def check(inp, pages, prefix, rows=None, bits=0):
+    d = Dev(inp)
+    out, lse = launch(d, pages, prefix)
+    assert dsa.get_device_error(d.ws) == bits
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in range(inp.batch):
+        for t in range(inp.n_q):
+            r = b * inp.n_q + t
+            if rows is None or r in rows:
+                check_row(inp, pages, prefix, b, t, o[r], l[r])
+    return d, out, lse
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("batch,n_q,prefix,tails", [
+    (1, 1, 0, [1]), (1, 1, 0, [63]), (1, 1, 64, [1]), (1, 1, 4096, [50]),
+    (2, 1, 128, [64, 65]), (3, 1, 640, [1, 200, 129]), (4, 1, 1024, [3, 70, 500, 64]),
+    (1, 4, 64, [4]), (2, 3, 192, [3, 67]), (2, 8, 0, [8, 700]), (5, 2, 2048, [2, 9, 66, 130, 1000]),
+])
+def test_matches_oracle(lat_fmt, batch, n_q, prefix, tails):
+    inp, pages = make(batch, n_q, prefix, tails, seed=batch + prefix, lat_fmt=lat_fmt)
+    check(inp, pages, prefix)
+
+
+def test_long_prefix_and_many_rows():
+    inp, pages = make(40, 1, 16384, [1 + 13 * i for i in range(40)], seed=5)
+    check(inp, pages, 16384, rows={0, 1, 17, 38, 39})
+
+
+def test_long_private_contexts():
+    inp, pages = make(3, 2, 0, [9000, 2, 20001], seed=6)
+    check(inp, pages, 0, rows={0, 2, 3, 5})
+
+
+def test_more_rows_than_a_wave_of_jobs():
+    inp, pages = make(150, 2, 128, [2 + i % 90 for i in range(150)], seed=7)
+    check(inp, pages, 128, rows={0, 1, 99, 201, 298, 299})
+
+
+def test_a_prompt_chunk():
+    inp, pages = make(1, 130, 256, [200], seed=8)
+    check(inp, pages, 256, rows={0, 64, 128, 129})
+
+
+def test_page_strides_and_holes():
+    inp, pages = make(2, 2, 320, [40, 300], seed=9, lat_page_pad=4096, holes=True)
+    check(inp, pages, 320)
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+def test_nan_in_hidden_tokens_stays_out(lat_fmt):
+    """NaN latents behind a context's end, and in a later new token that an earlier row must not see."""
+    inp, pages = make(2, 3, 64, [70, 10], seed=10, lat_fmt=lat_fmt)
+    size = 576 if lat_fmt == "fp8" else 352
+    for b, c in enumerate(inp.ctx):
+        page = inp.lat_pool[inp.block_table[b, (c - 1) // 64]]
+        page[((c - 1) % 64) * size:] = 0x7F
+    d = Dev(inp)
+    out, lse = launch(d, pages, 64)
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in range(2):
+        for t in range(2):  # the last row sees the token
+            check_row(inp, pages, 64, b, t, o[b * 3 + t], l[b * 3 + t])
+
+
+@pytest.mark.parametrize("exps", [(-100, -60), (-20, 20), (60, 90)])
+def test_query_magnitudes(exps):
+    """Queries far outside fp16's range (each head's own size), with logits kept moderate by one small
+    scale per call: a head's largest value decides its scaling."""
+    inp, pages = make(2, 1, 64, [30, 100], seed=11)
+    rng = np.random.default_rng(0)
+    e = rng.integers(exps[0], exps[1], (2, 1, 96, 1))
+    q = rng.standard_normal((2, 1, 96, 576)) * 2.0 ** e
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    inp.softmax_scale = 2.0 ** -(exps[1] + 3)
+    check(inp, pages, 64)
+
+
+def test_query_with_outliers_and_zeros():
+    inp, pages = make(1, 1, 64, [90], seed=12)
+    rng = np.random.default_rng(1)
+    q = rng.standard_normal((1, 1, 96, 576)) * 2.0 ** rng.integers(-12, 1, (1, 1, 96, 576))
+    q[0, 0, 5] = 0.0
+    q[0, 0, 6, 3] = 700.0
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    check(inp, pages, 64)
+
+
+def test_sharp_and_rising_scores():
+    """Scores that rise along the context (every tile raises the running maximum), fall along it, or have
+    one token far above the others first, last or in between."""
+    inp, pages = make(4, 1, 1024, [300, 300, 300, 300], seed=13)
+    inp.softmax_scale = 1.0
+    rng = np.random.default_rng(2)
+    from oracle.formats import bf16_decode
+    direction = np.sign(bf16_decode(inp.q[0, 0, 0]))
+    q = rng.standard_normal((4, 1, 96, 576)) * 0.05 + direction * rng.choice([-0.06, 0.06], (4, 1, 96, 1))
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    rows = inp.lat_pool.reshape(-1, 576)
+
+    def put(page, slot, level):  # latent = direction * level, as E4M3 codes
+        rows[page * 64 + slot] = gen.encode_e4m3(direction * level)
+
+    for i, pg in enumerate(pages):
+        for s in range(64):
+            put(pg, s, 0.05 * i)
+    for b, order in enumerate((1, -1, 0, 0)):
+        for s in range(300):
+            j = 1024 + s
+            level = {1: 0.8 + s / 400, -1: 1.6 - s / 400, 0: 0.1}[order]
+            put(inp.block_table[b, j // 64], j % 64, level)
+    put(inp.block_table[2, 1024 // 64], 0, 4.0)
+    put(inp.block_table[3, 1323 // 64], 1323 % 64, 4.0)
+    check(inp, pages, 1024)
+
+
+def test_a_heavy_first_token_and_a_long_light_rest():
+    """One token outweighs each of 60,000 others by about e^12: the rest still holds a fair share of the mass."""
+    inp, pages = make(1, 1, 60032, [20], seed=14)
+    rng = np.random.default_rng(3)
+    inp.softmax_scale = 1.0
+    q = np.full((1, 1, 96, 576), 0.0)
+    q[..., 0] = 1.5
+    q[..., 1:] = rng.standard_normal((1, 1, 96, 575)) * 0.01
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    rows = inp.lat_pool.reshape(-1, 576)
+    rows[:, 0] = 0x80
+    rows[pages[0] * 64, 0] = gen.encode_e4m3(np.array([11.0]))[0]
+    check(inp, pages, 60032)
+
+
+def test_bad_data_is_skipped_and_reported():
+    import torch
+
+    inp, pages = make(4, 2, 128, [90, 70, 2, 300], seed=15)
+    good_ctx = inp.ctx.copy()
+    inp.ctx[1] = 128 + 1                      # no room for its two new tokens
+    inp.ctx[2] = inp.max_pages * 64 + 1
+    d = Dev(inp)
+    out, lse = launch(d, pages, 128)
+    assert dsa.get_device_error(d.ws) == dsa.DSA_DEVERR_CTX
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for r in (2, 3, 4, 5):
+        assert (o[r] == 0).all() and np.isneginf(l[r]).all()
+    for b in (0, 3):
+        for t in range(2):
+            check_row(inp, pages, 128, b, t, o[b * 2 + t], l[b * 2 + t])
+    # a bad prefix page and a bad page of a request: their tokens are left out
+    inp.ctx[:] = good_ctx
+    d = Dev(inp)
+    bad = pages.copy()
+    bad[1] = -1
+    d.block_table[3, 3] = inp.num_pages
+    out, lse = launch(d, bad, 128)
+    assert dsa.get_device_error(d.ws) == dsa.DSA_DEVERR_BLOCK_TABLE
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    ref = S.O.sparse_mla
+    inp.block_table[:, :2] = pages
+    for b, t, keep in ((0, 0, list(range(64)) + list(range(128, 128 + 89))),
+                       (3, 1, list(range(64)) + list(range(128, 192)) + list(range(256, 428)))):
+        want, want_lse = ref(inp, b, t, np.array(keep))
+        assert np.abs(l[b * 2 + t] - want_lse).max() < 1e-4
+        assert np.abs(o[b * 2 + t] - want).max() < 2.0 ** -8 * np.abs(want).max() + 2.0 ** -9
+    # a request whose every page is bad, without a prefix: nothing to attend to
+    inp, pages = make(2, 1, 0, [64, 30], seed=16)
+    d = Dev(inp)
+    d.block_table[0, 0] = -1
+    out, lse = launch(d, pages, 0)
+    assert dsa.get_device_error(d.ws) == dsa.DSA_DEVERR_BLOCK_TABLE
+    assert (out[0] == 0).all() and torch.isneginf(lse[0]).all()
+    check_row(inp, pages, 0, 1, 0, bf16_to_np(out)[1], lse.cpu().numpy()[1])
+
+
+def test_without_lse_and_again():
+    import torch
+
+    inp, pages = make(6, 1, 512, [5, 60, 64, 200, 1, 33], seed=17)
+    d, out, lse = check(inp, pages, 512)
+    again, _ = launch(d, pages, 512, lse=False)
+    assert torch.equal(again, out)
+
+
+def test_agrees_with_sparse_attention_over_all_tokens():
+    """The same step through dsa_sparse_mla_decode with every visible token in its list. Both bounds apply."""
+    inp, pages = make(3, 2, 320, [100, 64, 700], seed=18)
+    d, out, lse = check(inp, pages, 320)
+    table = inp.block_table.copy()
+    table[:, :5] = pages
+    inp.block_table = table
+    d2 = Dev(inp)
+    import torch
+
+    idx = torch.full((6, 2048), -1, dtype=torch.int32)
+    for r in range(6):
+        L = int(inp.ctx[r // 2]) - 2 + r % 2 + 1
+        idx[r, :L] = torch.arange(L)
+    o2, l2 = d2.mla(idx.cuda())
+    assert (lse - l2).abs().max() < 1e-3
+    assert (out.float() - o2.float()).abs().max() < 2e-2
+
+
+def test_captured_graphs_share_a_workspace():
+    import torch
+
+    cases = []
+    for seed, (prefix, tails) in enumerate([(512, [3, 100, 64]), (0, [300, 20, 65]), (1024, [1, 1, 200])]):
+        inp, pages = make(3, 1, prefix, tails, seed=20 + seed)
+        d = Dev(inp)
+        cases.append((inp, pages, prefix, d))
+    big = max((c[3].ws for c in cases), key=lambda w: w.numel())
+    graphs = []
+    for inp, pages, prefix, d in cases:
+        pg = torch.from_numpy(pages).cuda() if prefix else None
+        out = torch.empty(3, 96, 512, dtype=torch.bfloat16, device="cuda")
+        lse = torch.empty(3, 96, dtype=torch.float32, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dsa.prefix_mla_decode(d.p, d.q, d.lat_pool, pg, prefix, d.block_table, d.ctx, out, lse, big)
+        graphs.append((g, out, lse, pg))
+    for i in (0, 1, 2, 1, 0):
+        g, out, lse, _ = graphs[i]
+        inp, pages, prefix, d = cases[i]
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        o, l = bf16_to_np(out), lse.cpu().numpy()
+        for b in range(3):
+            check_row(inp, pages, prefix, b, 0, o[b], l[b])
+
+
+def test_decode_after_it_on_the_same_workspace():
+    """The fused step keeps its results when the prefix attention has used the same workspace."""
+    import torch
+
+    inp = gen.make_inputs(2, 2, [3000, 700], seed=30, bt_mode="permuted")
+    d = Dev(inp)
+    first = d.decode()
+    again = d.decode()
+    out, lse = launch(d, inp.block_table[0, :0], 0)
+    after = d.decode()
+    assert dsa.get_device_error(d.ws) == 0
+    for x, y, z in zip(first, again, after):
+        assert torch.equal(x, y) and torch.equal(x, z)
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for r in range(4):
+        check_row(inp, inp.block_table[0, :0], 0, r // 2, r % 2, o[r], l[r])
+
+
+def test_on_a_side_stream():
+    import torch
+
+    inp, pages = make(4, 1, 256, [5, 60, 64, 200], seed=31)
+    d = Dev(inp)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        out, lse = launch(d, pages, 256)
+    st.synchronize()
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in range(4):
+        check_row(inp, pages, 256, b, 0, o[b], l[b])

@@ -1,0 +1,132 @@
+"""Host validation of the calls around the decode step (CPU: every case is
+rejected before any CUDA call) and the binding's own checks."""
+import ctypes
+
+import pytest
+
+import dsa_sparse_mla_paged_gb300 as dsa
+
+FAKE = 0x10000  # never dereferenced: validation fails before any CUDA call
+INVALID, UNSUPPORTED, WORKSPACE = dsa.DSA_ERR_INVALID, dsa.DSA_ERR_UNSUPPORTED, dsa.DSA_ERR_WORKSPACE
+
+
+def _params(**kw):
+    base = dict(batch=2, n_q=2, max_pages_per_req=10, num_pages=20, key_page_stride=8448, lat_page_stride=36864)
+    base.update(kw)
+    return dsa.make_params(**base)
+
+
+def _call(fn, p, args, /, **change):
+    need = dsa.workspace_size(p)
+    args = {**args, "ws": FAKE, "bytes": need, **change}
+    return getattr(dsa.load(), fn)(ctypes.byref(p), *args.values(), None)
+
+
+PREFIX = dict(q=FAKE, lat=FAKE, pages=FAKE, prefix=128, table=FAKE, ctx=FAKE, out=FAKE, lse=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=None), dict(q=FAKE + 2), dict(lat=FAKE + 8), dict(lat=None), dict(pages=None), dict(prefix=-64), dict(prefix=100),
+    dict(prefix=640), dict(table=None), dict(ctx=None), dict(out=None), dict(out=FAKE + 4), dict(ws=None), dict(ws=FAKE + 4)])
+def test_prefix_attention_rejects(lib, change):
+    assert _call("dsa_prefix_mla_decode", _params(), PREFIX, **change) == INVALID
+
+
+def test_prefix_attention_workspace(lib):
+    p = _params()
+    assert _call("dsa_prefix_mla_decode", p, PREFIX, bytes=dsa.workspace_size(p) - 1) == WORKSPACE
+    # no prefix needs no page list; one that leaves no room for the new tokens is refused
+    assert _call("dsa_prefix_mla_decode", p, PREFIX, pages=None, prefix=0, bytes=0) == WORKSPACE
+    assert _call("dsa_prefix_mla_decode", p, PREFIX, prefix=576, bytes=0) == WORKSPACE
+    assert _call("dsa_prefix_mla_decode", _params(n_q=65), PREFIX, prefix=576, bytes=0) == INVALID
+
+
+def _pools(*pools):
+    return dsa.make_pools(pools)
+
+
+RESIZE = dict(new=FAKE, pools=None, n=0, table=FAKE, ctx=FAKE, refs=FAKE)
+COMPACT = dict(pools=None, n=0, table=FAKE, ctx=FAKE, refs=FAKE, map=None, live=None)
+FORK = dict(n=2, src=FAKE, dst=FAKE, table=FAKE, ctx=FAKE, refs=FAKE)
+
+
+@pytest.mark.parametrize("fn,args", [("dsa_pages_resize", RESIZE), ("dsa_pages_compact", COMPACT)])
+def test_page_operations_reject(lib, fn, args):
+    p = _params()
+    for name in ("table", "ctx", "refs"):
+        assert _call(fn, p, args, **{name: None}) == INVALID
+    assert _call(fn, p, args, n=-1) == INVALID
+    assert _call(fn, p, args, n=1) == INVALID
+    good = (FAKE, 64, 64)
+    for bad in ((None, 64, 64), (FAKE + 8, 64, 64), (FAKE, 8, 64), (FAKE, 40, 64), (FAKE, 64, 48), (FAKE, 64, 72)):
+        pools, n = _pools(good, bad)
+        assert _call(fn, p, args, pools=pools, n=n) == INVALID, bad
+    pools, n = _pools(*[good] * 65)
+    assert _call(fn, p, args, pools=pools, n=n) == UNSUPPORTED
+    pools, n = _pools((FAKE, (1 << 32) + 16, 1 << 33))
+    assert _call(fn, p, args, pools=pools, n=n) == UNSUPPORTED
+    pools, n = _pools(*[good] * 64)
+    assert _call(fn, p, args, pools=pools, n=n, bytes=0) == WORKSPACE
+    assert _call(fn, p, args, ws=None) == INVALID
+
+
+def test_resize_and_fork_reject(lib):
+    p = _params()
+    assert _call("dsa_pages_resize", p, RESIZE, new=None) == INVALID
+    for change in (dict(n=-1), dict(n=3), dict(src=None), dict(dst=None), dict(table=None), dict(ctx=None),
+                   dict(refs=None)):
+        assert _call("dsa_pages_fork", p, FORK, **change) == INVALID, change
+    assert _call("dsa_pages_fork", p, FORK, bytes=0) == WORKSPACE
+    assert _call("dsa_pages_fork", p, FORK, n=0, src=None, dst=None) == dsa.DSA_OK  # nothing to launch
+
+
+VERIFY = dict(vocab=100, dtype=0, p=FAKE, ps=100, q=FAKE, qs=100, tokens=FAKE, counts=None, u=FAKE, ctx=FAKE, acc=FAKE, out=FAKE,
+              new=FAKE)
+
+
+@pytest.mark.parametrize("change", [
+    dict(vocab=0), dict(vocab=-1), dict(dtype=3), dict(dtype=-1), dict(p=None), dict(p=FAKE + 2), dict(ps=99), dict(q=FAKE + 1),
+    dict(qs=99), dict(dtype=1, p=FAKE + 1), dict(tokens=None), dict(u=None), dict(acc=None), dict(out=None), dict(ctx=None)])
+def test_verify_rejects(lib, change):
+    assert _call("dsa_verify_draft", _params(), VERIFY, **change) == INVALID
+
+
+def test_verify_limits(lib):
+    p = _params()
+    assert _call("dsa_verify_draft", p, VERIFY, vocab=(1 << 24) + 1, ps=1 << 25, qs=1 << 25) == UNSUPPORTED
+    assert _call("dsa_verify_draft", p, VERIFY, bytes=0) == WORKSPACE
+    assert _call("dsa_verify_draft", p, VERIFY, dtype=2, p=FAKE + 2, q=None, qs=0, bytes=0) == WORKSPACE
+    assert _call("dsa_verify_draft", p, VERIFY, ctx=None, new=None, bytes=0) == WORKSPACE
+    assert _call("dsa_verify_draft", _params(n_q=1), VERIFY, tokens=None, bytes=0) == WORKSPACE
+
+
+def test_null_params_and_bad_params(lib):
+    for fn, args in (("dsa_prefix_mla_decode", PREFIX), ("dsa_pages_resize", RESIZE), ("dsa_pages_fork", FORK),
+                     ("dsa_pages_compact", COMPACT), ("dsa_verify_draft", VERIFY)):
+        f = getattr(lib, fn)
+        assert f(None, *args.values(), FAKE, 0, None) == INVALID, fn
+        p = _params()
+        p.batch = 0
+        assert f(ctypes.byref(p), *args.values(), FAKE, 0, None) == INVALID, fn
+        p = _params()
+        p.page_size = 32
+        assert f(ctypes.byref(p), *args.values(), FAKE, 0, None) == UNSUPPORTED, fn
+
+
+def test_binding_checks():
+    import torch
+
+    p = _params()
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="length"):
+        dsa.pages_fork(p, i, i[:1], None, None, None, i)
+    t = torch.zeros(2, 2, 8)
+
+    def call(target, draft):
+        dsa.verify_draft(p, target, draft, i, None, i, None, i, i, None, i)
+
+    for target, draft in ((t.double(), None), (t[:1], None), (t.transpose(1, 2), None), (t[:, :, ::2], None), (t, t),
+                          (t, t[:, :1].to(torch.bfloat16)), (t, t[:, :1, :4].contiguous()),
+                          (torch.zeros(2, 3, 8)[:, :2], None)):
+        with pytest.raises(ValueError, match="verify_draft"):
+            call(target, draft)
