@@ -192,6 +192,8 @@ int sm_count();
 // Tiled TMA tensor map (cuTensorMapEncodeTiled through the runtime's driver entry point).
 bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
                 const uint64_t* strides, const uint32_t* box, bool swizzle128);
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // ---------------------------------------------------------------- launchers
 // (each returns cudaGetLastError() of its launches)

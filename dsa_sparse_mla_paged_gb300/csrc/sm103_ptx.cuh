@@ -262,7 +262,18 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
   return d;
 }
 
-// Same layout, MN-major operand: each 128-B row holds 64 consecutive MN
+// K-major operand in the 64-byte swizzle layout: rows of 64 B, 8-row atoms of 512 B.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= uint64_t((saddr >> 4) & 0x3FFF);
+  d |= uint64_t(1) << 16;
+  d |= uint64_t(512 >> 4) << 32;               // stride byte offset: 8 rows x 64 B
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(4) << 61;                      // swizzle: 64 B
+  return d;
+}
+
+// The 128-byte swizzle layout again, MN-major operand: each 128-B row holds 64 consecutive MN
 // elements (bf16) of one K index; 8 K-rows per 1024-B atom; `lbo` = bytes
 // between atoms along MN, `sbo` = bytes between 8-row groups along K.
 __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -276,7 +287,7 @@ __device__ __forceinline__ uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t lbo,
 }
 
 // Instruction descriptor: dense, D fp32, A/B formats, both K-major unless stated, M x N.
-//   fmt for kind::f8f6f4: 0 = E4M3; for kind::f16: 1 = BF16.
+//   fmt for kind::f8f6f4: 0 = E4M3; for kind::f16: 0 = FP16, 1 = BF16.
 __host__ __device__ constexpr uint32_t idesc(uint32_t a_fmt, uint32_t b_fmt, uint32_t m, uint32_t n,
                                              uint32_t a_mn_major = 0, uint32_t b_mn_major = 0) {
   return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | (a_mn_major << 15) | (b_mn_major << 16) |
@@ -301,7 +312,7 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
-// The same MMA with the A operand (M rows x K bf16) read from tensor memory:
+// The same MMA with the A operand (M rows x K 16-bit values) read from tensor memory:
 // row m in lane m, elements 2c and 2c + 1 of the row packed in column c (the
 // even one in the low half), one instruction's K = 16 in 8 columns.
 __device__ __forceinline__ void mma_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
