@@ -64,8 +64,9 @@ struct WsLayout {
   size_t opart;     // float [rows][splits][96][512]; dsa_prefix_mla_decode keeps its state (pfx_*) here
   size_t pfx_q;     // half [rows * 96][576] the scaled query
   size_t pfx_qs;    // float [rows * 96] its power-of-two scales
+  size_t pfx_len;   // int32 [rows] tokens past the prefix that a row sees
   size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
-  size_t pfx_lse;   // float [pfx_slots][128] partial log-sum-exps
+  size_t pfx_ml;    // float [pfx_slots][2][2][128] partial softmax maxima and sums
   size_t pfx_part;  // float [pfx_slots][128][512] partial outputs
   size_t lpart;     // float [rows][splits][96]
   size_t topk;      // int32 [rows][topk] (dsa_decode without topk_idx_out)
@@ -117,8 +118,9 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   size_t x = L.opart;
   L.pfx_q = x; x = align256(x + size_t(L.rows) * kHeads * kDQK * 2);
   L.pfx_qs = x; x = align256(x + size_t(L.rows) * kHeads * 4);
+  L.pfx_len = x; x = align256(x + size_t(L.rows) * 4);
   L.pfx_plan = x; x = align256(x + size_t(L.pfx_jobs) * 2 * 4);
-  L.pfx_lse = x; x = align256(x + size_t(L.pfx_slots) * kPfxTileRows * 4);
+  L.pfx_ml = x; x = align256(x + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
   L.pfx_part = x; x = align256(x + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
   o = x > o ? x : o;
   L.lpart = o; o = align256(o + size_t(L.rows) * L.splits * kHeads * 4);
@@ -192,8 +194,6 @@ int sm_count();
 // Tiled TMA tensor map (cuTensorMapEncodeTiled through the runtime's driver entry point).
 bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
                 const uint64_t* strides, const uint32_t* box, bool swizzle128);
-bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
-                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // ---------------------------------------------------------------- launchers
 // (each returns cudaGetLastError() of its launches)
