@@ -62,7 +62,7 @@ struct WsLayout {
   size_t gmax;      // uint32 [rows][gstride] order key of the largest score of each 32 tokens
   size_t gmax128;   // uint32 [rows][g128stride] the same per 128 tokens (dsa_decode; zero between calls)
   size_t opart;     // float [rows][splits][96][512]; dsa_prefix_mla_decode keeps its state (pfx_*) here
-  size_t pfx_q;     // half [rows * 96][576] the scaled query
+  size_t pfx_q;     // [72][rows * 96] 16-B chunks of the prepared query
   size_t pfx_qs;    // float [rows * 96] its power-of-two scales
   size_t pfx_len;   // int32 [rows] tokens past the prefix that a row sees
   size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
@@ -194,6 +194,8 @@ int sm_count();
 // Tiled TMA tensor map (cuTensorMapEncodeTiled through the runtime's driver entry point).
 bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
                 const uint64_t* strides, const uint32_t* box, bool swizzle128);
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dtype, const void* base, int rank, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // ---------------------------------------------------------------- launchers
 // (each returns cudaGetLastError() of its launches)

@@ -10,18 +10,19 @@
 // borders; each segment leaves an unnormalised partial output with its softmax
 // maximum and sum, and the merge kernel adds up the segments of a row's two jobs.
 //
-// The products take fp16 operands and fp32 sums. E4M3 and E2M1 x E4M3 values are exact
-// in fp16 (one conversion instruction for two values; to bf16 it takes four). The
-// query becomes fp16 with a power of two per head, which leaves every value exact
-// down to 2^-32 of the head's largest (prefix_query_kernel). Softmax weights are
-// scaled to at most 2^7 (2^15 until the running maximum is raised), so that fp16 holds
-// them to 11 bits down to 2^-21 of the maximum.
+// The second product takes fp16 operands: E4M3 and E2M1 x E4M3 values are exact in
+// fp16, and softmax weights are scaled to at most 2^7 (2^15 until the running maximum
+// is raised), so that fp16 holds them to 11 bits down to 2^-21 of the maximum. The
+// first product takes the FP8 latents as they lie in the cache, against the query as
+// the sum of an E4M3 and an E5M2 part (which together hold a bf16 value's 8 bits), or
+// NVFP4 latents as fp16 against the query in fp16. Sums are fp32 throughout.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "dsa_internal.cuh"
 #include "sm103_ptx.cuh"
@@ -41,34 +42,43 @@ namespace {
 // another's stores that is 1,024 cycles, and it ran at 3,000 cycles a tile.)
 //   CTA 0: warps 0..3, 4..7  softmax of the even and of the odd tiles: one query head
 //                            per thread; the two groups hand the running maximum on
-//          warps 8..15       converters: the page's 64 rows to fp16 (nine 128-B swizzled
-//                            K-blocks of 64 dims); at a new job Q to tensor memory
+//          warps 8..15       at a new job Q to tensor memory; NVFP4: two groups of
+//                            converters, the page's 64 rows to fp16 (nine K-blocks)
 //          warp  16          MMA: Q from tensor memory (288 columns), S in 3 x 64 columns
+//          warp  17          FP8: the page's rows by TMA, as they are
 //   CTA 1: warps 0..3        rescale O where the maximum was raised, write O at a job's end
-//          warps 8..15       converters: the 512 value dims, eight K-blocks read MN-major
+//          warps 4..15       three groups of converters: the 512 value dims to fp16 (eight
+//                            K-blocks of 64 dims, read MN-major)
 //          warp  16          MMA: O in all 512 columns, P from shared memory
-// A converter thread loads a piece of the next tile as soon as it has stored that
-// piece of this one, so that every load has a whole tile's time.
+// Conversion is what bounds the pair: cvt.f16x2.e4m3x2 issues once in about 12 cycles
+// per SM quarter, so 64 x 576 values would take 1,700 cycles; FP8 keys are therefore
+// multiplied unconverted, and FP8 values moved into fp16's bit fields by shifts and
+// masks (expand_bits). A converter group issues the loads of its next tile right after
+// it has stored one.
 // ---------------------------------------------------------------------------
 constexpr int kNT = 64;                      // tokens per tile: one page
 constexpr int kBlk = kNT * 128;              // 8,192 B: a K-block, 64 rows of 64 fp16
 constexpr int kKBlks = kDQK / 64;            // 9
 constexpr int kVBlks = kDNope / 64;          // 8
-constexpr int kKBuf = kKBlks * kBlk;         // 73,728
+constexpr int kKBuf = kKBlks * kBlk;         // 73,728 (NVFP4)
+constexpr int kKBuf8 = 4 * kBlk + kBlk / 2;  // 36,864 (FP8: 64 rows of 128 E4M3, and of 64 for the rope dims)
 constexpr int kVBuf = kVBlks * kBlk;         // 65,536
-constexpr int kKBufs = 2, kVBufs = 3, kSBufs = 3, kPBufs = 2;
+constexpr int kVBufs = 3, kSBufs = 3, kPBufs = 2;
+template <bool kNv>
+constexpr int kKBufs = kNv ? 2 : 4;
+static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
 // P: 8 chunks of 8 tokens, each 16 B per row in row order (the unswizzled core
 // matrices of the MMA, and 512 contiguous bytes for a warp's remote store)
 constexpr int kPChunk = 128 * 16;
 constexpr int kPBuf = 8 * kPChunk;           // 16,384
 constexpr uint32_t kPBytes = kPBuf + 128 * 4;  // P and the rescale factors, per tile
 constexpr int kMasks = 8;
-constexpr int kThreads = 640;                // five warpgroups; the last holds the MMA warp and three idle ones
-constexpr int kMmaWarp = 16;
+constexpr int kThreads = 640;                // five warpgroups; the last holds the MMA and the TMA warp and two idle ones
+constexpr int kMmaWarp = 16, kTmaWarp = 17;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 36;
+constexpr int kNumBars = 42;
 constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + 512);
-constexpr size_t kSmemS = kKBufs * kKBuf + 512 + kMasks * 8;
+constexpr size_t kSmemS = 2 * kKBuf + 512 + kMasks * 8;
 constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 16;
 static_assert(kSmem + 512 <= 232448, "shared memory of one CTA");
 constexpr float kPShift = 7.f;               // weights are 2^(z - max + 7)
@@ -76,7 +86,7 @@ constexpr float kLazy = 8.f;                 // the maximum in use is raised whe
 constexpr int kJobCost = 3;                  // what a job's start and end take, in tiles
 
 struct PfxArgs {
-  const uint4* q16;  // [72][rows * 96] chunks of 8 dims: 16 B per head, in head order
+  const uint4* q;    // [72][rows * 96] 16-B chunks of the prepared query, each head by head
   const float* qs;
   const uint8_t* lat;
   const int32_t* prefix_pages;
@@ -88,7 +98,8 @@ struct PfxArgs {
   int* err;
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
-  float scale_log2, lat_scale;
+  float scale_log2, out_scale;
+  int swapped;
 };
 
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
@@ -115,6 +126,7 @@ struct Walk {
     return k1 > k0;
   }
   __device__ __forceinline__ bool next(const PfxArgs& a) {
+#pragma unroll 1
     while (left > 0 && ++job < a.tiles + a.rows)
       if (take(a, 0)) return true;
     return false;
@@ -133,6 +145,17 @@ __device__ __forceinline__ void expand16(const uint4 w, uint4& lo, uint4& hi) {
   hi.x = half2_from_e4m3x2(w.z); hi.y = half2_from_e4m3x2(w.z >> 16);
   hi.z = half2_from_e4m3x2(w.w); hi.w = half2_from_e4m3x2(w.w >> 16);
 }
+
+// 16 E4M3 bytes -> 16 fp16 of 2^-8 times their values: E4M3's exponent and mantissa
+// at bits 13..7 and its sign at bit 15 are the fp16 of value * 2^(7 - 15), subnormals
+// included. The bytes 0 1 2 3 of a word come out in the order 0 2 1 3. NaN (0x7F)
+// becomes 1.875: a token with a NaN latent has NaN scores, which reach every output
+// of the rows that see it, and in a token that no row sees the values must not matter.
+__device__ __forceinline__ void expand_bits(uint32_t w, uint32_t& even, uint32_t& odd) {
+  even = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
+  odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
+}
+constexpr float kBitsScale = 256.f;
 
 // 8 E2M1 values times an E4M3 scale (a pair of fp16): 6 significant bits, exact.
 __device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
@@ -153,145 +176,165 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
   *reinterpret_cast<uint4*>(row + (((c + 1) ^ (tok & 7)) << 4)) = hi;
 }
 
-// A converter thread's share of a tile; warp w of 8 has nope K-block w. FP8: eight
-// 16-B pieces (8 tokens x 4 pieces a warp load: 64-B runs, and stores without bank
-// conflicts). NVFP4: four 16-B units (32 values, two scales). And kRope: one 16-B
-// piece of the rope dims. Tokens at or past `valid` are zeros.
+// A converter thread's share of a tile; warp w of 4 has nope K-blocks 2w and 2w + 1.
+// FP8: sixteen 16-B pieces (8 tokens x 4 pieces a warp load: 64-B runs, and stores
+// without bank conflicts). NVFP4: eight 16-B units (32 values, two scales; zeros for
+// tokens at or past `valid`, whose scales could be NaN). And kRope (NVFP4 keys): two
+// 16-B pieces of the rope dims.
 template <bool kNv, bool kRope>
 struct TileRegs {
-  static constexpr int kPieces = kNv ? 4 : 8;
-  uint4 v[kPieces];
-  uint32_t s[kNv ? 4 : 1];
-  uint4 rope;
-  __device__ __forceinline__ void load(int u, const uint8_t* page, int valid, int w, int lane) {
-    if constexpr (kNv) {
-      const int tok = u * 16 + (lane >> 1), unit = 2 * w + (lane & 1);
-      const uint8_t* row = page + tok * 352;
-      v[u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : make_uint4(0, 0, 0, 0);
-      s[u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
-    } else {
-      const int tok = u * 8 + (lane >> 2);
-      v[u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(page + tok * 576 + 64 * w + 16 * (lane & 3)))
-                         : make_uint4(0, 0, 0, 0);
+  static constexpr int kPieces = kNv ? 4 : 8;  // per K-block
+  uint4 v[2][kPieces];
+  uint32_t s[2][kNv ? 4 : 1];
+  uint4 rope[2];
+  __device__ __forceinline__ void load(const uint8_t* page, int valid, int w, int lane) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        if constexpr (kNv) {
+          const int tok = u * 16 + (lane >> 1), unit = 4 * w + 2 * b + (lane & 1);
+          const uint8_t* row = page + tok * 352;
+          v[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
+          s[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
+        } else {
+          const int tok = u * 8 + (lane >> 2);
+          v[b][u] = __ldg(reinterpret_cast<const uint4*>(page + tok * 576 + 64 * (2 * w + b) + 16 * (lane & 3)));
+        }
+      }
+    if constexpr (kRope) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ct = b * 128 + w * 32 + lane, tok = ct >> 2;
+        rope[b] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(page + tok * 352 + 288 + 16 * (ct & 3))) : zero;
+      }
     }
   }
-  __device__ __forceinline__ void load_rope(const uint8_t* page, int valid, int w, int lane) {
-    const int ct = w * 32 + lane, tok = ct >> 2;
-    rope = tok < valid ? __ldg(reinterpret_cast<const uint4*>(page + tok * (kNv ? 352 : 576) + (kNv ? 288 : 512) + 16 * (ct & 3)))
-                       : make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void store(int u, uint8_t* buf, int w, int lane) const {
-    uint8_t* blk = buf + w * kBlk;
-    if constexpr (kNv) {
-      const int tok = u * 16 + (lane >> 1), c0 = (lane & 1) * 4;
-      const uint32_t two = half2_from_e4m3x2(s[u]);
-      const __half2 h = *reinterpret_cast<const __half2*>(&two);
-      const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-      put2(blk, tok, c0, expand_e2m1(v[u].x, s0), expand_e2m1(v[u].y, s0));
-      put2(blk, tok, c0 + 2, expand_e2m1(v[u].z, s1), expand_e2m1(v[u].w, s1));
-    } else {
-      uint4 lo, hi;
-      expand16(v[u], lo, hi);
-      put2(blk, u * 8 + (lane >> 2), (lane & 3) * 2, lo, hi);
-    }
-  }
-  __device__ __forceinline__ void store_rope(uint8_t* buf, int w, int lane) const {
-    const int ct = w * 32 + lane;
+  __device__ __forceinline__ void store(uint8_t* buf, int w, int lane) const {
     uint4 lo, hi;
-    expand16(rope, lo, hi);
-    put2(buf + 8 * kBlk, ct >> 2, (ct & 3) * 2, lo, hi);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint8_t* blk = buf + (2 * w + b) * kBlk;
+#pragma unroll
+      for (int u = 0; u < kPieces; ++u) {
+        if constexpr (kNv) {
+          const int tok = u * 16 + (lane >> 1), c0 = (lane & 1) * 4;
+          const uint32_t two = half2_from_e4m3x2(s[b][u]);
+          const __half2 h = *reinterpret_cast<const __half2*>(&two);
+          const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+          put2(blk, tok, c0, expand_e2m1(v[b][u].x, s0), expand_e2m1(v[b][u].y, s0));
+          put2(blk, tok, c0 + 2, expand_e2m1(v[b][u].z, s1), expand_e2m1(v[b][u].w, s1));
+        } else {
+          expand_bits(v[b][u].x, lo.x, lo.y);
+          expand_bits(v[b][u].y, lo.z, lo.w);
+          expand_bits(v[b][u].z, hi.x, hi.y);
+          expand_bits(v[b][u].w, hi.z, hi.w);
+          put2(blk, u * 8 + (lane >> 2), (lane & 3) * 2, lo, hi);
+        }
+      }
+    }
+    if constexpr (kRope) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ct = b * 128 + w * 32 + lane;
+        expand16(rope[b], lo, hi);
+        put2(buf + 8 * kBlk, ct >> 2, (ct & 3) * 2, lo, hi);
+      }
+    }
   }
 };
 
-// The converter warps of either CTA (kRope: CTA 0, whose tiles have the rope dims).
-// full / free: the buffers' barriers; masks / mask_full: the valid tokens of a tile,
-// for the softmax (CTA 0). at_job(g, job): what CTA 0 does after a job's first tile.
-template <bool kNv, bool kRope, int kBufs, typename AtJob>
-__device__ __forceinline__ bool convert(const PfxArgs& a, Walk wk, int gtot, int job0, int unit, int units, int w,
-                                        int lane, uint8_t* bufs, uint32_t full, uint32_t free, unsigned long long* masks,
-                                        uint32_t mask_full, AtJob at_job) {
-  constexpr int kSize = kRope ? kKBuf : kVBuf;
-  TileRegs<kNv, kRope> t;
-  const int32_t* pages = nullptr;  // page numbers of the walk's job
-  int len = 0, k = 0;              // its tokens, and the next tile's place in it
-  auto enter = [&]() {
+// The page of tile k of the walk's job and its tokens that the job sees, over the
+// tiles of a run in order. A page number is loaded a tile before it is asked for.
+struct Pages {
+  Walk wk;
+  const int32_t* list;  // page numbers of the walk's job
+  int len, k;           // its tokens, and the next tile's place in it
+  int pg, left, begins; // the fetched tile: page number, tokens, the job that it begins (-1 none)
+  __device__ __forceinline__ void enter(const PfxArgs& a) {
     if (wk.job < a.tiles) {
-      pages = a.prefix_pages;
+      list = a.prefix_pages;
       len = a.prefix;
     } else {
       const int r = wk.job - a.tiles;
-      pages = a.table + size_t(r / a.n_q) * a.max_pages + a.prefix / kNT;
+      list = a.table + size_t(r / a.n_q) * a.max_pages + a.prefix / kNT;
       len = a.lens[r];
     }
     k = wk.k0;
-  };
-  // the next tile: its page number is loaded a tile ahead of its rows
-  int pg = -1, left = 0;
-  int begins = -1;                 // the job that the tile begins, -1 none
-  auto fetch = [&]() {
+    begins = wk.job;
+  }
+  __device__ __forceinline__ bool start(const PfxArgs& a, int job0, int unit, int units) {
+    if (!wk.start(a, job0, unit, units)) return false;
+    enter(a);
+    pg = __ldg(list + k);
+    left = min(kNT, len - k * kNT);
+    ++k;
+    return true;
+  }
+  __device__ __forceinline__ void fetch(const PfxArgs& a) {
     begins = -1;
     if (k >= wk.k1) {
       if (!wk.next(a)) return;
-      enter();
-      begins = wk.job;
+      enter(a);
     }
-    pg = __ldg(pages + k);
+    pg = __ldg(list + k);
     left = min(kNT, len - k * kNT);
     ++k;
-  };
-  if (gtot == 0 || !wk.start(a, job0, unit, units)) return true;
-  enter();
-  fetch();
-  int job = wk.job;                // the job that the loaded tile begins
-  const uint8_t* page;
-  int valid;
-  auto resolve = [&]() {
-    const bool good = pg >= 0 && pg < a.num_pages;
+  }
+  __device__ __forceinline__ bool good(const PfxArgs& a) const { return pg >= 0 && pg < a.num_pages; }
+};
+
+// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (kRope:
+// CTA 0). full / free: the buffers' barriers; masks / mask_full: the valid tokens of a
+// tile, for the softmax (CTA 0). at_job(job): what CTA 0 does at a job's first tile.
+template <bool kNv, bool kRope, int kBufs, int kGroups, typename AtJob>
+__device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int job0, int unit, int units, int group, int w, int lane,
+                                        uint8_t* bufs, uint32_t full, uint32_t free, unsigned long long* masks,
+                                        uint32_t mask_full, AtJob at_job) {
+  constexpr int kSize = kRope ? kKBuf : kVBuf;
+  TileRegs<kNv, kRope> t;
+  Pages pages;
+  if (gtot == 0 || !pages.start(a, job0, unit, units)) return true;
+  int valid = 0;
+  auto load = [&]() {
+    const bool good = pages.good(a);
     if (!good && kRope && w == 0 && lane == 0) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
-    valid = good ? left : 0;
-    page = a.lat + int64_t(good ? pg : 0) * a.stride;
+    valid = good ? pages.left : 0;
+    t.load(a.lat + int64_t(good ? pages.pg : 0) * a.stride, valid, w, lane);
   };
-  resolve();
-#pragma unroll
-  for (int u = 0; u < t.kPieces; ++u) t.load(u, page, valid, w, lane);
-  if constexpr (kRope) t.load_rope(page, valid, w, lane);
-  if (gtot > 1) fetch();
+  int job = pages.begins;  // the job that tile g begins, -1 none
+  if (group == 0) load();
+  if (gtot > 1) pages.fetch(a);
 #pragma unroll 1
-  for (int g = 0; g < gtot; ++g) {
-    const int buf = g % kBufs, now_valid = valid;
+  for (int g = 0, turn = 0; g < gtot; ++g, turn = turn + 1 == kGroups ? 0 : turn + 1) {
     const int now_job = job;
-    const bool more = g + 1 < gtot;
-    if (more) {
-      resolve();
-      job = begins;
-      if (g + 2 < gtot) fetch();
-    }
-    if (g >= kBufs && !ptx::mbar_wait(free + 8 * (buf), uint32_t(g / kBufs - 1) & 1u)) return false;
-    uint8_t* dst = bufs + buf * kSize;
-#pragma unroll
-    for (int u = 0; u < t.kPieces; ++u) {
-      t.store(u, dst, w, lane);
-      if (more) t.load(u, page, valid, w, lane);
-    }
-    if constexpr (kRope) {
-      t.store_rope(dst, w, lane);
-      if (more) t.load_rope(page, valid, w, lane);
-      if (w == 0 && lane == 0) {
-        masks[g % kMasks] = now_valid >= 64 ? ~0ull : (1ull << now_valid) - 1;
+    job = pages.begins;
+    if (turn == group) {
+      const int buf = g % kBufs;
+      if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
+      t.store(bufs + buf * kSize, w, lane);
+      if (kRope && w == 0 && lane == 0) {
+        masks[g % kMasks] = valid >= 64 ? ~0ull : (1ull << valid) - 1;
         ptx::mbar_arrive(mask_full + 8 * (g % kMasks));
       }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
     }
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(full + 8 * (buf));
-    if (now_job >= 0 && !at_job(g, now_job)) return false;
+    // (no tile is in the registers when the query goes through them)
+    if (kRope && now_job >= 0 && !at_job(now_job)) return false;
+    // tile g + 1, in flight while the other groups store theirs
+    if (g + 1 < gtot && (turn + 1) % kGroups == group) load();
+    if (g + 2 < gtot) pages.fetch(a);
   }
   return true;
 }
 
 template <bool kNv>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    prefix_mla_kernel(const __grid_constant__ PfxArgs a) {
+    prefix_mla_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
+                      const __grid_constant__ PfxArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr size_t kData = kSmemO > kSmemS ? kSmemO : kSmemS;
@@ -299,8 +342,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t bars = ptx::smem_u32(sm) + uint32_t(kData);
   const uint32_t mma_done = bars + 0 * 8;
   const uint32_t q_full = bars + 1 * 8;
-  const uint32_t k_full = bars + 2 * 8;      // [2]
-  const uint32_t k_free = bars + 4 * 8;      // [2]  S of the buffer's tile is done
+  const uint32_t q_free = bars + 40 * 8;     // every product with the job's query is done
+  const uint32_t k_full = bars + 2 * 8;      // [kKBufs]
+  const uint32_t k_free = bars + 36 * 8;     // [kKBufs]  S of the buffer's tile is done
   const uint32_t s_full = bars + 6 * 8;      // [3]
   const uint32_t s_free = bars + 9 * 8;      // [3]  the softmax has read S
   const uint32_t turn = bars + 12 * 8;       // [4]  by softmax warp: the tile's maximum is decided
@@ -313,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kData + kNumBars * 8);
   // CTA 0
   uint8_t* KB = sm;
-  float* m_run = reinterpret_cast<float*>(sm + kKBufs * kKBuf);  // [128] the running maximum in use
+  float* m_run = reinterpret_cast<float*>(sm + 2 * kKBuf);  // [128] the running maximum in use
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(m_run + 128);
   // CTA 1
   uint8_t* VB = sm;
@@ -329,9 +373,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     ptx::mbar_init(mma_done, 1);
     ptx::mbar_init(q_full, 8);
+    ptx::mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(k_full + 8 * (i), 8);
-      ptx::mbar_init(k_free + 8 * (i), 1);
       ptx::mbar_init(p_free + 8 * (i), 1);
       ptx::mbar_init(p_full + 8 * (i), 1);
       ptx::mbar_init(o_ok + 8 * (i), 4);
@@ -339,10 +382,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 3; ++i) {
       ptx::mbar_init(s_full + 8 * (i), 1);
       ptx::mbar_init(s_free + 8 * (i), 4);
-      ptx::mbar_init(v_full + 8 * (i), 8);
+      ptx::mbar_init(v_full + 8 * (i), 4);
       ptx::mbar_init(v_free + 8 * (i), 1);
     }
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(turn + 8 * (i), 1);
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(turn + 8 * i, 1);
+      ptx::mbar_init(k_full + 8 * i, kNv ? 4 : 1);
+      ptx::mbar_init(k_free + 8 * i, 1);
+    }
     for (int i = 0; i < kMasks; ++i) ptx::mbar_init(mask_full + 8 * (i), 1);
     ptx::fence_mbar_init();
   }
@@ -441,36 +488,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == kMmaWarp && half == 0) {
       // ---------------------------------------------------------- S = Q . C^T
-      const uint32_t id = ptx::idesc(0, 0, 128, kNT);
       const uint32_t kb0 = ptx::smem_u32(KB);
       int g = 0, qn = 0;
+#pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
         if (!ptx::mbar_wait(q_full, uint32_t(qn++) & 1u)) { ok = false; break; }
-        for (int k = wk.k0; k < wk.k1; ++k, ++g) {
-          const int buf = g % kKBufs, sb = g % kSBufs;
-          if (!ptx::mbar_wait(k_full + 8 * (buf), uint32_t(g / kKBufs) & 1u)) { ok = false; break; }
-          if (g >= kSBufs && !ptx::mbar_wait(s_free + 8 * (sb), uint32_t(g / kSBufs - 1) & 1u)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const uint32_t kb = kb0 + buf * kKBuf, s = tmem + kSCol + sb * kNT;
-          if (ptx::elect_one()) {
 #pragma unroll 1
-            for (int j = 0; j < kKBlks; ++j)
+        for (int k = wk.k0; k < wk.k1; ++k, ++g) {
+          const int buf = g % kKBufs<kNv>, sb = g % kSBufs;
+          if (!ptx::mbar_wait(k_full + 8 * buf, uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
+          if (g >= kSBufs && !ptx::mbar_wait(s_free + 8 * sb, uint32_t(g / kSBufs - 1) & 1u)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t kb = kb0 + buf * (kNv ? kKBuf : kKBuf8), s = tmem + kSCol + sb * kNT;
+          if (ptx::elect_one()) {
+            if constexpr (kNv) {
+              const uint32_t id = ptx::idesc(0, 0, 128, kNT);
+#pragma unroll 1
+              for (int j = 0; j < kKBlks; ++j)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                ptx::mma_f16_tmem_a(s, tmem + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id,
-                                    (j | kk) ? 1u : 0u);
-            ptx::mma_commit(k_free + 8 * (buf));
-            ptx::mma_commit(s_full + 8 * (sb));
+                for (int kk = 0; kk < 4; ++kk)
+                  ptx::mma_f16_tmem_a(s, tmem + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id,
+                                      (j | kk) ? 1u : 0u);
+            } else {
+#pragma unroll 1
+              for (int part = 0; part < 2; ++part) {  // the query's E4M3, then its E5M2 part
+                const uint32_t id = ptx::idesc(part, 0, 128, kNT), q = tmem + part * 144;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_f8_tmem_a(s, q + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id,
+                                       (part | j | kk) ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                  ptx::mma_f8_tmem_a(s, q + 128 + kk * 8, ptx::sdesc_sw64(kb + 4 * kBlk + kk * 32), id, 1u);
+              }
+            }
+            ptx::mma_commit(k_free + 8 * buf);
+            ptx::mma_commit(s_full + 8 * sb);
+            if (k + 1 == wk.k1) ptx::mma_commit(q_free);
           }
           __syncwarp();
         }
+      }
+    } else if (warp == kTmaWarp && half == 0 && !kNv) {
+      // ---------------------------------------------------------- FP8 keys
+      Pages pages;
+      if (gtot > 0 && pages.start(a, job0, unit0, units)) {
+        const uint32_t kb0 = ptx::smem_u32(KB);
+#pragma unroll 1
+        for (int g = 0; g < gtot; ++g) {
+          const int buf = g % kKBufs<kNv>;
+          const bool good = pages.good(a);
+          const int valid = good ? pages.left : 0, pg = good ? pages.pg : 0;
+          if (g + 1 < gtot) pages.fetch(a);
+          if (g >= kKBufs<kNv> && !ptx::mbar_wait(k_free + 8 * buf, uint32_t(g / kKBufs<kNv> - 1) & 1u)) { ok = false; break; }
+          if (lane == 0) {
+            if (!good) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+            masks[g % kMasks] = valid >= 64 ? ~0ull : (1ull << valid) - 1;
+            ptx::mbar_arrive(mask_full + 8 * (g % kMasks));
+            const uint32_t dst = kb0 + buf * kKBuf8, bar = k_full + 8 * buf;
+            ptx::mbar_arrive_expect_tx(bar, kKBuf8);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ptx::tma_load_3d(dst + j * kBlk, &kmap, bar, j * 128, 0, pg);
+            ptx::tma_load_3d(dst + 4 * kBlk, &rmap, bar, kDNope, 0, pg);
+          }
+          __syncwarp();
+        }
+        // no copy left in flight
+        if (!ok)
+          for (int i = 0; i < kKBufs<kNv>; ++i) ptx::mbar_wait(k_full + 8 * i, 0, 1 << 10);
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- O += P . V
       const uint32_t id = ptx::idesc(0, 0, 128, 256, 0, 1);
       const uint32_t vb0 = ptx::smem_u32(VB), pb0 = ptx::smem_u32(PB);
       int g = 0;
+#pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
+#pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
           const int buf = g % kVBufs, pb = g % kPBufs;
           if (!ptx::mbar_wait(v_full + 8 * (buf), uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
@@ -499,36 +595,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_wait(mma_done, 0);
     }
   } else if (warp >= 8) {
-    // ------------------------------------------------------------ converters
-    const int w = warp - 8;
+    // ------------------------------------------------------------ converters, query
+    const int w = warp & 3, group = (warp - 8) >> 2;
     if (half == 0) {
-      // the job's query: each warp 32 heads of five or four K-blocks
-      auto load_q = [&](int g, int job) {
-        // every product with the old query is done
-        if (g >= 1 && !ptx::mbar_wait(k_free + 8 * ((g - 1) % kKBufs), uint32_t((g - 1) / kKBufs) & 1u)) return false;
-        const int row = (w & 3) * 32 + lane;
+      // the job's query: each warp 32 heads of five or four times 32 columns
+      int jobs = 0;
+      auto load_q = [&](int job) {
+        if (jobs >= 1 && !ptx::mbar_wait(q_free, uint32_t(jobs - 1) & 1u)) return false;
+        ++jobs;
+        const int row = w * 32 + lane;
         const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
         const int heads = a.rows * kHeads;
         const bool in = hr < heads;
 #pragma unroll 1
-        for (int kb = w < 4 ? 0 : 5; kb < (w < 4 ? 5 : kKBlks); ++kb) {
+        for (int kb = group ? 5 : 0; kb < (group ? 9 : 5); ++kb) {
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 x = in ? __ldg(a.q16 + size_t(kb * 8 + i) * heads + hr) : make_uint4(0, 0, 0, 0);
+            const uint4 x = in ? __ldg(a.q + size_t(kb * 8 + i) * heads + hr) : make_uint4(0, 0, 0, 0);
             v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
           }
-          ptx::tmem_st32_u(tmem + (uint32_t((w & 3) * 32) << 16) + kb * 32, v);
+          ptx::tmem_st32_u(tmem + (uint32_t(w * 32) << 16) + kb * 32, v);
         }
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(q_full);
         return true;
       };
-      ok = convert<kNv, true, kKBufs>(a, wk, gtot, job0, unit0, units, w, lane, KB, k_full, k_free, masks, mask_full, load_q);
+      if constexpr (kNv) {
+        ok = convert<true, true, kKBufs<true>, 2>(a, gtot, job0, unit0, units, group, w, lane, KB, k_full, k_free, masks,
+                                                  mask_full, load_q);
+      } else {
+#pragma unroll 1
+        for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) ok = load_q(wk.job);
+      }
     } else {
-      ok = convert<kNv, false, kVBufs>(a, wk, gtot, job0, unit0, units, w, lane, VB, v_full, v_free, nullptr, 0,
-                                       [](int, int) { return true; });
+      ok = convert<kNv, false, kVBufs, 3>(a, gtot, job0, unit0, units, group + 1, w, lane, VB, v_full, v_free, nullptr, 0,
+                                          [](int) { return true; });
     }
   } else if (half == 0) {
     // ------------------------------------------------------------ softmax
@@ -540,11 +643,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t f_peer = ptx::mapa_shared(ptx::smem_u32(factor + row), 1);
     const uint32_t bar_peer = ptx::mapa_shared(p_full, 1);
     int g0 = 0;  // the segment's first tile
+#pragma unroll 1
     for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
       const int hr = (wk.job < a.tiles ? wk.job * kPfxTileRows : (wk.job - a.tiles) * kHeads) + row;
       const float cs = fmaxf(hr < a.rows * kHeads ? a.scale_log2 * a.qs[hr] : 1.f, 1.1754944e-38f);
       float m_mine = -INFINITY, l = 0.f;  // the maximum that l is relative to
       const int g1 = g0 + wk.k1 - wk.k0;
+#pragma unroll 1
       for (int g = g0 + ((g0 ^ group) & 1); g < g1; g += 2) {
         const int sb = g % kSBufs, pb = g % kPBufs;
         if (!ptx::mbar_wait(s_full + 8 * (sb), uint32_t(g / kSBufs) & 1u)) { ok = false; break; }
@@ -616,12 +721,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if (warp < 4) {
+    if (warp >= 4) {
+      ok = convert<kNv, false, kVBufs, 3>(a, gtot, job0, unit0, units, 0, warp & 3, lane, VB, v_full, v_free, nullptr, 0,
+                                          [](int) { return true; });
+    } else {
       // ---------------------------------------------------------- O: rescaling and output
       const int row = warp * 32 + lane;
       const uint32_t lane_base = uint32_t(warp * 32) << 16;
       int g = 0;
+#pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
+#pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
           const int pb = g % kPBufs;
           if (!ptx::mbar_wait_cluster(p_full + 8 * (pb), uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
@@ -678,17 +788,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The query as fp16: each head's 576 values times a power of two that takes its
-// largest into [2^14, 2^15). A bf16 value has 8 significant bits, so what is
-// above 2^-32 of the head's largest stays exact (fp16's subnormals are multiples
-// of 2^-24). One warp per head. Written in chunks of 8 dims, head by head, so that
-// 32 consecutive heads load 512 contiguous bytes into tensor memory wherever a
-// tile of heads starts.
+// The query, each head's 576 values times a power of two, one warp per head. For NVFP4
+// latents as fp16, the largest in [2^14, 2^15): a bf16 value has 8 significant bits,
+// so what is above 2^-32 of the largest stays exact (fp16's subnormals are multiples
+// of 2^-24). For FP8 latents as x = hi + lo, hi = E4M3(x) and lo = E5M2(x - hi), the
+// largest in [2^7, 2^8): hi has 4 bits of x, and the rest is at most 8 units of x's
+// last bit, which three bits hold, so the sum is exact where hi is not subnormal,
+// that is above 2^-13 of the largest; below, x - hi <= 2^-10 is off by at most 2^-13,
+// 2^-20 of the largest. Written in 16-B chunks, each head by head, so that
+// 32 consecutive heads load 512 contiguous bytes into tensor memory wherever a tile
+// of heads starts.
 // ---------------------------------------------------------------------------
 constexpr int kQueryWarps = 8;
 
+template <bool kNv>
 __global__ void __launch_bounds__(32 * kQueryWarps)
-    prefix_query_kernel(const uint32_t* __restrict__ q, int heads, uint32_t* __restrict__ q16, float* __restrict__ qs,
+    prefix_query_kernel(const uint32_t* __restrict__ q, int heads, uint32_t* __restrict__ prepared, float* __restrict__ qs,
                         const int32_t* __restrict__ ctx, int32_t* __restrict__ lens, int n_q, int prefix, int cap,
                         int* err) {
   pdl_trigger();
@@ -703,31 +818,54 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
   }
   const int hr = blockIdx.x * kQueryWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (hr >= heads) return;
+  // nine words (two values each) per lane; FP8 needs them in pairs (four values to a word)
   constexpr int kWords = kDQK / 2, kPer = kWords / 32;
-  uint32_t w[kPer];
+  uint32_t w[kPer + 1];
+  auto word = [&](int i) { return kNv ? i * 32 + lane : (i >> 1) * 64 + 2 * lane + (i & 1); };
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    w[i] = __ldg(q + size_t(hr) * kWords + i * 32 + lane);
+  for (int i = 0; i < kPer + 1; ++i) {
+    w[i] = word(i) < kWords && i < (kNv ? kPer : kPer + 1) ? __ldg(q + size_t(hr) * kWords + word(i)) : 0u;
     m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   // 2^-e in two factors: e reaches down to -147
-  const int e = m > 0.f && m < INFINITY ? ilogbf(m) - 14 : 0;
+  const int e = m > 0.f && m < INFINITY ? ilogbf(m) - (kNv ? 14 : 7) : 0;
   const float f0 = scalbnf(1.f, -e / 2), f1 = scalbnf(1.f, -e - (-e / 2));
+  if constexpr (kNv) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f0 * f1, __uint_as_float(w[i] & 0xFFFF0000u) * f0 * f1);
-    const int word = i * 32 + lane;
-    q16[(size_t(word >> 2) * heads + hr) * 4 + (word & 3)] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < kPer; ++i) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f0 * f1, __uint_as_float(w[i] & 0xFFFF0000u) * f0 * f1);
+      prepared[(size_t(word(i) >> 2) * heads + hr) * 4 + (word(i) & 3)] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer + 1; i += 2) {
+      if (word(i) >= kWords) continue;
+      uint32_t hi = 0, lo = 0;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const uint32_t two = w[i + (d >> 1)];
+        const float x = __uint_as_float(d & 1 ? two & 0xFFFF0000u : two << 16) * f0 * f1;
+        const __nv_fp8_storage_t h = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+        const __half_raw hv = __nv_cvt_fp8_to_halfraw(h, __NV_E4M3);
+        const __nv_fp8_storage_t l = __nv_cvt_float_to_fp8(x - __half2float(*reinterpret_cast<const __half*>(&hv)),
+                                                           __NV_SATFINITE, __NV_E5M2);
+        hi |= uint32_t(h) << (8 * d);
+        lo |= uint32_t(l) << (8 * d);
+      }
+      const int out = word(i) >> 1;  // the word of four dims: 16 dims a chunk
+      prepared[(size_t(out >> 2) * heads + hr) * 4 + (out & 3)] = hi;
+      prepared[(size_t(36 + (out >> 2)) * heads + hr) * 4 + (out & 3)] = lo;
+    }
   }
   if (lane == 0) qs[hr] = scalbnf(1.f, e);
 }
 
 // ---------------------------------------------------------------------------
 // Merge of a row's segments, those of its prefix tile and then those of its private
-// job: with M the largest maximum, out = lat_scale * sum_i 2^(m_i - M) O_i / L and
+// job: with M the largest maximum, out = scale * sum_i 2^(m_i - M) O_i / L and
 // L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums of their own;
 // its O is relative to the larger of their maxima). One CTA per (row, 3 heads),
 // 128 threads per head, 4 dims each.
@@ -766,12 +904,17 @@ __global__ void __launch_bounds__(128 * kMergeHeads) prefix_merge_kernel(PfxArgs
       acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
     }
     if (tot != 0.f) {  // NaN stays NaN
-      const float inv = a.lat_scale / tot;
+      const float inv = a.out_scale / tot;
       acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
       L = (mm - kPShift + log2f(tot)) * 0.6931471805599453f;
     } else {
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+  }
+  if (a.swapped) {  // expand_bits left dims 1 and 2 of four in each other's place
+    const float y = acc.y;
+    acc.y = acc.z;
+    acc.z = y;
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
   uint2 pk;
@@ -787,7 +930,7 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
                               const int32_t* prefix_pages, int prefix_len, const int32_t* block_table,
                               const int32_t* ctx_lens, void* out, float* lse, cudaStream_t st) {
   PfxArgs a;
-  a.q16 = reinterpret_cast<const uint4*>(ws + L.pfx_q);
+  a.q = reinterpret_cast<const uint4*>(ws + L.pfx_q);
   a.qs = reinterpret_cast<const float*>(ws + L.pfx_qs);
   a.lat = static_cast<const uint8_t*>(lat_pool);
   a.prefix_pages = prefix_pages;
@@ -806,17 +949,32 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   a.num_pages = p.num_pages;
   a.tiles = prefix_len > 0 ? L.pfx_tiles : 0;
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
-  a.lat_scale = p.latent_scale;
+  const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
+  a.out_scale = p.latent_scale * (nv ? 1.f : kBitsScale);
+  a.swapped = nv ? 0 : 1;
+  CUtensorMap kmap, rmap;
+  std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
+  std::memset(&rmap, 0, sizeof(rmap));
+  if (!nv) {
+    // [num_pages][64][576] bytes: 128 dims of a page's rows at a time, and the 64 rope dims
+    const uint64_t dims[3] = {uint64_t(kDQK), uint64_t(kPage), uint64_t(p.num_pages)};
+    const uint64_t strides[2] = {uint64_t(kDQK), uint64_t(p.lat_page_stride)};
+    const uint32_t box[3] = {128, kPage, 1}, rbox[3] = {64, kPage, 1};
+    if (!encode_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   const int heads = L.rows * kHeads;
-  cudaError_t e = launch_pdl(prefix_query_kernel, dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0,
-                             st, static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
+  cudaError_t e = launch_pdl(nv ? prefix_query_kernel<true> : prefix_query_kernel<false>,
+                             dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0, st,
+                             static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
                              reinterpret_cast<float*>(ws + L.pfx_qs), ctx_lens, lens, int(p.n_q), prefix_len, L.cap, a.err);
   if (e != cudaSuccess) return e;
-  auto kern = p.lat_fmt == DSA_LAT_NVFP4_352 ? prefix_mla_kernel<true> : prefix_mla_kernel<false>;
+  auto kern = nv ? prefix_mla_kernel<true> : prefix_mla_kernel<false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
   const int clusters = std::max(1, std::min(kPfxMaxClusters, sm_count() / 2));
-  e = launch_pdl(kern, dim3(2 * clusters), dim3(kThreads), kSmem, st, a);
+  e = launch_pdl(kern, dim3(2 * clusters), dim3(kThreads), kSmem, st, kmap, rmap, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(prefix_merge_kernel, dim3(L.rows, kHeads / kMergeHeads), dim3(128 * kMergeHeads), 0, st, a,
                     static_cast<__nv_bfloat16*>(out), lse);

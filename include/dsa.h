@@ -328,10 +328,11 @@ dsa_status_t dsa_topk_noalloc(const dsa_params_t* params, const float* scores, i
  *   logit_s = softmax_scale * q_h . c_s  (576 dims), 0 <= s < L_{b,t}
  *   out[h]  = sum_s softmax(logit)_s * c_s[0:512]          (bf16, RNE)
  *   lse[h]  = ln sum_s exp(logit_s)                        (fp32)
- * Products of the query (each head's 576 values scaled by a power of two) and
- * of the softmax weights are taken in fp16 with fp32 sums: the latents are
- * exact, a query value is exact unless it is below 2^-32 of its head's largest,
- * and a weight is rounded to 11 bits (or 2^-32 of the row's largest).
+ * Products have exact latents and fp32 sums. The query is scaled by a power of two per
+ * head and exact, except for values far below their head's largest: under 2^-13 of it they
+ * are off by at most 2^-20 of it (DSA_LAT_FP8_576, where the query is multiplied as an
+ * E4M3 and an E5M2 part), or under 2^-32 by 2^-39 (DSA_LAT_NVFP4_352, in fp16). A softmax
+ * weight is rounded to fp16's 11 bits (or to 2^-32 of the row's largest).
  *   prefix_pages int32 [prefix_len / 64] physical pages of the shared tokens
  *                (NULL if prefix_len is 0); rows of block_table need not repeat
  *                them: their first prefix_len / 64 entries are not read

@@ -21,10 +21,11 @@ def pages_of(n: int) -> int:
 # ---------------------------------------------------------------- attention
 
 
-def prefix_mla(inp, prefix_pages, prefix_len: int, b: int, t: int):
+def prefix_mla(inp, prefix_pages, prefix_len: int, b: int, t: int, query_error=None):
     """Row (b, t) over the shared tokens and then its own: (out, lse, mass, bulk),
     where mass[h] = sum_s p_s |c_s| (512 dims) and bulk = max_s scale * sum_d |q_d c_sd|,
-    the magnitudes that rounding errors are relative to."""
+    the magnitudes that rounding errors are relative to. query_error(q): bounds on how
+    far each query value is off; a fifth result is then max_s scale * sum_d error_d |c_sd|."""
     L = O.visible_len(inp.ctx[b], inp.n_q, t)
     saved = inp.block_table[b].copy()
     inp.block_table[b, :prefix_len // PAGE] = prefix_pages
@@ -33,7 +34,9 @@ def prefix_mla(inp, prefix_pages, prefix_len: int, b: int, t: int):
     q = bf16_decode(inp.q[b, t])
     out, lse = O.mla_attention(q, c, inp.softmax_scale)
     p = np.exp(inp.softmax_scale * (q @ c.T) - lse[:, None])
-    return out, lse, p @ np.abs(c[:, :512]), inp.softmax_scale * (np.abs(q) @ np.abs(c).T).max(axis=1)
+    size = np.abs(c).T
+    res = out, lse, p @ size[:512].T, inp.softmax_scale * (np.abs(q) @ size).max(axis=1)
+    return res if query_error is None else (*res, inp.softmax_scale * (query_error(q) @ size).max(axis=1))
 
 
 # ---------------------------------------------------------------- pages

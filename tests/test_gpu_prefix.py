@@ -3,7 +3,14 @@
 Bounds, derived from the arithmetic that include/dsa.h states:
 - a logit is a sum of 576 products in fp32: at most 64 roundings of a partial
   sum no larger than bulk = scale * sum |q c|, 2^-23 of it each (a factor of two
-  for accumulators that truncate), and 2^-22 for scaling: d = 66 * 2^-23 * bulk;
+  for accumulators that truncate), and 2^-22 for scaling: 66 * 2^-23 * bulk. With FP8
+  latents the query is E4M3(x) + E5M2(x - E4M3(x)), x scaled so that the head's largest
+  value is in [2^7, 2^8). x has 8 significant bits and E4M3 keeps the first 4 of them (rounded) down
+  to 2^-6; the rest is then at most 8 units in x's last place, and 0..8 have at most three
+  significant bits, as E5M2 has: exact. Below 2^-6 (2^-13 of a largest value of 2^7), E4M3 is a multiple of
+  2^-9, the rest at most 2^-10, and E5M2 rounds it by at most 2^-3 of itself: 2^-13, or 2^-20 of the
+  largest. So a query value under 2^-13 of its head's largest may be off by 2^-20 of
+  that largest, and d adds scale * sum over those values of 2^-20 max |q| |c|;
 - a weight exp(z) is off by a factor 1 + d, by 2^-21 in the exponential, and
   rounded to 11 bits (2^-11); the normaliser by d + 2^-21 and the rounding of its
   fp32 sum; splitting and merging adds a few 2^-22 on either;
@@ -48,8 +55,12 @@ def launch(d, pages, prefix, ws=None, stream=None, lse=True):
 
 
 def check_row(inp, pages, prefix, b, t, out, lse):
-    ref, ref_lse, mass, bulk = S.prefix_mla(inp, pages, prefix, b, t)
-    d = (66 * 2.0 ** -23 * bulk)[:, None]
+    def off(q):
+        top = np.abs(q).max(axis=1, keepdims=True)
+        return np.where(np.abs(q) < 2.0 ** -13 * top, 2.0 ** -20 * top, 0.0) * (inp.lat_fmt == "fp8")
+
+    ref, ref_lse, mass, bulk, extra = S.prefix_mla(inp, pages, prefix, b, t, off)
+    d = (66 * 2.0 ** -23 * bulk + extra)[:, None]
     bound = (2.0 ** -11 + 2 * d + 2.0 ** -18) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
     err = np.abs(out.astype(np.float64) - ref)
     assert np.isfinite(out).all()
