@@ -45,11 +45,11 @@ namespace {
 //          warps 8..15       at a new job Q to tensor memory; NVFP4: two groups of
 //                            converters, the page's 64 rows to fp16 (nine K-blocks)
 //          warp  16          MMA: Q from tensor memory (288 columns), S in 3 x 64 columns
-//          warp  17          FP8: the page's rows by TMA, as they are
+//          warp  17          the tiles' pages for the others; FP8: the rows by TMA, as they are
 //   CTA 1: warps 0..3        rescale O where the maximum was raised, write O at a job's end
 //          warps 4..15       three groups of converters: the 512 value dims to fp16 (eight
 //                            K-blocks of 64 dims, read MN-major)
-//          warp  16          MMA: O in all 512 columns, P from shared memory
+//          warps 16, 17      MMA: O in all 512 columns, P from shared memory; the tiles' pages
 // Conversion is what bounds the pair: cvt.f16x2.e4m3x2 issues once in about 12 cycles
 // per SM quarter, so 64 x 576 values would take 1,700 cycles; FP8 keys are therefore
 // multiplied unconverted, and FP8 values moved into fp16's bit fields by shifts and
@@ -72,14 +72,13 @@ static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
 constexpr int kPChunk = 128 * 16;
 constexpr int kPBuf = 8 * kPChunk;           // 16,384
 constexpr uint32_t kPBytes = kPBuf + 128 * 4;  // P and the rescale factors, per tile
-constexpr int kMasks = 8;
-constexpr int kThreads = 640;                // five warpgroups; the last holds the MMA and the TMA warp and two idle ones
-constexpr int kMmaWarp = 16, kTmaWarp = 17;
+constexpr int kThreads = 640;                // five warpgroups; the last holds the MMA and the feeding warp and two idle ones
+constexpr int kMmaWarp = 16, kFeedWarp = 17;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 42;
+constexpr int kNumBars = 50;
 constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + 512);
-constexpr size_t kSmemS = 2 * kKBuf + 512 + kMasks * 8;
-constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 16;
+constexpr size_t kSmemS = 2 * kKBuf + 512;
+constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 64 + 16;
 static_assert(kSmem + 512 <= 232448, "shared memory of one CTA");
 constexpr float kPShift = 7.f;               // weights are 2^(z - max + 7)
 constexpr float kLazy = 8.f;                 // the maximum in use is raised when passed by more than 2^8
@@ -245,88 +244,78 @@ struct TileRegs {
   }
 };
 
-// The page of tile k of the walk's job and its tokens that the job sees, over the
-// tiles of a run in order. A page number is loaded a tile before it is asked for.
-struct Pages {
+// What the warps of a CTA need to know of a tile, in a ring that one warp fills.
+struct Tile {
+  int page, valid;  // physical page, and how many of its tokens the job sees (0 for a bad page)
+};
+constexpr int kRing = 8;
+
+// The ring's producer (one warp): 32 page numbers of the walk's job at a time.
+// each(g, tile): what else it does for a tile (lane 0 has just published it).
+template <typename Each>
+__device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int unit, int units, int lane, bool report,
+                                     Tile* ring, uint32_t full, uint32_t free, Each each) {
   Walk wk;
-  const int32_t* list;  // page numbers of the walk's job
-  int len, k;           // its tokens, and the next tile's place in it
-  int pg, left, begins; // the fetched tile: page number, tokens, the job that it begins (-1 none)
-  __device__ __forceinline__ void enter(const PfxArgs& a) {
-    if (wk.job < a.tiles) {
-      list = a.prefix_pages;
-      len = a.prefix;
-    } else {
+  int g = 0;
+#pragma unroll 1
+  for (bool on = gtot > 0 && wk.start(a, job0, unit, units); on; on = wk.next(a)) {
+    const int32_t* list = a.prefix_pages;
+    int len = a.prefix;
+    if (wk.job >= a.tiles) {
       const int r = wk.job - a.tiles;
       list = a.table + size_t(r / a.n_q) * a.max_pages + a.prefix / kNT;
       len = a.lens[r];
     }
-    k = wk.k0;
-    begins = wk.job;
-  }
-  __device__ __forceinline__ bool start(const PfxArgs& a, int job0, int unit, int units) {
-    if (!wk.start(a, job0, unit, units)) return false;
-    enter(a);
-    pg = __ldg(list + k);
-    left = min(kNT, len - k * kNT);
-    ++k;
-    return true;
-  }
-  __device__ __forceinline__ void fetch(const PfxArgs& a) {
-    begins = -1;
-    if (k >= wk.k1) {
-      if (!wk.next(a)) return;
-      enter(a);
+    int mine = 0;
+#pragma unroll 1
+    for (int k = wk.k0; k < wk.k1; ++k, ++g) {
+      const int i = (k - wk.k0) & 31;
+      if (i == 0) mine = k + lane < wk.k1 ? __ldg(list + k + lane) : 0;
+      const int pg = __shfl_sync(0xffffffffu, mine, i);
+      const bool good = pg >= 0 && pg < a.num_pages;
+      const Tile t{good ? pg : 0, good ? min(kNT, len - k * kNT) : 0};
+      const int slot = g % kRing;
+      if (g >= kRing && !ptx::mbar_wait(free + 8 * slot, uint32_t(g / kRing - 1) & 1u)) return false;
+      if (lane == 0) {
+        if (!good && report) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+        ring[slot] = t;
+        ptx::mbar_arrive(full + 8 * slot);
+      }
+      if (!each(g, t)) return false;
     }
-    pg = __ldg(list + k);
-    left = min(kNT, len - k * kNT);
-    ++k;
   }
-  __device__ __forceinline__ bool good(const PfxArgs& a) const { return pg >= 0 && pg < a.num_pages; }
-};
+  return true;
+}
 
 // One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (kRope:
-// CTA 0). full / free: the buffers' barriers; masks / mask_full: the valid tokens of a
-// tile, for the softmax (CTA 0). at_job(job): what CTA 0 does at a job's first tile.
-template <bool kNv, bool kRope, int kBufs, int kGroups, typename AtJob>
-__device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int job0, int unit, int units, int group, int w, int lane,
-                                        uint8_t* bufs, uint32_t full, uint32_t free, unsigned long long* masks,
-                                        uint32_t mask_full, AtJob at_job) {
+// CTA 0, NVFP4). ring and its barriers as in feed; full / free: the buffers' barriers;
+// after(g): called once tile g is stored.
+template <bool kNv, bool kRope, int kBufs, int kGroups, typename After>
+__device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
+                                        uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
+                                        uint32_t free, After after) {
   constexpr int kSize = kRope ? kKBuf : kVBuf;
   TileRegs<kNv, kRope> t;
-  Pages pages;
-  if (gtot == 0 || !pages.start(a, job0, unit, units)) return true;
-  int valid = 0;
-  auto load = [&]() {
-    const bool good = pages.good(a);
-    if (!good && kRope && w == 0 && lane == 0) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
-    valid = good ? pages.left : 0;
-    t.load(a.lat + int64_t(good ? pages.pg : 0) * a.stride, valid, w, lane);
+  auto load = [&](int g) {
+    const int slot = g % kRing;
+    if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) return false;
+    const Tile tile = ring[slot];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
+    t.load(a.lat + int64_t(tile.page) * a.stride, tile.valid, w, lane);
+    return true;
   };
-  int job = pages.begins;  // the job that tile g begins, -1 none
-  if (group == 0) load();
-  if (gtot > 1) pages.fetch(a);
+  if (group < gtot && !load(group)) return false;
 #pragma unroll 1
-  for (int g = 0, turn = 0; g < gtot; ++g, turn = turn + 1 == kGroups ? 0 : turn + 1) {
-    const int now_job = job;
-    job = pages.begins;
-    if (turn == group) {
-      const int buf = g % kBufs;
-      if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
-      t.store(bufs + buf * kSize, w, lane);
-      if (kRope && w == 0 && lane == 0) {
-        masks[g % kMasks] = valid >= 64 ? ~0ull : (1ull << valid) - 1;
-        ptx::mbar_arrive(mask_full + 8 * (g % kMasks));
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
-    }
-    // (no tile is in the registers when the query goes through them)
-    if (kRope && now_job >= 0 && !at_job(now_job)) return false;
-    // tile g + 1, in flight while the other groups store theirs
-    if (g + 1 < gtot && (turn + 1) % kGroups == group) load();
-    if (g + 2 < gtot) pages.fetch(a);
+  for (int g = group; g < gtot; g += kGroups) {
+    const int buf = g % kBufs;
+    if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
+    t.store(bufs + buf * kSize, w, lane);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
+    if (!after(g)) return false;
+    if (g + kGroups < gtot && !load(g + kGroups)) return false;
   }
   return true;
 }
@@ -349,16 +338,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t s_free = bars + 9 * 8;      // [3]  the softmax has read S
   const uint32_t turn = bars + 12 * 8;       // [4]  by softmax warp: the tile's maximum is decided
   const uint32_t p_free = bars + 16 * 8;     // [2]  CTA 1 has multiplied the tile in this half of P
-  const uint32_t mask_full = bars + 18 * 8;  // [8]
+  const uint32_t ring_full = bars + 18 * 8;  // [8]
+  const uint32_t ring_free = bars + 41 * 8;  // [8]
   const uint32_t v_full = bars + 26 * 8;     // [3]
   const uint32_t v_free = bars + 29 * 8;     // [3]  P . V of the buffer's tile is done
   const uint32_t p_full = bars + 32 * 8;     // [2]  P and the factors have landed
   const uint32_t o_ok = bars + 34 * 8;       // [2]  O is rescaled for the tile
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kData + kNumBars * 8);
+  Tile* ring = reinterpret_cast<Tile*>(sm + kData + kNumBars * 8);  // [8]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
   uint8_t* KB = sm;
   float* m_run = reinterpret_cast<float*>(sm + 2 * kKBuf);  // [128] the running maximum in use
-  unsigned long long* masks = reinterpret_cast<unsigned long long*>(m_run + 128);
   // CTA 1
   uint8_t* VB = sm;
   uint8_t* PB = sm + kVBufs * kVBuf;
@@ -390,7 +380,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(k_full + 8 * i, kNv ? 4 : 1);
       ptx::mbar_init(k_free + 8 * i, 1);
     }
-    for (int i = 0; i < kMasks; ++i) ptx::mbar_init(mask_full + 8 * (i), 1);
+    for (int i = 0; i < kRing; ++i) {
+      ptx::mbar_init(ring_full + 8 * i, 1);
+      ptx::mbar_init(ring_free + 8 * i, half == 0 && kNv ? 8 : 4);  // a softmax and a converter group, or one of them
+    }
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -531,34 +524,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-    } else if (warp == kTmaWarp && half == 0 && !kNv) {
-      // ---------------------------------------------------------- FP8 keys
-      Pages pages;
-      if (gtot > 0 && pages.start(a, job0, unit0, units)) {
-        const uint32_t kb0 = ptx::smem_u32(KB);
-#pragma unroll 1
-        for (int g = 0; g < gtot; ++g) {
-          const int buf = g % kKBufs<kNv>;
-          const bool good = pages.good(a);
-          const int valid = good ? pages.left : 0, pg = good ? pages.pg : 0;
-          if (g + 1 < gtot) pages.fetch(a);
-          if (g >= kKBufs<kNv> && !ptx::mbar_wait(k_free + 8 * buf, uint32_t(g / kKBufs<kNv> - 1) & 1u)) { ok = false; break; }
-          if (lane == 0) {
-            if (!good) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
-            masks[g % kMasks] = valid >= 64 ? ~0ull : (1ull << valid) - 1;
-            ptx::mbar_arrive(mask_full + 8 * (g % kMasks));
-            const uint32_t dst = kb0 + buf * kKBuf8, bar = k_full + 8 * buf;
-            ptx::mbar_arrive_expect_tx(bar, kKBuf8);
+    } else if (warp == kFeedWarp) {
+      // ---------------------------------------------------------- tiles; FP8 keys by TMA
+      const uint32_t kb0 = ptx::smem_u32(KB);
+      ok = feed(a, gtot, job0, unit0, units, lane, half == 0, ring, ring_full, ring_free, [&](int g, const Tile& t) {
+        if (kNv || half == 1) return true;
+        const int buf = g % kKBufs<kNv>;
+        if (g >= kKBufs<kNv> && !ptx::mbar_wait(k_free + 8 * buf, uint32_t(g / kKBufs<kNv> - 1) & 1u)) return false;
+        if (lane == 0) {
+          const uint32_t dst = kb0 + buf * kKBuf8, bar = k_full + 8 * buf;
+          ptx::mbar_arrive_expect_tx(bar, kKBuf8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ptx::tma_load_3d(dst + j * kBlk, &kmap, bar, j * 128, 0, pg);
-            ptx::tma_load_3d(dst + 4 * kBlk, &rmap, bar, kDNope, 0, pg);
-          }
-          __syncwarp();
+          for (int j = 0; j < 4; ++j) ptx::tma_load_3d(dst + j * kBlk, &kmap, bar, j * 128, 0, t.page);
+          ptx::tma_load_3d(dst + 4 * kBlk, &rmap, bar, kDNope, 0, t.page);
         }
-        // no copy left in flight
-        if (!ok)
-          for (int i = 0; i < kKBufs<kNv>; ++i) ptx::mbar_wait(k_full + 8 * i, 0, 1 << 10);
-      }
+        __syncwarp();
+        return true;
+      });
+      // no copy left in flight
+      if (!ok && !kNv && half == 0)
+        for (int i = 0; i < 2 * kKBufs<kNv>; ++i) ptx::mbar_wait(k_full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- O += P . V
       const uint32_t id = ptx::idesc(0, 0, 128, 256, 0, 1);
@@ -622,15 +607,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) ptx::mbar_arrive(q_full);
         return true;
       };
+      bool on = gtot > 0 && wk.start(a, job0, unit0, units);
       if constexpr (kNv) {
-        ok = convert<true, true, kKBufs<true>, 2>(a, gtot, job0, unit0, units, group, w, lane, KB, k_full, k_free, masks,
-                                                  mask_full, load_q);
+        // between a group's tiles, when none is in its registers: the queries of the jobs
+        // that begin before its next one
+        int begin = 0;
+        auto queries = [&](int g) {
+#pragma unroll 1
+          while (on && begin <= g + 2) {
+            if (!load_q(wk.job)) return false;
+            begin += wk.k1 - wk.k0;
+            on = wk.next(a);
+          }
+          return true;
+        };
+        ok = queries(-2) && convert<true, true, kKBufs<true>, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB,
+                                                                 k_full, k_free, queries);
       } else {
 #pragma unroll 1
-        for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) ok = load_q(wk.job);
+        for (; on && ok; on = wk.next(a)) ok = load_q(wk.job);
       }
     } else {
-      ok = convert<kNv, false, kVBufs, 3>(a, gtot, job0, unit0, units, group + 1, w, lane, VB, v_full, v_free, nullptr, 0,
+      ok = convert<kNv, false, kVBufs, 3>(a, gtot, group + 1, w, lane, ring, ring_full, ring_free, VB, v_full, v_free,
                                           [](int) { return true; });
     }
   } else if (half == 0) {
@@ -657,17 +655,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float sv[64];
         ptx::tmem_ld32_nowait(tmem + lane_base + kSCol + sb * kNT, *reinterpret_cast<float(*)[32]>(&sv[0]));
         ptx::tmem_ld32_nowait(tmem + lane_base + kSCol + sb * kNT + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
-        if (!ptx::mbar_wait(mask_full + 8 * (g % kMasks), uint32_t(g / kMasks) & 1u)) ok = false;
-        const unsigned long long vm = masks[g % kMasks];
+        if (!ptx::mbar_wait(ring_full + 8 * (g % kRing), uint32_t(g / kRing) & 1u)) ok = false;
+        const int valid = ring[g % kRing].valid;
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[0]));
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[32]));
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(s_free + 8 * (sb));
+        if (lane == 0) {
+          ptx::mbar_arrive(s_free + 8 * (sb));
+          ptx::mbar_arrive(ring_free + 8 * (g % kRing));
+        }
         if (!ok) break;
-        if (vm != ~0ull) {
+        if (valid < kNT) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) sv[i] = ((vm >> i) & 1ull) ? sv[i] : -INFINITY;
+          for (int i = 0; i < kNT; ++i) sv[i] = i < valid ? sv[i] : -INFINITY;
         }
         float t0 = fmaxf(sv[0], sv[1]), t1 = fmaxf(sv[2], sv[3]);
 #pragma unroll
@@ -722,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if (warp >= 4) {
-      ok = convert<kNv, false, kVBufs, 3>(a, gtot, job0, unit0, units, 0, warp & 3, lane, VB, v_full, v_free, nullptr, 0,
+      ok = convert<kNv, false, kVBufs, 3>(a, gtot, 0, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free,
                                           [](int) { return true; });
     } else {
       // ---------------------------------------------------------- O: rescaling and output
