@@ -49,7 +49,8 @@ namespace {
 //   CTA 1: warps 0..3        rescale O where the maximum was raised, write O at a job's end
 //          warps 4..15       three groups of converters: the 512 value dims to fp16 (eight
 //                            K-blocks of 64 dims, read MN-major)
-//          warps 16, 17      MMA: O in all 512 columns, P from shared memory; the tiles' pages
+//          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
+//                            pages; what the MMA of a tile waits for
 // Conversion is what bounds the pair: cvt.f16x2.e4m3x2 issues once in about 12 cycles
 // per SM quarter, so 64 x 576 values would take 1,700 cycles; FP8 keys are therefore
 // multiplied unconverted, and FP8 values moved into fp16's bit fields by shifts and
@@ -71,15 +72,16 @@ static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
 // matrices of the MMA, and 512 contiguous bytes for a warp's remote store)
 constexpr int kPChunk = 128 * 16;
 constexpr int kPBuf = 8 * kPChunk;           // 16,384
-constexpr uint32_t kPBytes = kPBuf + 128 * 4;  // P and the rescale factors, per tile
-constexpr int kThreads = 640;                // five warpgroups; the last holds the MMA and the feeding warp and two idle ones
-constexpr int kMmaWarp = 16, kFeedWarp = 17;
+constexpr int kPSide = 128 * 4 + 16;         // the rescale factors, and by softmax warp whether one is not 1
+constexpr uint32_t kPBytes = kPBuf + kPSide;
+constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
+constexpr int kMmaWarp = 16, kFeedWarp = 17, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 50;
-constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + 512);
+constexpr int kNumBars = 52;
+constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + kPSide);
 constexpr size_t kSmemS = 2 * kKBuf + 512;
 constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 64 + 16;
-static_assert(kSmem + 512 <= 232448, "shared memory of one CTA");
+static_assert(kSmem + 256 <= 232448, "shared memory of one CTA, with the static variables");
 constexpr float kPShift = 7.f;               // weights are 2^(z - max + 7)
 constexpr float kLazy = 8.f;                 // the maximum in use is raised when passed by more than 2^8
 constexpr int kJobCost = 3;                  // what a job's start and end take, in tiles
@@ -343,7 +345,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t v_full = bars + 26 * 8;     // [3]
   const uint32_t v_free = bars + 29 * 8;     // [3]  P . V of the buffer's tile is done
   const uint32_t p_full = bars + 32 * 8;     // [2]  P and the factors have landed
-  const uint32_t o_ok = bars + 34 * 8;       // [2]  O is rescaled for the tile
+  const uint32_t go = bars + 49 * 8;         // [2]  all that P . V of a tile needs is there
+  const uint32_t ask = bars + 34 * 8;        // O is to be rescaled, or written
+  const uint32_t o_ok = bars + 35 * 8;       // and it is
   Tile* ring = reinterpret_cast<Tile*>(sm + kData + kNumBars * 8);  // [8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
@@ -352,9 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // CTA 1
   uint8_t* VB = sm;
   uint8_t* PB = sm + kVBufs * kVBuf;
-  float* factor = reinterpret_cast<float*>(PB + kPBufs * kPBuf);  // [2][128]
+  uint8_t* side = PB + kPBufs * kPBuf;  // [2] factors and flags
   __shared__ long long s_sum[kThreads / 32];
-  __shared__ int s_job, s_unit;
+  __shared__ int s_job, s_unit, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
 
   const int half = int(ptx::cluster_ctarank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -364,10 +368,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::mbar_init(mma_done, 1);
     ptx::mbar_init(q_full, 8);
     ptx::mbar_init(q_free, 1);
+    ptx::mbar_init(ask, 1);
+    ptx::mbar_init(o_ok, 4);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(p_free + 8 * (i), 1);
       ptx::mbar_init(p_full + 8 * (i), 1);
-      ptx::mbar_init(o_ok + 8 * (i), 4);
+      ptx::mbar_init(go + 8 * i, 1);
     }
     for (int i = 0; i < 3; ++i) {
       ptx::mbar_init(s_full + 8 * (i), 1);
@@ -554,8 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
           const int buf = g % kVBufs, pb = g % kPBufs;
-          if (!ptx::mbar_wait(v_full + 8 * (buf), uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
-          if (!ptx::mbar_wait(o_ok + 8 * (pb), uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
+          if (!ptx::mbar_wait(go + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t vb = vb0 + buf * kVBuf, p = pb0 + pb * kPBuf;
           if (ptx::elect_one()) {
@@ -566,12 +571,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ptx::mma_f16(tmem + n * 256, ptx::sdesc_plain(p + kk * 2 * kPChunk, kPChunk, 128),
                              ptx::sdesc_sw128_mn(vb + n * 4 * kBlk + kk * 16 * 128, kBlk, 1024), id,
                              (k > wk.k0 || kk > 0) ? 1u : 0u);
-            ptx::mma_commit(v_free + 8 * (buf));
-            ptx::mma_commit_to(p_free + 8 * (pb), 1);  // CTA 0's barrier
+            ptx::mma_commit(v_free + 8 * buf);
+            ptx::mma_commit_to(p_free + 8 * pb, 1);  // CTA 0's barrier
           }
           __syncwarp();
         }
       }
+    } else if (warp == kReadyWarp && half == 1) {
+      // ---------------------------------------------------------- what P . V waits for
+      // (in a warp of its own, a tile ahead: the MMA warp issues at the rate of the
+      // products, and each of these steps of its own would leave the tensor core idle)
+      int g = 0, asked = 0, answered = 0;
+      auto request = [&](int what) {
+        if (lane == 0) {
+          s_ask = what;
+          ptx::mbar_arrive(ask);
+        }
+        __syncwarp();
+        ++asked;
+      };
+      auto settled = [&]() {
+        while (answered < asked)
+          if (!ptx::mbar_wait(o_ok, uint32_t(answered++) & 1u)) return false;
+        return true;
+      };
+#pragma unroll 1
+      for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
+#pragma unroll 1
+        for (int k = wk.k0; k < wk.k1; ++k, ++g) {
+          const int buf = g % kVBufs, pb = g % kPBufs;
+          if (!ptx::mbar_wait_cluster(p_full + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
+          const uint4 flags = *reinterpret_cast<const uint4*>(side + pb * kPSide + 512);
+          // re-arm for the next tile in this slot: it is not sent before this one's P . V is done
+          if (lane == 0 && g + kPBufs < gtot) ptx::mbar_arrive_expect_tx(p_full + 8 * pb, kPBytes);
+          if (k > wk.k0 && (flags.x | flags.y | flags.z | flags.w)) request(g);
+          if (!settled()) { ok = false; break; }  // (at a job's first tile: the old output is written)
+          if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
+          // P came by ordinary (remote) stores; the tensor core reads it through the async proxy
+          ptx::fence_proxy_async_smem();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(go + 8 * pb);
+        }
+        if (ok) request(-1 - g);
+      }
+      if (ok) ok = settled();
     }
     if (warp == kMmaWarp) {
       // nothing of this warp's left in flight when the tensor memory is released
@@ -638,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = w * 32 + lane;
     const uint32_t lane_base = uint32_t(w * 32) << 16;
     const uint32_t p_peer = ptx::mapa_shared(ptx::smem_u32(PB) + row * 16, 1);
-    const uint32_t f_peer = ptx::mapa_shared(ptx::smem_u32(factor + row), 1);
+    const uint32_t f_peer = ptx::mapa_shared(ptx::smem_u32(side), 1);
     const uint32_t bar_peer = ptx::mapa_shared(p_full, 1);
     int g0 = 0;  // the segment's first tile
 #pragma unroll 1
@@ -708,7 +752,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::st_async_f4(dst + i * kPChunk, make_float4(__uint_as_float(pk[4 * i]), __uint_as_float(pk[4 * i + 1]),
                                                           __uint_as_float(pk[4 * i + 2]), __uint_as_float(pk[4 * i + 3])),
                            bar);
-        ptx::st_async_f1(f_peer + pb * 512, alpha, bar);
+        ptx::st_async_f1(f_peer + pb * kPSide + row * 4, alpha, bar);
+        const bool raised = __any_sync(0xffffffffu, alpha != 1.f);
+        if (lane == 0) ptx::st_async_f1(f_peer + pb * kPSide + 512 + w * 4, __uint_as_float(raised ? 1u : 0u), bar);
       }
       if (!ok) break;
       g0 = g1;
@@ -729,20 +775,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- O: rescaling and output
       const int row = warp * 32 + lane;
       const uint32_t lane_base = uint32_t(warp * 32) << 16;
-      int g = 0;
+      int asked = 0;
 #pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
+        int g;  // O is up to date, and still, once P . V of the tile before g is done
 #pragma unroll 1
-        for (int k = wk.k0; k < wk.k1; ++k, ++g) {
-          const int pb = g % kPBufs;
-          if (!ptx::mbar_wait_cluster(p_full + 8 * (pb), uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
-          const float alpha = factor[pb * 128 + row];
-          // re-arm for tile g + 2: it is not sent before P . V of this tile, for which every
-          // warp here has to arrive below
-          if (threadIdx.x == 0 && g + kPBufs < gtot) ptx::mbar_arrive_expect_tx(p_full + 8 * (pb), kPBytes);
-          if (k > wk.k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            if (!ptx::mbar_wait(v_free + 8 * ((g - 1) % kVBufs), uint32_t((g - 1) / kVBufs) & 1u)) { ok = false; break; }
-            ptx::tc_fence_after();
+        for (;;) {
+          if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u)) { ok = false; break; }
+          const int what = s_ask;
+          g = what < 0 ? -1 - what : what;
+          if (!ptx::mbar_wait(v_free + 8 * ((g - 1) % kVBufs), uint32_t((g - 1) / kVBufs) & 1u)) { ok = false; break; }
+          ptx::tc_fence_after();
+          if (what < 0) break;
+          const float alpha = reinterpret_cast<const float*>(side + (g % kPBufs) * kPSide)[row];
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < kDNope; c += 32) {
               float o[32];
@@ -752,15 +798,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ptx::tmem_st32(tmem + lane_base + c, o);
             }
           }
-          // P came by ordinary (remote) stores; the tensor core reads it through the async proxy
-          ptx::fence_proxy_async_smem();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(o_ok + 8 * (pb));
+          if (lane == 0) ptx::mbar_arrive(o_ok);
         }
         if (!ok) break;
-        if (!ptx::mbar_wait(v_free + 8 * ((g - 1) % kVBufs), uint32_t((g - 1) / kVBufs) & 1u)) { ok = false; break; }
-        ptx::tc_fence_after();
         float4* dst = reinterpret_cast<float4*>(a.part + (size_t(wk.job + clu) * kPfxTileRows + row) * kDNope);
         const bool real = wk.job < a.tiles || row < kHeads;
 #pragma unroll 1
@@ -772,8 +814,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) dst[c / 4 + j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
-        // the reads of O are ordered before the next job's first P . V (o_ok)
+        // the reads of O are ordered before the next job's first P . V
         ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(o_ok);
       }
     }
   }
