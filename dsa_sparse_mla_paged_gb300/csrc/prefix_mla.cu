@@ -51,11 +51,7 @@ namespace {
 //                            K-blocks of 64 dims, read MN-major)
 //          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
 //                            pages; what the MMA of a tile waits for
-// Conversion is what bounds the pair: cvt.f16x2.e4m3x2 issues once in about 12 cycles
-// per SM quarter, so 64 x 576 values would take 1,700 cycles; FP8 keys are therefore
-// multiplied unconverted, and FP8 values moved into fp16's bit fields by shifts and
-// masks (expand_bits). A converter group issues the loads of its next tile right after
-// it has stored one.
+// A converter group issues the loads of its next tile right after it has stored one.
 // ---------------------------------------------------------------------------
 constexpr int kNT = 64;                      // tokens per tile: one page
 constexpr int kBlk = kNT * 128;              // 8,192 B: a K-block, 64 rows of 64 fp16
@@ -64,7 +60,7 @@ constexpr int kVBlks = kDNope / 64;          // 8
 constexpr int kKBuf = kKBlks * kBlk;         // 73,728 (NVFP4)
 constexpr int kKBuf8 = 4 * kBlk + kBlk / 2;  // 36,864 (FP8: 64 rows of 128 E4M3, and of 64 for the rope dims)
 constexpr int kVBuf = kVBlks * kBlk;         // 65,536
-constexpr int kVBufs = 3, kSBufs = 3, kPBufs = 2;
+constexpr int kVBufs = 2, kSBufs = 3, kPBufs = 4;
 template <bool kNv>
 constexpr int kKBufs = kNv ? 2 : 4;
 static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
@@ -77,7 +73,7 @@ constexpr uint32_t kPBytes = kPBuf + kPSide;
 constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
 constexpr int kMmaWarp = 16, kFeedWarp = 17, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 52;
+constexpr int kNumBars = 70;
 constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + kPSide);
 constexpr size_t kSmemS = 2 * kKBuf + 512;
 constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 64 + 16;
@@ -99,8 +95,7 @@ struct PfxArgs {
   int* err;
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
-  float scale_log2, out_scale;
-  int swapped;
+  float scale_log2, lat_scale;
 };
 
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
@@ -134,37 +129,32 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ uint32_t half2_from_e4m3x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xFFFFu), __NV_E4M3);
-  return uint32_t(h.x) | uint32_t(h.y) << 16;
+// Four E4M3 bytes -> four fp16. (The header's conversion returns two halves that the
+// compiler packs again, which tripled the converters' instructions.)
+__device__ __forceinline__ void expand_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 // 16 E4M3 bytes -> 16 fp16, as two 16-B chunks.
 __device__ __forceinline__ void expand16(const uint4 w, uint4& lo, uint4& hi) {
-  lo.x = half2_from_e4m3x2(w.x); lo.y = half2_from_e4m3x2(w.x >> 16);
-  lo.z = half2_from_e4m3x2(w.y); lo.w = half2_from_e4m3x2(w.y >> 16);
-  hi.x = half2_from_e4m3x2(w.z); hi.y = half2_from_e4m3x2(w.z >> 16);
-  hi.z = half2_from_e4m3x2(w.w); hi.w = half2_from_e4m3x2(w.w >> 16);
+  expand_e4m3(w.x, lo.x, lo.y);
+  expand_e4m3(w.y, lo.z, lo.w);
+  expand_e4m3(w.z, hi.x, hi.y);
+  expand_e4m3(w.w, hi.z, hi.w);
 }
-
-// 16 E4M3 bytes -> 16 fp16 of 2^-8 times their values: E4M3's exponent and mantissa
-// at bits 13..7 and its sign at bit 15 are the fp16 of value * 2^(7 - 15), subnormals
-// included. The bytes 0 1 2 3 of a word come out in the order 0 2 1 3. NaN (0x7F)
-// becomes 1.875: a token with a NaN latent has NaN scores, which reach every output
-// of the rows that see it, and in a token that no row sees the values must not matter.
-__device__ __forceinline__ void expand_bits(uint32_t w, uint32_t& even, uint32_t& odd) {
-  even = ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u);
-  odd = ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u);
-}
-constexpr float kBitsScale = 256.f;
 
 // 8 E2M1 values times an E4M3 scale (a pair of fp16): 6 significant bits, exact.
 __device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
   uint32_t o[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), s);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), s);
     o[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
@@ -179,9 +169,9 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
 
 // A converter thread's share of a tile; warp w of 4 has nope K-blocks 2w and 2w + 1.
 // FP8: sixteen 16-B pieces (8 tokens x 4 pieces a warp load: 64-B runs, and stores
-// without bank conflicts). NVFP4: eight 16-B units (32 values, two scales; zeros for
-// tokens at or past `valid`, whose scales could be NaN). And kRope (NVFP4 keys): two
-// 16-B pieces of the rope dims.
+// without bank conflicts). NVFP4: eight 16-B units (32 values, two scales). And kRope
+// (NVFP4 keys): two 16-B pieces of the rope dims. Tokens at or past `valid` are zeros:
+// their weights are 0, but their bytes could be NaN.
 template <bool kNv, bool kRope>
 struct TileRegs {
   static constexpr int kPieces = kNv ? 4 : 8;  // per K-block
@@ -201,7 +191,9 @@ struct TileRegs {
           s[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
         } else {
           const int tok = u * 8 + (lane >> 2);
-          v[b][u] = __ldg(reinterpret_cast<const uint4*>(page + tok * 576 + 64 * (2 * w + b) + 16 * (lane & 3)));
+          v[b][u] = tok < valid
+                        ? __ldg(reinterpret_cast<const uint4*>(page + tok * 576 + 64 * (2 * w + b) + 16 * (lane & 3)))
+                        : zero;
         }
       }
     if constexpr (kRope) {
@@ -212,36 +204,37 @@ struct TileRegs {
       }
     }
   }
-  __device__ __forceinline__ void store(uint8_t* buf, int w, int lane) const {
-    uint4 lo, hi;
+  // 16 of the tokens, 16 step and up
+  __device__ __forceinline__ void store(int step, uint8_t* buf, int w, int lane) const {
+    const int row0 = 16 * step;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       uint8_t* blk = buf + (2 * w + b) * kBlk;
+      if constexpr (kNv) {
+        const int tok = row0 + (lane >> 1), c0 = (lane & 1) * 4;
+        uint32_t two, none;
+        expand_e4m3(s[b][step], two, none);
+        const __half2 h = *reinterpret_cast<const __half2*>(&two);
+        const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+        put2(blk, tok, c0, expand_e2m1(v[b][step].x, s0), expand_e2m1(v[b][step].y, s0));
+        put2(blk, tok, c0 + 2, expand_e2m1(v[b][step].z, s1), expand_e2m1(v[b][step].w, s1));
+      } else {
 #pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        if constexpr (kNv) {
-          const int tok = u * 16 + (lane >> 1), c0 = (lane & 1) * 4;
-          const uint32_t two = half2_from_e4m3x2(s[b][u]);
-          const __half2 h = *reinterpret_cast<const __half2*>(&two);
-          const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-          put2(blk, tok, c0, expand_e2m1(v[b][u].x, s0), expand_e2m1(v[b][u].y, s0));
-          put2(blk, tok, c0 + 2, expand_e2m1(v[b][u].z, s1), expand_e2m1(v[b][u].w, s1));
-        } else {
-          expand_bits(v[b][u].x, lo.x, lo.y);
-          expand_bits(v[b][u].y, lo.z, lo.w);
-          expand_bits(v[b][u].z, hi.x, hi.y);
-          expand_bits(v[b][u].w, hi.z, hi.w);
-          put2(blk, u * 8 + (lane >> 2), (lane & 3) * 2, lo, hi);
+        for (int u = 0; u < 2; ++u) {
+          uint4 lo, hi;
+          expand16(v[b][2 * step + u], lo, hi);
+          put2(blk, row0 + u * 8 + (lane >> 2), (lane & 3) * 2, lo, hi);
         }
       }
     }
-    if constexpr (kRope) {
+  }
+  __device__ __forceinline__ void store_rope(uint8_t* buf, int w, int lane) const {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ct = b * 128 + w * 32 + lane;
-        expand16(rope[b], lo, hi);
-        put2(buf + 8 * kBlk, ct >> 2, (ct & 3) * 2, lo, hi);
-      }
+    for (int b = 0; b < 2; ++b) {
+      uint4 lo, hi;
+      const int ct = b * 128 + w * 32 + lane;
+      expand16(rope[b], lo, hi);
+      put2(buf + 8 * kBlk, ct >> 2, (ct & 3) * 2, lo, hi);
     }
   }
 };
@@ -289,15 +282,16 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
   return true;
 }
 
-// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (kRope:
-// CTA 0, NVFP4). ring and its barriers as in feed; full / free: the buffers' barriers;
-// after(g): called once tile g is stored.
-template <bool kNv, bool kRope, int kBufs, int kGroups, typename After>
+// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA. kKeys (CTA
+// 0, NVFP4): all 576 dims, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
+// its barriers as in feed; full / free: the buffers' (or halves') barriers; turn: the groups take buffers in the order of their
+// tiles (a group that came early could take a buffer's barrier for one a round older,
+// which has the same parity); after(g): called once tile g is stored.
+template <bool kNv, bool kKeys, int kGroups, typename After>
 __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
                                         uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
-                                        uint32_t free, After after) {
-  constexpr int kSize = kRope ? kKBuf : kVBuf;
-  TileRegs<kNv, kRope> t;
+                                        uint32_t free, uint32_t turn, After after) {
+  TileRegs<kNv, kKeys> t;
   auto load = [&](int g) {
     const int slot = g % kRing;
     if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) return false;
@@ -310,12 +304,31 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
   if (group < gtot && !load(group)) return false;
 #pragma unroll 1
   for (int g = group; g < gtot; g += kGroups) {
-    const int buf = g % kBufs;
-    if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
-    t.store(bufs + buf * kSize, w, lane);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
+    if constexpr (kKeys) {
+      constexpr int kBufs = kKBufs<kNv>;
+      const int buf = g % kBufs;
+      if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
+      uint8_t* dst = bufs + buf * kKBuf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t.store(i, dst, w, lane);
+      t.store_rope(dst, w, lane);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
+    } else {
+      const int buf = g % kVBufs;
+      if (g > 0 && !ptx::mbar_wait(turn + 8 * ((g - 1) % kGroups), uint32_t((g - 1) / kGroups) & 1u)) return false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (g >= kVBufs && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kVBufs - 1) & 1u)) return false;
+        if (i == 1 && lane == 0) ptx::mbar_arrive(turn + 8 * group);
+        t.store(2 * i, bufs + buf * kVBuf, w, lane);
+        t.store(2 * i + 1, bufs + buf * kVBuf, w, lane);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full + 8 * (2 * buf + i));
+      }
+    }
     if (!after(g)) return false;
     if (g + kGroups < gtot && !load(g + kGroups)) return false;
   }
@@ -333,21 +346,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t bars = ptx::smem_u32(sm) + uint32_t(kData);
   const uint32_t mma_done = bars + 0 * 8;
   const uint32_t q_full = bars + 1 * 8;
-  const uint32_t q_free = bars + 40 * 8;     // every product with the job's query is done
-  const uint32_t k_full = bars + 2 * 8;      // [kKBufs]
-  const uint32_t k_free = bars + 36 * 8;     // [kKBufs]  S of the buffer's tile is done
-  const uint32_t s_full = bars + 6 * 8;      // [3]
-  const uint32_t s_free = bars + 9 * 8;      // [3]  the softmax has read S
-  const uint32_t turn = bars + 12 * 8;       // [4]  by softmax warp: the tile's maximum is decided
-  const uint32_t p_free = bars + 16 * 8;     // [2]  CTA 1 has multiplied the tile in this half of P
-  const uint32_t ring_full = bars + 18 * 8;  // [8]
-  const uint32_t ring_free = bars + 41 * 8;  // [8]
-  const uint32_t v_full = bars + 26 * 8;     // [3]
-  const uint32_t v_free = bars + 29 * 8;     // [3]  P . V of the buffer's tile is done
-  const uint32_t p_full = bars + 32 * 8;     // [2]  P and the factors have landed
-  const uint32_t go = bars + 49 * 8;         // [2]  all that P . V of a tile needs is there
-  const uint32_t ask = bars + 34 * 8;        // O is to be rescaled, or written
-  const uint32_t o_ok = bars + 35 * 8;       // and it is
+  const uint32_t q_free = bars + 2 * 8;      // every product with the job's query is done
+  const uint32_t k_full = bars + 3 * 8;      // [kKBufs]
+  const uint32_t k_free = bars + 7 * 8;      // [kKBufs]  S of the buffer's tile is done
+  const uint32_t s_full = bars + 11 * 8;     // [kSBufs]
+  const uint32_t s_free = bars + 14 * 8;     // [kSBufs]  the softmax has read S
+  const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's maximum is decided
+  const uint32_t ring_full = bars + 21 * 8;  // [kRing]
+  const uint32_t ring_free = bars + 29 * 8;  // [kRing]
+  const uint32_t p_free = bars + 37 * 8;     // [kPBufs]  P . V of the tile in this slot of P is done (either CTA)
+  const uint32_t p_full = bars + 41 * 8;     // [kPBufs]  P and the factors have landed
+  const uint32_t go = bars + 45 * 8;         // [kPBufs]  P and O are ready for P . V
+  const uint32_t v_full = bars + 49 * 8;     // [2 kVBufs] by half tile
+  const uint32_t v_free = bars + 54 * 8;     // [2 kVBufs]  its P . V is done
+  const uint32_t v_turn = bars + 60 * 8;     // [3]  by group: the tile's buffer is the group's
+  const uint32_t ask = bars + 67 * 8;        // O is to be rescaled, or written
+  const uint32_t o_ok = bars + 68 * 8;       // and it is
   Tile* ring = reinterpret_cast<Tile*>(sm + kData + kNumBars * 8);  // [8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
@@ -356,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // CTA 1
   uint8_t* VB = sm;
   uint8_t* PB = sm + kVBufs * kVBuf;
-  uint8_t* side = PB + kPBufs * kPBuf;  // [2] factors and flags
+  uint8_t* side = PB + kPBufs * kPBuf;  // [kPBufs] factors and flags
   __shared__ long long s_sum[kThreads / 32];
   __shared__ int s_job, s_unit, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
 
@@ -369,17 +383,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::mbar_init(q_full, 8);
     ptx::mbar_init(q_free, 1);
     ptx::mbar_init(ask, 1);
+    for (int i = 0; i < 3; ++i) ptx::mbar_init(v_turn + 8 * i, 4);
     ptx::mbar_init(o_ok, 4);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(p_free + 8 * (i), 1);
-      ptx::mbar_init(p_full + 8 * (i), 1);
+    for (int i = 0; i < kPBufs; ++i) {
+      ptx::mbar_init(p_free + 8 * i, 1);
+      ptx::mbar_init(p_full + 8 * i, 1);
       ptx::mbar_init(go + 8 * i, 1);
     }
-    for (int i = 0; i < 3; ++i) {
-      ptx::mbar_init(s_full + 8 * (i), 1);
-      ptx::mbar_init(s_free + 8 * (i), 4);
-      ptx::mbar_init(v_full + 8 * (i), 4);
-      ptx::mbar_init(v_free + 8 * (i), 1);
+    for (int i = 0; i < kSBufs; ++i) {
+      ptx::mbar_init(s_full + 8 * i, 1);
+      ptx::mbar_init(s_free + 8 * i, 4);
+    }
+    for (int i = 0; i < 2 * kVBufs; ++i) {
+      ptx::mbar_init(v_full + 8 * i, 4);
+      ptx::mbar_init(v_free + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(turn + 8 * i, 1);
@@ -471,9 +488,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       base += all;
     }
     gtot = int(block_sum(tiles));
-    // P of the first two tiles may arrive as soon as the pair has synced
+    // P of the first tiles may arrive as soon as the pair has synced
     if (half == 1 && threadIdx.x == 0)
-      for (int i = 0; i < 2 && i < gtot; ++i) ptx::mbar_arrive_expect_tx(p_full + 8 * (i), kPBytes);
+      for (int i = 0; i < kPBufs && i < gtot; ++i) ptx::mbar_arrive_expect_tx(p_full + 8 * (i), kPBytes);
   }
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before any remote arrive
@@ -509,10 +526,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   ptx::mma_f16_tmem_a(s, tmem + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id,
                                       (j | kk) ? 1u : 0u);
             } else {
-#pragma unroll 1
+#pragma unroll
               for (int part = 0; part < 2; ++part) {  // the query's E4M3, then its E5M2 part
                 const uint32_t id = ptx::idesc(part, 0, 128, kNT), q = tmem + part * 144;
-#pragma unroll 1
+#pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                   for (int kk = 0; kk < 4; ++kk)
@@ -558,23 +575,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
 #pragma unroll 1
-        for (int k = wk.k0; k < wk.k1; ++k, ++g) {
+        for (int k = wk.k0; k < wk.k1 && ok; ++k, ++g) {
           const int buf = g % kVBufs, pb = g % kPBufs;
           if (!ptx::mbar_wait(go + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const uint32_t vb = vb0 + buf * kVBuf, p = pb0 + pb * kPBuf;
-          if (ptx::elect_one()) {
 #pragma unroll 1
-            for (int kk = 0; kk < kNT / 16; ++kk)
+          for (int i = 0; i < 2; ++i) {  // 32 tokens of the tile
+            if (!ptx::mbar_wait(v_full + 8 * (2 * buf + i), uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t vb = vb0 + buf * kVBuf + i * 32 * 128, p = pb0 + pb * kPBuf + i * 4 * kPChunk;
+            if (ptx::elect_one()) {
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-                ptx::mma_f16(tmem + n * 256, ptx::sdesc_plain(p + kk * 2 * kPChunk, kPChunk, 128),
-                             ptx::sdesc_sw128_mn(vb + n * 4 * kBlk + kk * 16 * 128, kBlk, 1024), id,
-                             (k > wk.k0 || kk > 0) ? 1u : 0u);
-            ptx::mma_commit(v_free + 8 * buf);
-            ptx::mma_commit_to(p_free + 8 * pb, 1);  // CTA 0's barrier
+              for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                  ptx::mma_f16(tmem + n * 256, ptx::sdesc_plain(p + kk * 2 * kPChunk, kPChunk, 128),
+                               ptx::sdesc_sw128_mn(vb + n * 4 * kBlk + kk * 16 * 128, kBlk, 1024), id,
+                               (k > wk.k0 || i > 0 || kk > 0) ? 1u : 0u);
+              ptx::mma_commit(v_free + 8 * (2 * buf + i));
+              if (i) ptx::mma_commit_to(p_free + 8 * pb, 3);  // in both CTAs
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
     } else if (warp == kReadyWarp && half == 1) {
@@ -599,14 +620,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
-          const int buf = g % kVBufs, pb = g % kPBufs;
+          const int pb = g % kPBufs;
           if (!ptx::mbar_wait_cluster(p_full + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
           const uint4 flags = *reinterpret_cast<const uint4*>(side + pb * kPSide + 512);
           // re-arm for the next tile in this slot: it is not sent before this one's P . V is done
           if (lane == 0 && g + kPBufs < gtot) ptx::mbar_arrive_expect_tx(p_full + 8 * pb, kPBytes);
           if (k > wk.k0 && (flags.x | flags.y | flags.z | flags.w)) request(g);
           if (!settled()) { ok = false; break; }  // (at a job's first tile: the old output is written)
-          if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
           // P came by ordinary (remote) stores; the tensor core reads it through the async proxy
           ptx::fence_proxy_async_smem();
           ptx::tc_fence_before();
@@ -665,14 +685,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = queries(-2) && convert<true, true, kKBufs<true>, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB,
-                                                                 k_full, k_free, queries);
+        ok = queries(-2) && convert<true, true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
+                                                   queries);
       } else {
 #pragma unroll 1
         for (; on && ok; on = wk.next(a)) ok = load_q(wk.job);
       }
     } else {
-      ok = convert<kNv, false, kVBufs, 3>(a, gtot, group + 1, w, lane, ring, ring_full, ring_free, VB, v_full, v_free,
+      ok = convert<kNv, false, 3>(a, gtot, group + 1, w, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
                                           [](int) { return true; });
     }
   } else if (half == 0) {
@@ -769,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if (warp >= 4) {
-      ok = convert<kNv, false, kVBufs, 3>(a, gtot, 0, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free,
+      ok = convert<kNv, false, 3>(a, gtot, 0, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
                                           [](int) { return true; });
     } else {
       // ---------------------------------------------------------- O: rescaling and output
@@ -784,7 +804,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u)) { ok = false; break; }
           const int what = s_ask;
           g = what < 0 ? -1 - what : what;
-          if (!ptx::mbar_wait(v_free + 8 * ((g - 1) % kVBufs), uint32_t((g - 1) / kVBufs) & 1u)) { ok = false; break; }
+          if (!ptx::mbar_wait(p_free + 8 * ((g - 1) % kPBufs), uint32_t((g - 1) / kPBufs) & 1u)) { ok = false; break; }
           ptx::tc_fence_after();
           if (what < 0) break;
           const float alpha = reinterpret_cast<const float*>(side + (g % kPBufs) * kPSide)[row];
@@ -910,7 +930,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 
 // ---------------------------------------------------------------------------
 // Merge of a row's segments, those of its prefix tile and then those of its private
-// job: with M the largest maximum, out = scale * sum_i 2^(m_i - M) O_i / L and
+// job: with M the largest maximum, out = lat_scale * sum_i 2^(m_i - M) O_i / L and
 // L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums of their own;
 // its O is relative to the larger of their maxima). One CTA per (row, 3 heads),
 // 128 threads per head, 4 dims each.
@@ -949,17 +969,12 @@ __global__ void __launch_bounds__(128 * kMergeHeads) prefix_merge_kernel(PfxArgs
       acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
     }
     if (tot != 0.f) {  // NaN stays NaN
-      const float inv = a.out_scale / tot;
+      const float inv = a.lat_scale / tot;
       acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
       L = (mm - kPShift + log2f(tot)) * 0.6931471805599453f;
     } else {
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  }
-  if (a.swapped) {  // expand_bits left dims 1 and 2 of four in each other's place
-    const float y = acc.y;
-    acc.y = acc.z;
-    acc.z = y;
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
   uint2 pk;
@@ -995,8 +1010,7 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   a.tiles = prefix_len > 0 ? L.pfx_tiles : 0;
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
-  a.out_scale = p.latent_scale * (nv ? 1.f : kBitsScale);
-  a.swapped = nv ? 0 : 1;
+  a.lat_scale = p.latent_scale;
   CUtensorMap kmap, rmap;
   std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
   std::memset(&rmap, 0, sizeof(rmap));
