@@ -60,7 +60,7 @@ constexpr int kVBlks = kDNope / 64;          // 8
 constexpr int kKBuf = kKBlks * kBlk;         // 73,728 (NVFP4)
 constexpr int kKBuf8 = 4 * kBlk + kBlk / 2;  // 36,864 (FP8: 64 rows of 128 E4M3, and of 64 for the rope dims)
 constexpr int kVBuf = kVBlks * kBlk;         // 65,536
-constexpr int kVBufs = 2, kSBufs = 3, kPBufs = 4;
+constexpr int kVBufs = 2, kSBufs = 3, kPBufs = 3;
 template <bool kNv>
 constexpr int kKBufs = kNv ? 2 : 4;
 static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
@@ -823,7 +823,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) ptx::mbar_arrive(o_ok);
         }
         if (!ok) break;
-        float4* dst = reinterpret_cast<float4*>(a.part + (size_t(wk.job + clu) * kPfxTileRows + row) * kDNope);
+        // (four dims of all rows together, so that a warp's stores are whole lines)
+        float4* dst = reinterpret_cast<float4*>(a.part) + size_t(wk.job + clu) * kPfxTileRows * (kDNope / 4) + row;
         const bool real = wk.job < a.tiles || row < kHeads;
 #pragma unroll 1
         for (int c = 0; c < kDNope; c += 32) {
@@ -831,7 +832,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::tmem_ld32(tmem + lane_base + c, o);
           if (real) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) dst[c / 4 + j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+              dst[(c / 4 + j) * kPfxTileRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
         // the reads of O are ordered before the next job's first P . V
@@ -932,56 +934,100 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 // Merge of a row's segments, those of its prefix tile and then those of its private
 // job: with M the largest maximum, out = lat_scale * sum_i 2^(m_i - M) O_i / L and
 // L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums of their own;
-// its O is relative to the larger of their maxima). One CTA per (row, 3 heads),
-// 128 threads per head, 4 dims each.
+// its O is relative to the larger of their maxima). A warp has 32 heads, a lane each, 16
+// dims of them and every kSplit-th segment: a row alone has a segment from nearly
+// every pair, many rows have few each.
 // ---------------------------------------------------------------------------
-constexpr int kMergeHeads = 3;
+constexpr int kMergeWarps = 8;
 
-__global__ void __launch_bounds__(128 * kMergeHeads) prefix_merge_kernel(PfxArgs a, __nv_bfloat16* __restrict__ out,
-                                                                        float* __restrict__ lse) {
+template <int kSplit>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs a, __nv_bfloat16* __restrict__ out,
+                                                                       float* __restrict__ lse) {
+  constexpr int kParts = kMergeWarps / kSplit;  // warps with dims of their own
+  constexpr int kChunks = 4 * kParts;           // of four dims, of the CTA
+  constexpr int kPitch = kChunks + 1;
+  __shared__ float4 s_acc[kSplit > 1 ? kMergeWarps : 1][4][32];
+  __shared__ float2 s_ml[kSplit > 1 ? kMergeWarps : 1][32];
+  __shared__ uint2 s_out[32][kPitch];
   pdl_wait();
-  const int r = blockIdx.x, h = blockIdx.y * kMergeHeads + (threadIdx.x >> 7), d4 = threadIdx.x & 127;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
+  const int r = blockIdx.x, h = blockIdx.y * 32 + lane, c0 = blockIdx.z * kChunks + warp / kSplit * 4;
   const int hr = r * kHeads + h, job0 = hr / kPfxTileRows, job1 = a.tiles + r;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = -INFINITY;
+  float4 acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, tot = 0.f;
+  auto add = [&](int j, float w, const float4& v) {
+    acc[j].x = fmaf(w, v.x, acc[j].x); acc[j].y = fmaf(w, v.y, acc[j].y);
+    acc[j].z = fmaf(w, v.z, acc[j].z); acc[j].w = fmaf(w, v.w, acc[j].w);
+  };
   if (a.lens[r] > 0) {
-    const int c0 = a.prefix > 0 ? a.plan[2 * job0] : 0, n0 = a.prefix > 0 ? a.plan[2 * job0 + 1] - c0 + 1 : 0;
-    const int c1 = a.plan[2 * job1], n1 = a.plan[2 * job1 + 1] - c1 + 1;
+    const int f0 = a.prefix > 0 ? a.plan[2 * job0] : 0, n0 = a.prefix > 0 ? a.plan[2 * job0 + 1] - f0 + 1 : 0;
+    const int f1 = a.plan[2 * job1], n1 = a.plan[2 * job1 + 1] - f1 + 1;
     // segment i's slot and row
-    auto slot = [&](int i) { return i < n0 ? job0 + c0 + i : job1 + c1 + i - n0; };
+    auto slot = [&](int i) { return i < n0 ? job0 + f0 + i : job1 + f1 + i - n0; };
     auto row = [&](int i) { return i < n0 ? hr % kPfxTileRows : h; };
-    float m = -INFINITY;
-    for (int i = 0; i < n0 + n1; ++i) {
+#pragma unroll 4
+    for (int i = part; i < n0 + n1; i += kSplit) {
       const float* ml = a.ml + size_t(slot(i)) * 512 + row(i);
       m = fmaxf(m, fmaxf(__ldg(ml), __ldg(ml + 256)));
     }
     const float mm = m == -INFINITY ? 0.f : m;
-    float tot = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n0 + n1; ++i) {
+#pragma unroll 2
+    for (int i = part; i < n0 + n1; i += kSplit) {
       const float* ml = a.ml + size_t(slot(i)) * 512 + row(i);
+      const float4* o = reinterpret_cast<const float4*>(a.part) + size_t(slot(i)) * kPfxTileRows * (kDNope / 4) +
+                        c0 * kPfxTileRows + row(i);
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __ldg(o + j * kPfxTileRows);
       const float ma = __ldg(ml), mb = __ldg(ml + 256);
-      const float w = exp2f(fmaxf(ma, mb) - mm);
       tot = fmaf(exp2f(ma - mm), __ldg(ml + 128), tot);
       tot = fmaf(exp2f(mb - mm), __ldg(ml + 384), tot);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(a.part + (size_t(slot(i)) * kPfxTileRows + row(i)) * kDNope) + d4);
-      acc.x = fmaf(w, v.x, acc.x); acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z); acc.w = fmaf(w, v.w, acc.w);
-    }
-    if (tot != 0.f) {  // NaN stays NaN
-      const float inv = a.lat_scale / tot;
-      acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-      L = (mm - kPShift + log2f(tot)) * 0.6931471805599453f;
-    } else {
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const float w = exp2f(fmaxf(ma, mb) - mm);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) add(j, w, v[j]);
     }
   }
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-  uint2 pk;
-  pk.x = *reinterpret_cast<const uint32_t*>(&lo);
-  pk.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(out + size_t(hr) * kDNope + 4 * d4) = pk;
-  if (lse && d4 == 0) lse[hr] = L;
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_acc[warp][j][lane] = acc[j];
+    s_ml[warp][lane] = make_float2(m, tot);
+    __syncthreads();
+    if (part == 0) {
+      for (int i = 1; i < kSplit; ++i) m = fmaxf(m, s_ml[warp + i][lane].x);
+      const float mm = m == -INFINITY ? 0.f : m;
+      tot = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < kSplit; ++i) {
+        const float2 ml = s_ml[warp + i][lane];
+        const float w = exp2f(ml.x - mm);  // a warp without a segment has m = -infinity and weight 0
+        tot = fmaf(w, ml.y, tot);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add(j, w, s_acc[warp + i][j][lane]);
+      }
+    }
+  }
+  if (part == 0) {
+    const float inv = tot != 0.f ? a.lat_scale / tot : 0.f;  // NaN stays NaN
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = tot != 0.f ? make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      s_out[lane][warp / kSplit * 4 + j] =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    const float mm = m == -INFINITY ? 0.f : m;
+    if (lse && c0 == 0) lse[hr] = tot != 0.f ? (mm - kPShift + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * kChunks; i += 32 * kMergeWarps) {
+    const int row = i / kChunks, c = i % kChunks;
+    reinterpret_cast<uint2*>(out + size_t(r * kHeads + blockIdx.y * 32 + row) * kDNope)[blockIdx.z * kChunks + c] =
+        s_out[row][c];
+  }
 }
 
 }  // namespace
@@ -1035,8 +1081,11 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   const int clusters = std::max(1, std::min(kPfxMaxClusters, sm_count() / 2));
   e = launch_pdl(kern, dim3(2 * clusters), dim3(kThreads), kSmem, st, kmap, rmap, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefix_merge_kernel, dim3(L.rows, kHeads / kMergeHeads), dim3(128 * kMergeHeads), 0, st, a,
-                    static_cast<__nv_bfloat16*>(out), lse);
+  // a row has a little more than clusters / rows segments
+  const bool split = L.rows * 4 <= clusters;
+  return launch_pdl(split ? prefix_merge_kernel<kMergeWarps> : prefix_merge_kernel<1>,
+                    dim3(L.rows, kHeads / 32, kDNope / 4 / (split ? 4 : 4 * kMergeWarps)), dim3(32 * kMergeWarps), 0, st,
+                    a, static_cast<__nv_bfloat16*>(out), lse);
 }
 
 }  // namespace dsa
