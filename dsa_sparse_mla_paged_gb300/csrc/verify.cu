@@ -25,11 +25,11 @@ namespace dsa {
 
 namespace {
 
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxCluster = 8;
-constexpr int kVUnroll = 8;
-constexpr int kVMinRun = 32 * kVUnroll;  // a warp's shortest run of the vocabulary worth a warp
+constexpr int kVPerSM = 4;     // resident CTAs
+constexpr int kVUnit = 256;    // a warp's run of the vocabulary is a multiple: 32 lanes x 16 B of 16-bit values
 
 typedef unsigned long long u64;
 
@@ -48,6 +48,28 @@ __device__ __forceinline__ u64 fixed(float x, bool& bad) {
   return ok ? __float2ull_rz(x * 1152921504606846976.f) : 0ull;
 }
 
+// The same in three integers of a register each, x = h 2^-22 + m 2^-44 + l 2^-60, from
+// the mantissas of sums rounded towards zero (2 + x has steps of 2^-22, and so on): a
+// conversion to 64 bits costs several times as much. Only differences of two
+// values' integers are used, which drops the sums' exponents.
+struct Pieces {
+  uint32_t h, m, l;
+};
+__device__ __forceinline__ Pieces pieces(float x) {
+  constexpr float kMid = 1.f / (1 << 21), kLow = kMid / (1 << 16);
+  const float h = __fadd_rz(x, 2.f), r = x - (h - 2.f);
+  const float m = __fadd_rz(r, kMid), l = __fadd_rz(r - (m - kMid), kLow);
+  return {__float_as_uint(h), __float_as_uint(m), __float_as_uint(l)};
+}
+
+// x, or 0 for what is not in [0, 1]; `wrong` collects the bits of what was dropped (-0's
+// sign alone is not wrong).
+__device__ __forceinline__ float checked(float x, uint32_t& wrong) {
+  const float y = __float_as_uint(x) <= 0x3f800000u ? x : 0.f;
+  wrong |= __float_as_uint(x) ^ __float_as_uint(y);
+  return y;
+}
+
 struct VerifyArgs {
   VerifyIn in;
   int n_q;
@@ -63,6 +85,85 @@ __device__ __forceinline__ u64 weight(T pv, T qv, bool has_q, bool one_hot, int 
   if (!has_q) return p;
   const u64 q = fixed(as_float(qv), bad);
   return p > q ? p - q : 0ull;
+}
+
+// The weights of a warp's run, one lane's share of it: `sum` in units of 2^-60
+// modulo 2^64, and `coarse` in units of 2^-22 (rounded either way, and held at its top),
+// which tells whether `sum` has wrapped.
+struct Mass {
+  u64 sum = 0;
+  uint32_t coarse = 0, wrong = 0;
+  uint32_t h = 0, m = 0, l = 0;
+  __device__ __forceinline__ void add(float p, float q) {
+    p = checked(p, wrong);
+    q = checked(q, wrong);
+    const Pieces a = pieces(p), b = pieces(q);
+    if (p > q) {
+      h += a.h - b.h;
+      m += a.m - b.m;
+      l += a.l - b.l;
+    }
+  }
+  __device__ __forceinline__ void add(float p) { add(p, 0.f); }
+  // after at most 256 elements
+  __device__ __forceinline__ void flush() {
+    sum += (u64(h) << 38) + (u64(int64_t(int32_t(m))) << 16) + u64(int64_t(int32_t(l)));
+    coarse = min(coarse + h, 1u << 31);
+    h = m = l = 0;
+  }
+};
+
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / int(sizeof(T));
+  union {
+    uint4 u;
+    T e[kN];
+  };
+  __device__ __forceinline__ Vec() {}
+};
+
+// Elements [lo, hi), lo a multiple of kVUnit. kWide: rows on 16-B boundaries.
+template <typename T, bool kWide, bool kQ>
+__device__ __forceinline__ void gather(Mass& acc, const T* __restrict__ prow, const T* __restrict__ qrow, int lo, int hi,
+                                       int lane) {
+  int v = lo;
+  if constexpr (kWide) {
+    constexpr int kN = Vec<T>::kN, kU = kQ ? 2 : 4;
+#pragma unroll 1
+    for (; v + 32 * kN * kU <= hi; v += 32 * kN * kU) {
+      Vec<T> p[kU], q[kQ ? kU : 1];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        p[u].u = __ldg(reinterpret_cast<const uint4*>(prow + v) + 32 * u + lane);
+        if constexpr (kQ) q[u].u = __ldg(reinterpret_cast<const uint4*>(qrow + v) + 32 * u + lane);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          if constexpr (kQ) acc.add(as_float(p[u].e[j]), as_float(q[u].e[j]));
+          else acc.add(as_float(p[u].e[j]));
+        }
+      acc.flush();
+    }
+  }
+  constexpr int kU = 8;
+#pragma unroll 1
+  for (v += lane; v < hi; v += 32 * kU) {
+    T p[kU], q[kQ ? kU : 1];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      p[u] = v + 32 * u < hi ? prow[v + 32 * u] : T(0.f);
+      if constexpr (kQ) q[u] = v + 32 * u < hi ? qrow[v + 32 * u] : T(0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if constexpr (kQ) acc.add(as_float(p[u]), as_float(q[u]));
+      else acc.add(as_float(p[u]));
+    }
+    acc.flush();
+  }
 }
 
 __device__ __forceinline__ u64 capped(u64 v) { return v < kTooMuch ? v : kTooMuch; }
@@ -84,7 +185,7 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid_constant__ VerifyArgs a) {
   namespace cg = cooperative_groups;
   pdl_wait();
   cg::cluster_group cl = cg::this_cluster();
@@ -146,27 +247,26 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const __grid_constant
   const int64_t v0 = (int64_t(cta) * kVWarps + warp) * a.run;
   const int lo = int(v0 < V ? v0 : V), hi = int(v0 + a.run < V ? v0 + a.run : V);
   bool has_q = qrow != nullptr, one_hot = rejected && !Q, bad = false;
-  u64 sum = 0, total = 0, before = 0;
+  u64 total = 0, before = 0;
   for (int round = 0; round < 2; ++round) {
-    uint32_t coarse = 0;  // the sum in units of 2^-16: the integers of 2^-60 wrap at 16
-    sum = 0;
-    for (int v = lo + lane; v < hi; v += 32 * kVUnroll) {
-      T pv[kVUnroll], qv[kVUnroll];
-#pragma unroll
-      for (int j = 0; j < kVUnroll; ++j) {
-        const bool in_run = v + 32 * j < hi;
-        pv[j] = in_run ? prow[v + 32 * j] : T(0.f);
-        qv[j] = in_run && has_q ? qrow[v + 32 * j] : T(0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < kVUnroll; ++j) {
-        const u64 w = weight<T>(pv[j], qv[j], has_q, one_hot, v + 32 * j, x, bad);
-        sum += w;
-        coarse += uint32_t(w >> 44);
-      }
+    Mass acc;
+    const bool wide = ((reinterpret_cast<uintptr_t>(prow) | (has_q ? reinterpret_cast<uintptr_t>(qrow) : 0)) & 15) == 0;
+    if (has_q) {
+      if (wide) gather<T, true, true>(acc, prow, qrow, lo, hi, lane);
+      else gather<T, false, true>(acc, prow, qrow, lo, hi, lane);
+    } else {
+      if (wide) gather<T, true, false>(acc, prow, nullptr, lo, hi, lane);
+      else gather<T, false, false>(acc, prow, nullptr, lo, hi, lane);
     }
-    sum = warp_sum(sum);
-    if (warp_sum(coarse) > (4u << 16)) sum = kTooMuch;
+    bad |= (acc.wrong & 0x7fffffffu) != 0;
+    // (the draft's own token has no weight; what was dropped or wrong there is 0 or reported)
+    if (one_hot && lane == 0 && x >= lo && x < hi) {
+      const u64 own = fixed(as_float(prow[x]), bad);
+      acc.sum -= own;
+      acc.coarse -= min(acc.coarse, uint32_t(own >> 38));
+    }
+    u64 sum = warp_sum(acc.sum);
+    if (warp_sum(acc.coarse) > (5ull << 22)) sum = kTooMuch;
     if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     if (threadIdx.x < ctas) {
@@ -209,25 +309,30 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const __grid_constant
   int w = 0;
   for (; w < kVWarps && at + s_warp[w] <= thr; ++w) at += s_warp[w];
   if (w == kVWarps) return;
+  // (a thread has a piece of that run, and the one with the threshold walks its own)
   const int64_t r0 = (int64_t(cta) * kVWarps + w) * a.run;
   const int end = int(r0 + a.run < V ? r0 + a.run : V);
-  for (int c0 = int(r0); c0 < end; c0 += kVThreads) {
-    const int v = c0 + int(threadIdx.x);
-    u64 own = 0;
-    if (v < end) own = weight<T>(prow[v], has_q ? qrow[v] : T(0.f), has_q, one_hot, v, x, bad);
-    const u64 inc = warp_scan(own);
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = inc;
-    __syncthreads();
-    u64 pre = at, all = 0;
-    for (int i = 0; i < kVWarps; ++i) {
-      if (i < warp) pre += s_scan[i];
-      all += s_scan[i];
+  const int piece = (end - int(r0) + kVThreads - 1) / kVThreads;
+  const int64_t mine = r0 + int64_t(piece) * threadIdx.x;
+  const int v0t = int(mine < end ? mine : end), v1t = int(mine + piece < end ? mine + piece : end);
+  u64 own = 0;
+#pragma unroll 4
+  for (int v = v0t; v < v1t; ++v) own += weight<T>(prow[v], has_q ? qrow[v] : T(0.f), has_q, one_hot, v, x, bad);
+  const u64 inc = warp_scan(own);
+  if (lane == 31) s_scan[warp] = inc;
+  __syncthreads();
+  u64 pre = at + inc - own;
+  for (int i = 0; i < warp; ++i) pre += s_scan[i];
+  // exactly one thread, and one of its elements, has the threshold inside its weight
+  if (own && pre + own > thr && pre <= thr) {
+#pragma unroll 1
+    for (int v = v0t; v < v1t; ++v) {
+      pre += weight<T>(prow[v], has_q ? qrow[v] : T(0.f), has_q, one_hot, v, x, bad);
+      if (pre > thr) {
+        out[acc] = v;
+        break;
+      }
     }
-    // exactly one element has the threshold inside its weight
-    if (own && pre + inc > thr && pre + inc - own <= thr) out[acc] = v;
-    at += all;
-    if (at > thr) break;
   }
 }
 
@@ -238,10 +343,14 @@ cudaError_t launch_verify_draft(const dsa_params_t& p, const WsLayout& L, char* 
   a.in = in;
   a.n_q = p.n_q;
   a.err = reinterpret_cast<int*>(ws + L.err);
+  // as many CTAs to a request as are worth it and as run at once (the integers do not
+  // depend on the cut): past one wave, each CTA's chain of loads before its row is paid again
+  const int slots = sm_count() * kVPerSM;
   int ctas = 1;
-  while (ctas < kVMaxCluster && int64_t(ctas) * kVWarps * kVMinRun < in.vocab) ctas *= 2;
+  while (ctas < kVMaxCluster && int64_t(ctas) * kVWarps * kVUnit < in.vocab && 2 * ctas * int64_t(p.batch) <= slots)
+    ctas *= 2;
   const int per = (in.vocab + ctas * kVWarps - 1) / (ctas * kVWarps);
-  a.run = (per + 31) / 32 * 32;
+  a.run = (per + kVUnit - 1) / kVUnit * kVUnit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.batch) * ctas);
   cfg.blockDim = dim3(kVThreads);
