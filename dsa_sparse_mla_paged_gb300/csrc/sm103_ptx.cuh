@@ -267,6 +267,21 @@ __device__ __forceinline__ void fma2(float& a, float& b, float m, float c) {
       : "f"(m), "f"(c));
 }
 
+__device__ __forceinline__ float2 add2_rz(float2 a, float2 b) {
+  asm("{\n\t.reg .b64 t, u;\n\tmov.b64 t, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tadd.rz.f32x2 t, t, u;\n\t"
+      "mov.b64 {%0, %1}, t;\n}\n"
+      : "+f"(a.x), "+f"(a.y)
+      : "f"(b.x), "f"(b.y));
+  return a;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) {
+  asm("{\n\t.reg .b64 t, u;\n\tmov.b64 t, {%0, %1};\n\tmov.b64 u, {%2, %3};\n\tsub.rn.f32x2 t, t, u;\n\t"
+      "mov.b64 {%0, %1}, t;\n}\n"
+      : "+f"(a.x), "+f"(a.y)
+      : "f"(b.x), "f"(b.y));
+  return a;
+}
+
 // Bounded wait that acquires at cluster scope (data written by another CTA).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t limit = (1u << 24)) {
 #pragma unroll 1

@@ -29,7 +29,8 @@ constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxCluster = 8;
 constexpr int kVPerSM = 4;     // resident CTAs
-constexpr int kVUnit = 256;    // a warp's run of the vocabulary is a multiple: 32 lanes x 16 B of 16-bit values
+constexpr int kVUnit = 256;    // a part of a warp's run is a multiple: 32 lanes x 16 B of 16-bit values
+constexpr int kVParts = 4;     // parts of a warp's run with sums of their own
 
 typedef unsigned long long u64;
 
@@ -48,32 +49,28 @@ __device__ __forceinline__ u64 fixed(float x, bool& bad) {
   return ok ? __float2ull_rz(x * 1152921504606846976.f) : 0ull;
 }
 
-// The same in three integers of a register each, x = h 2^-22 + m 2^-44 + l 2^-60, from
-// the mantissas of sums rounded towards zero (2 + x has steps of 2^-22, and so on): a
-// conversion to 64 bits costs several times as much. Only differences of two
-// values' integers are used, which drops the sums' exponents.
+// Two values in [0, 1], each in three integers of a register, x = h 2^-22 + m 2^-44 +
+// l 2^-60, from the mantissas of sums rounded towards zero (2 + x has steps of 2^-22,
+// and so on), two at a time: a conversion to 64 bits takes several times as long.
+// Only differences of two values' integers are used, which drops the sums' exponents.
 struct Pieces {
-  uint32_t h, m, l;
+  float2 h, m, l;
 };
-__device__ __forceinline__ Pieces pieces(float x) {
+__device__ __forceinline__ Pieces pieces(float2 x) {
   constexpr float kMid = 1.f / (1 << 21), kLow = kMid / (1 << 16);
-  const float h = __fadd_rz(x, 2.f), r = x - (h - 2.f);
-  const float m = __fadd_rz(r, kMid), l = __fadd_rz(r - (m - kMid), kLow);
-  return {__float_as_uint(h), __float_as_uint(m), __float_as_uint(l)};
+  Pieces o;
+  o.h = ptx::add2_rz(x, make_float2(2.f, 2.f));
+  const float2 r = ptx::sub2(x, ptx::sub2(o.h, make_float2(2.f, 2.f)));
+  o.m = ptx::add2_rz(r, make_float2(kMid, kMid));
+  o.l = ptx::add2_rz(ptx::sub2(r, ptx::sub2(o.m, make_float2(kMid, kMid))), make_float2(kLow, kLow));
+  return o;
 }
-
-// x, or 0 for what is not in [0, 1]; `wrong` collects the bits of what was dropped (-0's
-// sign alone is not wrong).
-__device__ __forceinline__ float checked(float x, uint32_t& wrong) {
-  const float y = __float_as_uint(x) <= 0x3f800000u ? x : 0.f;
-  wrong |= __float_as_uint(x) ^ __float_as_uint(y);
-  return y;
-}
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
 
 struct VerifyArgs {
   VerifyIn in;
   int n_q;
-  int run;  // elements of a warp's run
+  int run, part;  // elements of a warp's run, and of a part of it
   int* err;
 };
 
@@ -87,30 +84,52 @@ __device__ __forceinline__ u64 weight(T pv, T qv, bool has_q, bool one_hot, int 
   return p > q ? p - q : 0ull;
 }
 
-// The weights of a warp's run, one lane's share of it: `sum` in units of 2^-60
-// modulo 2^64, and `coarse` in units of 2^-22 (rounded either way, and held at its top),
-// which tells whether `sum` has wrapped.
+// The weights of a lane's elements: `sum` in units of 2^-60 modulo 2^64, and `coarse`
+// in units of 2^-22 (rounded either way, and held at its top), which tells whether
+// `sum` has wrapped. kFast: for values in [0, 1]; `top` tells whether all were.
+template <bool kFast>
 struct Mass {
   u64 sum = 0;
-  uint32_t coarse = 0, wrong = 0;
+  uint32_t coarse = 0, top = 0;
   uint32_t h = 0, m = 0, l = 0;
+  bool bad = false;
   __device__ __forceinline__ void add(float p, float q) {
-    p = checked(p, wrong);
-    q = checked(q, wrong);
-    const Pieces a = pieces(p), b = pieces(q);
-    if (p > q) {
-      h += a.h - b.h;
-      m += a.m - b.m;
-      l += a.l - b.l;
+    if constexpr (kFast) {
+      top = max(top, max(bits(p), bits(q)));
+      const Pieces a = pieces(make_float2(p, q));
+      if (p > q) {
+        h += bits(a.h.x) - bits(a.h.y);
+        m += bits(a.m.x) - bits(a.m.y);
+        l += bits(a.l.x) - bits(a.l.y);
+      }
+    } else {
+      const u64 a = fixed(p, bad), b = fixed(q, bad);
+      if (a > b) {
+        sum += a - b;
+        h += uint32_t((a - b) >> 38);
+      }
     }
   }
-  __device__ __forceinline__ void add(float p) { add(p, 0.f); }
+  // two elements without a q
+  __device__ __forceinline__ void add_two(float p0, float p1) {
+    if constexpr (kFast) {
+      top = max(top, max(bits(p0), bits(p1)));
+      const Pieces a = pieces(make_float2(p0, p1));
+      h += bits(a.h.x) - bits(2.f) + (bits(a.h.y) - bits(2.f));
+      m += bits(a.m.x) - kMidBits + (bits(a.m.y) - kMidBits);
+      l += bits(a.l.x) - kLowBits + (bits(a.l.y) - kLowBits);
+    } else {
+      add(p0, 0.f);
+      add(p1, 0.f);
+    }
+  }
   // after at most 256 elements
   __device__ __forceinline__ void flush() {
-    sum += (u64(h) << 38) + (u64(int64_t(int32_t(m))) << 16) + u64(int64_t(int32_t(l)));
+    if constexpr (kFast) sum += (u64(h) << 38) + (u64(int64_t(int32_t(m))) << 16) + u64(int64_t(int32_t(l)));
     coarse = min(coarse + h, 1u << 31);
     h = m = l = 0;
   }
+  static constexpr uint32_t kMidBits = uint32_t(127 - 21) << 23, kLowBits = uint32_t(127 - 37) << 23;
 };
 
 template <typename T>
@@ -122,49 +141,6 @@ struct Vec {
   };
   __device__ __forceinline__ Vec() {}
 };
-
-// Elements [lo, hi), lo a multiple of kVUnit. kWide: rows on 16-B boundaries.
-template <typename T, bool kWide, bool kQ>
-__device__ __forceinline__ void gather(Mass& acc, const T* __restrict__ prow, const T* __restrict__ qrow, int lo, int hi,
-                                       int lane) {
-  int v = lo;
-  if constexpr (kWide) {
-    constexpr int kN = Vec<T>::kN, kU = kQ ? 2 : 4;
-#pragma unroll 1
-    for (; v + 32 * kN * kU <= hi; v += 32 * kN * kU) {
-      Vec<T> p[kU], q[kQ ? kU : 1];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        p[u].u = __ldg(reinterpret_cast<const uint4*>(prow + v) + 32 * u + lane);
-        if constexpr (kQ) q[u].u = __ldg(reinterpret_cast<const uint4*>(qrow + v) + 32 * u + lane);
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          if constexpr (kQ) acc.add(as_float(p[u].e[j]), as_float(q[u].e[j]));
-          else acc.add(as_float(p[u].e[j]));
-        }
-      acc.flush();
-    }
-  }
-  constexpr int kU = 8;
-#pragma unroll 1
-  for (v += lane; v < hi; v += 32 * kU) {
-    T p[kU], q[kQ ? kU : 1];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      p[u] = v + 32 * u < hi ? prow[v + 32 * u] : T(0.f);
-      if constexpr (kQ) q[u] = v + 32 * u < hi ? qrow[v + 32 * u] : T(0.f);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if constexpr (kQ) acc.add(as_float(p[u]), as_float(q[u]));
-      else acc.add(as_float(p[u]));
-    }
-    acc.flush();
-  }
-}
 
 __device__ __forceinline__ u64 capped(u64 v) { return v < kTooMuch ? v : kTooMuch; }
 
@@ -184,13 +160,77 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {
   return v;
 }
 
+// Elements [lo, hi), lo a multiple of kVUnit. wide: rows on 16-B boundaries.
+template <typename T, bool kQ, bool kFast>
+__device__ __forceinline__ void gather(Mass<kFast>& acc, const T* __restrict__ prow, const T* __restrict__ qrow, int lo,
+                                       int hi, int lane, bool wide) {
+  int v = lo;
+  if (wide) {
+    constexpr int kN = Vec<T>::kN, kU = kQ ? 2 : 4;
+#pragma unroll 1
+    for (; v + 32 * kN * kU <= hi; v += 32 * kN * kU) {
+      Vec<T> p[kU], q[kQ ? kU : 1];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        p[u].u = __ldg(reinterpret_cast<const uint4*>(prow + v) + 32 * u + lane);
+        if constexpr (kQ) q[u].u = __ldg(reinterpret_cast<const uint4*>(qrow + v) + 32 * u + lane);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int j = 0; j < kN; j += kQ ? 1 : 2) {
+          if constexpr (kQ) acc.add(as_float(p[u].e[j]), as_float(q[u].e[j]));
+          else acc.add_two(as_float(p[u].e[j]), as_float(p[u].e[j + 1]));
+        }
+      acc.flush();
+    }
+  }
+  constexpr int kU = 8;
+#pragma unroll 1
+  for (v += lane; v < hi; v += 32 * kU) {
+    T p[kU], q[kQ ? kU : 1];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      p[u] = v + 32 * u < hi ? prow[v + 32 * u] : T(0.f);
+      if constexpr (kQ) q[u] = v + 32 * u < hi ? qrow[v + 32 * u] : T(0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; u += kQ ? 1 : 2) {
+      if constexpr (kQ) acc.add(as_float(p[u]), as_float(q[u]));
+      else acc.add_two(as_float(p[u]), as_float(p[u + 1]));
+    }
+    acc.flush();
+  }
+}
+
+// A warp's elements [lo, hi): the sum in every lane, kTooMuch where it has wrapped.
+template <typename T, bool kFast>
+__device__ __forceinline__ u64 warp_mass(const T* prow, const T* qrow, int lo, int hi, int x, bool wide, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  Mass<kFast> acc;
+  if (qrow) gather<T, true>(acc, prow, qrow, lo, hi, lane, wide);
+  else gather<T, false>(acc, prow, qrow, lo, hi, lane, wide);
+  if constexpr (kFast) {
+    // a value above 1, a NaN or a sign (-0's too): value by value
+    if (__any_sync(0xffffffffu, acc.top > bits(1.f))) return warp_mass<T, false>(prow, qrow, lo, hi, x, wide, bad);
+  }
+  bad |= acc.bad;
+  if (lane == 0 && x >= lo && x < hi) {  // the token that has no weight
+    const u64 own = fixed(as_float(prow[x]), bad);
+    acc.sum -= own;
+    acc.coarse -= min(acc.coarse, uint32_t(own >> 38));
+  }
+  const u64 sum = warp_sum(acc.sum);
+  return warp_sum(acc.coarse) > (5ull << 22) ? kTooMuch : sum;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid_constant__ VerifyArgs a) {
   namespace cg = cooperative_groups;
   pdl_wait();
   cg::cluster_group cl = cg::this_cluster();
   __shared__ int s_acc, s_count, s_flags;
-  __shared__ u64 s_warp[kVWarps], s_cta[2][kVMaxCluster];
+  __shared__ u64 s_part[kVWarps * kVParts], s_cta[2][kVMaxCluster];
   __shared__ u64 s_scan[kVWarps];
   const VerifyIn& in = a.in;
   const int cta = int(cl.block_rank()), ctas = int(cl.num_blocks());
@@ -244,34 +284,23 @@ __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid
   const u64 u64th = __float2ull_rz(uc * 18446744073709551616.f);
 
   // ---- sums over the warp runs; a second round with p alone if p - q has no mass
-  const int64_t v0 = (int64_t(cta) * kVWarps + warp) * a.run;
-  const int lo = int(v0 < V ? v0 : V), hi = int(v0 + a.run < V ? v0 + a.run : V);
+  const int part = a.part, run = a.run;
+  const int64_t v0 = (int64_t(cta) * kVWarps + warp) * run;
+  const int lo = int(v0 < V ? v0 : V), hi = int(v0 + run < V ? v0 + run : V);
   bool has_q = qrow != nullptr, one_hot = rejected && !Q, bad = false;
   u64 total = 0, before = 0;
   for (int round = 0; round < 2; ++round) {
-    Mass acc;
-    const bool wide = ((reinterpret_cast<uintptr_t>(prow) | (has_q ? reinterpret_cast<uintptr_t>(qrow) : 0)) & 15) == 0;
-    if (has_q) {
-      if (wide) gather<T, true, true>(acc, prow, qrow, lo, hi, lane);
-      else gather<T, false, true>(acc, prow, qrow, lo, hi, lane);
-    } else {
-      if (wide) gather<T, true, false>(acc, prow, nullptr, lo, hi, lane);
-      else gather<T, false, false>(acc, prow, nullptr, lo, hi, lane);
+    const T* q = has_q ? qrow : nullptr;
+    const bool wide = ((reinterpret_cast<uintptr_t>(prow) | reinterpret_cast<uintptr_t>(q)) & 15) == 0;
+    for (int i = 0; i < kVParts; ++i) {
+      const int l = min(lo + i * part, hi), r = min(l + part, hi);
+      const u64 sum = warp_mass<T, true>(prow, q, l, r, one_hot ? x : -1, wide, bad);
+      if (lane == 0) s_part[warp * kVParts + i] = sum;
     }
-    bad |= (acc.wrong & 0x7fffffffu) != 0;
-    // (the draft's own token has no weight; what was dropped or wrong there is 0 or reported)
-    if (one_hot && lane == 0 && x >= lo && x < hi) {
-      const u64 own = fixed(as_float(prow[x]), bad);
-      acc.sum -= own;
-      acc.coarse -= min(acc.coarse, uint32_t(own >> 38));
-    }
-    u64 sum = warp_sum(acc.sum);
-    if (warp_sum(acc.coarse) > (5ull << 22)) sum = kTooMuch;
-    if (lane == 0) s_warp[warp] = sum;
     __syncthreads();
     if (threadIdx.x < ctas) {
       u64 t = 0;
-      for (int i = 0; i < kVWarps; ++i) t = capped(t + s_warp[i]);
+      for (int i = 0; i < kVWarps * kVParts; ++i) t = capped(t + s_part[i]);
       *cl.map_shared_rank(&s_cta[round][cta], threadIdx.x) = t;
     }
     cl.sync();
@@ -307,11 +336,11 @@ __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid
   if (!drawn || thr < before) return;
   u64 at = before;
   int w = 0;
-  for (; w < kVWarps && at + s_warp[w] <= thr; ++w) at += s_warp[w];
-  if (w == kVWarps) return;
-  // (a thread has a piece of that run, and the one with the threshold walks its own)
-  const int64_t r0 = (int64_t(cta) * kVWarps + w) * a.run;
-  const int end = int(r0 + a.run < V ? r0 + a.run : V);
+  for (; w < kVWarps * kVParts && at + s_part[w] <= thr; ++w) at += s_part[w];
+  if (w == kVWarps * kVParts) return;
+  // (a thread has a piece of that part, and the one with the threshold walks its own)
+  const int64_t w0 = (int64_t(cta) * kVWarps + w / kVParts) * run, r0 = w0 + w % kVParts * part;
+  const int end = int(min(int64_t(V), min(w0 + run, r0 + part)));
   const int piece = (end - int(r0) + kVThreads - 1) / kVThreads;
   const int64_t mine = r0 + int64_t(piece) * threadIdx.x;
   const int v0t = int(mine < end ? mine : end), v1t = int(mine + piece < end ? mine + piece : end);
@@ -349,8 +378,9 @@ cudaError_t launch_verify_draft(const dsa_params_t& p, const WsLayout& L, char* 
   int ctas = 1;
   while (ctas < kVMaxCluster && int64_t(ctas) * kVWarps * kVUnit < in.vocab && 2 * ctas * int64_t(p.batch) <= slots)
     ctas *= 2;
-  const int per = (in.vocab + ctas * kVWarps - 1) / (ctas * kVWarps);
-  a.run = (per + kVUnit - 1) / kVUnit * kVUnit;
+  auto units = [](int n, int by) { return (n + by * kVUnit - 1) / (by * kVUnit); };
+  a.run = units(in.vocab, ctas * kVWarps) * kVUnit;
+  a.part = units(a.run, kVParts) * kVUnit;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.batch) * ctas);
   cfg.blockDim = dim3(kVThreads);
