@@ -10,12 +10,15 @@
 // borders; each segment leaves an unnormalised partial output with its softmax
 // maximum and sum, and the merge kernel adds up the segments of a row's two jobs.
 //
-// The second product takes fp16 operands: E4M3 and E2M1 x E4M3 values are exact in
-// fp16, and softmax weights are scaled to at most 2^7 (2^15 until the running maximum
-// is raised), so that fp16 holds them to 11 bits down to 2^-21 of the maximum. The
-// first product takes the FP8 latents as they lie in the cache, against the query as
-// the sum of an E4M3 and an E5M2 part (which together hold a bf16 value's 8 bits), or
-// NVFP4 latents as fp16 against the query in fp16. Sums are fp32 throughout.
+// Both products take FP8 latents as they lie in the cache, by TMA, and their other operand
+// as the sum of two FP8 parts, which costs what one product in fp16 does: the query as
+// E4M3 + E5M2, which holds a bf16 value's 8 bits, and a softmax weight as E5M2 + E4M3
+// (scaled to at most 2^6, 2^12 until the running maximum is raised), within 2^-8 of
+// it, as bf16 would be, or 2^-16 of the row's largest. (With weights and values in fp16 the
+// values have to be converted, 96 KB through shared memory per tile beside the 96 KB
+// that the product reads: 1.78 k cycles a tile where 1.03 k are the product's.) NVFP4 latents
+// have six bits a value, too many for E4M3: they are converted to fp16, which holds
+// them exactly, the query and the weights (to 11 bits) too. Sums are fp32 throughout.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -36,7 +39,7 @@ namespace {
 // SM's tensor memory, so the pair divides the two products: CTA 0 (scores) multiplies
 // S = Q . C^T over all 576 dims and runs the softmax, CTA 1 (output) multiplies
 // O += P . V. Per 64-token tile they cost 1,152 and 1,024 tensor-core cycles at full
-// rate, and what crosses between them is P alone: 16 KB of fp16, one way. (A
+// rate, and what crosses between them is P alone: 16 KB, one way. (A
 // division by latent dims balances better, 1,088 each, but has to add partial scores,
 // 32 KB of fp32 each way per tile; at the 32 B a cycle that an SM takes from
 // another's stores that is 1,024 cycles, and it ran at 3,000 cycles a tile.)
@@ -44,13 +47,15 @@ namespace {
 //                            per thread; the two groups hand the running maximum on
 //          warps 8..15       at a new job Q to tensor memory; NVFP4: two groups of
 //                            converters, the page's 64 rows to fp16 (nine K-blocks)
-//          warp  16          MMA: Q from tensor memory (288 columns), S in 3 x 64 columns
+//          warp  16          MMA of the even tiles: Q from tensor memory (288 columns), S in 3 x 64 columns
 //          warp  17          the tiles' pages for the others; FP8: the rows by TMA, as they are
-//   CTA 1: warps 0..3        rescale O where the maximum was raised, write O at a job's end
-//          warps 4..15       three groups of converters: the 512 value dims to fp16 (eight
-//                            K-blocks of 64 dims, read MN-major)
+//          warp  18          MMA of the odd tiles
+//   CTA 1: warps 0..15       rescale O where the maximum was raised, write O at a job's end.
+//                            NVFP4: warps 0..3; and 4..15 three groups of converters: the
+//                            512 value dims to fp16 (eight K-blocks of 64 dims, read MN-major)
 //          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
-//                            pages; what the MMA of a tile waits for
+//                            pages, FP8: and their 512 value dims by TMA; what the MMA of a
+//                            tile waits for
 // A converter group issues the loads of its next tile right after it has stored one.
 // ---------------------------------------------------------------------------
 constexpr int kNT = 64;                      // tokens per tile: one page
@@ -59,11 +64,16 @@ constexpr int kKBlks = kDQK / 64;            // 9
 constexpr int kVBlks = kDNope / 64;          // 8
 constexpr int kKBuf = kKBlks * kBlk;         // 73,728 (NVFP4)
 constexpr int kKBuf8 = 4 * kBlk + kBlk / 2;  // 36,864 (FP8: 64 rows of 128 E4M3, and of 64 for the rope dims)
-constexpr int kVBuf = kVBlks * kBlk;         // 65,536
-constexpr int kVBufs = 2, kSBufs = 3, kPBufs = 3;
+constexpr int kVBuf = kVBlks * kBlk;         // 65,536 (NVFP4)
+constexpr int kVBuf8 = 4 * kBlk;             // 32,768 (FP8: 64 rows of 128 E4M3)
+constexpr int kSBufs = 3;
 template <bool kNv>
 constexpr int kKBufs = kNv ? 2 : 4;
-static_assert(2 * kKBuf == 4 * kKBuf8, "either kind of key buffers");
+template <bool kNv>
+constexpr int kVBufs = kNv ? 2 : 4;
+template <bool kNv>
+constexpr int kPBufs = kNv ? 3 : 4;          // (NVFP4: with 4, less of L1 is left to the converters' loads: 225 for 199 us)
+static_assert(2 * kKBuf == 4 * kKBuf8 && 2 * kVBuf == 4 * kVBuf8, "either kind of buffers");
 // P: 8 chunks of 8 tokens, each 16 B per row in row order (the unswizzled core
 // matrices of the MMA, and 512 contiguous bytes for a warp's remote store)
 constexpr int kPChunk = 128 * 16;
@@ -71,15 +81,19 @@ constexpr int kPBuf = 8 * kPChunk;           // 16,384
 constexpr int kPSide = 128 * 4 + 16;         // the rescale factors, and by softmax warp whether one is not 1
 constexpr uint32_t kPBytes = kPBuf + kPSide;
 constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
-constexpr int kMmaWarp = 16, kFeedWarp = 17, kReadyWarp = 18;
+constexpr int kMmaWarp = 16, kFeedWarp = 17, kMmaWarp2 = 18, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
 constexpr int kNumBars = 70;
-constexpr size_t kSmemO = kVBufs * kVBuf + kPBufs * (kPBuf + kPSide);
-constexpr size_t kSmemS = 2 * kKBuf + 512;
-constexpr size_t kSmem = 1024 + (kSmemO > kSmemS ? kSmemO : kSmemS) + kNumBars * 8 + 64 + 16;
-static_assert(kSmem + 256 <= 232448, "shared memory of one CTA, with the static variables");
-constexpr float kPShift = 7.f;               // weights are 2^(z - max + 7)
-constexpr float kLazy = 8.f;                 // the maximum in use is raised when passed by more than 2^8
+template <bool kNv>
+constexpr size_t kData = 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
+static_assert(kData<true> >= 2 * kKBuf + 512 && kData<false> >= 2 * kKBuf + 512, "CTA 0's buffers");
+template <bool kNv>
+constexpr size_t kSmem = 1024 + kData<kNv> + kNumBars * 8 + 64 + 16;
+static_assert(kSmem<true> + 256 <= 232448 && kSmem<false> + 256 <= 232448, "shared memory, with the static variables");
+template <bool kNv>
+constexpr float kPShift = kNv ? 7.f : 6.f;   // weights are 2^(z - max + kPShift), and
+template <bool kNv>
+constexpr float kLazy = kNv ? 8.f : 6.f;     // max is raised when a tile passes it by more than 2^kLazy
 constexpr int kJobCost = 3;                  // what a job's start and end take, in tiles
 
 struct PfxArgs {
@@ -95,7 +109,7 @@ struct PfxArgs {
   int* err;
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
-  float scale_log2, lat_scale;
+  float scale_log2, lat_scale, shift;
 };
 
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
@@ -167,34 +181,25 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
   *reinterpret_cast<uint4*>(row + (((c + 1) ^ (tok & 7)) << 4)) = hi;
 }
 
-// A converter thread's share of a tile; warp w of 4 has nope K-blocks 2w and 2w + 1.
-// FP8: sixteen 16-B pieces (8 tokens x 4 pieces a warp load: 64-B runs, and stores
-// without bank conflicts). NVFP4: eight 16-B units (32 values, two scales). And kRope
-// (NVFP4 keys): two 16-B pieces of the rope dims. Tokens at or past `valid` are zeros:
-// their weights are 0, but their bytes could be NaN.
-template <bool kNv, bool kRope>
+// A converter thread's share of an NVFP4 tile; warp w of 4 has nope K-blocks 2w and 2w + 1:
+// eight 16-B units (32 values, two scales), and for keys (kRope) two 16-B pieces of the
+// rope dims. Tokens at or past `valid` are zeros: their weights are 0, but their
+// bytes could be NaN.
+template <bool kRope>
 struct TileRegs {
-  static constexpr int kPieces = kNv ? 4 : 8;  // per K-block
-  uint4 v[2][kPieces];
-  uint32_t s[2][kNv ? 4 : 1];
+  uint4 v[2][4];
+  uint32_t s[2][4];
   uint4 rope[2];
   __device__ __forceinline__ void load(const uint8_t* page, int valid, int w, int lane) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int u = 0; u < kPieces; ++u) {
-        if constexpr (kNv) {
-          const int tok = u * 16 + (lane >> 1), unit = 4 * w + 2 * b + (lane & 1);
-          const uint8_t* row = page + tok * 352;
-          v[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
-          s[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
-        } else {
-          const int tok = u * 8 + (lane >> 2);
-          v[b][u] = tok < valid
-                        ? __ldg(reinterpret_cast<const uint4*>(page + tok * 576 + 64 * (2 * w + b) + 16 * (lane & 3)))
-                        : zero;
-        }
+      for (int u = 0; u < 4; ++u) {
+        const int tok = u * 16 + (lane >> 1), unit = 4 * w + 2 * b + (lane & 1);
+        const uint8_t* row = page + tok * 352;
+        v[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
+        s[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
       }
     if constexpr (kRope) {
 #pragma unroll
@@ -206,26 +211,16 @@ struct TileRegs {
   }
   // 16 of the tokens, 16 step and up
   __device__ __forceinline__ void store(int step, uint8_t* buf, int w, int lane) const {
-    const int row0 = 16 * step;
+    const int tok = 16 * step + (lane >> 1), c0 = (lane & 1) * 4;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       uint8_t* blk = buf + (2 * w + b) * kBlk;
-      if constexpr (kNv) {
-        const int tok = row0 + (lane >> 1), c0 = (lane & 1) * 4;
-        uint32_t two, none;
-        expand_e4m3(s[b][step], two, none);
-        const __half2 h = *reinterpret_cast<const __half2*>(&two);
-        const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-        put2(blk, tok, c0, expand_e2m1(v[b][step].x, s0), expand_e2m1(v[b][step].y, s0));
-        put2(blk, tok, c0 + 2, expand_e2m1(v[b][step].z, s1), expand_e2m1(v[b][step].w, s1));
-      } else {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          uint4 lo, hi;
-          expand16(v[b][2 * step + u], lo, hi);
-          put2(blk, row0 + u * 8 + (lane >> 2), (lane & 3) * 2, lo, hi);
-        }
-      }
+      uint32_t two, none;
+      expand_e4m3(s[b][step], two, none);
+      const __half2 h = *reinterpret_cast<const __half2*>(&two);
+      const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+      put2(blk, tok, c0, expand_e2m1(v[b][step].x, s0), expand_e2m1(v[b][step].y, s0));
+      put2(blk, tok, c0 + 2, expand_e2m1(v[b][step].z, s1), expand_e2m1(v[b][step].w, s1));
     }
   }
   __device__ __forceinline__ void store_rope(uint8_t* buf, int w, int lane) const {
@@ -238,6 +233,17 @@ struct TileRegs {
     }
   }
 };
+
+// Four weights as fp16 -> their E5M2 part and the E4M3 part of the rest.
+__device__ __forceinline__ void split_weights(__half2 a, __half2 b, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 x, y;\n\t.reg .b32 u, v;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 x, %2;\n\tcvt.rn.satfinite.e5m2x2.f16x2 y, %3;\n\tmov.b32 %0, {x, y};\n\t"
+      "cvt.rn.f16x2.e5m2x2 u, x;\n\tcvt.rn.f16x2.e5m2x2 v, y;\n\t"
+      "sub.rn.f16x2 u, %2, u;\n\tsub.rn.f16x2 v, %3, v;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, u;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, v;\n\tmov.b32 %1, {x, y};\n}\n"
+      : "=&r"(hi), "=r"(lo)
+      : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+}
 
 // What the warps of a CTA need to know of a tile, in a ring that one warp fills.
 struct Tile {
@@ -282,16 +288,16 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
   return true;
 }
 
-// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA. kKeys (CTA
-// 0, NVFP4): all 576 dims, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
+// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (NVFP4).
+// kKeys (CTA 0): all 576 dims, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
 // its barriers as in feed; full / free: the buffers' (or halves') barriers; turn: the groups take buffers in the order of their
 // tiles (a group that came early could take a buffer's barrier for one a round older,
 // which has the same parity); after(g): called once tile g is stored.
-template <bool kNv, bool kKeys, int kGroups, typename After>
+template <bool kKeys, int kGroups, typename After>
 __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
                                         uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
                                         uint32_t free, uint32_t turn, After after) {
-  TileRegs<kNv, kKeys> t;
+  TileRegs<kKeys> t;
   auto load = [&](int g) {
     const int slot = g % kRing;
     if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) return false;
@@ -305,7 +311,7 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
 #pragma unroll 1
   for (int g = group; g < gtot; g += kGroups) {
     if constexpr (kKeys) {
-      constexpr int kBufs = kKBufs<kNv>;
+      constexpr int kBufs = kKBufs<true>;
       const int buf = g % kBufs;
       if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
       uint8_t* dst = bufs + buf * kKBuf;
@@ -316,11 +322,11 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
     } else {
-      const int buf = g % kVBufs;
+      const int buf = g % kVBufs<true>;
       if (g > 0 && !ptx::mbar_wait(turn + 8 * ((g - 1) % kGroups), uint32_t((g - 1) / kGroups) & 1u)) return false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        if (g >= kVBufs && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kVBufs - 1) & 1u)) return false;
+        if (g >= kVBufs<true> && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kVBufs<true> - 1) & 1u)) return false;
         if (i == 1 && lane == 0) ptx::mbar_arrive(turn + 8 * group);
         t.store(2 * i, bufs + buf * kVBuf, w, lane);
         t.store(2 * i + 1, bufs + buf * kVBuf, w, lane);
@@ -341,9 +347,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                       const __grid_constant__ PfxArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr size_t kData = kSmemO > kSmemS ? kSmemO : kSmemS;
   // the barriers have the same place in both CTAs
-  const uint32_t bars = ptx::smem_u32(sm) + uint32_t(kData);
+  const uint32_t bars = ptx::smem_u32(sm) + uint32_t(kData<kNv>);
   const uint32_t mma_done = bars + 0 * 8;
   const uint32_t q_full = bars + 1 * 8;
   const uint32_t q_free = bars + 2 * 8;      // every product with the job's query is done
@@ -357,20 +362,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t p_free = bars + 37 * 8;     // [kPBufs]  P . V of the tile in this slot of P is done (either CTA)
   const uint32_t p_full = bars + 41 * 8;     // [kPBufs]  P and the factors have landed
   const uint32_t go = bars + 45 * 8;         // [kPBufs]  P and O are ready for P . V
-  const uint32_t v_full = bars + 49 * 8;     // [2 kVBufs] by half tile
-  const uint32_t v_free = bars + 54 * 8;     // [2 kVBufs]  its P . V is done
+  const uint32_t v_full = bars + 49 * 8;     // [4] NVFP4: by half tile
+  const uint32_t v_free = bars + 54 * 8;     // [4]  its P . V is done
   const uint32_t v_turn = bars + 60 * 8;     // [3]  by group: the tile's buffer is the group's
   const uint32_t ask = bars + 67 * 8;        // O is to be rescaled, or written
   const uint32_t o_ok = bars + 68 * 8;       // and it is
-  Tile* ring = reinterpret_cast<Tile*>(sm + kData + kNumBars * 8);  // [8]
+  Tile* ring = reinterpret_cast<Tile*>(sm + kData<kNv> + kNumBars * 8);  // [8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
   uint8_t* KB = sm;
   float* m_run = reinterpret_cast<float*>(sm + 2 * kKBuf);  // [128] the running maximum in use
   // CTA 1
   uint8_t* VB = sm;
-  uint8_t* PB = sm + kVBufs * kVBuf;
-  uint8_t* side = PB + kPBufs * kPBuf;  // [kPBufs] factors and flags
+  uint8_t* PB = sm + 2 * kVBuf;
+  uint8_t* side = PB + kPBufs<kNv> * kPBuf;  // [kPBufs] factors and flags
   __shared__ long long s_sum[kThreads / 32];
   __shared__ int s_job, s_unit, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
 
@@ -379,13 +384,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int nclu = int(gridDim.x) >> 1, clu = int(blockIdx.x) >> 1;
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(mma_done, 1);
+    ptx::mbar_init(mma_done, half == 0 ? 2 : 1);
     ptx::mbar_init(q_full, 8);
-    ptx::mbar_init(q_free, 1);
+    ptx::mbar_init(q_free, 2);
     ptx::mbar_init(ask, 1);
     for (int i = 0; i < 3; ++i) ptx::mbar_init(v_turn + 8 * i, 4);
-    ptx::mbar_init(o_ok, 4);
-    for (int i = 0; i < kPBufs; ++i) {
+    ptx::mbar_init(o_ok, kNv ? 4 : 16);
+    for (int i = 0; i < kPBufs<kNv>; ++i) {
       ptx::mbar_init(p_free + 8 * i, 1);
       ptx::mbar_init(p_full + 8 * i, 1);
       ptx::mbar_init(go + 8 * i, 1);
@@ -394,8 +399,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(s_full + 8 * i, 1);
       ptx::mbar_init(s_free + 8 * i, 4);
     }
-    for (int i = 0; i < 2 * kVBufs; ++i) {
-      ptx::mbar_init(v_full + 8 * i, 4);
+    for (int i = 0; i < 4; ++i) {
+      ptx::mbar_init(v_full + 8 * i, kNv ? 4 : 1);
       ptx::mbar_init(v_free + 8 * i, 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -405,7 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kRing; ++i) {
       ptx::mbar_init(ring_full + 8 * i, 1);
-      ptx::mbar_init(ring_free + 8 * i, half == 0 && kNv ? 8 : 4);  // a softmax and a converter group, or one of them
+      // who reads it: a softmax and a converter group, or one of them, or the warp that readies tiles
+      ptx::mbar_init(ring_free + 8 * i, kNv ? (half == 0 ? 8 : 4) : (half == 0 ? 4 : 1));
     }
     ptx::fence_mbar_init();
   }
@@ -490,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gtot = int(block_sum(tiles));
     // P of the first tiles may arrive as soon as the pair has synced
     if (half == 1 && threadIdx.x == 0)
-      for (int i = 0; i < kPBufs && i < gtot; ++i) ptx::mbar_arrive_expect_tx(p_full + 8 * (i), kPBytes);
+      for (int i = 0; i < kPBufs<kNv> && i < gtot; ++i) ptx::mbar_arrive_expect_tx(p_full + 8 * (i), kPBytes);
   }
   __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before any remote arrive
@@ -499,11 +505,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool ok = true;
   Walk wk;
 
+  // CTA 1: rescaling and writing columns [c0, c1) of O, one warp of four a quarter of the rows
+  auto output = [&](int c0, int c1) {
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = uint32_t((warp & 3) * 32) << 16;
+    int asked = 0;
+#pragma unroll 1
+    for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on; on = wk.next(a)) {
+#pragma unroll 1
+      for (;;) {
+        if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u)) return false;
+        const int what = s_ask;
+        // O is up to date, and still, once P . V of the tile before g is done
+        const int g = what < 0 ? -1 - what : what;
+        if (!ptx::mbar_wait(p_free + 8 * ((g - 1) % kPBufs<kNv>), uint32_t((g - 1) / kPBufs<kNv>) & 1u)) return false;
+        ptx::tc_fence_after();
+        if (what < 0) break;
+        const float alpha = reinterpret_cast<const float*>(side + (g % kPBufs<kNv>) * kPSide)[row];
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 32) {
+            float o[32];
+            ptx::tmem_ld32(tmem + lane_base + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            ptx::tmem_st32(tmem + lane_base + c, o);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(o_ok);
+      }
+      // (four dims of all rows together, so that a warp's stores are whole lines)
+      float4* dst = reinterpret_cast<float4*>(a.part) + size_t(wk.job + clu) * kPfxTileRows * (kDNope / 4) + row;
+      const bool real = wk.job < a.tiles || row < kHeads;
+#pragma unroll 1
+      for (int c = c0; c < c1; c += 32) {
+        float o[32];
+        ptx::tmem_ld32(tmem + lane_base + c, o);
+        if (real) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[(c / 4 + j) * kPfxTileRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      // the reads of O are ordered before the next job's first P . V
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(o_ok);
+    }
+    return true;
+  };
+
+  // CTA 1, NVFP4, warps 4..15
+  auto values = [&]() {
+    return convert<false, 3>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
+                             [](int) { return true; });
+  };
+
   // registers: the five warpgroups start with 96 each (480) and go on with 104, 104, 96, 96 and 80 (480)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == kMmaWarp && half == 0) {
+    if ((warp == kMmaWarp || warp == kMmaWarp2) && half == 0) {
       // ---------------------------------------------------------- S = Q . C^T
+      // (the even and the odd tiles by a warp each: a wait takes its turn behind the products
+      // that its warp has issued, and while one waits the other's keep the tensor core busy)
       const uint32_t kb0 = ptx::smem_u32(KB);
       int g = 0, qn = 0;
 #pragma unroll 1
@@ -511,6 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ptx::mbar_wait(q_full, uint32_t(qn++) & 1u)) { ok = false; break; }
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
+          if ((g & 1) != (warp == kMmaWarp2)) continue;
           const int buf = g % kKBufs<kNv>, sb = g % kSBufs;
           if (!ptx::mbar_wait(k_full + 8 * buf, uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
           if (g >= kSBufs && !ptx::mbar_wait(s_free + 8 * sb, uint32_t(g / kSBufs - 1) & 1u)) { ok = false; break; }
@@ -540,59 +607,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   ptx::mma_f8_tmem_a(s, q + 128 + kk * 8, ptx::sdesc_sw64(kb + 4 * kBlk + kk * 32), id, 1u);
               }
             }
-            ptx::mma_commit(k_free + 8 * buf);
             ptx::mma_commit(s_full + 8 * sb);
-            if (k + 1 == wk.k1) ptx::mma_commit(q_free);
+            ptx::mma_commit(k_free + 8 * buf);
           }
           __syncwarp();
         }
+        if (ok && ptx::elect_one()) ptx::mma_commit(q_free);
+        __syncwarp();
       }
     } else if (warp == kFeedWarp) {
-      // ---------------------------------------------------------- tiles; FP8 keys by TMA
-      const uint32_t kb0 = ptx::smem_u32(KB);
+      // ---------------------------------------------------------- tiles; FP8 rows by TMA
+      const uint32_t dst0 = ptx::smem_u32(sm), full = half == 0 ? k_full : v_full, free = half == 0 ? k_free : v_free;
+      const uint32_t bytes = half == 0 ? kKBuf8 : kVBuf8;
+      constexpr int kBufs = 4;
+      static_assert(kNv || (kKBufs<kNv> == kBufs && kVBufs<kNv> == kBufs), "FP8 buffers");
       ok = feed(a, gtot, job0, unit0, units, lane, half == 0, ring, ring_full, ring_free, [&](int g, const Tile& t) {
-        if (kNv || half == 1) return true;
-        const int buf = g % kKBufs<kNv>;
-        if (g >= kKBufs<kNv> && !ptx::mbar_wait(k_free + 8 * buf, uint32_t(g / kKBufs<kNv> - 1) & 1u)) return false;
+        if (kNv) return true;
+        const int buf = g % kBufs;
+        if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
         if (lane == 0) {
-          const uint32_t dst = kb0 + buf * kKBuf8, bar = k_full + 8 * buf;
-          ptx::mbar_arrive_expect_tx(bar, kKBuf8);
+          const uint32_t dst = dst0 + buf * bytes, bar = full + 8 * buf;
+          ptx::mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
           for (int j = 0; j < 4; ++j) ptx::tma_load_3d(dst + j * kBlk, &kmap, bar, j * 128, 0, t.page);
-          ptx::tma_load_3d(dst + 4 * kBlk, &rmap, bar, kDNope, 0, t.page);
+          if (half == 0) ptx::tma_load_3d(dst + 4 * kBlk, &rmap, bar, kDNope, 0, t.page);
         }
         __syncwarp();
         return true;
       });
       // no copy left in flight
-      if (!ok && !kNv && half == 0)
-        for (int i = 0; i < 2 * kKBufs<kNv>; ++i) ptx::mbar_wait(k_full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+      if (!ok && !kNv)
+        for (int i = 0; i < 2 * kBufs; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- O += P . V
-      const uint32_t id = ptx::idesc(0, 0, 128, 256, 0, 1);
       const uint32_t vb0 = ptx::smem_u32(VB), pb0 = ptx::smem_u32(PB);
       int g = 0;
 #pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1 && ok; ++k, ++g) {
-          const int buf = g % kVBufs, pb = g % kPBufs;
-          if (!ptx::mbar_wait(go + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
+          const int buf = g % kVBufs<kNv>, pb = g % kPBufs<kNv>;
+          const uint32_t vpar = uint32_t(g / kVBufs<kNv>) & 1u, p0 = pb0 + pb * kPBuf;
+          if (!ptx::mbar_wait(go + 8 * pb, uint32_t(g / kPBufs<kNv>) & 1u)) { ok = false; break; }
+          if constexpr (kNv) {
+            const uint32_t id = ptx::idesc(0, 0, 128, 256, 0, 1);
 #pragma unroll 1
-          for (int i = 0; i < 2; ++i) {  // 32 tokens of the tile
-            if (!ptx::mbar_wait(v_full + 8 * (2 * buf + i), uint32_t(g / kVBufs) & 1u)) { ok = false; break; }
+            for (int i = 0; i < 2; ++i) {  // 32 tokens of the tile
+              if (!ptx::mbar_wait(v_full + 8 * (2 * buf + i), vpar)) { ok = false; break; }
+              ptx::tc_fence_after();
+              const uint32_t vb = vb0 + buf * kVBuf + i * 32 * 128, p = p0 + i * 4 * kPChunk;
+              if (ptx::elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                  for (int n = 0; n < 2; ++n)
+                    ptx::mma_f16(tmem + n * 256, ptx::sdesc_plain(p + kk * 2 * kPChunk, kPChunk, 128),
+                                 ptx::sdesc_sw128_mn(vb + n * 4 * kBlk + kk * 16 * 128, kBlk, 1024), id,
+                                 (k > wk.k0 || i > 0 || kk > 0) ? 1u : 0u);
+                ptx::mma_commit(v_free + 8 * (2 * buf + i));
+                if (i) ptx::mma_commit_to(p_free + 8 * pb, 3);  // in both CTAs
+              }
+              __syncwarp();
+            }
+          } else {
+            if (!ptx::mbar_wait(v_full + 8 * buf, vpar)) { ok = false; break; }
             ptx::tc_fence_after();
-            const uint32_t vb = vb0 + buf * kVBuf + i * 32 * 128, p = pb0 + pb * kPBuf + i * 4 * kPChunk;
+            const uint32_t vb = vb0 + buf * kVBuf8;
             if (ptx::elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
+              for (int part = 0; part < 2; ++part)  // the weights' E5M2, then their E4M3 part
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                  ptx::mma_f16(tmem + n * 256, ptx::sdesc_plain(p + kk * 2 * kPChunk, kPChunk, 128),
-                               ptx::sdesc_sw128_mn(vb + n * 4 * kBlk + kk * 16 * 128, kBlk, 1024), id,
-                               (k > wk.k0 || i > 0 || kk > 0) ? 1u : 0u);
-              ptx::mma_commit(v_free + 8 * (2 * buf + i));
-              if (i) ptx::mma_commit_to(p_free + 8 * pb, 3);  // in both CTAs
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                  for (int n = 0; n < 2; ++n)
+                    ptx::mma_f8f6f4(tmem + n * 256, ptx::sdesc_plain(p0 + (part * 4 + kk * 2) * kPChunk, kPChunk, 128),
+                                    ptx::sdesc_sw128_mn(vb + n * 2 * kBlk + kk * 32 * 128, kBlk, 1024),
+                                    ptx::idesc(1 - part, 0, 128, 256, 0, 1), (k > wk.k0 || part > 0 || kk > 0) ? 1u : 0u);
+              ptx::mma_commit(v_free + 8 * buf);
+              ptx::mma_commit_to(p_free + 8 * pb, 3);
             }
             __syncwarp();
           }
@@ -620,11 +712,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
-          const int pb = g % kPBufs;
-          if (!ptx::mbar_wait_cluster(p_full + 8 * pb, uint32_t(g / kPBufs) & 1u)) { ok = false; break; }
+          const int pb = g % kPBufs<kNv>;
+          if (!ptx::mbar_wait_cluster(p_full + 8 * pb, uint32_t(g / kPBufs<kNv>) & 1u)) { ok = false; break; }
+          if constexpr (!kNv) {
+            // Rows that the job does not see: their weights are 0, but their bytes could be NaN.
+            // (This tile's P was sent after the product kPBufs tiles ago, so its buffer's
+            // barrier is at most a round from this tile's.)
+            static_assert(kPBufs<kNv> <= kVBufs<kNv>, "the buffer's last product is done");
+            const int slot = g % kRing, buf = g % kVBufs<kNv>;
+            if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) { ok = false; break; }
+            const int valid = ring[slot].valid;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
+            if (valid < kNT) {
+              if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs<kNv>) & 1u)) { ok = false; break; }
+              uint8_t* v = VB + buf * kVBuf8 + (lane >> 3) * kBlk + (lane & 7) * 16;
+              for (int t = valid; t < kNT; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
+            }
+          }
           const uint4 flags = *reinterpret_cast<const uint4*>(side + pb * kPSide + 512);
           // re-arm for the next tile in this slot: it is not sent before this one's P . V is done
-          if (lane == 0 && g + kPBufs < gtot) ptx::mbar_arrive_expect_tx(p_full + 8 * pb, kPBytes);
+          if (lane == 0 && g + kPBufs<kNv> < gtot) ptx::mbar_arrive_expect_tx(p_full + 8 * pb, kPBytes);
           if (k > wk.k0 && (flags.x | flags.y | flags.z | flags.w)) request(g);
           if (!settled()) { ok = false; break; }  // (at a job's first tile: the old output is written)
           // P came by ordinary (remote) stores; the tensor core reads it through the async proxy
@@ -637,8 +745,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = settled();
     }
-    if (warp == kMmaWarp) {
-      // nothing of this warp's left in flight when the tensor memory is released
+    if (warp == kMmaWarp || (warp == kMmaWarp2 && half == 0)) {
+      // nothing of these warps' left in flight when the tensor memory is released
       if (ptx::elect_one()) ptx::mma_commit(mma_done);
       __syncwarp();
       ptx::mbar_wait(mma_done, 0);
@@ -685,15 +793,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = queries(-2) && convert<true, true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
+        ok = queries(-2) && convert<true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
                                                    queries);
       } else {
 #pragma unroll 1
         for (; on && ok; on = wk.next(a)) ok = load_q(wk.job);
       }
     } else {
-      ok = convert<kNv, false, 3>(a, gtot, group + 1, w, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
-                                          [](int) { return true; });
+      if constexpr (kNv)
+        ok = values();
+      else
+        ok = output((warp >> 2) * 128, (warp >> 2) * 128 + 128);
     }
   } else if (half == 0) {
     // ------------------------------------------------------------ softmax
@@ -713,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int g1 = g0 + wk.k1 - wk.k0;
 #pragma unroll 1
       for (int g = g0 + ((g0 ^ group) & 1); g < g1; g += 2) {
-        const int sb = g % kSBufs, pb = g % kPBufs;
+        const int sb = g % kSBufs, pb = g % kPBufs<kNv>;
         if (!ptx::mbar_wait(s_full + 8 * (sb), uint32_t(g / kSBufs) & 1u)) { ok = false; break; }
         ptx::tc_fence_after();
         float sv[64];
@@ -744,7 +854,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // the maximum in use passes from tile to tile
         if (g >= 1 && !ptx::mbar_wait(turn + 8 * (w), uint32_t(g - 1) & 1u)) { ok = false; break; }
         const float m_old = g == g0 ? -INFINITY : m_run[row];
-        const bool raise = tmax > m_old + kLazy;
+        const bool raise = tmax > m_old + kLazy<kNv>;
         const float m_use = m_old == -INFINITY || raise ? tmax : m_old;
         m_run[row] = m_use;
         __syncwarp();
@@ -752,20 +862,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float alpha = raise && m_old != -INFINITY ? ptx::ex2_approx(m_old - m_use) : 1.f;
         if (m_mine != m_use && m_mine != -INFINITY) l *= ptx::ex2_approx(m_mine - m_use);
         m_mine = m_use;
-        const float off = m_use == -INFINITY ? 0.f : kPShift - m_use;
+        const float off = m_use == -INFINITY ? 0.f : kPShift<kNv> - m_use;
         float p0 = 0.f, p1 = 0.f;
         uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        auto weights = [&](int i) {
           ptx::fma2(sv[2 * i], sv[2 * i + 1], cs, off);
           const float x = ptx::ex2_approx(sv[2 * i]), y = ptx::ex2_approx(sv[2 * i + 1]);
           ptx::add2(p0, p1, x, y);
-          const __half2 h = __floats2half2_rn(x, y);
-          pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+          return __floats2half2_rn(x, y);
+        };
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const __half2 h0 = weights(i), h1 = weights(i + 1);
+          if constexpr (kNv) {
+            pk[i] = *reinterpret_cast<const uint32_t*>(&h0);
+            pk[i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+          } else {
+            split_weights(h0, h1, pk[i / 2], pk[16 + i / 2]);
+          }
         }
         l += p0 + p1;
-        // this half of P is free once P . V of two tiles ago is done
-        if (g >= kPBufs && !ptx::mbar_wait_cluster(p_free + 8 * (pb), uint32_t(g / kPBufs - 1) & 1u)) { ok = false; break; }
+        // this slot of P is free once P . V of the tile before in it is done
+        if (g >= kPBufs<kNv> && !ptx::mbar_wait_cluster(p_free + 8 * (pb), uint32_t(g / kPBufs<kNv> - 1) & 1u)) { ok = false; break; }
         const uint32_t dst = p_peer + pb * kPBuf, bar = bar_peer + pb * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -788,60 +906,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    if (warp >= 4) {
-      ok = convert<kNv, false, 3>(a, gtot, 0, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
-                                          [](int) { return true; });
-    } else {
-      // ---------------------------------------------------------- O: rescaling and output
-      const int row = warp * 32 + lane;
-      const uint32_t lane_base = uint32_t(warp * 32) << 16;
-      int asked = 0;
-#pragma unroll 1
-      for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
-        int g;  // O is up to date, and still, once P . V of the tile before g is done
-#pragma unroll 1
-        for (;;) {
-          if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u)) { ok = false; break; }
-          const int what = s_ask;
-          g = what < 0 ? -1 - what : what;
-          if (!ptx::mbar_wait(p_free + 8 * ((g - 1) % kPBufs), uint32_t((g - 1) / kPBufs) & 1u)) { ok = false; break; }
-          ptx::tc_fence_after();
-          if (what < 0) break;
-          const float alpha = reinterpret_cast<const float*>(side + (g % kPBufs) * kPSide)[row];
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < kDNope; c += 32) {
-              float o[32];
-              ptx::tmem_ld32(tmem + lane_base + c, o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              ptx::tmem_st32(tmem + lane_base + c, o);
-            }
-          }
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(o_ok);
-        }
-        if (!ok) break;
-        // (four dims of all rows together, so that a warp's stores are whole lines)
-        float4* dst = reinterpret_cast<float4*>(a.part) + size_t(wk.job + clu) * kPfxTileRows * (kDNope / 4) + row;
-        const bool real = wk.job < a.tiles || row < kHeads;
-#pragma unroll 1
-        for (int c = 0; c < kDNope; c += 32) {
-          float o[32];
-          ptx::tmem_ld32(tmem + lane_base + c, o);
-          if (real) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[(c / 4 + j) * kPfxTileRows] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-          }
-        }
-        // the reads of O are ordered before the next job's first P . V
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(o_ok);
-      }
-    }
+    if constexpr (kNv)
+      ok = warp >= 4 ? values() : output(0, kDNope);
+    else
+      ok = output((warp >> 2) * 128, (warp >> 2) * 128 + 128);
   }
   if (!ok) atomicOr(a.err, DSA_DEVERR_TIMEOUT);
   __syncwarp();
@@ -1020,7 +1088,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
     const float mm = m == -INFINITY ? 0.f : m;
-    if (lse && c0 == 0) lse[hr] = tot != 0.f ? (mm - kPShift + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+    if (lse && c0 == 0) lse[hr] = tot != 0.f ? (mm - a.shift + log2f(tot)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * kChunks; i += 32 * kMergeWarps) {
@@ -1057,6 +1125,7 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
   a.lat_scale = p.latent_scale;
+  a.shift = nv ? kPShift<true> : kPShift<false>;
   CUtensorMap kmap, rmap;
   std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
   std::memset(&rmap, 0, sizeof(rmap));
@@ -1075,11 +1144,12 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
                              static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
                              reinterpret_cast<float*>(ws + L.pfx_qs), ctx_lens, lens, int(p.n_q), prefix_len, L.cap, a.err);
   if (e != cudaSuccess) return e;
+  const size_t smem = nv ? kSmem<true> : kSmem<false>;
   auto kern = nv ? prefix_mla_kernel<true> : prefix_mla_kernel<false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int clusters = std::max(1, std::min(kPfxMaxClusters, sm_count() / 2));
-  e = launch_pdl(kern, dim3(2 * clusters), dim3(kThreads), kSmem, st, kmap, rmap, a);
+  e = launch_pdl(kern, dim3(2 * clusters), dim3(kThreads), smem, st, kmap, rmap, a);
   if (e != cudaSuccess) return e;
   // a row has a little more than clusters / rows segments
   const bool split = L.rows * 4 <= clusters;

@@ -332,7 +332,9 @@ dsa_status_t dsa_topk_noalloc(const dsa_params_t* params, const float* scores, i
  * head and exact, except for values far below their head's largest: under 2^-13 of it they
  * are off by at most 2^-20 of it (DSA_LAT_FP8_576, where the query is multiplied as an
  * E4M3 and an E5M2 part), or under 2^-32 by 2^-39 (DSA_LAT_NVFP4_352, in fp16). A softmax
- * weight is rounded to fp16's 11 bits (or to 2^-32 of the row's largest).
+ * weight is rounded to fp16's 11 bits, or to 2^-32 of the row's largest (DSA_LAT_NVFP4_352);
+ * or it too is multiplied as an E5M2 and an E4M3 part, which together are within 2^-8 of
+ * it, as bf16 would be, or within 2^-16 of the row's largest (DSA_LAT_FP8_576).
  *   prefix_pages int32 [prefix_len / 64] physical pages of the shared tokens
  *                (NULL if prefix_len is 0); rows of block_table need not repeat
  *                them: their first prefix_len / 64 entries are not read

@@ -25,7 +25,8 @@ def prefix_mla(inp, prefix_pages, prefix_len: int, b: int, t: int, query_error=N
     """Row (b, t) over the shared tokens and then its own: (out, lse, mass, bulk),
     where mass[h] = sum_s p_s |c_s| (512 dims) and bulk = max_s scale * sum_d |q_d c_sd|,
     the magnitudes that rounding errors are relative to. query_error(q): bounds on how
-    far each query value is off; a fifth result is then max_s scale * sum_d error_d |c_sd|."""
+    far each query value is off; further results are then max_s scale * sum_d error_d |c_sd|
+    and max_s p_s * sum_s |c_s|."""
     L = O.visible_len(inp.ctx[b], inp.n_q, t)
     saved = inp.block_table[b].copy()
     inp.block_table[b, :prefix_len // PAGE] = prefix_pages
@@ -36,7 +37,9 @@ def prefix_mla(inp, prefix_pages, prefix_len: int, b: int, t: int, query_error=N
     p = np.exp(inp.softmax_scale * (q @ c.T) - lse[:, None])
     size = np.abs(c).T
     res = out, lse, p @ size[:512].T, inp.softmax_scale * (np.abs(q) @ size).max(axis=1)
-    return res if query_error is None else (*res, inp.softmax_scale * (query_error(q) @ size).max(axis=1))
+    if query_error is None:
+        return res
+    return *res, inp.softmax_scale * (query_error(q) @ size).max(axis=1), p.max(axis=1)[:, None] * size[:512].sum(axis=1)
 
 
 # ---------------------------------------------------------------- pages

@@ -12,9 +12,16 @@ Bounds, derived from the arithmetic that include/dsa.h states:
   largest. So a query value under 2^-13 of its head's largest may be off by 2^-20 of
   that largest, and d adds scale * sum over those values of 2^-20 max |q| |c|;
 - a weight exp(z) is off by a factor 1 + d, by 2^-21 in the exponential, and
-  rounded to 11 bits (2^-11); the normaliser by d + 2^-21 and the rounding of its
-  fp32 sum; splitting and merging adds a few 2^-22 on either;
-- so lse is off by d + 2^-19 + 2^-22 |lse|, and out by (2^-11 + 2 d + 2^-18) * mass with
+  rounded to w. NVFP4 latents: fp16's 11 bits, w = 2^-11. FP8 latents: to fp16 (2^-11) and then to
+  hi + lo, hi = E5M2(P) and lo = E4M3(P - hi), of P = 2^6 exp(z - m) with a running maximum m, raised
+  when it is passed by a factor of 2^6 (so P <= 2^12). P in [2^e, 2^(e + 1)): hi has steps of 2^(e - 2),
+  so |P - hi| <= 2^(e - 3) (at most 2^8; E4M3 ends at 448), which is 2^(e - 3) itself, exact in E4M3, or
+  below it, where E4M3's half step is at most 2^(e - 4 - 4): 2^-8 of P. Where P - hi is under 2^-6, E4M3's
+  half step is 2^-10. m is at most the row's final maximum, so that is at most 2^-16 of the row's largest
+  weight: w = 2^-8 + 2^-11, and out adds 2^-16 (1 + 2^-10) * tail with tail = max p * sum |c|;
+- the normaliser is off by d + 2^-21 and the rounding of its fp32 sum (it adds weights before they
+  are rounded); splitting and merging adds a few 2^-22 on either;
+- so lse is off by d + 2^-19 + 2^-22 |lse|, and out by (w + 2 d + 2^-18) * mass with
   mass = sum p |c|, plus the bf16 rounding, 2^-8 |out| (2^-133 among subnormals).
 Nothing here is measured first."""
 import numpy as np
@@ -59,9 +66,10 @@ def check_row(inp, pages, prefix, b, t, out, lse):
         top = np.abs(q).max(axis=1, keepdims=True)
         return np.where(np.abs(q) < 2.0 ** -13 * top, 2.0 ** -20 * top, 0.0) * (inp.lat_fmt == "fp8")
 
-    ref, ref_lse, mass, bulk, extra = S.prefix_mla(inp, pages, prefix, b, t, off)
+    ref, ref_lse, mass, bulk, extra, tail = S.prefix_mla(inp, pages, prefix, b, t, off)
     d = (66 * 2.0 ** -23 * bulk + extra)[:, None]
-    bound = (2.0 ** -11 + 2 * d + 2.0 ** -18) * mass + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
+    w, floor = (2.0 ** -8 + 2.0 ** -11, 2.0 ** -16 + 2.0 ** -26) if inp.lat_fmt == "fp8" else (2.0 ** -11, 0.0)
+    bound = (w + 2 * d + 2.0 ** -18) * mass + floor * tail + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
     err = np.abs(out.astype(np.float64) - ref)
     assert np.isfinite(out).all()
     assert (err <= bound).all(), f"({b}, {t}): {(err / bound).max():.2f} of the bound at {np.unravel_index((err / bound).argmax(), err.shape)}"
