@@ -94,6 +94,7 @@ template <bool kNv>
 constexpr float kPShift = kNv ? 7.f : 6.f;   // weights are 2^(z - max + kPShift), and
 template <bool kNv>
 constexpr float kLazy = kNv ? 8.f : 6.f;     // max is raised when a tile passes it by more than 2^kLazy
+constexpr int kMinUnits = 3;
 constexpr int kJobCost = 3;                  // what a job's start and end take, in tiles
 
 struct PfxArgs {
@@ -447,9 +448,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int per = a.tiles ? a.prefix / kNT + kJobCost : 1;  // units of a prefix job
     const int64_t shared = int64_t(a.tiles) * per;
     const int64_t line = shared + block_sum(mine);
-    // no pair among those that work goes without a unit: a job's segments are those of
-    // consecutive pairs
-    const int64_t used = min(int64_t(nclu), line);
+    // A pair has at least kMinUnits, so that a short line leaves the merge less (one request
+    // of 4,096 tokens: 23.5 us, 24.4 with at least two, 26.0 with one, 25.5 with four),
+    // and no pair among those that work goes without: a job's segments are those of
+    // consecutive pairs.
+    const int64_t used = min(int64_t(nclu), (line + kMinUnits - 1) / kMinUnits);
     const int64_t lo = clu < used ? line * clu / used : line, hi = clu < used ? line * (clu + 1) / used : line;
     units = int(hi - lo);
     // tiles of the prefix jobs among the line's first x units
