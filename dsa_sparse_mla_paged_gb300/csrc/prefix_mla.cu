@@ -83,7 +83,7 @@ constexpr uint32_t kPBytes = kPBuf + kPSide;
 constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
 constexpr int kMmaWarp = 16, kFeedWarp = 17, kMmaWarp2 = 18, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 70;
+constexpr int kNumBars = 76;
 template <bool kNv>
 constexpr size_t kData = 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
 static_assert(kData<true> >= 2 * kKBuf + 512 && kData<false> >= 2 * kKBuf + 512, "CTA 0's buffers");
@@ -356,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t k_full = bars + 3 * 8;      // [kKBufs]
   const uint32_t k_free = bars + 7 * 8;      // [kKBufs]  S of the buffer's tile is done
   const uint32_t s_full = bars + 11 * 8;     // [kSBufs]
-  const uint32_t s_free = bars + 14 * 8;     // [kSBufs]  the softmax has read S
+  const uint32_t s_free = bars + 70 * 8;     // [2 kSBufs]  the softmax has read S of a tile (modulo 6)
   const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's maximum is decided
   const uint32_t ring_full = bars + 21 * 8;  // [kRing]
   const uint32_t ring_free = bars + 29 * 8;  // [kRing]
@@ -398,8 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSBufs; ++i) {
       ptx::mbar_init(s_full + 8 * i, 1);
-      ptx::mbar_init(s_free + 8 * i, 4);
     }
+    for (int i = 0; i < 2 * kSBufs; ++i) ptx::mbar_init(s_free + 8 * i, 4);
     for (int i = 0; i < 4; ++i) {
       ptx::mbar_init(v_full + 8 * i, kNv ? 4 : 1);
       ptx::mbar_init(v_free + 8 * i, 1);
@@ -583,7 +583,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if ((g & 1) != (warp == kMmaWarp2)) continue;
           const int buf = g % kKBufs<kNv>, sb = g % kSBufs;
           if (!ptx::mbar_wait(k_full + 8 * buf, uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
-          if (g >= kSBufs && !ptx::mbar_wait(s_free + 8 * sb, uint32_t(g / kSBufs - 1) & 1u)) { ok = false; break; }
+          // S of the tile three before has been read. (It has a barrier that only tiles of its
+          // own kind, odd or even, use: they are read in order, so the barrier is at most a
+          // round back. One for all tiles in this place could be two rounds back, which
+          // has the same parity.)
+          if (g >= kSBufs) {
+            const int t = g - kSBufs;
+            if (!ptx::mbar_wait(s_free + 8 * (t % (2 * kSBufs)), uint32_t(t / (2 * kSBufs)) & 1u)) { ok = false; break; }
+          }
           ptx::tc_fence_after();
           const uint32_t kb = kb0 + buf * (kNv ? kKBuf : kKBuf8), s = tmem + kSCol + sb * kNT;
           if (ptx::elect_one()) {
@@ -839,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive(s_free + 8 * (sb));
+          ptx::mbar_arrive(s_free + 8 * (g % (2 * kSBufs)));
           ptx::mbar_arrive(ring_free + 8 * (g % kRing));
         }
         if (!ok) break;
