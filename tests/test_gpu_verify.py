@@ -185,3 +185,31 @@ def test_captured_twice_with_one_workspace():
         args[6].fill_(-9), args[7].fill_(-9)
         g.replay()
         assert np.array_equal(args[6].cpu().numpy(), ref[0]) and np.array_equal(args[7].cpu().numpy(), ref[1])
+
+
+@pytest.mark.parametrize("dtype", NAMES)
+@pytest.mark.parametrize("V", [9, 255, 5003, 20011])
+def test_rows_on_every_boundary(dtype, V):
+    """Row strides of 8k + 1 and 8k + 3 elements: p's and q's rows differ by every shift. NaN lies between rows."""
+    import torch
+
+    rng = np.random.default_rng(V)
+    B, n = 17, 2
+    target, draft, _ = _rows(rng, B, n, V, dtype)
+    tokens = (draft.double() - target[:, :1].double()).argmax(-1).numpy().astype(np.int32)
+    u = np.stack([np.full(B, 0.999), rng.random(B)], 1).astype(np.float32)
+
+    def spread(x, residue):
+        rows, stride = x.reshape(-1, V), (V + 15) // 8 * 8 + residue
+        buf = torch.full((len(rows) * stride,), float("nan"), dtype=x.dtype, device="cuda")
+        view = buf.as_strided((x.shape[0], x.shape[1], V), (x.shape[1] * stride, stride, 1))
+        view.copy_(x)
+        return view
+
+    for src in (draft, None):
+        got = _run(spread(target, 1), None if src is None else spread(src, 3), tokens, None, u, np.full(B, 70))
+        ref = S.verify_draft(target.double().numpy(), None if src is None else src.double().numpy(), tokens, None, u, np.full(B, 70))
+        for g, r in zip(got[:3], ref):
+            assert np.array_equal(g, r)
+        assert got[3] == ref[3] == 0
+        assert (got[0] == 0).sum() >= B // 2
