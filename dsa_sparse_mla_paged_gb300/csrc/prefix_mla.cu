@@ -378,13 +378,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* PB = sm + 2 * kVBuf;
   uint8_t* side = PB + kPBufs<kNv> * kPBuf;  // [kPBufs] factors and flags
   __shared__ long long s_sum[kThreads / 32];
-  __shared__ int s_job, s_unit, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
+  __shared__ int s_job, s_unit, s_tiles, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
 
   const int half = int(ptx::cluster_ctarank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nclu = int(gridDim.x) >> 1, clu = int(blockIdx.x) >> 1;
 
   if (threadIdx.x == 0) {
+    s_tiles = 0;
     ptx::mbar_init(mma_done, half == 0 ? 2 : 1);
     ptx::mbar_init(q_full, 8);
     ptx::mbar_init(q_free, 2);
@@ -429,25 +430,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- the line's length, this pair's run of it, its tiles and the job it starts in
   int units, gtot;
   {
-    auto block_sum = [&](long long v) {
-#pragma unroll
-      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      __syncthreads();
-      if (lane == 0) s_sum[warp] = v;
-      __syncthreads();
-      long long t = 0;
-      for (int i = 0; i < kThreads / 32; ++i) t += s_sum[i];
-      return t;
-    };
     auto row_units = [&](int r) {
-      const int n = job_tiles(a, a.tiles + r);
-      return n > 0 ? n + kJobCost : 0;
+      const int n = r < a.rows ? job_tiles(a, a.tiles + r) : 0;
+      return n > 0 ? (long long)(n + kJobCost) : 0ll;
     };
-    long long mine = 0;
-    for (int r = threadIdx.x; r < a.rows; r += kThreads) mine += row_units(r);
+    auto warp_scan = [&](long long v) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      return v;
+    };
+    // rows in chunks of a thread each: a chunk's units before this thread's row, and in all
+    constexpr int kWarps = kThreads / 32;
+    auto chunk_scan = [&](long long n, long long& before, long long& all) {
+      const long long up = warp_scan(n);
+      if (lane == 31) s_sum[warp] = up;
+      __syncthreads();
+      const long long sums = warp_scan(lane < kWarps ? s_sum[lane] : 0ll);
+      before = up - n + (warp ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0ll);
+      all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+    };
+    long long n = row_units(threadIdx.x), before, all;
+    chunk_scan(n, before, all);
+    int64_t line = all;
+    for (int r0 = kThreads; r0 < a.rows; r0 += kThreads) {
+      long long b, more;
+      __syncthreads();
+      chunk_scan(row_units(r0 + int(threadIdx.x)), b, more);
+      line += more;
+    }
     const int per = a.tiles ? a.prefix / kNT + kJobCost : 1;  // units of a prefix job
     const int64_t shared = int64_t(a.tiles) * per;
-    const int64_t line = shared + block_sum(mine);
+    line += shared;
     // A pair has at least kMinUnits, so that a short line leaves the merge less (one request
     // of 4,096 tokens: 23.5 us, 24.4 with at least two, 26.0 with one, 25.5 with four),
     // and no pair among those that work goes without: a job's segments are those of
@@ -460,48 +476,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       x = min(x, shared);
       return x / per * (per - kJobCost) + max(int64_t(0), x % per - kJobCost);
     };
-    long long tiles = 0;
     if (threadIdx.x == 0) {
-      tiles = prefix_tiles(hi) - prefix_tiles(lo);
+      const int t = int(prefix_tiles(hi) - prefix_tiles(lo));
+      if (t) atomicAdd(&s_tiles, t);
       if (lo < shared) {
         s_job = int(lo / per);
         s_unit = int(lo % per);
       }
     }
     int64_t base = shared;
-    for (int r0 = 0; r0 < a.rows && hi > base; r0 += kThreads) {
-      const int r = r0 + int(threadIdx.x);
-      const long long n = r < a.rows ? row_units(r) : 0;
-      long long up = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, up, o);
-        if (lane >= o) up += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = up;
-      __syncthreads();
-      long long before = base + up - n, all = 0;
-      for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) before += s_sum[i];
-        all += s_sum[i];
-      }
+    for (int r0 = 0;;) {
       if (n > 0) {
-        const long long t0 = before + kJobCost, t1 = before + n;  // its tiles
-        tiles += max(0ll, min(t1, (long long)hi) - max(t0, (long long)lo));
-        if (lo >= before && lo < t1) {
-          s_job = a.tiles + r;
-          s_unit = int(lo - before);
+        const int64_t first = base + before, t0 = first + kJobCost, t1 = first + n;  // its tiles
+        const int t = int(max(int64_t(0), min(t1, hi) - max(t0, lo)));
+        if (t) atomicAdd(&s_tiles, t);
+        if (lo >= first && lo < t1) {
+          s_job = a.tiles + r0 + int(threadIdx.x);
+          s_unit = int(lo - first);
         }
       }
       base += all;
+      r0 += kThreads;
+      if (r0 >= a.rows || hi <= base) break;
+      n = row_units(r0 + int(threadIdx.x));
+      __syncthreads();
+      chunk_scan(n, before, all);
     }
-    gtot = int(block_sum(tiles));
+    __syncthreads();
+    gtot = s_tiles;
     // P of the first tiles may arrive as soon as the pair has synced
     if (half == 1 && threadIdx.x == 0)
       for (int i = 0; i < kPBufs<kNv> && i < gtot; ++i) ptx::mbar_arrive_expect_tx(p_full + 8 * (i), kPBytes);
   }
-  __syncthreads();
   ptx::cluster_sync();  // the peer's barriers exist before any remote arrive
   const int job0 = s_job;
   const int unit0 = s_unit;
@@ -768,21 +774,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the job's query: each warp 32 heads of five or four times 32 columns
       int jobs = 0;
       auto load_q = [&](int job) {
-        if (jobs >= 1 && !ptx::mbar_wait(q_free, uint32_t(jobs - 1) & 1u)) return false;
-        ++jobs;
         const int row = w * 32 + lane;
         const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
         const int heads = a.rows * kHeads;
         const bool in = hr < heads;
-#pragma unroll 1
-        for (int kb = group ? 5 : 0; kb < (group ? 9 : 5); ++kb) {
-          uint32_t v[32];
+        auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 x = in ? __ldg(a.q + size_t(kb * 8 + i) * heads + hr) : make_uint4(0, 0, 0, 0);
             v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
           }
-          ptx::tmem_st32_u(tmem + (uint32_t(w * 32) << 16) + kb * 32, v);
+        };
+        // blocks of columns are loaded ahead, the first before the old query is let go: one at a
+        // time after that took 4.3 us a job. (NVFP4: one ahead, as the converters' registers allow.)
+        constexpr int kAhead = kNv ? 1 : 2;
+        const int kb0 = group ? 5 : 0, kb1 = group ? 9 : 5;
+        uint32_t v[kAhead][32];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(kb0 + i, v[i]);
+        if (jobs >= 1 && !ptx::mbar_wait(q_free, uint32_t(jobs - 1) & 1u)) return false;
+        ++jobs;
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+          if (kb0 + i < kb1) ptx::tmem_st32_u(tmem + (uint32_t(w * 32) << 16) + (kb0 + i) * 32, v[i % kAhead]);
+          if (kb0 + i + kAhead < kb1) load(kb0 + i + kAhead, v[i % kAhead]);
         }
         ptx::tc_fence_before();
         __syncwarp();

@@ -116,6 +116,12 @@ def test_more_rows_than_a_wave_of_jobs():
     check(inp, pages, 128, rows={0, 1, 99, 201, 298, 299})
 
 
+@pytest.mark.parametrize("prefix", [0, 64])
+def test_more_rows_than_threads_of_a_block(prefix):
+    inp, pages = make(700, 2, prefix, [2 + (i * 7) % 200 for i in range(700)], seed=8)
+    check(inp, pages, prefix, rows={0, 639, 640, 641, 1279, 1280, 1398, 1399})
+
+
 def test_a_prompt_chunk():
     inp, pages = make(1, 130, 256, [200], seed=8)
     check(inp, pages, 256, rows={0, 64, 128, 129})
