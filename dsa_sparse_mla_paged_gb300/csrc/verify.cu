@@ -5,15 +5,16 @@
 // One cluster of up to 8 CTAs per request. Every CTA runs the few draft tests
 // (one lane per draft, exact in fp64), then reads its slice of the one row of p
 // (and of q after a rejection) that the draw needs, each element once. A
-// warp owns a contiguous run of the vocabulary in four parts and sums their weights; the
+// warp owns a contiguous run of the vocabulary in two parts and sums their weights; the
 // CTAs' sums meet in distributed shared memory, and the CTA that holds the threshold
 // goes over the one part again to find the token.
 //
-// Bounds: for a large batch the arithmetic (about 17 instructions per pair of values) and the
-// two rows' bytes, near enough to each other: 64 requests of 131,072 fp32 values, 67 MB, take
-// 17 us (3.9 TB/s), 256 of 100,003 bf16 values, 102 MB, 34 us (3.0 TB/s; rows on any boundary).
-// For a small one the chain of dependent loads (token -> probabilities -> row -> threshold):
-// one request of 32,000 takes 6.7 us.
+// Bounds: the chain of dependent loads (token -> probabilities -> row -> sums -> threshold), 6.7
+// us for one request of 32,000 values; and for a large batch, after that, each warp's turns of
+// loads and of arithmetic (about 17 instructions per pair of values; a third of the issue
+// slots are used): 64 requests of 131,072 fp32 values, 67 MB, take 16.7 us (4.0 TB/s), 256 of
+// 100,003 bf16 values, rows on any boundary, 102 MB, 32.2 us (3.2 TB/s). Loading a step ahead
+// of the sums made it slower (38 us), and so did more CTAs than run at once (37).
 //
 // Weights are 64-bit integers (multiples of 2^-60): integer sums are exact in any
 // order, so the token does not depend on how the vocabulary is cut, and no
@@ -36,7 +37,9 @@ constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxCluster = 8;
 constexpr int kVPerSM = 4;     // resident CTAs
 constexpr int kVUnit = 256;    // a part of a warp's run is a multiple: 32 lanes x 16 B of 16-bit values
-constexpr int kVParts = 4;     // parts of a warp's run with sums of their own
+// Parts of a warp's run with sums of their own: the search for the token goes over one again
+// (256 requests of 100,003 bf16 values: one part 35.9 us, two 32.2, four 33.0).
+constexpr int kVParts = 2;
 
 typedef unsigned long long u64;
 
