@@ -83,7 +83,7 @@ constexpr uint32_t kPBytes = kPBuf + kPSide;
 constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
 constexpr int kMmaWarp = 16, kFeedWarp = 17, kMmaWarp2 = 18, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 76;
+constexpr int kNumBars = 77;
 template <bool kNv>
 constexpr size_t kData = 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
 static_assert(kData<true> >= 2 * kKBuf + 512 && kData<false> >= 2 * kKBuf + 512, "CTA 0's buffers");
@@ -95,7 +95,7 @@ constexpr float kPShift = kNv ? 7.f : 6.f;   // weights are 2^(z - max + kPShift
 template <bool kNv>
 constexpr float kLazy = kNv ? 8.f : 6.f;     // max is raised when a tile passes it by more than 2^kLazy
 constexpr int kMinUnits = 3;
-constexpr int kJobCost = 3;                  // what a job's start and end take, in tiles
+constexpr int kJobCost = 4;                  // what a job's start and end take, in tiles
 
 struct PfxArgs {
   const uint4* q;    // [72][rows * 96] 16-B chunks of the prepared query, each head by head
@@ -351,7 +351,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // the barriers have the same place in both CTAs
   const uint32_t bars = ptx::smem_u32(sm) + uint32_t(kData<kNv>);
   const uint32_t mma_done = bars + 0 * 8;
-  const uint32_t q_full = bars + 1 * 8;
+  const uint32_t q_full = bars + 1 * 8;      // a later job's query is there
+  const uint32_t q_first = bars + 76 * 8;    // the first job's
   const uint32_t q_free = bars + 2 * 8;      // every product with the job's query is done
   const uint32_t k_full = bars + 3 * 8;      // [kKBufs]
   const uint32_t k_free = bars + 7 * 8;      // [kKBufs]  S of the buffer's tile is done
@@ -388,6 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     s_tiles = 0;
     ptx::mbar_init(mma_done, half == 0 ? 2 : 1);
     ptx::mbar_init(q_full, 8);
+    ptx::mbar_init(q_first, 16);
     ptx::mbar_init(q_free, 2);
     ptx::mbar_init(ask, 1);
     for (int i = 0; i < 3; ++i) ptx::mbar_init(v_turn + 8 * i, 4);
@@ -547,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // (four dims of all rows together, so that a warp's stores are whole lines)
       float4* dst = reinterpret_cast<float4*>(a.part) + size_t(wk.job + clu) * kPfxTileRows * (kDNope / 4) + row;
-      const bool real = wk.job < a.tiles || row < kHeads;
+      const bool real = wk.job < a.tiles ? wk.job * kPfxTileRows + row < a.rows * kHeads : row < kHeads;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
         float o[32];
@@ -572,6 +574,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                              [](int) { return true; });
   };
 
+  // CTA 0: 32 heads of a job's query, `blocks` times 32 columns from block kb0, to tensor memory
+  auto query_blocks = [&](int job, int kb0, auto blocks, uint32_t bar, auto until) {
+    const int row = (warp & 3) * 32 + lane;
+    const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
+    const int heads = a.rows * kHeads;
+    const bool in = hr < heads;
+    auto load = [&](int kb, uint32_t (&v)[32]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 x = in ? __ldg(a.q + size_t(kb * 8 + i) * heads + hr) : make_uint4(0, 0, 0, 0);
+        v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+      }
+    };
+    // blocks are loaded ahead, the first before the old query is let go: one at a time
+    // after that took 4.3 us a job. (NVFP4: one ahead, as the converters' registers allow.)
+    constexpr int kBlocks = decltype(blocks)::value, kAhead = kNv ? 1 : 2;
+    uint32_t v[kAhead][32];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(kb0 + i, v[i]);
+    if (!until()) return false;
+#pragma unroll
+    for (int i = 0; i < kBlocks; ++i) {
+      ptx::tmem_st32_u(tmem + (uint32_t((warp & 3) * 32) << 16) + (kb0 + i) * 32, v[i % kAhead]);
+      if (i + kAhead < kBlocks) load(kb0 + i + kAhead, v[i % kAhead]);
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+    return true;
+  };
+  constexpr std::integral_constant<int, 2> two{};
+  constexpr std::integral_constant<int, 3> three{};
+  constexpr std::integral_constant<int, 4> four{};
+  constexpr std::integral_constant<int, 5> five{};
+  // the first query, when nothing else is to be done: the nine blocks by four groups of warps
+  auto first_query = [&](int job) {
+    auto now = [] { return true; };
+    const int quarter = warp >> 2;
+    return quarter == 0 ? query_blocks(job, 0, three, q_first, now) : query_blocks(job, 1 + 2 * quarter, two, q_first, now);
+  };
+
   // registers: the five warpgroups start with 96 each (480) and go on with 104, 104, 96, 96 and 80 (480)
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -583,7 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int g = 0, qn = 0;
 #pragma unroll 1
       for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
-        if (!ptx::mbar_wait(q_full, uint32_t(qn++) & 1u)) { ok = false; break; }
+        if (!(qn == 0 ? ptx::mbar_wait(q_first, 0) : ptx::mbar_wait(q_full, uint32_t(qn - 1) & 1u))) { ok = false; break; }
+        ++qn;
 #pragma unroll 1
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
           if ((g & 1) != (warp == kMmaWarp2)) continue;
@@ -771,38 +815,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ converters, query
     const int w = warp & 3, group = (warp - 8) >> 2;
     if (half == 0) {
-      // the job's query: each warp 32 heads of five or four times 32 columns
       int jobs = 0;
       auto load_q = [&](int job) {
-        const int row = w * 32 + lane;
-        const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
-        const int heads = a.rows * kHeads;
-        const bool in = hr < heads;
-        auto load = [&](int kb, uint32_t (&v)[32]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = in ? __ldg(a.q + size_t(kb * 8 + i) * heads + hr) : make_uint4(0, 0, 0, 0);
-            v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
-          }
-        };
-        // blocks of columns are loaded ahead, the first before the old query is let go: one at a
-        // time after that took 4.3 us a job. (NVFP4: one ahead, as the converters' registers allow.)
-        constexpr int kAhead = kNv ? 1 : 2;
-        const int kb0 = group ? 5 : 0, kb1 = group ? 9 : 5;
-        uint32_t v[kAhead][32];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(kb0 + i, v[i]);
-        if (jobs >= 1 && !ptx::mbar_wait(q_free, uint32_t(jobs - 1) & 1u)) return false;
-        ++jobs;
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-          if (kb0 + i < kb1) ptx::tmem_st32_u(tmem + (uint32_t(w * 32) << 16) + (kb0 + i) * 32, v[i % kAhead]);
-          if (kb0 + i + kAhead < kb1) load(kb0 + i + kAhead, v[i % kAhead]);
-        }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(q_full);
-        return true;
+        if (jobs++ == 0) return first_query(job);
+        auto until = [&] { return ptx::mbar_wait(q_free, uint32_t(jobs - 2) & 1u); };
+        return group == 0 ? query_blocks(job, 0, five, q_full, until) : query_blocks(job, 5, four, q_full, until);
       };
       bool on = gtot > 0 && wk.start(a, job0, unit0, units);
       if constexpr (kNv) {
@@ -844,6 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
       const int hr = (wk.job < a.tiles ? wk.job * kPfxTileRows : (wk.job - a.tiles) * kHeads) + row;
       const float cs = fmaxf(hr < a.rows * kHeads ? a.scale_log2 * a.qs[hr] : 1.f, 1.1754944e-38f);
+      if (g0 == 0) first_query(wk.job);
       float m_mine = -INFINITY, l = 0.f;  // the maximum that l is relative to
       const int g1 = g0 + wk.k1 - wk.k0;
 #pragma unroll 1
@@ -1060,12 +1078,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
     // segment i's slot and row
     auto slot = [&](int i) { return i < n0 ? job0 + f0 + i : job1 + f1 + i - n0; };
     auto row = [&](int i) { return i < n0 ? hr % kPfxTileRows : h; };
-#pragma unroll 4
-    for (int i = part; i < n0 + n1; i += kSplit) {
-      const float* ml = a.ml + size_t(slot(i)) * 512 + row(i);
-      m = fmaxf(m, fmaxf(__ldg(ml), __ldg(ml + 256)));
-    }
-    const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll 2
     for (int i = part; i < n0 + n1; i += kSplit) {
       const float* ml = a.ml + size_t(slot(i)) * 512 + row(i);
@@ -1074,12 +1086,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
       float4 v[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = __ldg(o + j * kPfxTileRows);
-      const float ma = __ldg(ml), mb = __ldg(ml + 256);
-      tot = fmaf(exp2f(ma - mm), __ldg(ml + 128), tot);
-      tot = fmaf(exp2f(mb - mm), __ldg(ml + 384), tot);
-      const float w = exp2f(fmaxf(ma, mb) - mm);
+      const float ma = __ldg(ml), mb = __ldg(ml + 256), la = __ldg(ml + 128), lb = __ldg(ml + 384);
+      const float top = fmaxf(ma, mb), old = m;
+      m = fmaxf(m, top);
+      const float mm = m == -INFINITY ? 0.f : m;
+      const float keep = exp2f(old - mm), w = exp2f(top - mm);
+      tot = fmaf(exp2f(ma - mm), la, fmaf(exp2f(mb - mm), lb, tot * keep));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) add(j, w, v[j]);
+      for (int j = 0; j < 4; ++j) {
+        acc[j].x *= keep; acc[j].y *= keep; acc[j].z *= keep; acc[j].w *= keep;
+        add(j, w, v[j]);
+      }
     }
   }
   if constexpr (kSplit > 1) {
