@@ -251,3 +251,27 @@ def test_captured_and_replayed_on_another_stream():
         bits |= S.pages_compact(s.table, s.ctx, s.refs, s.views())[2]
     assert bits == S.ERR_PAGES
     s.check(bits)
+
+
+def test_pages_beyond_four_gigabytes():
+    """A pool whose pages lie 96 MB apart (offsets pass 32 bits): copied on write, then packed."""
+    import torch
+
+    s = State([500, 90, 4000, 0], shared=0, pools=((4096, 4096),), num_pages=90, width=70).upload()
+    far = 96 << 20
+    pool = torch.empty(90 * far, dtype=torch.uint8, device="cuda").view(90, far)
+    pool[:, :4096] = s.d["pools"][0]
+    s.plan = dsa.make_pools([(pool, 4096, far)])
+    dsa.pages_fork(s.p, _dev([0]), _dev([3]), s.d["table"], s.d["ctx"], s.d["refs"], s.ws)
+    dsa.pages_resize(s.p, _dev([510, 0, 4001, 501]), s.plan, s.d["table"], s.d["ctx"], s.d["refs"], s.ws)
+    dsa.pages_compact(s.p, s.plan, s.d["table"], s.d["ctx"], s.d["refs"], None, None, s.ws)
+    views = s.views()
+    assert S.pages_fork(s.table, s.ctx, s.refs, [0], [3]) == 0
+    assert S.pages_resize(s.table, s.ctx, s.refs, [510, 0, 4001, 501], views) == 0
+    live = S.pages_compact(s.table, s.ctx, s.refs, views)[1]
+    assert dsa.get_device_error(s.ws) == 0
+    assert np.array_equal(s.d["table"].cpu().numpy(), s.table) and np.array_equal(s.d["refs"].cpu().numpy(), s.refs)
+    held = [s.table[b, j] for b in range(4) for j in range(S.pages_of(int(s.ctx[b])))]
+    assert max(held) < live
+    whole = [s.table[b, j] for b in range(4) for j in range(int(s.ctx[b]) // 64)]  # the rest may be unspecified
+    assert np.array_equal(pool[:, :4096].cpu().numpy()[whole], views[0][whole])

@@ -345,3 +345,52 @@ def test_on_a_side_stream():
     o, l = bf16_to_np(out), lse.cpu().numpy()
     for b in range(4):
         check_row(inp, pages, 256, b, 0, o[b], l[b])
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+def test_pages_beyond_four_gigabytes(lat_fmt):
+    """Pages 64 MB apart: offsets pass 32 bits within the pool."""
+    import torch
+
+    inp, pages = make(3, 2, 1024, [2, 600, 1500], seed=32, lat_fmt=lat_fmt)
+    d = Dev(inp)
+    far = 1 << 26
+    assert inp.num_pages > 64
+    pool = torch.empty(inp.num_pages * far, dtype=torch.uint8, device="cuda").view(-1, far)
+    pool[:, :inp.lat_page_stride] = d.lat_pool
+    d.lat_pool = pool
+    d.p.lat_page_stride = far
+    out, lse = launch(d, pages, 1024)
+    assert dsa.get_device_error(d.ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for r in range(6):
+        check_row(inp, pages, 1024, r // 2, r % 2, o[r], l[r])
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own on two streams, over one another, beside the fused decode."""
+    import torch
+
+    cases = [make(6, 2, 512, [2, 70, 400, 1300, 64, 9], seed=33), make(20, 1, 2048, [1 + 31 * i for i in range(20)], seed=34, lat_fmt="nvfp4")]
+    devs = [Dev(inp) for inp, _ in cases]
+    other = Dev(gen.make_inputs(2, 1, [5000, 300], seed=35))
+    alone = [launch(d, pages, prefix) for d, (_, pages), prefix in zip(devs, cases, (512, 2048))]
+    step = [x.clone() for x in other.decode()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got, steps = ([], []), []
+    for _ in range(12):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(launch(devs[i], cases[i][1], (512, 2048)[i]))
+        with torch.cuda.stream(streams[2]):
+            steps.append([x.clone() for x in other.decode()])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert dsa.get_device_error(devs[i].ws) == 0
+        for out, lse in got[i]:
+            assert torch.equal(out.view(torch.int16), alone[i][0].view(torch.int16)) and torch.equal(lse, alone[i][1])
+    assert dsa.get_device_error(other.ws) == 0
+    for s in steps:
+        for x, y in zip(s, step):
+            assert torch.equal(x, y)

@@ -213,3 +213,18 @@ def test_rows_on_every_boundary(dtype, V):
             assert np.array_equal(g, r)
         assert got[3] == ref[3] == 0
         assert (got[0] == 0).sum() >= B // 2
+
+
+def test_rows_beyond_four_gigabytes():
+    import torch
+
+    rng = np.random.default_rng(21)
+    target, draft, tokens = _rows(rng, 5, 4, 3001, "bfloat16")
+    far = 1 << 28  # elements between rows
+    wide = lambda x: torch.empty(x.shape[0] * x.shape[1] * far, dtype=x.dtype, device="cuda").as_strided(
+        x.shape, (x.shape[1] * far, far, 1)).copy_(x)
+    u = rng.random((5, 4), dtype=np.float32)
+    got = _run(wide(target), wide(draft), tokens, None, u, np.full(5, 70))
+    ref = S.verify_draft(target.double().numpy(), draft.double().numpy(), tokens, None, u, np.full(5, 70))
+    for g, r in zip(got, ref):
+        assert np.array_equal(g, r)
