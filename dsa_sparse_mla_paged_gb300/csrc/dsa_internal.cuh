@@ -61,13 +61,7 @@ struct WsLayout {
   size_t cand;      // uint64 [rows][kCandCap] top-k candidates (key << 32 | token)
   size_t gmax;      // uint32 [rows][gstride] order key of the largest score of each 32 tokens
   size_t gmax128;   // uint32 [rows][g128stride] the same per 128 tokens (dsa_decode; zero between calls)
-  size_t opart;     // float [rows][splits][96][512]; dsa_prefix_mla_decode keeps its state (pfx_*) here
-  size_t pfx_q;     // [72][rows * 96] 16-B chunks of the prepared query
-  size_t pfx_qs;    // float [rows * 96] its power-of-two scales
-  size_t pfx_len;   // int32 [rows] tokens past the prefix that a row sees
-  size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
-  size_t pfx_ml;    // float [pfx_slots][2][2][128] partial softmax maxima and sums
-  size_t pfx_part;  // float [pfx_slots][128][512] partial outputs
+  size_t opart;     // float [rows][splits][96][512]
   size_t lpart;     // float [rows][splits][96]
   size_t topk;      // int32 [rows][topk] (dsa_decode without topk_idx_out)
   size_t dcp_key;   // uint32 [rows][kDcpMaxWorld][topk] shard lists: bf16 keys by position
@@ -77,10 +71,17 @@ struct WsLayout {
   size_t fe_q;      // fp32 [rows][32][128] the front end's head outputs
   size_t fe_cnt;    // int32 [33][kFeMaxPasses] the front end's arrival counters
   size_t dcp_keys16;  // uint16 [rows][W][S] shard-major score keys, W * S <= cap + 8 * kDcpMaxWorld
+  size_t scores;    // float [rows][cap]
+  // the serving operators', behind the decode step's, whose places stay as they were
   size_t pg_head;   // int32 [16] totals of a page operation
   size_t pg_req;    // int32 [3][batch] a page operation's plan per request (or fork pair)
   size_t pg_list;   // int32 [3][num_pages] its page lists
-  size_t scores;    // float [rows][cap]
+  size_t pfx_q;     // [72][rows * 96] 16-B chunks of the prepared query
+  size_t pfx_qs;    // float [rows * 96] its power-of-two scales
+  size_t pfx_len;   // int32 [rows] tokens past the prefix that a row sees
+  size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
+  size_t pfx_ml;    // float [pfx_slots][2][2][128] partial softmax maxima and sums
+  size_t pfx_part;  // float [pfx_slots][128][512] partial outputs
   size_t total;
   int rows, cap, max_chunks, splits, gstride, g128stride;
   int pfx_tiles, pfx_jobs, pfx_slots;
@@ -110,19 +111,6 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   L.gmax = o; o = align256(o + size_t(L.rows) * L.gstride * 4);
   L.gmax128 = o; o = align256(o + size_t(L.rows) * L.g128stride * 4);
   L.opart = o; o = align256(o + size_t(L.rows) * L.splits * kHeads * kDNope * 4);
-  // the prefix attention's partials: one slot per job (a tile of 128 query
-  // heads on the prefix, or a row on its own tokens) and cut between CTA pairs
-  L.pfx_tiles = (L.rows * kHeads + kPfxTileRows - 1) / kPfxTileRows;
-  L.pfx_jobs = L.pfx_tiles + L.rows;
-  L.pfx_slots = L.pfx_jobs + kPfxMaxClusters;
-  size_t x = L.opart;
-  L.pfx_q = x; x = align256(x + size_t(L.rows) * kHeads * kDQK * 2);
-  L.pfx_qs = x; x = align256(x + size_t(L.rows) * kHeads * 4);
-  L.pfx_len = x; x = align256(x + size_t(L.rows) * 4);
-  L.pfx_plan = x; x = align256(x + size_t(L.pfx_jobs) * 2 * 4);
-  L.pfx_ml = x; x = align256(x + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
-  L.pfx_part = x; x = align256(x + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
-  o = x > o ? x : o;
   L.lpart = o; o = align256(o + size_t(L.rows) * L.splits * kHeads * 4);
   L.topk = o; o = align256(o + size_t(L.rows) * p.topk * 4);
   L.dcp_key = o; o = align256(o + size_t(L.rows) * kDcpMaxWorld * p.topk * 4);
@@ -132,10 +120,21 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   L.fe_q = o; o = align256(o + size_t(L.rows) * kIdxHeads * kIdxDim * 4);
   L.fe_cnt = o; o = align256(o + size_t(kIdxHeads + 1) * kFeMaxPasses * 4);
   L.dcp_keys16 = o; o = align256(o + size_t(L.rows) * (size_t(L.cap) + 8 * kDcpMaxWorld) * 2);
+  L.scores = o; o = align256(o + size_t(L.rows) * L.cap * 4);
   L.pg_head = o; o = align256(o + 64);
   L.pg_req = o; o = align256(o + size_t(3) * p.batch * 4);
   L.pg_list = o; o = align256(o + size_t(3) * p.num_pages * 4);
-  L.scores = o; o = align256(o + size_t(L.rows) * L.cap * 4);
+  // the prefix attention's partials: one slot per job (a tile of 128 query
+  // heads on the prefix, or a row on its own tokens) and cut between CTA pairs
+  L.pfx_tiles = (L.rows * kHeads + kPfxTileRows - 1) / kPfxTileRows;
+  L.pfx_jobs = L.pfx_tiles + L.rows;
+  L.pfx_slots = L.pfx_jobs + kPfxMaxClusters;
+  L.pfx_q = o; o = align256(o + size_t(L.rows) * kHeads * kDQK * 2);
+  L.pfx_qs = o; o = align256(o + size_t(L.rows) * kHeads * 4);
+  L.pfx_len = o; o = align256(o + size_t(L.rows) * 4);
+  L.pfx_plan = o; o = align256(o + size_t(L.pfx_jobs) * 2 * 4);
+  L.pfx_ml = o; o = align256(o + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
+  L.pfx_part = o; o = align256(o + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
   L.total = o;
   return L;
 }
