@@ -81,7 +81,7 @@ struct WsLayout {
   size_t pfx_len;   // int32 [rows] tokens past the prefix that a row sees
   size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
   size_t pfx_ml;    // float [pfx_slots][2][2][128] partial softmax maxima and sums
-  size_t pfx_part;  // float [pfx_slots][128][512] partial outputs
+  size_t pfx_part;  // float [pfx_slots][512 / 4][128][4] partial outputs
   size_t total;
   int rows, cap, max_chunks, splits, gstride, g128stride;
   int pfx_tiles, pfx_jobs, pfx_slots;

@@ -80,9 +80,10 @@ constexpr int kKBufs = kNv ? 2 : 4;
 template <bool kNv>
 constexpr int kVBufs = kNv ? 2 : 4;
 template <bool kNv>
-constexpr int kPBufs = kNv ? 3 : 4;          // (NVFP4: with 4, less of L1 is left to the converters' loads: 225 for 199 us)
+constexpr int kPBufs = kNv ? 3 : 4;          // (NVFP4: 4 leave the converters' loads less L1: 225 for 199 us)
 static_assert(2 * kKBuf == 4 * kKBuf8 && 2 * kVBuf == 4 * kVBuf8, "either kind of buffers");
-// P: 8 chunks of 8 tokens, each 16 B per row in row order (the unswizzled core
+// P: 8 chunks, of 8 tokens in fp16 or of 16 tokens of the E5M2 (0..3) or the E4M3 part
+// (4..7), each 16 B per row in row order (the unswizzled core
 // matrices of the MMA, and 512 contiguous bytes for a warp's remote store)
 constexpr int kPChunk = 128 * 16;
 constexpr int kPBuf = 8 * kPChunk;           // 16,384
@@ -114,7 +115,7 @@ struct PfxArgs {
   const int32_t* lens;  // [rows] private tokens that a row sees (0: an invalid context length)
   int32_t* plan;  // [jobs][2] first and last CTA pair of a job
   float* ml;      // [slots][2 groups][2][128] softmax maxima (base 2) and sums
-  float* part;    // [slots][128][512]
+  float* part;    // [slots][512 / 4][128][4] unnormalised outputs
   int* err;
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
