@@ -984,9 +984,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // that is above 2^-13 of the largest; below, x - hi <= 2^-10 is off by at most 2^-13,
 // 2^-20 of the largest. Written in 16-B chunks, each head by head, so that
 // 32 consecutive heads load 512 contiguous bytes into tensor memory wherever a tile
-// of heads starts.
+// of heads starts; a block's eight heads go through shared memory and out as whole
+// lines (64 rows: 4.8 us, 5.9 written word by word with scalar conversions).
 // ---------------------------------------------------------------------------
 constexpr int kQueryWarps = 8;
+static_assert(kHeads % kQueryWarps == 0, "whole blocks");
+
+// Two values' E4M3 parts and the E5M2 parts of the rests, a's in the low byte.
+__device__ __forceinline__ void split_query(float a, float b, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l, p, q;\n\t.reg .b32 u;\n\t.reg .f32 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %3, %2;\n\tcvt.rn.f16x2.e4m3x2 u, h;\n\tmov.b32 {p, q}, u;\n\t"
+      "cvt.f32.f16 x, p;\n\tcvt.f32.f16 y, q;\n\tsub.rn.f32 x, %2, x;\n\tsub.rn.f32 y, %3, y;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 l, y, x;\n\tcvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n}\n"
+      : "=&r"(hi), "=r"(lo)
+      : "f"(a), "f"(b));
+}
 
 template <bool kNv>
 __global__ void __launch_bounds__(32 * kQueryWarps)
@@ -1003,8 +1015,10 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
     if (!good) atomicOr(err, DSA_DEVERR_CTX);
     lens[r] = good ? c - n_q + (r - b * n_q) + 1 - prefix : 0;
   }
-  const int hr = blockIdx.x * kQueryWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (hr >= heads) return;
+  constexpr int kChunks = 2 * kDQK / 16, kPitch = 4 * kQueryWarps + 4;  // words of a chunk of all heads, padded
+  __shared__ __align__(16) uint32_t s_out[kChunks * kPitch];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hr = blockIdx.x * kQueryWarps + warp;
+  auto put = [&](int chunk0, int i, uint32_t v) { s_out[(chunk0 + (i >> 2)) * kPitch + warp * 4 + (i & 3)] = v; };
   // nine words (two values each) per lane; FP8 needs them in pairs (four values to a word)
   constexpr int kWords = kDQK / 2, kPer = kWords / 32;
   uint32_t w[kPer + 1];
@@ -1024,30 +1038,29 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f0 * f1, __uint_as_float(w[i] & 0xFFFF0000u) * f0 * f1);
-      prepared[(size_t(word(i) >> 2) * heads + hr) * 4 + (word(i) & 3)] = *reinterpret_cast<const uint32_t*>(&h);
+      put(0, word(i), *reinterpret_cast<const uint32_t*>(&h));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kPer + 1; i += 2) {
       if (word(i) >= kWords) continue;
-      uint32_t hi = 0, lo = 0;
+      uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const uint32_t two = w[i + (d >> 1)];
-        const float x = __uint_as_float(d & 1 ? two & 0xFFFF0000u : two << 16) * f0 * f1;
-        const __nv_fp8_storage_t h = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-        const __half_raw hv = __nv_cvt_fp8_to_halfraw(h, __NV_E4M3);
-        const __nv_fp8_storage_t l = __nv_cvt_float_to_fp8(x - __half2float(*reinterpret_cast<const __half*>(&hv)),
-                                                           __NV_SATFINITE, __NV_E5M2);
-        hi |= uint32_t(h) << (8 * d);
-        lo |= uint32_t(l) << (8 * d);
-      }
+      for (int d = 0; d < 2; ++d)
+        split_query(__uint_as_float(w[i + d] << 16) * f0 * f1, __uint_as_float(w[i + d] & 0xFFFF0000u) * f0 * f1, hi[d],
+                    lo[d]);
       const int out = word(i) >> 1;  // the word of four dims: 16 dims a chunk
-      prepared[(size_t(out >> 2) * heads + hr) * 4 + (out & 3)] = hi;
-      prepared[(size_t(36 + (out >> 2)) * heads + hr) * 4 + (out & 3)] = lo;
+      put(0, out, hi[0] | hi[1] << 16);
+      put(kChunks / 2, out, lo[0] | lo[1] << 16);
     }
   }
   if (lane == 0) qs[hr] = scalbnf(1.f, e);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
+    const int chunk = i / kQueryWarps, h = i % kQueryWarps;
+    reinterpret_cast<uint4*>(prepared)[size_t(chunk) * heads + blockIdx.x * kQueryWarps + h] =
+        *reinterpret_cast<const uint4*>(s_out + chunk * kPitch + h * 4);
+  }
 }
 
 // ---------------------------------------------------------------------------
