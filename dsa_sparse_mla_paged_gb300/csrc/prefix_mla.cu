@@ -1069,7 +1069,8 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 // L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums of their own;
 // its O is relative to the larger of their maxima). A warp has 32 heads, a lane each, 16
 // dims of them and every kSplit-th segment: a row alone has a segment from nearly
-// every pair, many rows have few each.
+// every pair, many rows have few each. The partial outputs' bytes bound it: 64 rows, 33 MB, 8.1 us;
+// 252 rows, 99 MB, 24 us.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
