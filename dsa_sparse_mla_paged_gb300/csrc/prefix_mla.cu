@@ -370,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's maximum is decided
   const uint32_t ring_full = bars + 21 * 8;  // [kRing]
   const uint32_t ring_free = bars + 29 * 8;  // [kRing]
-  const uint32_t p_free = bars + 37 * 8;     // [kPBufs]  P . V of the tile in this slot of P is done (either CTA)
+  const uint32_t p_free = bars + 37 * 8;     // [kPBufs]  P . V of the tile in this slot of P is done (CTA 0; NVFP4: both)
   const uint32_t p_full = bars + 41 * 8;     // [kPBufs]  P and the factors have landed
   const uint32_t go = bars + 45 * 8;         // [kPBufs]  P and O are ready for P . V
   const uint32_t v_full = bars + 49 * 8;     // [4] NVFP4: by half tile
@@ -538,7 +538,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int what = s_ask;
         // O is up to date, and still, once P . V of the tile before g is done
         const int g = what < 0 ? -1 - what : what;
-        if (!ptx::mbar_wait(p_free + 8 * ((g - 1) % kPBufs<kNv>), uint32_t((g - 1) / kPBufs<kNv>) & 1u)) return false;
+        // (FP8: by the barrier of its values, which comes sooner than the one that both CTAs
+        // get; it is at most a phase back, as the tile's values came before it was asked for.
+        // NVFP4's could be two back.)
+        const uint32_t done = kNv ? p_free : v_free, of = kNv ? kPBufs<kNv> : kVBufs<kNv>, t = uint32_t(g - 1);
+        if (!ptx::mbar_wait(done + 8 * (t % of), (t / of) & 1u)) return false;
         ptx::tc_fence_after();
         if (what < 0) break;
         const float alpha = reinterpret_cast<const float*>(side + (g % kPBufs<kNv>) * kPSide)[row];
@@ -753,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                     ptx::sdesc_sw128_mn(vb + n * 2 * kBlk + kk * 32 * 128, kBlk, 1024),
                                     ptx::idesc(1 - part, 0, 128, 256, 0, 1), (k > wk.k0 || part > 0 || kk > 0) ? 1u : 0u);
               ptx::mma_commit(v_free + 8 * buf);
-              ptx::mma_commit_to(p_free + 8 * pb, 3);
+              ptx::mma_commit_to(p_free + 8 * pb, 1);
             }
             __syncwarp();
           }
@@ -784,17 +788,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int pb = g % kPBufs<kNv>;
           if (!ptx::mbar_wait_cluster(p_full + 8 * pb, uint32_t(g / kPBufs<kNv>) & 1u)) { ok = false; break; }
           if constexpr (!kNv) {
-            // Rows that the job does not see: their weights are 0, but their bytes could be NaN.
-            // (This tile's P was sent after the product kPBufs tiles ago, so its buffer's
-            // barrier is at most a round from this tile's.)
+            // The tile's values, and zeros for rows that the job does not see: their weights
+            // are 0, but their bytes could be NaN. (This tile's P was sent after the product
+            // kPBufs tiles ago, so its buffer's barrier is at most a phase back.)
             static_assert(kPBufs<kNv> <= kVBufs<kNv>, "the buffer's last product is done");
             const int slot = g % kRing, buf = g % kVBufs<kNv>;
             if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) { ok = false; break; }
             const int valid = ring[slot].valid;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
+            if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs<kNv>) & 1u)) { ok = false; break; }
             if (valid < kNT) {
-              if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs<kNv>) & 1u)) { ok = false; break; }
               uint8_t* v = VB + buf * kVBuf8 + (lane >> 3) * kBlk + (lane & 7) * 16;
               for (int t = valid; t < kNT; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
             }
@@ -819,6 +823,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ptx::elect_one()) ptx::mma_commit(mma_done);
       __syncwarp();
       ptx::mbar_wait(mma_done, 0);
+      // nor of the other CTA's arrivals here, when this one exits
+      if (half == 0 && warp == kMmaWarp && ok)
+        for (int g = max(0, gtot - kPBufs<kNv>); g < gtot && ok; ++g)
+          ok = ptx::mbar_wait_cluster(p_free + 8 * (g % kPBufs<kNv>), uint32_t(g / kPBufs<kNv>) & 1u);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters, query
