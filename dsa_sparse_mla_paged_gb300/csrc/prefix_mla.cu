@@ -22,8 +22,8 @@
 //
 // Measured (one GB300): 13 x 2 rows on 262,144 shared tokens 875 us (1.62 PFLOP/s; the
 // clock falls under the power limit, 995 us when it is warm), 64 rows on 32,768 and 1,900 of
-// their own 272 us (1.66 PFLOP/s), 24 rows on 8,111 of their own 40 us, one row on 4,096 20 us;
-// NVFP4, 8 x 6 rows on 16,384 and 700 of their own 205 us (0.82 PFLOP/s). An FP8 tile takes about
+// their own 269 us (1.67 PFLOP/s), 24 rows on 8,111 of their own 38 us, one row on 4,096 20 us;
+// NVFP4, 8 x 6 rows on 16,384 and 700 of their own 207 us (0.81 PFLOP/s). An FP8 tile takes about
 // 1,430 cycles; the scores' products, at 1,165, bound it, and an NVFP4 tile about 2,600: its
 // K-blocks' stores and products share CTA 0's shared memory (without the stores 152 us,
 // without the arithmetic of the conversion 206).
