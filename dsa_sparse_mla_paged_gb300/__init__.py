@@ -296,11 +296,16 @@ def _prob_rows(name, t, rows):
     code = {"torch.float32": DSA_PROB_F32, "torch.bfloat16": DSA_PROB_BF16, "torch.float16": DSA_PROB_F16}.get(str(t.dtype))
     if code is None:
         raise ValueError(f"verify_draft: {name} is {t.dtype}, not float32, bfloat16 or float16")
-    stride = t.stride(-2) if t.dim() > 1 and t.shape[-2] > 1 else t.stride(0) if t.dim() == 3 else t.shape[-1]
-    even = t.dim() < 3 or t.shape[0] == 1 or t.shape[1] == 1 or t.stride(0) == t.shape[1] * t.stride(1)
-    if t.numel() != rows * t.shape[-1] or t.stride(-1) != 1 or not even:
+    vocab, even, stride, span = t.shape[-1], t.stride(-1) == 1 or t.shape[-1] == 1, None, 0
+    for n, d in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n > 1:
+            even &= stride is None or d == span  # the next dimension goes on where this one ends
+            stride = d if stride is None else stride
+            span = d * n
+    # (rows that share elements, as those of an expanded tensor do, have no such stride)
+    if t.numel() != rows * vocab or not even or (stride is not None and stride < vocab):
         raise ValueError(f"verify_draft: {name} is not {rows} equally spaced rows")
-    return code, max(stride, t.shape[-1])
+    return code, stride or vocab
 
 
 def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_lens, n_accepted, out_tokens, new_lens, ws,

@@ -130,3 +130,41 @@ def test_binding_checks():
                           (torch.zeros(2, 3, 8)[:, :2], None)):
         with pytest.raises(ValueError, match="verify_draft"):
             call(target, draft)
+
+
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_binding_refuses_rows_that_share_elements(n_q):
+    """Expanded and overlapping rows: the kernel would read past the storage's end."""
+    import torch
+
+    p = _params(batch=4, n_q=n_q)
+    i = torch.zeros(4 * n_q, dtype=torch.int32)
+    u = torch.zeros(4, n_q)
+    good_t, good_d = torch.rand(4, n_q, 50), torch.rand(4, max(n_q - 1, 1), 50) if n_q > 1 else None
+
+    def call(target, draft):
+        dsa.verify_draft(p, target, draft, i[:4 * (n_q - 1)].view(4, n_q - 1), None, u, None, i[:4], i.view(4, n_q), None, i)
+
+    one, line = torch.rand(50), torch.rand(800)
+    cases = [one.expand(4, n_q, 50), one.expand(4 * n_q, 50), torch.rand(4, 1, 50).expand(4, max(n_q, 2), 50)[:, :n_q]
+             if n_q > 1 else torch.rand(1, 1, 50).expand(4, 1, 50), torch.rand(1, n_q, 50).expand(4, n_q, 50),
+             line.as_strided((4, n_q, 50), (7 * n_q, 7, 1)), line.as_strided((4 * n_q, 50), (49, 1)),
+             torch.rand(2, 2, n_q, 50).transpose(0, 1)]
+    for bad in cases:
+        with pytest.raises(ValueError, match="verify_draft"):
+            call(bad, good_d)
+        if n_q > 1:
+            with pytest.raises(ValueError, match="verify_draft"):
+                call(good_t, bad[..., :n_q - 1, :] if bad.dim() >= 3 else bad[:4 * (n_q - 1)])
+
+
+def test_binding_takes_one_row_of_any_stride():
+    """A single row has no distance to the next: the stride passed on is at least the vocabulary."""
+    import torch
+
+    for t in (torch.rand(50), torch.rand(1, 50), torch.rand(1, 1, 50), torch.rand(50).expand(1, 1, 50),
+              torch.rand(3, 50)[::2][:1], torch.rand(400).as_strided((1, 1, 50), (3, 7, 1))):
+        assert dsa._prob_rows("target", t, 1)[1] >= 50
+    assert dsa._prob_rows("target", torch.rand(4, 2, 60)[:, :, 5:55], 8)[1] == 60
+    assert dsa._prob_rows("target", torch.rand(4, 3, 60)[:, 1:2], 4)[1] == 180
+    assert dsa._prob_rows("target", torch.rand(2, 2, 3, 60), 12)[1] == 60
