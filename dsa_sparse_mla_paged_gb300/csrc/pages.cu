@@ -137,6 +137,7 @@ __device__ void plan_requests(const PagesArgs& a, long long* warp_sums) {
 template <bool kCompact>
 __global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPlanCtas, 1, 1) pages_plan_kernel(PagesArgs a) {
   namespace cg = cooperative_groups;
+  ptx::cluster_arrive();
   pdl_wait();
   __shared__ long long warp_sums64[32];
   __shared__ int warp_sums[32];
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPlanCtas, 1, 1
   for (int p = p0 + int(threadIdx.x); p < p1; p += kPlanThreads) mine += a.refs[p] > 0;
   int total;
   block_scan<int>(mine, warp_sums, total);
+  ptx::cluster_wait();  // every CTA has started: their shared memory can be written
   if (threadIdx.x < kPlanCtas) *cl.map_shared_rank(counts + me, threadIdx.x) = total;
   cl.sync();
   int before = 0, live = 0;

@@ -282,6 +282,7 @@ __device__ __forceinline__ u64 warp_mass(const T* prow, const T* qrow, int lo, i
 template <typename T>
 __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid_constant__ VerifyArgs a) {
   namespace cg = cooperative_groups;
+  ptx::cluster_arrive();
   pdl_wait();
   cg::cluster_group cl = cg::this_cluster();
   __shared__ int s_acc, s_count, s_flags;
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid
       if (lane == 0) s_part[w] = sum;
     }
     __syncthreads();
+    if (round == 0) ptx::cluster_wait();  // every CTA has started: their shared memory can be written
     if (threadIdx.x < ctas) {
       u64 t = 0;
       for (int i = 0; i < kVWarps * kVParts; ++i) t = capped(t + s_part[i]);
