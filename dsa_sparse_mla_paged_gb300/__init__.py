@@ -268,10 +268,22 @@ def make_pools(pools):
     return (PagePool * max(len(pools), 1))(*[PagePool(_ptr(b), int(n), int(s)) for b, n, s in pools]), len(pools)
 
 
+def _array(fn, name, t, dtype, n):
+    """The address of a dense array of at least n elements (int64 tokens, or a row expanded over the
+    batch, would be read as something else, or past their end). None and addresses pass."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} is not a contiguous {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
 def pages_resize(params, new_lens, pools, block_table, ctx_lens, page_refs, ws, stream=None):
     """Grow, shrink or free every request to `new_lens` (negative: as it is); `pools` from make_pools."""
+    import torch
+
     _check("dsa_pages_resize", load().dsa_pages_resize(
-        ctypes.byref(params), _ptr(new_lens), pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
+        ctypes.byref(params), _array("pages_resize", "new_lens", new_lens, torch.int32, params.batch), pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
         _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
@@ -279,8 +291,12 @@ def pages_fork(params, src, dst, block_table, ctx_lens, page_refs, ws, stream=No
     """Slots dst[i] share the pages of requests src[i] (int32 tensors of one length)."""
     if src.numel() != dst.numel():
         raise ValueError("pages_fork: src and dst differ in length")
+    import torch
+
+    n = src.numel()
     _check("dsa_pages_fork", load().dsa_pages_fork(
-        ctypes.byref(params), src.numel(), _ptr(src), _ptr(dst), _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
+        ctypes.byref(params), n, _array("pages_fork", "src", src, torch.int32, n),
+        _array("pages_fork", "dst", dst, torch.int32, n), _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs),
         _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
@@ -312,6 +328,8 @@ def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_len
                  stream=None):
     """Accept or reject the drafted tokens and draw the next one. `target` [B, n_q, vocab] and `draft`
     [B, n_q - 1, vocab] (or None) are probabilities; `n_draft`, `ctx_lens`, `new_lens` may be None."""
+    import torch
+
     code, p_stride = _prob_rows("target", target, params.batch * params.n_q)
     q_stride = 0
     if draft is not None and params.n_q > 1:
@@ -320,9 +338,12 @@ def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_len
             raise ValueError("verify_draft: target and draft differ in type or vocabulary")
     else:
         draft = None
+    B, n_q, name = params.batch, params.n_q, "verify_draft"
     _check("dsa_verify_draft", load().dsa_verify_draft(
         ctypes.byref(params), target.shape[-1], code, _ptr(target), p_stride, _ptr(draft), q_stride,
-        _ptr(draft_tokens) if params.n_q > 1 else None, _ptr(n_draft), _ptr(uniforms), _ptr(ctx_lens),
+        _array(name, "draft_tokens", draft_tokens, torch.int32, B * (n_q - 1)) if n_q > 1 else None,
+        _array(name, "n_draft", n_draft, torch.int32, B), _array(name, "uniforms", uniforms, torch.float32, B * n_q),
+        _array(name, "ctx_lens", ctx_lens, torch.int32, B),
         _ptr(n_accepted), _ptr(out_tokens), _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 

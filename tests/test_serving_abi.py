@@ -168,3 +168,30 @@ def test_binding_takes_one_row_of_any_stride():
     assert dsa._prob_rows("target", torch.rand(4, 2, 60)[:, :, 5:55], 8)[1] == 60
     assert dsa._prob_rows("target", torch.rand(4, 3, 60)[:, 1:2], 4)[1] == 180
     assert dsa._prob_rows("target", torch.rand(2, 2, 3, 60), 12)[1] == 60
+
+
+def test_binding_refuses_arrays_of_other_types_and_sizes():
+    """int64 tokens, one row of numbers for the whole batch, slices of wider arrays."""
+    import torch
+
+    p = _params(batch=4, n_q=3)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    good = dict(tokens=i(4, 2), counts=i(4), u=torch.zeros(4, 3), ctx=i(4))
+
+    def verify(**change):
+        a = {**good, **change}
+        dsa.verify_draft(p, torch.rand(4, 3, 9), torch.rand(4, 2, 9), a["tokens"], a["counts"], a["u"], a["ctx"], i(4), i(4, 3),
+                         i(4), i(1))
+
+    for name, bad in (("tokens", i(4, 2).long()), ("tokens", i(1, 2).expand(4, 2)), ("tokens", i(4, 3)[:, :2]),
+                      ("tokens", i(3, 2)), ("counts", i(4).long()), ("counts", i(1).expand(4)), ("counts", i(3)),
+                      ("u", torch.zeros(1, 3).expand(4, 3)), ("u", torch.zeros(4, 3).double()), ("u", torch.zeros(4, 2)),
+                      ("u", torch.zeros(3, 4).t()), ("ctx", i(4).float()), ("ctx", i(8)[::2])):
+        with pytest.raises(ValueError, match="verify_draft: "):
+            verify(**{name: bad})
+    for src, dst in ((i(2).long(), i(2)), (i(2), i(1).expand(2)), (i(4)[::2], i(2))):
+        with pytest.raises(ValueError, match="pages_fork: "):
+            dsa.pages_fork(p, src, dst, None, None, None, i(1))
+    for new in (i(4).long(), i(3), i(1).expand(4)):
+        with pytest.raises(ValueError, match="pages_resize: "):
+            dsa.pages_resize(p, new, dsa.make_pools([]), None, None, None, i(1))
