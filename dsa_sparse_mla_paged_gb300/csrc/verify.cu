@@ -314,8 +314,10 @@ __global__ void __launch_bounds__(kVThreads, kVPerSM) verify_kernel(const __grid
           flags |= DSA_DEVERR_DRAFT;
           pass = false;
         } else {
-          const float p = as_float(P[(size_t(b) * a.n_q + i) * in.p_stride + x]);
-          const float q = Q ? as_float(Q[(size_t(b) * most + i) * in.q_stride + x]) : 1.f;
+          float p = as_float(P[(size_t(b) * a.n_q + i) * in.p_stride + x]);
+          float q = Q ? as_float(Q[(size_t(b) * most + i) * in.q_stride + x]) : 1.f;
+          if (!(p >= 0.f && p <= 1.f)) flags |= DSA_DEVERR_PROB, p = 0.f;
+          if (!(q >= 0.f && q <= 1.f)) flags |= DSA_DEVERR_PROB, q = 0.f;
           pass = double(in.uniforms[size_t(b) * a.n_q + i]) * double(q) < double(p);
         }
       }

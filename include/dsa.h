@@ -450,10 +450,11 @@ typedef enum { DSA_PROB_F32 = 0, DSA_PROB_BF16 = 1, DSA_PROB_F16 = 2 } dsa_prob_
  *   out_tokens   int32 [B, n_q]: the a accepted drafts, the next token, then -1
  *   new_lens     int32 [B] or NULL (needs ctx_lens): ctx_b - n_q + 1 + a, what is left of the
  *                context, as dsa_pages_resize takes it
- * Entries outside [0, 1] (NaN among them) count as 0 and set DSA_DEVERR_PROB, and so do
- * weights that sum to 0 or to more than 4, where the next token is -1. A draft token
- * out of [0, vocab) does not pass; it and a count outside [0, n_q - 1] (clamped) set DSA_DEVERR_DRAFT;
- * ctx_b < n_q gives new_lens -1 and DSA_DEVERR_CTX. A last uniform number outside [0, 1) is clamped into it. */
+ * Entries outside [0, 1] (NaN among them), in the draft tests and in the rows drawn from, count as 0
+ * and set DSA_DEVERR_PROB, and so do weights that sum to 0 or to more than 4, where the next token is -1.
+ * A draft token out of [0, vocab) does not pass; it and a count outside [0, n_q - 1] (clamped) set
+ * DSA_DEVERR_DRAFT; ctx_b < n_q gives new_lens -1 and DSA_DEVERR_CTX. A last uniform number outside
+ * [0, 1) is clamped into it. */
 dsa_status_t dsa_verify_draft(const dsa_params_t* params, int32_t vocab, int32_t dtype, const void* p_target,
                               int64_t p_stride, const void* p_draft, int64_t q_stride, const int32_t* draft_tokens,
                               const int32_t* n_draft, const float* uniforms, const int32_t* ctx_lens,

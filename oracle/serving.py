@@ -169,7 +169,7 @@ def verify_draft(target, draft, tokens, n_draft, uniforms, ctx):
         if not 0 <= k <= n_q - 1:
             err |= ERR_DRAFT
             k = min(max(k, 0), n_q - 1)
-        # a token out of range is reported even behind a rejected draft of the same 32
+        # a token out of range, or an entry that is no probability, is reported even behind a rejected draft of the same 32
         a = k
         for i in range(k):
             x = int(tokens[b, i])
@@ -177,8 +177,11 @@ def verify_draft(target, draft, tokens, n_draft, uniforms, ctx):
                 err |= ERR_DRAFT
                 a = min(a, i)
                 continue
-            q = 1.0 if draft is None else float(draft[b, i, x])
-            if not float(uniforms[b, i]) * q < float(target[b, i, x]):
+            p, q = float(target[b, i, x]), 1.0 if draft is None else float(draft[b, i, x])
+            if not (0 <= p <= 1 and 0 <= q <= 1):
+                err |= ERR_PROB
+                p, q = (v if 0 <= v <= 1 else 0.0 for v in (p, q))
+            if not float(uniforms[b, i]) * q < p:
                 a = min(a, i)
         p = [_units(float(v)) for v in target[b, a]]
         q = [0] * V

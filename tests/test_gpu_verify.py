@@ -228,3 +228,25 @@ def test_rows_beyond_four_gigabytes():
     ref = S.verify_draft(target.double().numpy(), draft.double().numpy(), tokens, None, u, np.full(5, 70))
     for g, r in zip(got, ref):
         assert np.array_equal(g, r)
+
+
+@pytest.mark.parametrize("dtype", NAMES)
+def test_entries_that_are_no_probabilities_in_the_draft_tests(dtype):
+    """What a draft is tested with counts as 0 like any other entry outside [0, 1]: in p it does not pass, in q it
+    does, and both are reported."""
+    import torch
+
+    rng = np.random.default_rng(31)
+    for bad in (float("inf"), 1.5, float("nan"), -0.25):
+        for where in ("p", "q"):
+            target, draft, tokens = _rows(rng, 4, 4, 200, dtype)
+            t, d = target.clone(), draft.clone()
+            for b, i in ((0, 0), (1, 1), (2, 2)):
+                (t if where == "p" else d)[b, i, int(tokens[b, i])] = bad
+            u = np.full((4, 4), 2.0 ** -10, np.float32)
+            acc, _, _, bits = _check(t, d, tokens, None, u, np.full(4, 60))
+            assert bits == S.ERR_PROB
+            if where == "p":
+                assert acc[0] == 0 and acc[1] <= 1 and acc[2] <= 2
+            if where == "p":
+                assert _check(t, None, tokens, None, u, np.full(4, 60))[3] == S.ERR_PROB

@@ -119,6 +119,18 @@ def test_verify_edges():
     assert S.verify_draft(t, d, [[0]], None, [[0.5, 0.5]], [70])[1].tolist() == [[2, -1]]
 
 
+def test_entries_that_are_no_probabilities_count_as_zero_in_the_draft_tests():
+    for bad in (np.inf, 1.5, np.nan, -0.25):
+        t, d = np.full((1, 2, 4), 0.25), np.full((1, 1, 4), 0.25)
+        t[0, 0, 2] = bad  # p(x) counts as 0: the draft does not pass
+        acc, out, _, err = S.verify_draft(t, d, [[2]], None, [[0.0, 0.5]], [70])
+        assert acc[0] == 0 and err == S.ERR_PROB and out[0, 0] in (0, 1, 3)
+        t, d = np.full((1, 2, 4), 0.25), np.full((1, 1, 4), 0.25)
+        d[0, 0, 2] = bad  # q(x) counts as 0: u q < p holds
+        acc, out, _, err = S.verify_draft(t, d, [[2]], None, [[0.9375, 0.5]], [70])
+        assert acc[0] == 1 and err == S.ERR_PROB and out[0].tolist() == [2, 2]
+
+
 def test_prefix_mla_is_dense_attention():
     inp = gen.make_inputs(2, 2, [200, 150], seed=3, bt_mode="permuted")
     pages = inp.block_table[0, :1].copy()
