@@ -56,7 +56,7 @@ struct PagesArgs {
   int32_t* from;   // [batch] page to copy before it is written, -1 none; fork: pairs with this source
   int32_t* list;   // [num_pages] free pages by rank; compact: destinations
   int32_t* list2;  // [num_pages] compact: live pages by rank
-  int32_t* rank;   // [num_pages] compact: rank of a live page, -1 free
+  int32_t* rank;   // [num_pages] compact: rank of a live page, -1 free; resize: whether the call found it live
   int32_t* err;
   int batch, max_pages, cap, num_pages, n;
 };
@@ -108,6 +108,9 @@ __device__ void plan_requests(const PagesArgs& a, long long* warp_sums) {
             if (pg < 0 || pg >= a.num_pages) {
               atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
               need = -1;
+            } else if (a.refs[pg] < 1) {  // a free page, which another request may get
+              atomicOr(a.err, DSA_DEVERR_PAGES);
+              need = -1;
             } else if (a.refs[pg] > 1) {
               from = pg;
               ++need;
@@ -130,8 +133,8 @@ __device__ void plan_requests(const PagesArgs& a, long long* warp_sums) {
   }
 }
 
-// Ranks the pages in number order. Resize: list[rank] = free page, and the
-// number of free pages. Compact: rank[p] of every live page (-1 for a free one),
+// Ranks the pages in number order. Resize: list[rank] = free page, the number of
+// free pages, and rank[p], whether p is live. Compact: rank[p] of every live page (-1 for a free one),
 // list2[rank] = live page, list[k] = the k-th free page below the number of live
 // pages, and that number with the rank of the first live page at or above it.
 template <bool kCompact>
@@ -178,6 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kPlanCtas, 1, 1
       if (p == live) a.head[kHdFirstHigh] = li;
     } else {
       if (!is_live) a.list[p - li] = p;
+      a.rank[p] = is_live;
     }
   }
 }
@@ -230,8 +234,10 @@ __global__ void __launch_bounds__(kApplyThreads) pages_resize_kernel(const __gri
     }
     for (int j = want + int(threadIdx.x); j < have; j += kApplyThreads) {
       const int pg = row[j];
-      if (pg >= 0 && pg < a.num_pages) drop_ref(a, pg);
-      else atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+      // (a page that was free may be another request's by now: its count is not touched)
+      if (pg < 0 || pg >= a.num_pages) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+      else if (a.rank[pg]) drop_ref(a, pg);
+      else atomicOr(a.err, DSA_DEVERR_PAGES);
       row[j] = -1;
     }
     __syncthreads();  // every thread has read ctx[b]

@@ -385,9 +385,9 @@ typedef struct {
  *   every later one that needs pages keep their length, and
  *   DSA_DEVERR_NO_PAGES is set.
  * A request with ctx_b or new_lens[b] above max_pages_per_req * 64, or with a
- * negative ctx_b (DSA_DEVERR_CTX), or whose partly filled page is a bad entry
- * (DSA_DEVERR_BLOCK_TABLE), keeps its length; bad entries that are released are
- * skipped. */
+ * negative ctx_b (DSA_DEVERR_CTX), keeps its length, and so does one that grows and
+ * whose partly filled page is a bad entry (DSA_DEVERR_BLOCK_TABLE) or has no references
+ * (DSA_DEVERR_PAGES); such entries that are released are skipped. */
 dsa_status_t dsa_pages_resize(const dsa_params_t* params, const int32_t* new_lens, const dsa_page_pool_t* pools,
                               int32_t n_pools, int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, void* ws,
                               size_t ws_bytes, cudaStream_t stream);

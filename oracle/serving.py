@@ -49,7 +49,7 @@ def pages_resize(table, ctx, refs, new_lens, pools):
     """One request after another, in place. Returns the error bits."""
     err, cap = 0, table.shape[1] * PAGE
     start, state = refs.copy(), "ok"
-    free = [p for p in range(len(refs)) if refs[p] == 0]
+    free = [p for p in range(len(refs)) if refs[p] <= 0]
     for b, new in enumerate(new_lens):
         old = int(ctx[b])
         if new < 0:
@@ -62,7 +62,7 @@ def pages_resize(table, ctx, refs, new_lens, pools):
                 pg = table[b, j]
                 if not 0 <= pg < len(refs):
                     err |= ERR_BLOCK_TABLE
-                elif refs[pg] <= 0:
+                elif start[pg] <= 0 or refs[pg] <= 0:
                     err |= ERR_PAGES
                 else:
                     refs[pg] -= 1
@@ -74,6 +74,9 @@ def pages_resize(table, ctx, refs, new_lens, pools):
             copy = int(table[b, old // PAGE])
             if not 0 <= copy < len(refs):
                 err |= ERR_BLOCK_TABLE
+                continue
+            if start[copy] <= 0:
+                err |= ERR_PAGES
                 continue
             if start[copy] <= 1:
                 copy = -1

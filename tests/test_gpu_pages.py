@@ -146,6 +146,20 @@ def test_resize_bad_state_and_arguments():
     s.check(bits)
 
 
+def test_resize_leaves_pages_without_references_alone():
+    s = State([100, 64, 64], pools=POOLS, spare=5)
+    s.refs[s.table[0, 1]] = 0                       # an open page that is free: nothing is appended to it
+    s.upload()
+    _resize(s, [101, 65, 0])
+    assert s.ctx.tolist() == [100, 65, 0]
+    for lens, new in (([64, 100], [65, 0]), ([100, 64], [0, 65])):
+        s = State(lens, pools=POOLS, num_pages=3)
+        s.refs[s.table[lens.index(100), 1]] = -2    # released, and handed out by the same call
+        s.upload()
+        _resize(s, new)
+        assert sorted(s.refs.tolist()) == [0, 1, 1]
+
+
 def test_resize_without_pools_and_with_negative_length():
     s = State([100, 70], 64, pools=(), spare=10).upload()
     _resize(s, [200, 0])

@@ -65,6 +65,23 @@ def test_resize_without_enough_pages_serves_a_prefix_of_the_requests():
     _check(table, ctx, refs)
 
 
+def test_resize_leaves_pages_without_references_alone():
+    # request 0's open page has no references: it is free, and another request may get it
+    table, ctx, refs, pools = _state([100, 64, 64], num_pages=8)
+    lost = table[0, 1]
+    refs[lost] = 0
+    first = min(p for p in range(8) if refs[p] == 0)
+    assert S.pages_resize(table, ctx, refs, [101, 65, 0], pools) == S.ERR_PAGES
+    assert ctx.tolist() == [100, 65, 0] and table[1, 1] == first and refs[first] == 1
+    # released, and handed out by the same call: the new holder keeps it, in either order
+    for lens, new in (([64, 100], [65, 0]), ([100, 64], [0, 65])):
+        table, ctx, refs, pools = _state(lens, num_pages=3)
+        lost = table[lens.index(100), 1]
+        refs[lost] = 0
+        assert S.pages_resize(table, ctx, refs, new, pools) == S.ERR_PAGES
+        assert table[lens.index(64), 1] == lost and refs[lost] == 1
+
+
 def test_fork_refuses_taken_slots():
     table, ctx, refs, pools = _state([100, 0, 0, 50])
     err = S.pages_fork(table, ctx, refs, [0, 0, 3, 0, 9], [1, 1, 2, 3, 2])
