@@ -62,6 +62,11 @@ dsa_status_t check_mla_args(const void* q, const void* lat_pool, const int32_t* 
   return DSA_OK;
 }
 
+// The page operations' loops over the pages count in 32 bits, past the end by a block's stride.
+dsa_status_t check_page_count(const dsa_params_t* p) {
+  return p->num_pages > (1 << 30) ? DSA_ERR_UNSUPPORTED : DSA_OK;
+}
+
 dsa_status_t check_pools(const dsa_page_pool_t* pools, int32_t n_pools) {
   if (n_pools < 0 || (n_pools > 0 && !pools)) return DSA_ERR_INVALID;
   if (n_pools > kMaxPools) return DSA_ERR_UNSUPPORTED;
@@ -250,6 +255,7 @@ dsa_status_t dsa_pages_resize(const dsa_params_t* params, const int32_t* new_len
   dsa_status_t s = check_params(params);
   if (s != DSA_OK) return s;
   if (!new_lens || !block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  if ((s = check_page_count(params)) != DSA_OK) return s;
   if ((s = check_pools(pools, n_pools)) != DSA_OK) return s;
   WsLayout L;
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
@@ -264,6 +270,7 @@ dsa_status_t dsa_pages_fork(const dsa_params_t* params, int32_t n, const int32_t
   if (s != DSA_OK) return s;
   if (n < 0 || n > params->batch || (n > 0 && (!src || !dst))) return DSA_ERR_INVALID;
   if (!block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  if ((s = check_page_count(params)) != DSA_OK) return s;
   WsLayout L;
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
   if (n == 0) return DSA_OK;
@@ -277,6 +284,7 @@ dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t
   dsa_status_t s = check_params(params);
   if (s != DSA_OK) return s;
   if (!block_table || !ctx_lens || !page_refs) return DSA_ERR_INVALID;
+  if ((s = check_page_count(params)) != DSA_OK) return s;
   if ((s = check_pools(pools, n_pools)) != DSA_OK) return s;
   WsLayout L;
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;

@@ -362,7 +362,8 @@ dsa_status_t dsa_prefix_mla_decode(const dsa_params_t* params, const void* q, co
  *               address: keys, latents, those of every layer. Page p of a pool
  *               is page_bytes at base + p * page_stride (base 16-B aligned,
  *               sizes multiples of 16, page_bytes <= page_stride)
- * The calls change block_table, ctx_lens and page_refs in place. */
+ * At most 2^30 pages (DSA_ERR_UNSUPPORTED). The calls change block_table, ctx_lens and
+ * page_refs in place. */
 typedef struct {
   void* base;
   int64_t page_bytes;

@@ -195,3 +195,11 @@ def test_binding_refuses_arrays_of_other_types_and_sizes():
     for new in (i(4).long(), i(3), i(1).expand(4)):
         with pytest.raises(ValueError, match="pages_resize: "):
             dsa.pages_resize(p, new, dsa.make_pools([]), None, None, None, i(1))
+
+
+def test_page_operations_limit_the_number_of_pages(lib):
+    """Their page loops count in 32 bits."""
+    for n, status in ((1 << 30, WORKSPACE), ((1 << 30) + 1, UNSUPPORTED), (2 ** 31 - 1, UNSUPPORTED)):
+        p = _params(num_pages=n)
+        for fn, args in (("dsa_pages_resize", RESIZE), ("dsa_pages_compact", COMPACT), ("dsa_pages_fork", FORK)):
+            assert _call(fn, p, args, bytes=0) == status, (fn, n)
