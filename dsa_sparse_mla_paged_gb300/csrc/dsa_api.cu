@@ -306,8 +306,9 @@ dsa_status_t dsa_verify_draft(const dsa_params_t* params, int32_t vocab, int32_t
   if (p_draft && ((reinterpret_cast<uintptr_t>(p_draft) & mis) || q_stride < vocab)) return DSA_ERR_INVALID;
   if (params->n_q > 1 && !draft_tokens) return DSA_ERR_INVALID;
   if (!uniforms || !n_accepted || !out_tokens || (new_lens && !ctx_lens)) return DSA_ERR_INVALID;
-  WsLayout L;
-  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  const WsLayout L = ws_layout(*params);
+  if (!ws || !aligned16(ws)) return DSA_ERR_INVALID;
+  if (ws_bytes < L.q8) return DSA_ERR_WORKSPACE;  // the error word is all it uses
   const VerifyIn in{p_target, p_draft, p_stride, q_stride, draft_tokens, n_draft, uniforms, ctx_lens,
                     n_accepted, out_tokens, new_lens, vocab, dtype};
   return cuda_status(launch_verify_draft(*params, L, static_cast<char*>(ws), in, stream));

@@ -72,7 +72,7 @@ struct WsLayout {
   size_t fe_cnt;    // int32 [33][kFeMaxPasses] the front end's arrival counters
   size_t dcp_keys16;  // uint16 [rows][W][S] shard-major score keys, W * S <= cap + 8 * kDcpMaxWorld
   size_t scores;    // float [rows][cap]
-  // the serving operators', behind the decode step's, whose places stay as they were
+  // the serving operators' (in the room of opart, or behind scores)
   size_t pg_head;   // int32 [16] totals of a page operation
   size_t pg_req;    // int32 [3][batch] a page operation's plan per request (or fork pair)
   size_t pg_list;   // int32 [3][num_pages] its page lists
@@ -121,21 +121,40 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   L.fe_cnt = o; o = align256(o + size_t(kIdxHeads + 1) * kFeMaxPasses * 4);
   L.dcp_keys16 = o; o = align256(o + size_t(L.rows) * (size_t(L.cap) + 8 * kDcpMaxWorld) * 2);
   L.scores = o; o = align256(o + size_t(L.rows) * L.cap * 4);
-  L.pg_head = o; o = align256(o + 64);
-  L.pg_req = o; o = align256(o + size_t(3) * p.batch * 4);
-  L.pg_list = o; o = align256(o + size_t(3) * p.num_pages * 4);
+  // The serving operators' scratch holds nothing between calls, and neither do the sparse attention's
+  // partials: the page operations' and the prefix attention's regions each take that room if
+  // they fit (at the full top-k from 8 rows on), else they lie behind the decode step's.
+  const size_t room = L.lpart - L.opart;
+  size_t total = o;
+  auto group = [&](auto layout) {
+    const size_t size = layout(0);
+    const size_t at = size <= room ? L.opart : o;
+    total = at + size > total ? at + size : total;
+    layout(at);
+  };
+  group([&](size_t at) {
+    const size_t from = at;
+    L.pg_head = at; at = align256(at + 64);
+    L.pg_req = at; at = align256(at + size_t(3) * p.batch * 4);
+    L.pg_list = at; at = align256(at + size_t(3) * p.num_pages * 4);
+    return at - from;
+  });
   // the prefix attention's partials: one slot per job (a tile of 128 query
   // heads on the prefix, or a row on its own tokens) and cut between CTA pairs
   L.pfx_tiles = (L.rows * kHeads + kPfxTileRows - 1) / kPfxTileRows;
   L.pfx_jobs = L.pfx_tiles + L.rows;
   L.pfx_slots = L.pfx_jobs + kPfxMaxClusters;
-  L.pfx_q = o; o = align256(o + size_t(L.rows) * kHeads * kDQK * 2);
-  L.pfx_qs = o; o = align256(o + size_t(L.rows) * kHeads * 4);
-  L.pfx_len = o; o = align256(o + size_t(L.rows) * 4);
-  L.pfx_plan = o; o = align256(o + size_t(L.pfx_jobs) * 2 * 4);
-  L.pfx_ml = o; o = align256(o + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
-  L.pfx_part = o; o = align256(o + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
-  L.total = o;
+  group([&](size_t at) {
+    const size_t from = at;
+    L.pfx_q = at; at = align256(at + size_t(L.rows) * kHeads * kDQK * 2);
+    L.pfx_qs = at; at = align256(at + size_t(L.rows) * kHeads * 4);
+    L.pfx_len = at; at = align256(at + size_t(L.rows) * 4);
+    L.pfx_plan = at; at = align256(at + size_t(L.pfx_jobs) * 2 * 4);
+    L.pfx_ml = at; at = align256(at + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
+    L.pfx_part = at; at = align256(at + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
+    return at - from;
+  });
+  L.total = total;
   return L;
 }
 

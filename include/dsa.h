@@ -63,7 +63,7 @@ typedef enum {
   DSA_OK = 0,
   DSA_ERR_INVALID = 1,      /* a null pointer, a bad size or a misaligned buffer */
   DSA_ERR_UNSUPPORTED = 2,  /* a size or format this build does not implement */
-  DSA_ERR_WORKSPACE = 3,    /* ws_bytes below dsa_workspace_size() */
+  DSA_ERR_WORKSPACE = 3,    /* ws_bytes below dsa_workspace_size() (dsa_verify_draft: below 256) */
   DSA_ERR_CUDA = 4,         /* a CUDA launch or runtime call failed */
   DSA_ERR_TIMEOUT = 5       /* a bounded device wait gave up (dsa_get_device_error) */
 } dsa_status_t;
@@ -123,7 +123,9 @@ typedef struct {
 /* Bytes of workspace the calls below need for `params`. The workspace holds
  * the device error word, the quantised indexer query, the top-k candidates,
  * the split-KV partial outputs and (for dsa_decode) the fp32 scores of every
- * row over max_pages_per_req * page_size tokens. */
+ * row over max_pages_per_req * page_size tokens. The scratch of dsa_prefix_mla_decode
+ * and of the page operations shares the room of the partial outputs where it fits (0.6 MB a
+ * row and 21 MB; 12 B a page). */
 dsa_status_t dsa_workspace_size(const dsa_params_t* params, size_t* bytes);
 
 /* Stage 1, the lightning indexer ("K3.1 Pro 中的稀疏注意力"), with the FP8 query
@@ -451,6 +453,7 @@ typedef enum { DSA_PROB_F32 = 0, DSA_PROB_BF16 = 1, DSA_PROB_F16 = 2 } dsa_prob_
  *   out_tokens   int32 [B, n_q]: the a accepted drafts, the next token, then -1
  *   new_lens     int32 [B] or NULL (needs ctx_lens): ctx_b - n_q + 1 + a, what is left of the
  *                context, as dsa_pages_resize takes it
+ *   ws           any workspace of at least 256 bytes: only its error word is used
  * Entries outside [0, 1] (NaN among them), in the draft tests and in the rows drawn from, count as 0
  * and set DSA_DEVERR_PROB, and so do weights that sum to 0 or to more than 4, where the next token is -1.
  * A draft token out of [0, vocab) does not pass; it and a count outside [0, n_q - 1] (clamped) set

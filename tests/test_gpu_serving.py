@@ -193,3 +193,37 @@ def test_a_server_of_speculative_steps(lat_fmt, captured):
     s.resize([0] * B)
     s.same()
     assert (s.refs > 0).sum() == PREFIX // 64
+
+
+def test_operators_between_decode_steps_on_one_workspace():
+    """The fused step, the front end's counters and the serving operators take turns on one workspace whose room they
+    share: every step gives the bits of the first."""
+    import torch
+
+    from dsa_testlib import Dev
+
+    inp = gen.make_inputs(12, 1, [3000, 700, 64, 65, 900, 2300, 128, 1, 400, 2049, 77, 1500], seed=50, bt_mode="permuted")
+    d = Dev(inp)
+    own = dsa.make_params(batch=12, n_q=1, max_pages_per_req=inp.max_pages, num_pages=1, key_page_stride=8448,
+                          lat_page_stride=36864)
+    assert d.ws.numel() == dsa.workspace_size(own)  # no room beyond the decode step's
+    first = [x.clone() for x in d.decode()]
+    z = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device="cuda")
+    table, ctx, refs = z(12, inp.max_pages), z(12), z(inp.num_pages)
+    lens = torch.arange(12, dtype=torch.int32, device="cuda") * 70
+    pools = dsa.make_pools([])
+    out, lse = z(12, 96, 512, dtype=torch.bfloat16), z(12, 96, dtype=torch.float32)
+    target, acc, tok = torch.full((12, 1, 50), 0.02, device="cuda"), z(12), z(12, 1)
+    got = []
+    for _ in range(3):
+        dsa.prefix_mla_decode(d.p, d.q, d.lat_pool, None, 0, d.block_table, d.ctx, out, lse, d.ws)
+        got.append(out.clone())
+        got += [x.clone() for x in d.decode()]
+        dsa.pages_resize(d.p, lens, pools, table, ctx, refs, d.ws)
+        dsa.pages_compact(d.p, pools, table, ctx, refs, None, None, d.ws)
+        got += [out.clone()] + [x.clone() for x in d.decode()]
+        dsa.verify_draft(d.p, target, None, None, None, z(12, 1, dtype=torch.float32), None, acc, tok, None, d.ws[:256])
+    assert dsa.get_device_error(d.ws) == 0
+    for i, x in enumerate(got):
+        assert torch.equal(x, got[0] if i % 4 == 0 else first[i % 4 - 1]), i
+    assert (ctx == lens).all() and (refs > 0).sum() == sum(-(-70 * i // 64) for i in range(12))

@@ -203,3 +203,29 @@ def test_page_operations_limit_the_number_of_pages(lib):
         p = _params(num_pages=n)
         for fn, args in (("dsa_pages_resize", RESIZE), ("dsa_pages_compact", COMPACT), ("dsa_pages_fork", FORK)):
             assert _call(fn, p, args, bytes=0) == status, (fn, n)
+
+
+def _size(batch, n_q, topk, max_pages, num_pages=1000):
+    return dsa.workspace_size(_params(batch=batch, n_q=n_q, topk=topk, max_pages_per_req=max_pages, num_pages=num_pages))
+
+
+@pytest.mark.parametrize("case,size", [  # what the decode step's own regions come to
+    ((8, 1, 2048, 1024), 31335424), ((64, 1, 2048, 1024), 250561536), ((12, 6, 2048, 700), 272677632),
+    ((1, 2048, 2048, 2344), 9083921152), ((256, 8, 2048, 1600), 8482808576)])
+def test_serving_scratch_shares_the_decode_steps_workspace(lib, case, size):
+    assert _size(*case) == size
+    assert _size(*case, num_pages=50000) == size  # the page lists too
+
+
+def test_workspace_of_few_rows(lib):
+    """The prefix attention's partials of 76 CTA pairs do not fit in a few rows' room: 21 MB more."""
+    for case, own in (((1, 1, 2048, 64), 3554304), ((2, 1, 2048, 10), 7047680), ((64, 1, 128, 1024), 45229056)):
+        rows = case[0] * case[1]
+        assert own < _size(*case) <= own + rows * 0.6e6 + 21e6
+
+
+def test_verification_takes_a_workspace_of_its_error_word(lib):
+    p = _params(batch=256, n_q=8, max_pages_per_req=1600)
+    assert _call("dsa_verify_draft", p, VERIFY, bytes=255) == WORKSPACE
+    assert _call("dsa_verify_draft", p, VERIFY, bytes=256, ws=FAKE + 8) == INVALID
+    assert _call("dsa_verify_draft", p, VERIFY, bytes=256, ws=None) == INVALID
