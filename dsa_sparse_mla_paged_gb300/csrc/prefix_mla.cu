@@ -1041,7 +1041,9 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   // 2^-e in two factors: e reaches down to -147
   const int e = m > 0.f && m < INFINITY ? ilogbf(m) - (kNv ? 14 : 7) : 0;
-  const float f0 = scalbnf(1.f, -e / 2), f1 = scalbnf(1.f, -e - (-e / 2));
+  // An infinity makes each logit infinite or NaN, and the softmax NaN: the whole head is NaN
+  // (a saturating conversion would make it finite).
+  const float f0 = m < INFINITY ? scalbnf(1.f, -e / 2) : __uint_as_float(0x7FC00000u), f1 = scalbnf(1.f, -e - (-e / 2));
   if constexpr (kNv) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {

@@ -344,6 +344,7 @@ dsa_status_t dsa_topk_noalloc(const dsa_params_t* params, const float* scores, i
  *                max_pages_per_req * page_size
  *   block_table, ctx_lens, q, lat_pool, out, lse  as dsa_sparse_mla_decode;
  *                ctx_b counts the prefix, and prefix_len + n_q <= ctx_b
+ * A head whose query holds an infinity or a NaN gets NaN in out and lse; the others are not affected.
  * Errors: a row whose ctx_b is out of that range gets out = 0, lse = -inf and
  * DSA_DEVERR_CTX; the tokens of a page outside [0, num_pages) are left out
  * (DSA_DEVERR_BLOCK_TABLE). `topk` and the key fields of params are not used. */

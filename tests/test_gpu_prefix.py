@@ -394,3 +394,27 @@ def test_two_streams_at_once():
     for s in steps:
         for x, y in zip(s, step):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_queries_that_are_not_finite(lat_fmt, value):
+    """Such a head is NaN (an infinite logit makes the softmax NaN), beside small and large other values;
+    the other heads, in its tile and its row, are what they were."""
+    inp, pages = make(3, 2, 192, [70, 3, 130], seed=36, lat_fmt=lat_fmt)
+    d = Dev(inp)
+    hit = [(0, 0, 3, 0), (0, 1, 95, 575), (2, 0, 31, 300), (2, 1, 64, 511)]
+    for b, t, h, i in hit:
+        d.q.view(3, 2, 96, 576)[b, t, h, i] = value
+    d.q.view(3, 2, 96, 576)[2, 0, 31, 7] = 1e30
+    out, lse = launch(d, pages, 192)
+    assert dsa.get_device_error(d.ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b, t, h, _ in hit:
+        assert np.isnan(o[2 * b + t, h]).all() and np.isnan(l[2 * b + t, h]), (b, t, h)
+        # the head's own values of the oracle stand in, so that the row's others can be checked as they are
+        ref, ref_lse = S.prefix_mla(inp, pages, 192, b, t)[:2]
+        o[2 * b + t, h], l[2 * b + t, h] = ref[h], ref_lse[h]
+    for b in range(3):
+        for t in range(2):
+            check_row(inp, pages, 192, b, t, o[2 * b + t], l[2 * b + t])
