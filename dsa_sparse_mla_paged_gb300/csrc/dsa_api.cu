@@ -241,8 +241,7 @@ dsa_status_t dsa_prefix_mla_decode(const dsa_params_t* params, const void* q, co
   if (prefix_len < 0 || prefix_len % params->page_size || (prefix_len > 0 && !prefix_pages)) return DSA_ERR_INVALID;
   if (int64_t(prefix_len) + params->n_q > int64_t(params->max_pages_per_req) * params->page_size)
     return DSA_ERR_INVALID;
-  // a CTA pair counts its tiles in 31 bits
-  if (int64_t(params->batch) * params->n_q * params->max_pages_per_req > (int64_t(1) << 36)) return DSA_ERR_UNSUPPORTED;
+  if (int64_t(params->batch) * params->n_q * params->max_pages_per_req > kPfxMaxTiles) return DSA_ERR_UNSUPPORTED;
   WsLayout L;
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
   return cuda_status(launch_prefix_mla(*params, L, static_cast<char*>(ws), q, lat_pool, prefix_pages, prefix_len,

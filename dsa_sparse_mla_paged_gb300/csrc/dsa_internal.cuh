@@ -46,6 +46,7 @@ constexpr int kFeMaxPasses = kFeMaxRows / 4;
 // pair per two of the GPU's 152 SMs)
 constexpr int kPfxMaxClusters = 76;
 constexpr int kPfxTileRows = 128;  // query heads (row * 96 + head) of one work tile
+constexpr int64_t kPfxMaxTiles = int64_t(1) << 36;  // rows times pages of a call: a CTA pair counts its tiles in 31 bits
 
 // page operations: at most this many pools in a call
 constexpr int kMaxPools = 64;

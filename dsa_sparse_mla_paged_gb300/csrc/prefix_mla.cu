@@ -103,6 +103,15 @@ template <bool kNv>
 constexpr float kPShift = kNv ? 7.f : 6.f;   // weights are 2^(z - max + kPShift), and
 template <bool kNv>
 constexpr float kLazy = kNv ? 8.f : 6.f;     // max is raised when a tile passes it by more than 2^kLazy
+// Poll limit of a wait that may last for a whole run of this many units (for the next rescale or output,
+// for the products with a query). A poll that finds nothing sleeps for 3.9 us (measured) and a tile takes
+// 0.8 to 1.4 us: one poll a unit is enough, and four leave room for a slow clock. The other waits see a few
+// tiles; the default limit gives them 4 s.
+constexpr uint32_t kPolls = 1u << 20;
+__host__ __device__ constexpr uint32_t run_polls(int64_t units) {
+  return units < int64_t(0xFFFFFFFFu - kPolls) / 4 ? kPolls + 4 * uint32_t(units) : 0xFFFFFFFFu;
+}
+static_assert(run_polls(kPfxMaxTiles / kPfxMaxClusters) >= kPfxMaxTiles / kPfxMaxClusters, "the longest run");
 constexpr int kMinUnits = 3;
 constexpr int kJobCost = 4;                  // what a job's start and end take, in tiles (3: 284 us, 4: 275, 5: 276)
 
@@ -534,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on; on = wk.next(a)) {
 #pragma unroll 1
       for (;;) {
-        if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u)) return false;
+        if (!ptx::mbar_wait(ask, uint32_t(asked++) & 1u, run_polls(units))) return false;
         const int what = s_ask;
         // O is up to date, and still, once P . V of the tile before g is done
         const int g = what < 0 ? -1 - what : what;
@@ -835,7 +844,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int jobs = 0;
       auto load_q = [&](int job) {
         if (jobs++ == 0) return first_query(job);
-        auto until = [&] { return ptx::mbar_wait(q_free, uint32_t(jobs - 2) & 1u); };
+        auto until = [&] { return ptx::mbar_wait(q_free, uint32_t(jobs - 2) & 1u, run_polls(units)); };
         return group == 0 ? query_blocks(job, 0, five, q_full, until) : query_blocks(job, 5, four, q_full, until);
       };
       bool on = gtot > 0 && wk.start(a, job0, unit0, units);

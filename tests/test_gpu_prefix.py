@@ -418,3 +418,45 @@ def test_queries_that_are_not_finite(lat_fmt, value):
     for b in range(3):
         for t in range(2):
             check_row(inp, pages, 192, b, t, o[2 * b + t], l[2 * b + t])
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+def test_runs_of_forty_thousand_tiles(lat_fmt):
+    """64 rows on 4 M shared tokens (64 pages, 1,024 times): waits that last for a pair's whole run do not give up.
+    Against the distinct tokens with 1,024 times the weight; 8 products a tile are added to an output,
+    each off by at most 2^-23 of it."""
+    import torch
+
+    from oracle.formats import bf16_decode
+
+    n, times = 64, 1024
+    inp, pages = make(64, 1, n * 64, [1] * 64, seed=37, lat_fmt=lat_fmt)
+    own = inp.block_table[:, n].copy()
+    prefix = n * 64 * times
+    d = Dev(inp)
+    p = dsa.make_params(batch=64, n_q=1, max_pages_per_req=n * times + 1, num_pages=inp.num_pages, key_page_stride=8448,
+                        lat_page_stride=inp.lat_page_stride, lat_fmt=d.p.lat_fmt, softmax_scale=inp.softmax_scale,
+                        latent_scale=inp.latent_scale, topk=1)
+    ws = torch.zeros(dsa.workspace_size(p), dtype=torch.uint8, device="cuda")
+    table = torch.zeros(64, n * times + 1, dtype=torch.int32, device="cuda")
+    table[:, -1] = torch.from_numpy(own).cuda()
+    ctx = torch.full((64,), prefix + 1, dtype=torch.int32, device="cuda")
+    out = torch.empty(64, 96, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(64, 96, dtype=torch.float32, device="cuda")
+    dsa.prefix_mla_decode(p, d.q, d.lat_pool, torch.from_numpy(np.tile(pages, times)).cuda(), prefix, table, ctx, out, lse, ws)
+    assert dsa.get_device_error(ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    inp.block_table[:, :n] = pages
+    adds = 8 * (48 * n * times / 76 + 64) * 2.0 ** -23
+    for b in (0, 31, 63):
+        c = S.O.dequant_latents(inp, b, np.arange(n * 64 + 1))
+        q = bf16_decode(inp.q[b, 0])
+        z = inp.softmax_scale * (q @ c.T) + np.log(np.append(np.full(n * 64, times), 1))
+        top = z.max(axis=1, keepdims=True)
+        want_lse = top[:, 0] + np.log(np.exp(z - top).sum(axis=1))
+        w = np.exp(z - want_lse[:, None])
+        want, mass = w @ c[:, :512], w @ np.abs(c[:, :512])
+        bulk = inp.softmax_scale * (np.abs(q) @ np.abs(c).T).max(axis=1)
+        dz = (66 * 2.0 ** -23 + 2.0 ** -20) * bulk
+        assert (np.abs(l[b] - want_lse) <= dz + adds / 8 + 2.0 ** -19 + 2.0 ** -22 * np.abs(want_lse)).all()
+        assert (np.abs(o[b] - want) <= (2.0 ** -7 + 2 * dz[:, None] + adds) * mass + 2.0 ** -8 * np.abs(want)).all()
