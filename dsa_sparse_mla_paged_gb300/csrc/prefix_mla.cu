@@ -12,13 +12,15 @@
 //
 // Both products take FP8 latents as they lie in the cache, by TMA, and their other operand
 // as the sum of two FP8 parts, which costs what one product in fp16 does: the query as
-// E4M3 + E5M2, which holds a bf16 value's 8 bits, and a softmax weight as E5M2 + E4M3
-// (scaled to at most 2^6, 2^12 until the running maximum is raised), within 2^-8 of
-// it, as bf16 would be, or 2^-16 of the row's largest. (With weights and values in fp16 the
+// E4M3 + E5M2, which holds a bf16 value's 8 bits, and a softmax weight as E4M3 + E5M2 too,
+// within 2^-8 of it, as bf16 would be, or 2^-10 of the largest in its tile. (With weights and values in fp16 the
 // values have to be converted, 96 KB through shared memory per tile beside the 96 KB
 // that the product reads: 1.78 k cycles a tile where 1.03 k are the product's.) NVFP4 latents
 // have six bits a value, too many for E4M3: they are converted to fp16, which holds
-// them exactly, the query and the weights (to 11 bits) too. Sums are fp32 throughout.
+// them exactly, the query and the weights (to 11 bits, or 2^-20 of the tile's largest) too. For that
+// the row's reference exponent follows the tiles down as well as up: after one dominant token
+// (an attention sink), or among many, the others' weights keep their bits, which
+// adds up over the thousands of them. Sums are fp32 throughout.
 //
 // Measured (one GB300): 13 x 2 rows on 262,144 shared tokens 875 us (1.62 PFLOP/s; the
 // clock falls under the power limit, 995 us when it is warm), 64 rows on 32,768 and 1,900 of
@@ -95,14 +97,31 @@ constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
 constexpr int kNumBars = 77;
 template <bool kNv>
 constexpr size_t kData = 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
-static_assert(kData<true> >= 2 * kKBuf + 512 && kData<false> >= 2 * kKBuf + 512, "CTA 0's buffers");
+static_assert(kData<true> >= 2 * kKBuf + 1024 && kData<false> >= 2 * kKBuf + 1024, "CTA 0's buffers");
 template <bool kNv>
 constexpr size_t kSmem = 1024 + kData<kNv> + kNumBars * 8 + 64 + 16;
 static_assert(kSmem<true> + 256 <= 232448 && kSmem<false> + 256 <= 232448, "shared memory, with the static variables");
+// A weight is 2^(z - ref), with a reference per row that is a whole number, so that rescaling is exact.
+// The largest weight of a tile is kept between 2^kLeast and 2^kMost: the segment's first tile puts ref where its
+// largest is in [2^kFirst, 2^(kFirst + 1)), a tile above kMost raises ref to bring it to kRaised, and one below kLeast
+// lowers ref to bring it to kLowered. Both moves are short, as most tiles of a row are alike, and a move
+// by any of a tile's rows costs a rescale of O, about 0.7 us. (FP8, 64 rows on 32,768 tokens with logits of
+// a deviation of 1.3, 2.1, 3.1 and 5.2: 282, 292, 348, 516 us, against 275, 301, 410, 440 when ref
+// only rose, to 2^6 above 2^12, and the weights after a sink lost their bits. A third E5M2
+// part for tiles whose weights are all small, voted on by the four warps: 317, 395, 495, 627.)
+// ref is never more than kTopDrop below the segment's highest, which bounds O and the sums.
 template <bool kNv>
-constexpr float kPShift = kNv ? 7.f : 6.f;   // weights are 2^(z - max + kPShift), and
+constexpr float kFirst = kNv ? 7.f : 2.f;
 template <bool kNv>
-constexpr float kLazy = kNv ? 8.f : 6.f;     // max is raised when a tile passes it by more than 2^kLazy
+constexpr float kMost = kNv ? 15.f : 12.f;
+template <bool kNv>
+constexpr float kRaised = kNv ? 12.f : 8.f;
+template <bool kNv>
+constexpr float kLeast = kNv ? -5.f : -4.f;
+template <bool kNv>
+constexpr float kLowered = kNv ? 4.f : 0.f;
+constexpr float kTopDrop = 40.f;
+constexpr float kLarge = 8.f;                // FP8: the order of a row's two parts changes above 2^kLarge
 // Poll limit of a wait that may last for a whole run of this many units (for the next rescale or output,
 // for the products with a query). A poll that finds nothing sleeps for 3.9 us (measured) and a tile takes
 // 0.8 to 1.4 us: one poll a unit is enough, and four leave room for a slow clock. The other waits see a few
@@ -123,12 +142,12 @@ struct PfxArgs {
   const int32_t* table;
   const int32_t* lens;  // [rows] private tokens that a row sees (0: an invalid context length)
   int32_t* plan;  // [jobs][2] first and last CTA pair of a job
-  float* ml;      // [slots][2 groups][2][128] softmax maxima (base 2) and sums
+  float* ml;      // [slots][2][2][128] references (base 2) and sums: of the group with the last tile, which O has too; the other's
   float* part;    // [slots][512 / 4][128][4] unnormalised outputs
   int* err;
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
-  float scale_log2, lat_scale, shift;
+  float scale_log2, lat_scale;
 };
 
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
@@ -253,16 +272,32 @@ struct TileRegs {
   }
 };
 
-// Four weights as fp16 -> their E5M2 part and the E4M3 part of the rest.
-__device__ __forceinline__ void split_weights(__half2 a, __half2 b, uint32_t& hi, uint32_t& lo) {
+// Four weights as fp16 -> their E4M3 part and the E5M2 part of the rest, for weights up to 2^kLarge. E4M3 is off by half
+// of its step, 2^-4 of the weight, which needs three bits, or by 2^-10 of weights under 2^-6: the two parts
+// together are within 2^-8 of the weight, or 2^-14.
+__device__ __forceinline__ void split_small(uint32_t a, uint32_t b, uint32_t& e5m2, uint32_t& e4m3) {
+  asm("{\n\t.reg .b16 x, y;\n\t.reg .b32 u, v;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 x, %2;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, %3;\n\tmov.b32 %1, {x, y};\n\t"
+      "cvt.rn.f16x2.e4m3x2 u, x;\n\tcvt.rn.f16x2.e4m3x2 v, y;\n\t"
+      "sub.rn.f16x2 u, %2, u;\n\tsub.rn.f16x2 v, %3, v;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 x, u;\n\tcvt.rn.satfinite.e5m2x2.f16x2 y, v;\n\tmov.b32 %0, {x, y};\n\t}\n"
+      : "=r"(e5m2), "=&r"(e4m3)
+      : "r"(a), "r"(b));
+}
+// The other way round, for weights up to 2^kMost: off by 2^-3 of the weight, at most 2^8 (E4M3 ends at 448), and then
+// by 2^-8 of it, or 2^-10.
+__device__ __forceinline__ void split_large(uint32_t a, uint32_t b, uint32_t& e5m2, uint32_t& e4m3) {
   asm("{\n\t.reg .b16 x, y;\n\t.reg .b32 u, v;\n\t"
       "cvt.rn.satfinite.e5m2x2.f16x2 x, %2;\n\tcvt.rn.satfinite.e5m2x2.f16x2 y, %3;\n\tmov.b32 %0, {x, y};\n\t"
       "cvt.rn.f16x2.e5m2x2 u, x;\n\tcvt.rn.f16x2.e5m2x2 v, y;\n\t"
       "sub.rn.f16x2 u, %2, u;\n\tsub.rn.f16x2 v, %3, v;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 x, u;\n\tcvt.rn.satfinite.e4m3x2.f16x2 y, v;\n\tmov.b32 %1, {x, y};\n}\n"
-      : "=&r"(hi), "=r"(lo)
-      : "r"(*reinterpret_cast<const uint32_t*>(&a)), "r"(*reinterpret_cast<const uint32_t*>(&b)));
+      : "=&r"(e5m2), "=r"(e4m3)
+      : "r"(a), "r"(b));
 }
+
+// 2^x of a whole number, exactly; 0 below 2^-126.
+__device__ __forceinline__ float pow2_whole(float x) { return __int_as_float((min(max(int(x), -127), 127) + 127) << 23); }
 
 // What the warps of a CTA need to know of a tile, in a ring that one warp fills.
 struct Tile {
@@ -391,7 +426,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
   uint8_t* KB = sm;
-  float* m_run = reinterpret_cast<float*>(sm + 2 * kKBuf);  // [128] the running maximum in use
+  float* m_run = reinterpret_cast<float*>(sm + 2 * kKBuf);  // [128] the reference in use
+  float* m_top = m_run + 128;                               // [128] the highest of the segment
   // CTA 1
   uint8_t* VB = sm;
   uint8_t* PB = sm + 2 * kVBuf;
@@ -601,7 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
     const int heads = a.rows * kHeads;
-    const bool in = hr < heads;
+    // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too)
+    const bool in = job < a.tiles ? hr < heads : row < kHeads;
     auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -888,7 +925,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int hr = (wk.job < a.tiles ? wk.job * kPfxTileRows : (wk.job - a.tiles) * kHeads) + row;
       const float cs = fmaxf(hr < a.rows * kHeads ? a.scale_log2 * a.qs[hr] : 1.f, 1.1754944e-38f);
       if (g0 == 0) first_query(wk.job);
-      float m_mine = -INFINITY, l = 0.f;  // the maximum that l is relative to
+      float m_mine = -INFINITY, l = 0.f;  // the reference that l is relative to
       const int g1 = g0 + wk.k1 - wk.k0;
 #pragma unroll 1
       for (int g = g0 + ((g0 ^ group) & 1); g < g1; g += 2) {
@@ -920,34 +957,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           t1 = fmaxf(t1, fmaxf(sv[i + 2], sv[i + 3]));
         }
         const float tmax = fmaxf(t0, t1) * cs;
-        // the maximum in use passes from tile to tile
+        // the reference in use passes from tile to tile
         if (g >= 1 && !ptx::mbar_wait(turn + 8 * (w), uint32_t(g - 1) & 1u)) { ok = false; break; }
         const float m_old = g == g0 ? -INFINITY : m_run[row];
-        const bool raise = tmax > m_old + kLazy<kNv>;
-        const float m_use = m_old == -INFINITY || raise ? tmax : m_old;
-        m_run[row] = m_use;
+        float m_use = m_old, alpha = 1.f;
+        bool moved = false;
+        if (__any_sync(0xffffffffu, !(tmax - m_old <= kMost<kNv> && tmax - m_old >= kLeast<kNv>))) {
+          const bool first = m_old == -INFINITY;
+          const float top = first ? -INFINITY : m_top[row];
+          if (first) m_use = floorf(tmax) - kFirst<kNv>;
+          else if (tmax - m_old > kMost<kNv>) m_use = floorf(tmax) - kRaised<kNv>;
+          else if (tmax - m_old < kLeast<kNv> && tmax != -INFINITY) m_use = fmaxf(floorf(tmax) - kLowered<kNv>, top - kTopDrop);
+          m_run[row] = m_use;
+          m_top[row] = fmaxf(top, m_use);
+          if (!first) alpha = pow2_whole(m_old - m_use);
+          moved = __any_sync(0xffffffffu, alpha != 1.f);
+        }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(turn + 8 * (w));
-        const float alpha = raise && m_old != -INFINITY ? ptx::ex2_approx(m_old - m_use) : 1.f;
-        if (m_mine != m_use && m_mine != -INFINITY) l *= ptx::ex2_approx(m_mine - m_use);
+        if (m_mine != m_use && m_mine != -INFINITY) l *= pow2_whole(m_mine - m_use);
         m_mine = m_use;
-        const float off = m_use == -INFINITY ? 0.f : kPShift<kNv> - m_use;
+        const float off = m_use == -INFINITY ? 0.f : -m_use;
         float p0 = 0.f, p1 = 0.f;
         uint32_t pk[32];
-        auto weights = [&](int i) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
           ptx::fma2(sv[2 * i], sv[2 * i + 1], cs, off);
           const float x = ptx::ex2_approx(sv[2 * i]), y = ptx::ex2_approx(sv[2 * i + 1]);
           ptx::add2(p0, p1, x, y);
-          return __floats2half2_rn(x, y);
-        };
+          const __half2 h = __floats2half2_rn(x, y);
+          pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        if constexpr (!kNv) {
+          if (tmax - m_use > kLarge) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const __half2 h0 = weights(i), h1 = weights(i + 1);
-          if constexpr (kNv) {
-            pk[i] = *reinterpret_cast<const uint32_t*>(&h0);
-            pk[i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+            for (int i = 0; i < 32; i += 2) split_large(pk[i], pk[i + 1], pk[i], pk[i + 1]);
           } else {
-            split_weights(h0, h1, pk[i / 2], pk[16 + i / 2]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) split_small(pk[i], pk[i + 1], pk[i], pk[i + 1]);
           }
         }
         l += p0 + p1;
@@ -955,17 +1002,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (g >= kPBufs<kNv> && !ptx::mbar_wait_cluster(p_free + 8 * (pb), uint32_t(g / kPBufs<kNv> - 1) & 1u)) { ok = false; break; }
         const uint32_t dst = p_peer + pb * kPBuf, bar = bar_peer + pb * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          ptx::st_async_f4(dst + i * kPChunk, make_float4(__uint_as_float(pk[4 * i]), __uint_as_float(pk[4 * i + 1]),
-                                                          __uint_as_float(pk[4 * i + 2]), __uint_as_float(pk[4 * i + 3])),
+        for (int i = 0; i < 8; ++i) {
+          // (FP8: the words of the two parts alternate; chunks 0..3 are the E5M2 part's)
+          const int at = kNv ? 4 * i : 8 * (i & 3) + (i >> 2), by = kNv ? 1 : 2;
+          ptx::st_async_f4(dst + i * kPChunk, make_float4(__uint_as_float(pk[at]), __uint_as_float(pk[at + by]),
+                                                          __uint_as_float(pk[at + 2 * by]), __uint_as_float(pk[at + 3 * by])),
                            bar);
+        }
         ptx::st_async_f1(f_peer + pb * kPSide + row * 4, alpha, bar);
-        const bool raised = __any_sync(0xffffffffu, alpha != 1.f);
-        if (lane == 0) ptx::st_async_f1(f_peer + pb * kPSide + 512 + w * 4, __uint_as_float(raised ? 1u : 0u), bar);
+        if (lane == 0) ptx::st_async_f1(f_peer + pb * kPSide + 512 + w * 4, __uint_as_float(moved ? 1u : 0u), bar);
       }
       if (!ok) break;
       g0 = g1;
-      float* ml = a.ml + (size_t(wk.job + clu) * 2 + group) * 256 + row;
+      // (the reference of the segment's last tile is O's)
+      float* ml = a.ml + (size_t(wk.job + clu) * 2 + ((group ^ (g1 - 1)) & 1)) * 256 + row;
       ml[0] = m_mine;
       ml[128] = l;
       if (threadIdx.x == 0) {
@@ -1084,9 +1134,9 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 
 // ---------------------------------------------------------------------------
 // Merge of a row's segments, those of its prefix tile and then those of its private
-// job: with M the largest maximum, out = lat_scale * sum_i 2^(m_i - M) O_i / L and
-// L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums of their own;
-// its O is relative to the larger of their maxima). A warp has 32 heads, a lane each, 16
+// job: with M the largest reference, out = lat_scale * sum_i 2^(m_i - M) O_i / L and
+// L = sum_i 2^(m_i - M) l_i (a segment's two softmax groups have sums and references m of their
+// own; its O has the first one's). A warp has 32 heads, a lane each, 16
 // dims of them and every kSplit-th segment: a row alone has a segment from nearly
 // every pair, many rows have few each. The partial outputs' bytes bound it: 64 rows, 33 MB, 8.1 us;
 // 252 rows, 99 MB, 24 us.
@@ -1129,10 +1179,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = __ldg(o + j * kPfxTileRows);
       const float ma = __ldg(ml), mb = __ldg(ml + 256), la = __ldg(ml + 128), lb = __ldg(ml + 384);
-      const float top = fmaxf(ma, mb), old = m;
-      m = fmaxf(m, top);
+      const float old = m;
+      m = fmaxf(m, fmaxf(ma, mb));
       const float mm = m == -INFINITY ? 0.f : m;
-      const float keep = exp2f(old - mm), w = exp2f(top - mm);
+      const float keep = exp2f(old - mm), w = exp2f(ma - mm);
       tot = fmaf(exp2f(ma - mm), la, fmaf(exp2f(mb - mm), lb, tot * keep));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -1172,7 +1222,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
           make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
     const float mm = m == -INFINITY ? 0.f : m;
-    if (lse && c0 == 0) lse[hr] = tot != 0.f ? (mm - a.shift + log2f(tot)) * 0.6931471805599453f : -INFINITY;
+    if (lse && c0 == 0) lse[hr] = tot != 0.f ? (mm + log2f(tot)) * 0.6931471805599453f : -INFINITY;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * kChunks; i += 32 * kMergeWarps) {
@@ -1209,7 +1259,6 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
   a.lat_scale = p.latent_scale;
-  a.shift = nv ? kPShift<true> : kPShift<false>;
   CUtensorMap kmap, rmap;
   std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
   std::memset(&rmap, 0, sizeof(rmap));

@@ -334,9 +334,11 @@ dsa_status_t dsa_topk_noalloc(const dsa_params_t* params, const float* scores, i
  * head and exact, except for values far below their head's largest: under 2^-13 of it they
  * are off by at most 2^-20 of it (DSA_LAT_FP8_576, where the query is multiplied as an
  * E4M3 and an E5M2 part), or under 2^-32 by 2^-39 (DSA_LAT_NVFP4_352, in fp16). A softmax
- * weight is rounded to fp16's 11 bits, or to 2^-32 of the row's largest (DSA_LAT_NVFP4_352);
- * or it too is multiplied as an E5M2 and an E4M3 part, which together are within 2^-8 of
- * it, as bf16 would be, or within 2^-16 of the row's largest (DSA_LAT_FP8_576).
+ * weight, too, is multiplied as two FP8 parts (DSA_LAT_FP8_576) or in fp16: within 2^-8 (2^-11) of
+ * itself, or else within 2^-10 (2^-20) of the largest weight among the 64 tokens of its page and 2^-16
+ * (2^-32) of the row's largest; weights under 2^-56 of the row's largest may be lost. So a token
+ * that outweighs all others takes bits from those of its own page alone, and out is off by
+ * about 2^-8 (2^-11) of sum_s p_s |c_s|.
  *   prefix_pages int32 [prefix_len / 64] physical pages of the shared tokens
  *                (NULL if prefix_len is 0); rows of block_table need not repeat
  *                them: their first prefix_len / 64 entries are not read

@@ -460,3 +460,135 @@ def test_runs_of_forty_thousand_tiles(lat_fmt):
         dz = (66 * 2.0 ** -23 + 2.0 ** -20) * bulk
         assert (np.abs(l[b] - want_lse) <= dz + adds / 8 + 2.0 ** -19 + 2.0 ** -22 * np.abs(want_lse)).all()
         assert (np.abs(o[b] - want) <= (2.0 ** -7 + 2 * dz[:, None] + adds) * mass + 2.0 ** -8 * np.abs(want)).all()
+
+
+def check_row_by_tiles(inp, pages, prefix, b, t, out, lse):
+    """As check_row, with a bound that is relative to sum p |c| of each dim and says what a weight may lose tile by tile.
+    A weight P = 2^(z - ref) is split as follows (FP8). Rows whose largest in the tile is at most 2^8: E4M3(P) is off by half a
+    step, 2^(e - 4) for P in [2^e, 2^(e + 1)) or 2^-10 for P under 2^-6, and E5M2 of that by an eighth of it at most (half
+    of a step of a quarter), or of a part of it: 2^-8 of P, or 2^-14. Rows above, up to 2^12: E5M2 first, 2^(e - 3), then E4M3: 2^-8
+    of P, or 2^-10. ref is chosen so that a tile's largest is 2^2 or more in a segment's first tile, 2^-4 or more in every
+    other, and a tile's largest above 2^12 brings itself to 2^8; and it is lowered where that is broken, except by more than
+    2^40 in all. So what is not within 2^-8 (and 2^-11, from fp16) of a weight is within 2^-14 / 2^-4 (or 2^-10 / 2^8) of the
+    largest in its tile and 2^-14 / 2^2 of the row's largest, or, past the limit, 2^-14 / 2^42 of it. NVFP4: fp16 leaves 2^-11, or
+    2^-25 with a tile's largest at 2^-5 or more, and 2^7 or more in a segment's first. The fp32 sums: 8 products a tile,
+    each off by at most 2^-23 of the sum so far, and sums are at most sum p |c|."""
+    from oracle.formats import bf16_decode
+
+    table = inp.block_table[b].copy()
+    inp.block_table[b, :prefix // 64] = pages
+    L = S.O.visible_len(inp.ctx[b], inp.n_q, t)
+    c = S.O.dequant_latents(inp, b, np.arange(L))
+    inp.block_table[b] = table
+    q = bf16_decode(inp.q[b, t])
+    z = inp.softmax_scale * (q @ c.T)
+    top = z.max(axis=1, keepdims=True)
+    want_lse = top[:, 0] + np.log(np.exp(z - top).sum(axis=1))
+    p, size = np.exp(z - want_lse[:, None]), np.abs(c[:, :512])
+    want, mass = p @ c[:, :512], p @ size
+    starts = np.arange(0, L, 64)
+    peak, tiles = np.maximum.reduceat(p, starts, axis=1), np.add.reduceat(size, starts, axis=0)
+    low, far, w = (2.0 ** -10, 2.0 ** -16, 2.0 ** -8 + 2.0 ** -11) if inp.lat_fmt == "fp8" else (2.0 ** -20, 2.0 ** -32, 2.0 ** -11)
+    lost = np.minimum(low * peak, far * p.max(axis=1, keepdims=True)) @ tiles + 2.0 ** -56 * p.max(axis=1, keepdims=True) * size.sum(axis=0)
+    dz = (66 * 2.0 ** -23 * inp.softmax_scale * (np.abs(q) @ np.abs(c).T).max(axis=1))[:, None]
+    if inp.lat_fmt == "fp8":  # query values far below their head's largest
+        big = np.abs(q).max(axis=1, keepdims=True)
+        dz += inp.softmax_scale * (np.where(np.abs(q) < 2.0 ** -13 * big, 2.0 ** -20 * big, 0.0) @ np.abs(c).T).max(axis=1)[:, None]
+    adds = 8 * len(starts) * 2.0 ** -23
+    bound = (w + 2 * dz + adds + 2.0 ** -18) * mass + (1 + 2.0 ** -6) * lost + 2.0 ** -8 * np.abs(want) + 2.0 ** -133
+    err = np.abs(out.astype(np.float64) - want)
+    assert np.isfinite(out).all()
+    assert (err <= bound).all(), f"({b}, {t}): {(err / bound).max():.2f} of the bound at {np.unravel_index((err / bound).argmax(), err.shape)}, err/mass {(err / mass).max():.2e}"
+    assert (np.abs(lse - want_lse) <= dz[:, 0] + adds / 8 + 2.0 ** -19 + 2.0 ** -22 * np.abs(want_lse)).all()
+
+
+def put_tokens(inp, pages_of_tokens, slots, level, rows=None):
+    """Latents whose dim 575 (of the logits alone) is `level`, all other values zero, or left as they are with rows."""
+    size = 576 if inp.lat_fmt == "fp8" else 352
+    pool = inp.lat_pool.reshape(-1, inp.lat_page_stride)[:, :64 * size].reshape(-1, 64, size)
+    level = np.broadcast_to(np.asarray(level, np.float64), np.shape(slots))
+    for pg, s, v in zip(np.ravel(pages_of_tokens), np.ravel(slots), np.ravel(level)):
+        row = pool[pg, s]
+        if rows is None:
+            row[:] = 0
+        row[size - 1] = gen.encode_e4m3(np.array([v]))[0]
+
+
+def plain_light(inp, rng, equal):
+    """Every latent: dim 575 zero; equal: the same values for all tokens."""
+    size = 576 if inp.lat_fmt == "fp8" else 352
+    pool = inp.lat_pool.reshape(-1, inp.lat_page_stride)[:, :64 * size].reshape(-1, size)
+    assert np.shares_memory(pool, inp.lat_pool)
+    if equal:
+        pool[:] = pool[int(rng.integers(len(pool)))]
+    pool[:, size - 1] = 0
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("equal", [True, False])
+@pytest.mark.parametrize("gap", [3, 5, 8, 11, 14, 18, 30, 60])
+def test_a_heavy_first_token_whose_own_values_are_zero(lat_fmt, equal, gap):
+    """Attention sinks: one token outweighs each of 16,000 others by e^gap to e^(1.75 gap) (by head), and adds nothing to the
+    output, which is the others' sum. Many rows, so that it shares its segment with thousands of them."""
+    inp, pages = make(40, 1, 16384, [1 + 5 * i for i in range(40)], seed=60 + gap, lat_fmt=lat_fmt)
+    rng = np.random.default_rng(gap)
+    plain_light(inp, rng, equal)
+    put_tokens(inp, pages[:1], [0], 2.0 * gap)
+    inp.softmax_scale = 0.5
+    q = np.zeros((40, 1, 96, 576)) if equal else rng.standard_normal((40, 1, 96, 576)) * 2.0 / 24
+    q[..., 575] = 1 + np.arange(96) / 128
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    d = Dev(inp)
+    out, lse = launch(d, pages, 16384)
+    assert dsa.get_device_error(d.ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in (0, 7, 39):
+        check_row_by_tiles(inp, pages, 16384, b, 0, o[b], l[b])
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("every", [1, 40, 64, 333])
+def test_heavy_tokens_here_and_there(lat_fmt, every):
+    """Heavy tokens without values of their own, of random heights, again and again along each row's own tokens: the
+    weights' reference goes up and down."""
+    inp, pages = make(3, 2, 64, [700, 5000, 1300], seed=80 + every, lat_fmt=lat_fmt)
+    rng = np.random.default_rng(every)
+    plain_light(inp, rng, False)
+    inp.softmax_scale = 0.5
+    for b in range(3):
+        at = np.arange(64, int(inp.ctx[b]))[::every]
+        put_tokens(inp, inp.block_table[b, at // 64], at % 64, rng.uniform(0, 60, len(at)), rows=True if every == 1 else None)
+    q = rng.standard_normal((3, 2, 96, 576)) / 24
+    q[..., 575] = 1 + np.arange(96) / 128
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    d = Dev(inp)
+    out, lse = launch(d, pages, 64)
+    assert dsa.get_device_error(d.ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in range(3):
+        for t in range(2):
+            check_row_by_tiles(inp, pages, 64, b, t, o[2 * b + t], l[2 * b + t])
+
+
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("step", [-30.0, -4.0, -0.7, 0.7, 4.0, 30.0])
+def test_stairs(lat_fmt, step):
+    """Logits that fall or rise by `step` nats from tile to tile, over up to 800: through every threshold, and past the
+    limit of how far the reference is lowered; then one more tile as at the start."""
+    inp, pages = make(2, 1, 64 * 26, [64, 130], seed=90, lat_fmt=lat_fmt)
+    rng = np.random.default_rng(1)
+    plain_light(inp, rng, False)
+    inp.softmax_scale = 1.0
+    levels = step * (np.arange(26) - 13)
+    levels[-1] = levels[0]
+    for pg, v in zip(pages, levels):
+        put_tokens(inp, np.full(64, pg), np.arange(64), v, rows=True)
+    q = rng.standard_normal((2, 1, 96, 576)) / 24
+    q[..., 575] = 1.0
+    inp.q = gen.f32_to_bf16_bits(q.astype(np.float32))
+    d = Dev(inp)
+    out, lse = launch(d, pages, 64 * 26)
+    assert dsa.get_device_error(d.ws) == 0
+    o, l = bf16_to_np(out), lse.cpu().numpy()
+    for b in range(2):
+        check_row_by_tiles(inp, pages, 64 * 26, b, 0, o[b], l[b])
