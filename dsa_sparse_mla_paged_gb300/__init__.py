@@ -253,21 +253,6 @@ def decode(params, q_idx, w, key_pool, q, lat_pool, block_table, ctx_lens, out, 
         _stream(stream)))
 
 
-def prefix_mla_decode(params, q, lat_pool, prefix_pages, prefix_len, block_table, ctx_lens, out, lse, ws,
-                      stream=None):
-    """Dense attention of a batch whose contexts start with the same `prefix_len` tokens
-    (int32 page numbers `prefix_pages`, None without a prefix)."""
-    _check("dsa_prefix_mla_decode", load().dsa_prefix_mla_decode(
-        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _ptr(prefix_pages), int(prefix_len), _ptr(block_table),
-        _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
-
-
-def make_pools(pools):
-    """The page operations' pool list from (tensor or address, page_bytes, page_stride) triples."""
-    pools = list(pools)
-    return (PagePool * max(len(pools), 1))(*[PagePool(_ptr(b), int(n), int(s)) for b, n, s in pools]), len(pools)
-
-
 def _array(fn, name, t, dtype, n):
     """The address of a dense array of at least n elements (int64 tokens, or a row expanded over the
     batch, would be read as something else, or past their end). None and addresses pass."""
@@ -276,6 +261,24 @@ def _array(fn, name, t, dtype, n):
     if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} is not a contiguous {dtype} tensor of {n} elements")
     return t.data_ptr()
+
+
+def prefix_mla_decode(params, q, lat_pool, prefix_pages, prefix_len, block_table, ctx_lens, out, lse, ws,
+                      stream=None):
+    """Dense attention of a batch whose contexts start with the same `prefix_len` tokens
+    (int32 page numbers `prefix_pages`, None without a prefix)."""
+    import torch
+
+    pages = _array("prefix_mla_decode", "prefix_pages", prefix_pages, torch.int32, int(prefix_len) // params.page_size)
+    _check("dsa_prefix_mla_decode", load().dsa_prefix_mla_decode(
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), pages, int(prefix_len), _ptr(block_table),
+        _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def make_pools(pools):
+    """The page operations' pool list from (tensor or address, page_bytes, page_stride) triples."""
+    pools = list(pools)
+    return (PagePool * max(len(pools), 1))(*[PagePool(_ptr(b), int(n), int(s)) for b, n, s in pools]), len(pools)
 
 
 def pages_resize(params, new_lens, pools, block_table, ctx_lens, page_refs, ws, stream=None):

@@ -229,3 +229,12 @@ def test_verification_takes_a_workspace_of_its_error_word(lib):
     assert _call("dsa_verify_draft", p, VERIFY, bytes=255) == WORKSPACE
     assert _call("dsa_verify_draft", p, VERIFY, bytes=256, ws=FAKE + 8) == INVALID
     assert _call("dsa_verify_draft", p, VERIFY, bytes=256, ws=None) == INVALID
+
+
+def test_binding_refuses_page_lists_of_other_types_and_sizes():
+    import torch
+
+    p = _params()
+    for pages in (torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)[::2]):
+        with pytest.raises(ValueError, match="prefix_mla_decode: prefix_pages"):
+            dsa.prefix_mla_decode(p, FAKE, FAKE, pages, 128, FAKE, FAKE, FAKE, None, torch.zeros(1))
