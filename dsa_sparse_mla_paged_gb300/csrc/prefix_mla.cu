@@ -127,10 +127,8 @@ constexpr float kLarge = 8.f;                // FP8: the order of a row's two pa
 // 0.8 to 1.4 us: one poll a unit is enough, and four leave room for a slow clock. The other waits see a few
 // tiles; the default limit gives them 4 s.
 constexpr uint32_t kPolls = 1u << 20;
-__host__ __device__ constexpr uint32_t run_polls(int64_t units) {
-  return units < int64_t(0xFFFFFFFFu - kPolls) / 4 ? kPolls + 4 * uint32_t(units) : 0xFFFFFFFFu;
-}
-static_assert(run_polls(kPfxMaxTiles / kPfxMaxClusters) >= kPfxMaxTiles / kPfxMaxClusters, "the longest run");
+__host__ __device__ constexpr uint32_t run_polls(int units) { return kPolls + 4 * uint32_t(units); }
+static_assert(kPolls + 4 * (kPfxMaxTiles / kPfxMaxClusters) < 0xFFFFFFFFll, "the longest run's limit");
 constexpr int kMinUnits = 3;
 constexpr int kJobCost = 4;                  // what a job's start and end take, in tiles (3: 284 us, 4: 275, 5: 276)
 
@@ -637,8 +635,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
     const int heads = a.rows * kHeads;
-    // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too)
-    const bool in = job < a.tiles ? hr < heads : row < kHeads;
+    // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too. Not for NVFP4, whose
+    // converters have no registers to spare: 215 for 210 us)
+    const bool in = kNv || job < a.tiles ? hr < heads : row < kHeads;
     auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
