@@ -310,11 +310,20 @@ def pages_compact(params, pools, block_table, ctx_lens, page_refs, page_map, liv
         _ptr(live), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
+_PROB_TYPES = {}  # (torch is imported with the first call)
+
+
 def _prob_rows(name, t, rows):
     """(dtype code, row stride) of a tensor of `rows` equally spaced rows of probabilities."""
-    code = {"torch.float32": DSA_PROB_F32, "torch.bfloat16": DSA_PROB_BF16, "torch.float16": DSA_PROB_F16}.get(str(t.dtype))
+    if not _PROB_TYPES:
+        import torch
+
+        _PROB_TYPES.update({torch.float32: DSA_PROB_F32, torch.bfloat16: DSA_PROB_BF16, torch.float16: DSA_PROB_F16})
+    code = _PROB_TYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"verify_draft: {name} is {t.dtype}, not float32, bfloat16 or float16")
+    if t.is_contiguous() and t.numel() == rows * t.shape[-1]:
+        return code, t.shape[-1]
     vocab, even, stride, span = t.shape[-1], t.stride(-1) == 1 or t.shape[-1] == 1, None, 0
     for n, d in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n > 1:
