@@ -22,13 +22,15 @@
 // (an attention sink), or among many, the others' weights keep their bits, which
 // adds up over the thousands of them. Sums are fp32 throughout.
 //
-// Measured (one GB300): 13 x 2 rows on 262,144 shared tokens 875 us (1.62 PFLOP/s; the
-// clock falls under the power limit, 995 us when it is warm), 64 rows on 32,768 and 1,900 of
-// their own 269 us (1.67 PFLOP/s), 24 rows on 8,111 of their own 38 us, one row on 4,096 20 us;
-// NVFP4, 8 x 6 rows on 16,384 and 700 of their own 207 us (0.81 PFLOP/s). An FP8 tile takes about
+// Measured (one GB300, call after call, where the clock falls under the power limit): 13 x 2 rows
+// on 262,144 shared tokens 990 to 1,090 us by the card (1.44 to 1.31 PFLOP/s; 882 us with pauses between
+// calls), 64 rows on 32,768 and 1,900 of their own 297 to 317 us (1.52 to 1.43 PFLOP/s; 282 with pauses),
+// 24 rows on 8,111 of their own 41.5 us, one row on 4,096 20.4 us; NVFP4, 8 x 6 rows on 16,384 and 700
+// of their own 212 us (0.79 PFLOP/s). An FP8 tile takes about
 // 1,430 cycles; the scores' products, at 1,165, bound it, and an NVFP4 tile about 2,600: its
 // K-blocks' stores and products share CTA 0's shared memory (without the stores 152 us,
-// without the arithmetic of the conversion 206).
+// without the arithmetic of the conversion 206). Registers are at their limit of 96: the NVFP4 kernel
+// spills 80 bytes a thread, the FP8 one 8.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
