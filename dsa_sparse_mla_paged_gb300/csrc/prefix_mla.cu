@@ -8,7 +8,7 @@
 // so that a token hidden from a row never enters its products, whatever it holds).
 // The line is cut into equal runs, one per CTA pair, and a run into segments at job
 // borders; each segment leaves an unnormalised partial output with its softmax
-// maximum and sum, and the merge kernel adds up the segments of a row's two jobs.
+// reference and sum, and the merge kernel adds up the segments of a row's two jobs.
 //
 // Both products take FP8 latents as they lie in the cache, by TMA, and their other operand
 // as the sum of two FP8 parts, which costs what one product in fp16 does: the query as
@@ -56,13 +56,13 @@ namespace {
 // 32 KB of fp32 each way per tile; at the 32 B a cycle that an SM takes from
 // another's stores that is 1,024 cycles, and it ran at 3,000 cycles a tile.)
 //   CTA 0: warps 0..3, 4..7  softmax of the even and of the odd tiles: one query head
-//                            per thread; the two groups hand the running maximum on
+//                            per thread; the two groups hand the reference on
 //          warps 8..15       at a new job Q to tensor memory; NVFP4: two groups of
 //                            converters, the page's 64 rows to fp16 (nine K-blocks)
 //          warp  16          MMA of the even tiles: Q from tensor memory (288 columns), S in 3 x 64 columns
 //          warp  17          the tiles' pages for the others; FP8: the rows by TMA, as they are
 //          warp  18          MMA of the odd tiles
-//   CTA 1: warps 0..15       rescale O where the maximum was raised, write O at a job's end.
+//   CTA 1: warps 0..15       rescale O where the reference has moved, write O at a job's end.
 //                            NVFP4: warps 0..3; and 4..15 three groups of converters: the
 //                            512 value dims to fp16 (eight K-blocks of 64 dims, read MN-major)
 //          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
@@ -411,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t k_free = bars + 7 * 8;      // [kKBufs]  S of the buffer's tile is done
   const uint32_t s_full = bars + 11 * 8;     // [kSBufs]
   const uint32_t s_free = bars + 70 * 8;     // [2 kSBufs]  the softmax has read S of a tile (modulo 6)
-  const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's maximum is decided
+  const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's reference is decided
   const uint32_t ring_full = bars + 21 * 8;  // [kRing]
   const uint32_t ring_free = bars + 29 * 8;  // [kRing]
   const uint32_t p_free = bars + 37 * 8;     // [kPBufs]  P . V of the tile in this slot of P is done (CTA 0; NVFP4: both)
@@ -638,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
     const int heads = a.rows * kHeads;
     // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too. Not for NVFP4, whose
-    // converters have no registers to spare: 215 for 210 us)
+    // converters have no registers to spare: 214.7 for 212.8 us)
     const bool in = kNv || job < a.tiles ? hr < heads : row < kHeads;
     auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
