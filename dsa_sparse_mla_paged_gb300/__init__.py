@@ -6,7 +6,8 @@ exceptions. There is no fallback: if libdsa.so is missing, ``load()`` raises.
 
 Entry points mirror include/dsa.h: ``workspace_size``, ``indexer_scores``,
 ``indexer_frontend``, ``indexer_prefill_scores``, ``topk``, ``topk_noalloc``, ``dcp_topk_merge``, ``lse_combine``, ``sparse_mla_decode``,
-``decode``, ``prefix_mla_decode``, ``pages_resize``, ``pages_fork``, ``pages_compact``, ``verify_draft``, ``get_device_error``, ``selftest_wait_timeout``, ``status_string``.
+``decode``, ``prefix_mla_decode``, ``pages_resize``, ``pages_fork``, ``pages_compact``, ``verify_draft``,
+``latent_frontend``, ``window_mla_decode``, ``attention_mass``, ``tokens_evict``, ``get_device_error``, ``selftest_wait_timeout``, ``status_string``.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ DSA_Q_PREPARED = 0x2
 DSA_DEVERR_BLOCK_TABLE, DSA_DEVERR_CTX, DSA_DEVERR_TOPK_INDEX, DSA_DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 DSA_DEVERR_PAGES, DSA_DEVERR_NO_PAGES, DSA_DEVERR_DRAFT, DSA_DEVERR_PROB = 0x10, 0x20, 0x40, 0x80
 DSA_PROB_F32, DSA_PROB_BF16, DSA_PROB_F16 = 0, 1, 2
+DSA_TOKEN_KEY_FP8, DSA_TOKEN_KEY_MXFP4, DSA_TOKEN_LAT_FP8, DSA_TOKEN_LAT_NVFP4 = 0, 1, 2, 3
 
 # Kernels one dsa_decode launches (q quantisation, indexer, top-k, sparse MLA,
 # split combine); kept in step with csrc/.
@@ -44,6 +46,10 @@ EXPORTS = (
     "dsa_pages_fork",
     "dsa_pages_compact",
     "dsa_verify_draft",
+    "dsa_latent_frontend",
+    "dsa_window_mla_decode",
+    "dsa_attention_mass",
+    "dsa_tokens_evict",
     "dsa_get_device_error",
     "dsa_selftest_wait_timeout",
     "dsa_status_string",
@@ -60,6 +66,21 @@ class PagePool(ctypes.Structure):
     """dsa_page_pool_t."""
 
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
+class LatentDims(ctypes.Structure):
+    """dsa_latent_dims_t."""
+
+    _fields_ = [("q_nope_row", ctypes.c_int64), ("q_nope_head", ctypes.c_int64), ("q_rope_row", ctypes.c_int64),
+                ("q_rope_head", ctypes.c_int64), ("c_kv_row", ctypes.c_int64), ("k_rope_row", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("interleaved", ctypes.c_int32)]
+
+
+class TokenPool(ctypes.Structure):
+    """dsa_token_pool_t."""
+
+    _fields_ = [("base", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("layers", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
 class Params(ctypes.Structure):
@@ -136,6 +157,11 @@ def load() -> ctypes.CDLL:
         "dsa_pages_compact": [P, ctypes.POINTER(PagePool), ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp],
         "dsa_verify_draft": [P, ctypes.c_int32, ctypes.c_int32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz,
                              vp],
+        "dsa_latent_frontend": [P, ctypes.POINTER(LatentDims), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_window_mla_decode": [P, vp, vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, vp, vp, sz, vp],
+        "dsa_attention_mass": [P, vp, vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp, i64, vp, sz, vp],
+        "dsa_tokens_evict": [P, vp, ctypes.c_int32, ctypes.c_int32, vp, i64, ctypes.POINTER(TokenPool), ctypes.c_int32, vp, vp,
+                             vp, vp, vp, sz, vp],
         "dsa_get_device_error": [vp, vp, ctypes.POINTER(ctypes.c_int32)],
         "dsa_selftest_wait_timeout": [vp, sz, ctypes.c_uint32, vp],
         "dsa_status_string": [ctypes.c_int],
@@ -357,6 +383,105 @@ def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_len
         _array(name, "n_draft", n_draft, torch.int32, B), _array(name, "uniforms", uniforms, torch.float32, B * n_q),
         _array(name, "ctx_lens", ctx_lens, torch.int32, B),
         _ptr(n_accepted), _ptr(out_tokens), _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _strided(fn, name, t, rows, heads, width):
+    """(address, elements between rows, elements between heads) of a bf16 tensor of `rows` rows (of `heads` heads, 0: none) of
+    `width` values each; its leading dimensions are the rows. None and addresses pass as they are (dense)."""
+    import torch
+
+    if t is None or isinstance(t, int):
+        return t, width * max(heads, 1), width
+    inner = (heads, width) if heads else (width,)
+    lead, strides = t.shape[:t.dim() - len(inner)], t.stride()
+    if t.dtype is not torch.bfloat16 or tuple(t.shape[t.dim() - len(inner):]) != inner or strides[-1] != 1:
+        raise ValueError(f"{fn}: {name} is not a bfloat16 tensor of rows of {' x '.join(map(str, inner))} values")
+    n, row = 1, None
+    for size, d in zip(reversed(lead), reversed(strides[:len(lead)])):
+        if size > 1:
+            if row is not None and d != row * n:
+                raise ValueError(f"{fn}: {name} is not {rows} equally spaced rows")
+            row = d if row is None else row
+            n *= size
+    if n != rows:
+        raise ValueError(f"{fn}: {name} has {n} rows, not {rows}")
+    return t.data_ptr(), row or width * max(heads, 1), strides[-2] if heads else 0
+
+
+def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv_freq, positions, lat_pool, block_table,
+                    ctx_lens, q_out, ws, eps=1e-6, interleaved=True, stream=None):
+    """Norms, rotation, the query [rows, 96, 576] and the new tokens' latents written into lat_pool. `q_nope`
+    [rows, 96, 512], `q_rope` [rows, 96, 64], `c_kv` [rows, 512] and `k_rope` [rows, 64] may be strided (slices of the
+    projections' outputs); `gamma_q` None: no norm of the query; `q_out` None: the cache alone; `c_kv` None: the query alone."""
+    import torch
+
+    fn, rows = "latent_frontend", params.batch * params.n_q
+    dims = LatentDims(eps=eps, interleaved=int(bool(interleaved)))
+    if q_out is not None:
+        q_nope, dims.q_nope_row, dims.q_nope_head = _strided(fn, "q_nope", q_nope, rows, 96, 512)
+        q_rope, dims.q_rope_row, dims.q_rope_head = _strided(fn, "q_rope", q_rope, rows, 96, 64)
+        q_out, gamma_q = _array(fn, "q_out", q_out, torch.bfloat16, rows * 96 * 576), _array(fn, "gamma_q", gamma_q, torch.bfloat16, 512)
+    if c_kv is not None:
+        c_kv, dims.c_kv_row, _ = _strided(fn, "c_kv", c_kv, rows, 0, 512)
+        k_rope, dims.k_rope_row, _ = _strided(fn, "k_rope", k_rope, rows, 0, 64)
+        gamma_kv = _array(fn, "gamma_kv", gamma_kv, torch.bfloat16, 512)
+    _check("dsa_latent_frontend", load().dsa_latent_frontend(
+        ctypes.byref(params), ctypes.byref(dims), _ptr(q_nope), _ptr(q_rope), gamma_q, c_kv, _ptr(k_rope), gamma_kv,
+        _array(fn, "inv_freq", inv_freq, torch.float32, 32), _array(fn, "positions", positions, torch.int32, rows), _ptr(lat_pool),
+        _ptr(block_table), _ptr(ctx_lens), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def window_mla_decode(params, q, lat_pool, sinks, window, block_table, ctx_lens, out, lse, ws, stream=None):
+    """Attention to each row's last `window` tokens and the request's first `sinks`."""
+    _check("dsa_window_mla_decode", load().dsa_window_mla_decode(
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), int(sinks), int(window), _ptr(block_table), _ptr(ctx_lens), _ptr(out),
+        _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _per_token(fn, name, t, dtype, batch):
+    """(address, row stride) of a tensor [batch, tokens]."""
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != batch or t.stride(1) != 1 or (batch > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{fn}: {name} is not a {dtype} tensor [{batch}, tokens]")
+    return t.data_ptr(), t.stride(0) if batch > 1 else t.shape[1], t.shape[1]
+
+
+def attention_mass(params, q, lat_pool, sinks, window, block_table, ctx_lens, lse, fresh, mass, ws, stream=None):
+    """Add the weight that the step's rows give every token to `mass` [B, tokens]; `lse` is the attention's. The
+    last `fresh` tokens of each context are set instead."""
+    import torch
+
+    at, stride, width = _per_token("attention_mass", "mass", mass, torch.float32, params.batch)
+    if width < params.max_pages_per_req * params.page_size:
+        raise ValueError("attention_mass: mass has fewer tokens than the block table's pages")
+    _check("dsa_attention_mass", load().dsa_attention_mass(
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), int(sinks), int(window), _ptr(block_table), _ptr(ctx_lens),
+        _array("attention_mass", "lse", lse, torch.float32, params.batch * params.n_q * 96), int(fresh), at, stride, _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+
+
+def make_token_pools(pools):
+    """tokens_evict's pool list from (tensor or address, DSA_TOKEN_*, layers, layer_stride, page_stride) tuples (bytes)."""
+    pools = list(pools)
+    return (TokenPool * max(len(pools), 1))(*[TokenPool(_ptr(t), int(page), int(layer), int(n), int(fmt))
+                                              for t, fmt, n, layer, page in pools]), len(pools)
+
+
+def tokens_evict(params, budgets, sinks, recent, mass, pools, block_table, ctx_lens, page_refs, kept, ws, stream=None):
+    """Cut every request with more than budgets[b] tokens (negative: as it is) to its first `sinks`, its last `recent` and those
+    of the largest `mass` [B, tokens] between; `pools` from make_token_pools, `kept` int32 [B, tokens] like mass, or None."""
+    import torch
+
+    fn = "tokens_evict"
+    at, stride, width = _per_token(fn, "mass", mass, torch.float32, params.batch)
+    if width < params.max_pages_per_req * params.page_size:
+        raise ValueError("tokens_evict: mass has fewer tokens than the block table's pages")
+    if kept is not None:
+        kept, kept_stride, kept_width = _per_token(fn, "kept", kept, torch.int32, params.batch)
+        if (kept_stride, kept_width) != (stride, width):
+            raise ValueError("tokens_evict: kept and mass differ in shape or strides")
+    _check("dsa_tokens_evict", load().dsa_tokens_evict(
+        ctypes.byref(params), _array(fn, "budgets", budgets, torch.int32, params.batch), int(sinks), int(recent), at, stride,
+        pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs), kept, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def get_device_error(ws, stream=None) -> int:

@@ -80,6 +80,30 @@ dsa_status_t check_pools(const dsa_page_pool_t* pools, int32_t n_pools) {
   return DSA_OK;
 }
 
+// (sizes of a page in a token pool, by dsa_token_fmt_t)
+constexpr int64_t kTokenPage[4] = {kPage * 132, kPage * 68, kPage * 576, kPage * 352};
+
+dsa_status_t check_token_pools(const dsa_params_t* p, const dsa_token_pool_t* pools, int32_t n_pools) {
+  if (n_pools < 0 || (n_pools > 0 && !pools)) return DSA_ERR_INVALID;
+  if (n_pools > kMaxPools) return DSA_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_pools; ++i) {
+    const dsa_token_pool_t& q = pools[i];
+    if (!q.base || !aligned16(q.base) || q.fmt < DSA_TOKEN_KEY_FP8 || q.fmt > DSA_TOKEN_LAT_NVFP4 || q.layers < 1)
+      return DSA_ERR_INVALID;
+    if (q.layers > 4096) return DSA_ERR_UNSUPPORTED;
+    const int64_t page = kTokenPage[q.fmt];
+    if (q.page_stride < page || (q.page_stride & 15)) return DSA_ERR_INVALID;
+    if (q.page_stride > (int64_t(1) << 40) || q.layer_stride > (int64_t(1) << 50)) return DSA_ERR_UNSUPPORTED;
+    if (q.layers == 1) continue;
+    if (q.layer_stride < page || (q.layer_stride & 15)) return DSA_ERR_INVALID;
+    // layers inside a page's row, or pages inside a layer
+    if (q.page_stride < (q.layers - 1) * q.layer_stride + page &&
+        q.layer_stride < (int64_t(p->num_pages) - 1) * q.page_stride + page)
+      return DSA_ERR_INVALID;
+  }
+  return DSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -289,6 +313,90 @@ dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
   return cuda_status(launch_pages_compact(*params, L, static_cast<char*>(ws), pools, n_pools, block_table, ctx_lens,
                                           page_refs, page_map, live, stream));
+}
+
+dsa_status_t dsa_latent_frontend(const dsa_params_t* params, const dsa_latent_dims_t* dims, const void* q_nope,
+                                 const void* q_rope, const void* gamma_q, const void* c_kv, const void* k_rope,
+                                 const void* gamma_kv, const float* inv_freq, const int32_t* positions,
+                                 void* lat_pool, const int32_t* block_table, const int32_t* ctx_lens, void* q_out,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (!dims || !(dims->eps >= 1e-30f) || !(dims->eps <= 1e30f) || (dims->interleaved != 0 && dims->interleaved != 1))
+    return DSA_ERR_INVALID;
+  if ((!q_out && !c_kv) || !inv_freq || !ctx_lens) return DSA_ERR_INVALID;
+  if (!aligned16(inv_freq) || (reinterpret_cast<uintptr_t>(positions) & 3)) return DSA_ERR_INVALID;
+  auto input = [](const void* x, std::initializer_list<int64_t> strides, int64_t least) {
+    if (!x || !aligned16(x)) return false;
+    for (int64_t d : strides)
+      if (d < least || (d & 7) || d > (int64_t(1) << 40)) return false;
+    return true;
+  };
+  if (q_out) {
+    // (rows of heads, or heads of rows)
+    if (!input(q_nope, {dims->q_nope_row, dims->q_nope_head}, kDNope) ||
+        !input(q_rope, {dims->q_rope_row, dims->q_rope_head}, kDRope) || !aligned16(q_out) || !aligned16(gamma_q))
+      return DSA_ERR_INVALID;
+  }
+  if (c_kv) {
+    if (!input(c_kv, {dims->c_kv_row}, kDNope) || !input(k_rope, {dims->k_rope_row}, kDRope) || !input(gamma_kv, {}, 0) ||
+        !input(lat_pool, {}, 0) || !block_table)
+      return DSA_ERR_INVALID;
+  }
+  const WsLayout L = ws_layout(*params);
+  if (!ws || !aligned16(ws)) return DSA_ERR_INVALID;
+  if (ws_bytes < L.q8) return DSA_ERR_WORKSPACE;  // the error word is all it uses
+  const LatentIn in{q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv_freq, positions, lat_pool, block_table, ctx_lens,
+                    q_out, dims->q_nope_row, dims->q_nope_head, dims->q_rope_row, dims->q_rope_head, dims->c_kv_row,
+                    dims->k_rope_row, dims->eps};
+  return cuda_status(launch_latent_frontend(*params, reinterpret_cast<int*>(static_cast<char*>(ws) + L.err), in,
+                                            dims->interleaved == 1, stream));
+}
+
+dsa_status_t dsa_window_mla_decode(const dsa_params_t* params, const void* q, const void* lat_pool, int32_t sinks,
+                                   int32_t window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if ((s = check_mla_args(q, lat_pool, block_table, ctx_lens, out)) != DSA_OK) return s;
+  if (sinks < 0 || window < 1 || (reinterpret_cast<uintptr_t>(lse) & 3)) return DSA_ERR_INVALID;
+  if (int64_t(params->batch) * params->n_q * params->max_pages_per_req > kPfxMaxTiles / 2) return DSA_ERR_UNSUPPORTED;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_window_mla(*params, L, static_cast<char*>(ws), q, lat_pool, sinks, window, block_table, ctx_lens,
+                                       out, lse, stream));
+}
+
+dsa_status_t dsa_attention_mass(const dsa_params_t* params, const void* q, const void* lat_pool, int32_t sinks,
+                                int32_t window, const int32_t* block_table, const int32_t* ctx_lens,
+                                const float* lse, int32_t fresh, float* mass, int64_t mass_stride, void* ws,
+                                size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if ((s = check_mla_args(q, lat_pool, block_table, ctx_lens, mass)) != DSA_OK) return s;
+  if (sinks < 0 || window < 1 || fresh < 0 || !lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return DSA_ERR_INVALID;
+  if (mass_stride < int64_t(params->max_pages_per_req) * params->page_size) return DSA_ERR_INVALID;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_attention_mass(*params, L, static_cast<char*>(ws), q, lat_pool, sinks, window, block_table,
+                                           ctx_lens, lse, fresh, mass, mass_stride, stream));
+}
+
+dsa_status_t dsa_tokens_evict(const dsa_params_t* params, const int32_t* budgets, int32_t sinks, int32_t recent,
+                              float* mass, int64_t token_stride, const dsa_token_pool_t* pools, int32_t n_pools,
+                              int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, int32_t* kept, void* ws,
+                              size_t ws_bytes, cudaStream_t stream) {
+  dsa_status_t s = check_params(params);
+  if (s != DSA_OK) return s;
+  if (!budgets || !mass || !block_table || !ctx_lens || !page_refs || sinks < 0 || recent < 0) return DSA_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(mass) & 3) || (reinterpret_cast<uintptr_t>(kept) & 3)) return DSA_ERR_INVALID;
+  if (token_stride < int64_t(params->max_pages_per_req) * params->page_size) return DSA_ERR_INVALID;
+  if ((s = check_page_count(params)) != DSA_OK) return s;
+  if ((s = check_token_pools(params, pools, n_pools)) != DSA_OK) return s;
+  WsLayout L;
+  if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
+  return cuda_status(launch_tokens_evict(*params, L, static_cast<char*>(ws), budgets, sinks, recent, mass, token_stride, pools,
+                                         n_pools, block_table, ctx_lens, page_refs, kept, stream));
 }
 
 dsa_status_t dsa_verify_draft(const dsa_params_t* params, int32_t vocab, int32_t dtype, const void* p_target,

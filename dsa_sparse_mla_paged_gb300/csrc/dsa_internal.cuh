@@ -83,6 +83,11 @@ struct WsLayout {
   size_t pfx_plan;  // int32 [pfx_jobs][2] first and last CTA pair of each job
   size_t pfx_ml;    // float [pfx_slots][2][2][128] partial softmax maxima and sums
   size_t pfx_part;  // float [pfx_slots][512 / 4][128][4] partial outputs
+  size_t ev_list;   // int32 [batch][cap] eviction: the tokens that stay (in the room of scores)
+  size_t ev_head;   // int64 [4] its totals and its barrier
+  size_t ev_req;    // int64 [batch] first item of a request's moves; then int32 [5][batch] its plan
+  size_t ev_page;   // int32 [batch][max_pages] rank of a page's fresh page among the request's, -1: rewritten in place
+  size_t ev_free;   // int32 [num_pages] free pages by rank
   size_t total;
   int rows, cap, max_chunks, splits, gstride, g128stride;
   int pfx_tiles, pfx_jobs, pfx_slots;
@@ -153,6 +158,17 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
     L.pfx_plan = at; at = align256(at + size_t(L.pfx_jobs) * 2 * 4);
     L.pfx_ml = at; at = align256(at + size_t(L.pfx_slots) * 4 * kPfxTileRows * 4);
     L.pfx_part = at; at = align256(at + size_t(L.pfx_slots) * kPfxTileRows * kDNope * 4);
+    return at - from;
+  });
+  // eviction: its list is as large as one row's scores a request, and takes their room (they, too, hold
+  // nothing between calls)
+  L.ev_list = L.scores;
+  group([&](size_t at) {
+    const size_t from = at;
+    L.ev_head = at; at = align256(at + 32);
+    L.ev_req = at; at = align256(at + size_t(28) * p.batch);
+    L.ev_page = at; at = align256(at + size_t(p.batch) * p.max_pages_per_req * 4);
+    L.ev_free = at; at = align256(at + size_t(p.num_pages) * 4);
     return at - from;
   });
   L.total = total;
@@ -336,6 +352,13 @@ cudaError_t launch_idx_frontend(const dsa_params_t& p, const WsLayout& L, char* 
 cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
                               const int32_t* prefix_pages, int prefix_len, const int32_t* block_table,
                               const int32_t* ctx_lens, void* out, float* lse, cudaStream_t st);
+cudaError_t launch_window_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
+                              int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
+                              float* lse, cudaStream_t st);
+// The query as the dense attention's tensor cores take it (pfx_q, pfx_qs) and each row's visible tokens past
+// `prefix` (pfx_len).
+cudaError_t launch_prefix_query(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const int32_t* ctx_lens,
+                                int prefix, cudaStream_t st);
 cudaError_t launch_pages_resize(const dsa_params_t& p, const WsLayout& L, char* ws, const int32_t* new_lens,
                                 const dsa_page_pool_t* pools, int n_pools, int32_t* block_table, int32_t* ctx_lens,
                                 int32_t* page_refs, cudaStream_t st);
@@ -359,6 +382,30 @@ struct VerifyIn {
   int vocab, dtype;
 };
 cudaError_t launch_verify_draft(const dsa_params_t& p, const WsLayout& L, char* ws, const VerifyIn& in, cudaStream_t st);
+struct LatentIn {
+  const void* q_nope;
+  const void* q_rope;
+  const void* gamma_q;
+  const void* c_kv;
+  const void* k_rope;
+  const void* gamma_kv;
+  const float* inv_freq;
+  const int32_t* positions;
+  void* lat_pool;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  void* q_out;
+  int64_t q_nope_row, q_nope_head, q_rope_row, q_rope_head, c_kv_row, k_rope_row;  // elements
+  float eps;
+};
+cudaError_t launch_latent_frontend(const dsa_params_t& p, int* err, const LatentIn& in, bool interleaved, cudaStream_t st);
+cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
+                                  int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens,
+                                  const float* lse, int fresh, float* mass, int64_t mass_stride, cudaStream_t st);
+cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* ws, const int32_t* budgets, int sinks,
+                                int recent, float* mass, int64_t token_stride, const dsa_token_pool_t* pools, int n_pools,
+                                int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, int32_t* kept,
+                                cudaStream_t st);
 // early: the call follows this library's own kernels in one chain (dsa_decode),
 // so the query and the set-up may be fetched before the wait on the top-k.
 cudaError_t launch_sparse_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q,

@@ -148,14 +148,34 @@ struct PfxArgs {
   int64_t stride;
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
   float scale_log2, lat_scale;
+  int sinks, window;  // (kWin)
 };
 
+// What a row of `len` visible tokens sees through a sliding window: its tokens [0, head) and [first, len), in tiles that
+// are the pages of the first part and then those of the second. (A page that both parts end in is two tiles. Where
+// the parts meet, head is 0 and the second is everything.)
+struct Window {
+  int head, first, n_head, n;
+  __device__ __forceinline__ Window(const PfxArgs& a, int len) {
+    first = max(0, len - a.window);
+    head = a.sinks;
+    if (first <= head) first = head = 0;
+    n_head = (head + kNT - 1) / kNT;
+    n = len > 0 ? n_head + (len + kNT - 1) / kNT - first / kNT : 0;
+  }
+  __device__ __forceinline__ int page(int k) const { return k < n_head ? k : first / kNT + k - n_head; }
+};
+
+// kWin: a sliding window and sinks instead of a shared prefix (every job is a row's).
+template <bool kWin>
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
+  if constexpr (kWin) return Window(a, a.lens[job]).n;
   return job < a.tiles ? a.prefix / kNT : (a.lens[job - a.tiles] + kNT - 1) / kNT;
 }
 
 // A CTA pair's run of the line, segment by segment. The line is measured in units: a
 // job with n > 0 tiles has kJobCost + n, the tiles at its end.
+template <bool kWin>
 struct Walk {
   int job, k0, k1, n;  // the current segment: tiles [k0, k1) of a job of n
   int left;            // units of the run after it
@@ -165,7 +185,7 @@ struct Walk {
     return take(a, unit) || next(a);
   }
   __device__ __forceinline__ bool take(const PfxArgs& a, int unit) {
-    n = job_tiles(a, job);
+    n = job_tiles<kWin>(a, job);
     if (n == 0) return false;
     const int units = min(kJobCost + n - unit, left);
     left -= units;
@@ -221,29 +241,30 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
 
 // A converter thread's share of an NVFP4 tile; warp w of 4 has nope K-blocks 2w and 2w + 1:
 // eight 16-B units (32 values, two scales), and for keys (kRope) two 16-B pieces of the
-// rope dims. Tokens at or past `valid` are zeros: their weights are 0, but their
+// rope dims. Tokens at or past `valid`, or before `from`, are zeros: their weights are 0, but their
 // bytes could be NaN.
 template <bool kRope>
 struct TileRegs {
   uint4 v[2][4];
   uint32_t s[2][4];
   uint4 rope[2];
-  __device__ __forceinline__ void load(const uint8_t* page, int valid, int w, int lane) {
+  __device__ __forceinline__ void load(const uint8_t* page, int from, int valid, int w, int lane) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto in = [&](int tok) { return tok >= from && tok < valid; };
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int tok = u * 16 + (lane >> 1), unit = 4 * w + 2 * b + (lane & 1);
         const uint8_t* row = page + tok * 352;
-        v[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
-        s[b][u] = tok < valid ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
+        v[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
+        s[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
       }
     if constexpr (kRope) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int ct = b * 128 + w * 32 + lane, tok = ct >> 2;
-        rope[b] = tok < valid ? __ldg(reinterpret_cast<const uint4*>(page + tok * 352 + 288 + 16 * (ct & 3))) : zero;
+        rope[b] = in(tok) ? __ldg(reinterpret_cast<const uint4*>(page + tok * 352 + 288 + 16 * (ct & 3))) : zero;
       }
     }
   }
@@ -301,34 +322,45 @@ __device__ __forceinline__ float pow2_whole(float x) { return __int_as_float((mi
 
 // What the warps of a CTA need to know of a tile, in a ring that one warp fills.
 struct Tile {
-  int page, valid;  // physical page, and how many of its tokens the job sees (0 for a bad page)
+  int page, valid;  // physical page, and how many of its tokens the job sees (0 for a bad page); kWin: 256 times
+                    // the first of them added
+  template <bool kWin>
+  __device__ __forceinline__ int from() const { return kWin ? valid >> 8 : 0; }
+  template <bool kWin>
+  __device__ __forceinline__ int to() const { return kWin ? valid & 255 : valid; }
 };
 constexpr int kRing = 8;
 
 // The ring's producer (one warp): 32 page numbers of the walk's job at a time.
 // each(g, tile): what else it does for a tile (lane 0 has just published it).
-template <typename Each>
+template <bool kWin, typename Each>
 __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int unit, int units, int lane, bool report,
                                      Tile* ring, uint32_t full, uint32_t free, Each each) {
-  Walk wk;
+  Walk<kWin> wk;
   int g = 0;
 #pragma unroll 1
   for (bool on = gtot > 0 && wk.start(a, job0, unit, units); on; on = wk.next(a)) {
     const int32_t* list = a.prefix_pages;
     int len = a.prefix;
-    if (wk.job >= a.tiles) {
+    if (kWin || wk.job >= a.tiles) {
       const int r = wk.job - a.tiles;
       list = a.table + size_t(r / a.n_q) * a.max_pages + a.prefix / kNT;
       len = a.lens[r];
     }
+    const Window win(a, len);
     int mine = 0;
 #pragma unroll 1
     for (int k = wk.k0; k < wk.k1; ++k, ++g) {
       const int i = (k - wk.k0) & 31;
-      if (i == 0) mine = k + lane < wk.k1 ? __ldg(list + k + lane) : 0;
+      if (i == 0) mine = k + lane < wk.k1 ? __ldg(list + (kWin ? win.page(k + lane) : k + lane)) : 0;
       const int pg = __shfl_sync(0xffffffffu, mine, i);
       const bool good = pg >= 0 && pg < a.num_pages;
-      const Tile t{good ? pg : 0, good ? min(kNT, len - k * kNT) : 0};
+      int valid = min(kNT, len - k * kNT);
+      if constexpr (kWin) {
+        const int at = win.page(k) * kNT;
+        valid = k < win.n_head ? min(kNT, win.head - at) : min(kNT, len - at) | max(0, win.first - at) << 8;
+      }
+      const Tile t{good ? pg : 0, good ? valid : 0};
       const int slot = g % kRing;
       if (g >= kRing && !ptx::mbar_wait(free + 8 * slot, uint32_t(g / kRing - 1) & 1u)) return false;
       if (lane == 0) {
@@ -347,7 +379,7 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
 // its barriers as in feed; full / free: the buffers' (or halves') barriers; turn: the groups take buffers in the order of their
 // tiles (a group that came early could take a buffer's barrier for one a round older,
 // which has the same parity); after(g): called once tile g is stored.
-template <bool kKeys, int kGroups, typename After>
+template <bool kWin, bool kKeys, int kGroups, typename After>
 __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
                                         uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
                                         uint32_t free, uint32_t turn, After after) {
@@ -358,7 +390,7 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
     const Tile tile = ring[slot];
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
-    t.load(a.lat + int64_t(tile.page) * a.stride, tile.valid, w, lane);
+    t.load(a.lat + int64_t(tile.page) * a.stride, tile.from<kWin>(), tile.to<kWin>(), w, lane);
     return true;
   };
   if (group < gtot && !load(group)) return false;
@@ -395,7 +427,7 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
   return true;
 }
 
-template <bool kNv>
+template <bool kNv, bool kWin>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_mla_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
                       const __grid_constant__ PfxArgs a) {
@@ -487,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int units, gtot;
   {
     auto row_units = [&](int r) {
-      const int n = r < a.rows ? job_tiles(a, a.tiles + r) : 0;
+      const int n = r < a.rows ? job_tiles<kWin>(a, a.tiles + r) : 0;
       return n > 0 ? (long long)(n + kJobCost) : 0ll;
     };
     auto warp_scan = [&](long long v) {
@@ -568,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int job0 = s_job;
   const int unit0 = s_unit;
   bool ok = true;
-  Walk wk;
+  Walk<kWin> wk;
 
   // CTA 1: rescaling and writing columns [c0, c1) of O, one warp of four a quarter of the rows
   auto output = [&](int c0, int c1) {
@@ -628,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // CTA 1, NVFP4, warps 4..15
   auto values = [&]() {
-    return convert<false, 3>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
+    return convert<kWin, false, 3>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
                              [](int) { return true; });
   };
 
@@ -741,7 +773,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = half == 0 ? kKBuf8 : kVBuf8;
       constexpr int kBufs = 4;
       static_assert(kNv || (kKBufs<kNv> == kBufs && kVBufs<kNv> == kBufs), "FP8 buffers");
-      ok = feed(a, gtot, job0, unit0, units, lane, half == 0, ring, ring_full, ring_free, [&](int g, const Tile& t) {
+      ok = feed<kWin>(a, gtot, job0, unit0, units, lane, half == 0, ring, ring_full, ring_free, [&](int g, const Tile& t) {
         if (kNv) return true;
         const int buf = g % kBufs;
         if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
@@ -841,12 +873,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             static_assert(kPBufs<kNv> <= kVBufs<kNv>, "the buffer's last product is done");
             const int slot = g % kRing, buf = g % kVBufs<kNv>;
             if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) { ok = false; break; }
-            const int valid = ring[slot].valid;
+            const int from = ring[slot].template from<kWin>(), valid = ring[slot].template to<kWin>();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
             if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs<kNv>) & 1u)) { ok = false; break; }
+            uint8_t* v = VB + buf * kVBuf8 + (lane >> 3) * kBlk + (lane & 7) * 16;
+            for (int t = 0; t < from; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
             if (valid < kNT) {
-              uint8_t* v = VB + buf * kVBuf8 + (lane >> 3) * kBlk + (lane & 7) * 16;
               for (int t = valid; t < kNT; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
             }
           }
@@ -899,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = queries(-2) && convert<true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
+        ok = queries(-2) && convert<kWin, true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
                                                    queries);
       } else {
 #pragma unroll 1
@@ -937,7 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32_nowait(tmem + lane_base + kSCol + sb * kNT, *reinterpret_cast<float(*)[32]>(&sv[0]));
         ptx::tmem_ld32_nowait(tmem + lane_base + kSCol + sb * kNT + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
         if (!ptx::mbar_wait(ring_full + 8 * (g % kRing), uint32_t(g / kRing) & 1u)) ok = false;
-        const int valid = ring[g % kRing].valid;
+        const int from = ring[g % kRing].template from<kWin>(), valid = ring[g % kRing].template to<kWin>();
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[0]));
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[32]));
         ptx::tc_fence_before();
@@ -947,9 +980,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ptx::mbar_arrive(ring_free + 8 * (g % kRing));
         }
         if (!ok) break;
-        if (valid < kNT) {
+        if (valid < kNT || from > 0) {
 #pragma unroll
-          for (int i = 0; i < kNT; ++i) sv[i] = i < valid ? sv[i] : -INFINITY;
+          for (int i = 0; i < kNT; ++i) sv[i] = i >= from && i < valid ? sv[i] : -INFINITY;
         }
         float t0 = fmaxf(sv[0], sv[1]), t1 = fmaxf(sv[2], sv[3]);
 #pragma unroll
@@ -1235,28 +1268,36 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
 
 }  // namespace
 
-cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
-                              const int32_t* prefix_pages, int prefix_len, const int32_t* block_table,
-                              const int32_t* ctx_lens, void* out, float* lse, cudaStream_t st) {
-  PfxArgs a;
+cudaError_t launch_prefix_query(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const int32_t* ctx_lens,
+                                int prefix, cudaStream_t st) {
+  const int heads = L.rows * kHeads;
+  return launch_pdl(p.lat_fmt == DSA_LAT_NVFP4_352 ? prefix_query_kernel<true> : prefix_query_kernel<false>,
+                    dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0, st,
+                    static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
+                    reinterpret_cast<float*>(ws + L.pfx_qs), ctx_lens, reinterpret_cast<int32_t*>(ws + L.pfx_len), int(p.n_q),
+                    prefix, L.cap, reinterpret_cast<int*>(ws + L.err));
+}
+
+// Query, products, merge. `a` has the prefix or the window.
+template <bool kWin>
+static cudaError_t launch_dense(const dsa_params_t& p, const WsLayout& L, char* ws, PfxArgs a, const void* q,
+                                const void* lat_pool, const int32_t* block_table, const int32_t* ctx_lens, void* out,
+                                float* lse, cudaStream_t st) {
   a.q = reinterpret_cast<const uint4*>(ws + L.pfx_q);
   a.qs = reinterpret_cast<const float*>(ws + L.pfx_qs);
   a.lat = static_cast<const uint8_t*>(lat_pool);
-  a.prefix_pages = prefix_pages;
   a.table = block_table;
-  int32_t* lens = reinterpret_cast<int32_t*>(ws + L.pfx_len);
-  a.lens = lens;
+  a.lens = reinterpret_cast<const int32_t*>(ws + L.pfx_len);
   a.plan = reinterpret_cast<int32_t*>(ws + L.pfx_plan);
   a.ml = reinterpret_cast<float*>(ws + L.pfx_ml);
   a.part = reinterpret_cast<float*>(ws + L.pfx_part);
   a.err = reinterpret_cast<int*>(ws + L.err);
   a.stride = p.lat_page_stride;
-  a.prefix = prefix_len;
   a.n_q = p.n_q;
   a.rows = L.rows;
   a.max_pages = p.max_pages_per_req;
   a.num_pages = p.num_pages;
-  a.tiles = prefix_len > 0 ? L.pfx_tiles : 0;
+  a.tiles = a.prefix > 0 ? L.pfx_tiles : 0;
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
   a.lat_scale = p.latent_scale;
@@ -1272,14 +1313,10 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
         !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  const int heads = L.rows * kHeads;
-  cudaError_t e = launch_pdl(nv ? prefix_query_kernel<true> : prefix_query_kernel<false>,
-                             dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0, st,
-                             static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
-                             reinterpret_cast<float*>(ws + L.pfx_qs), ctx_lens, lens, int(p.n_q), prefix_len, L.cap, a.err);
+  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, a.prefix, st);
   if (e != cudaSuccess) return e;
   const size_t smem = nv ? kSmem<true> : kSmem<false>;
-  auto kern = nv ? prefix_mla_kernel<true> : prefix_mla_kernel<false>;
+  auto kern = nv ? prefix_mla_kernel<true, kWin> : prefix_mla_kernel<false, kWin>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const int clusters = std::max(1, std::min(kPfxMaxClusters, sm_count() / 2));
@@ -1291,6 +1328,24 @@ cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws
   return launch_pdl(split ? prefix_merge_kernel<kMergeWarps> : prefix_merge_kernel<1>,
                     dim3(L.rows, kHeads / 32, kDNope / 4 / (split ? 4 : 4 * kMergeWarps)), dim3(32 * kMergeWarps), 0, st,
                     a, static_cast<__nv_bfloat16*>(out), lse);
+}
+
+cudaError_t launch_prefix_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
+                              const int32_t* prefix_pages, int prefix_len, const int32_t* block_table,
+                              const int32_t* ctx_lens, void* out, float* lse, cudaStream_t st) {
+  PfxArgs a = {};
+  a.prefix_pages = prefix_pages;
+  a.prefix = prefix_len;
+  return launch_dense<false>(p, L, ws, a, q, lat_pool, block_table, ctx_lens, out, lse, st);
+}
+
+cudaError_t launch_window_mla(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
+                              int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
+                              float* lse, cudaStream_t st) {
+  PfxArgs a = {};
+  a.sinks = sinks;
+  a.window = window;
+  return launch_dense<true>(p, L, ws, a, q, lat_pool, block_table, ctx_lens, out, lse, st);
 }
 
 }  // namespace dsa

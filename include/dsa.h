@@ -43,7 +43,7 @@
  *   be ordered (same stream, or synchronised by the caller).
  * - Launch failures return DSA_ERR_CUDA.
  * - Results are deterministic: the same inputs give the same bits, whatever
- *   the batch composition (dsa_prefix_mla_decode: the same call gives the same
+ *   the batch composition (dsa_prefix_mla_decode, dsa_window_mla_decode: the same call gives the same
  *   bits, but how it cuts the contexts depends on the whole batch).
  */
 #ifndef DSA_H_
@@ -63,7 +63,7 @@ typedef enum {
   DSA_OK = 0,
   DSA_ERR_INVALID = 1,      /* a null pointer, a bad size or a misaligned buffer */
   DSA_ERR_UNSUPPORTED = 2,  /* a size or format this build does not implement */
-  DSA_ERR_WORKSPACE = 3,    /* ws_bytes below dsa_workspace_size() (dsa_verify_draft: below 256) */
+  DSA_ERR_WORKSPACE = 3,    /* ws_bytes below dsa_workspace_size() (dsa_verify_draft, dsa_latent_frontend: below 256) */
   DSA_ERR_CUDA = 4,         /* a CUDA launch or runtime call failed */
   DSA_ERR_TIMEOUT = 5       /* a bounded device wait gave up (dsa_get_device_error) */
 } dsa_status_t;
@@ -94,7 +94,7 @@ typedef enum { DSA_LAT_FP8_576 = 0, DSA_LAT_NVFP4_352 = 1 } dsa_lat_fmt_t;
 #define DSA_DEVERR_TOPK_INDEX 0x4   /* a top-k index outside [-1, L_{b,t}) */
 #define DSA_DEVERR_TIMEOUT 0x8      /* a bounded in-kernel wait gave up (results unspecified) */
 #define DSA_DEVERR_PAGES 0x10       /* a refused fork pair, or a reference count below what the tables hold */
-#define DSA_DEVERR_NO_PAGES 0x20    /* dsa_pages_resize: not enough free pages */
+#define DSA_DEVERR_NO_PAGES 0x20    /* dsa_pages_resize, dsa_tokens_evict: not enough free pages */
 #define DSA_DEVERR_DRAFT 0x40       /* dsa_verify_draft: a draft token or count out of range */
 #define DSA_DEVERR_PROB 0x80        /* dsa_verify_draft: a row that is not one of probabilities */
 
@@ -425,6 +425,121 @@ dsa_status_t dsa_pages_fork(const dsa_params_t* params, int32_t n, const int32_t
 dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t* pools, int32_t n_pools,
                                int32_t* block_table, const int32_t* ctx_lens, int32_t* page_refs, int32_t* page_map,
                                int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Strides of the front end's inputs, in elements (multiples of 8). */
+typedef struct {
+  int64_t q_nope_row, q_nope_head; /* between rows, and between a row's heads, of q_nope */
+  int64_t q_rope_row, q_rope_head; /* of q_rope */
+  int64_t c_kv_row, k_rope_row;    /* between rows of c_kv and of k_rope */
+  float eps;                       /* RMS norm epsilon, 1e-30 .. 1e30 */
+  int32_t interleaved;             /* rotation pairs: 1 (2i, 2i + 1), 0 (i, i + 32) */
+} dsa_latent_dims_t;
+
+/* The attention's front end: norms, rotation, the query as the attention takes it, and the new
+ * tokens' latents written into the cache (the index keys are dsa_indexer_frontend's). For row
+ * (b, t), with position p (positions[row], or the token's slot ctx_b - n_q + t without positions)
+ * and angles a_i = p * inv_freq[i], i < 32 (in fp64, so that far positions keep them):
+ *   norm(x) = x * r, r = 1 / sqrt(mean(x^2) + eps) over 512 values; rot(x): each pair (x0, x1) of the
+ *             64 rotary values becomes (x0 cos a_i - x1 sin a_i, x1 cos a_i + x0 sin a_i)
+ *   latent:   v = norm(c_kv) * gamma_kv * (1 / latent_scale) and rot(k_rope) * (1 / latent_scale), in
+ *             fp32 with a rounding after each step (r rounded from fp64), written in lat_fmt to the slot
+ *             of token ctx_b - n_q + t. DSA_LAT_FP8_576: E4M3 codes (nearest even, saturating).
+ *             DSA_LAT_NVFP4_352: per 16 values s = E4M3(amax / 6) and E2M1(v / s) (nearest even,
+ *             saturating, the sign kept; 0 where s is 0); a block with a NaN gets a NaN scale
+ *   query:    per head norm(q_nope) * gamma_q (q_nope itself without gamma_q) and rot(q_rope), bf16
+ * The sums of a query head's squares are fp32: they overflow for values above 2^59.
+ *   q_nope bf16 rows of 96 heads of 512 values, q_rope of 64, by the strides in dims
+ *   c_kv   bf16 rows of 512 values, k_rope of 64; gamma_q, gamma_kv bf16 [512]; inv_freq fp32 [32]
+ *   positions int32 [B * n_q] or NULL
+ *   q_out  bf16 [B * n_q, 96, 576]. It may be the input's own place (q_nope = q_out, q_rope =
+ *          q_out + 512, with q_out's strides); no other overlap
+ * q_out NULL: the cache alone (the query's pointers are not used); c_kv NULL: the query alone.
+ * All of them 16-B aligned but positions (4). ws: any workspace of at least 256 bytes (its error word).
+ * A row with an invalid ctx_b or block-table entry writes no latent and sets DSA_DEVERR_CTX /
+ * DSA_DEVERR_BLOCK_TABLE. */
+dsa_status_t dsa_latent_frontend(const dsa_params_t* params, const dsa_latent_dims_t* dims, const void* q_nope,
+                                 const void* q_rope, const void* gamma_q, const void* c_kv, const void* k_rope,
+                                 const void* gamma_kv, const float* inv_freq, const int32_t* positions,
+                                 void* lat_pool, const int32_t* block_table, const int32_t* ctx_lens, void* q_out,
+                                 void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Attention with a sliding window and sinks: row (b, t) attends to the tokens s < L_{b,t} with
+ * s < sinks or s >= L_{b,t} - window (the window counts the row's own token; if the two meet, the row
+ * attends to all of its tokens). With c_s as in dsa_sparse_mla_decode:
+ *   logit_s = softmax_scale * q_h . c_s;  out[h] = sum_s softmax(logit)_s * c_s[0:512] (bf16, RNE);
+ *   lse[h] = ln sum_s exp(logit_s) (fp32)
+ * in the arithmetic of dsa_prefix_mla_decode. Pages that hold no token that some row sees are not read,
+ * and neither are their block-table entries (a released page's entry may be -1).
+ *   sinks  >= 0, window >= 1
+ *   q, lat_pool, block_table, ctx_lens, out, lse  as dsa_prefix_mla_decode
+ * Errors as dsa_prefix_mla_decode: a row whose ctx_b is out of range gets out = 0, lse = -inf and
+ * DSA_DEVERR_CTX; the tokens of a bad page are left out (DSA_DEVERR_BLOCK_TABLE); a row that sees no good
+ * page gets out = 0, lse = -inf. */
+dsa_status_t dsa_window_mla_decode(const dsa_params_t* params, const void* q, const void* lat_pool, int32_t sinks,
+                                   int32_t window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Accumulated attention weight of every cached token, for eviction (dsa_tokens_evict):
+ *   mass[b][s] += sum over rows t that see s, and heads h, of exp(softmax_scale * q_h . c_s - lse[b,t,h])
+ * where row (b, t) sees what dsa_window_mla_decode lets it see (window >= max_pages_per_req *
+ * page_size: all of its tokens, as dsa_prefix_mla_decode does) and lse is that call's result. The products
+ * are those of that call; the sums are fp32, over the heads and then the rows, in an order that depends
+ * on nothing but the row (the same bits in any batch).
+ * Entries of tokens that no row sees are left as they are. A head whose lse is not finite adds nothing;
+ * a token whose latent holds a NaN gets NaN.
+ *   fresh  >= 0: the last `fresh` tokens of each context (new ones, whose entries hold what an
+ *          earlier token left there) are set instead of added to
+ *   mass   fp32 [B, mass_stride], mass_stride >= max_pages_per_req * page_size
+ * Errors: a request with an invalid ctx_b changes nothing (DSA_DEVERR_CTX); the tokens of a bad page
+ * change nothing (DSA_DEVERR_BLOCK_TABLE). */
+dsa_status_t dsa_attention_mass(const dsa_params_t* params, const void* q, const void* lat_pool, int32_t sinks,
+                                int32_t window, const int32_t* block_table, const int32_t* ctx_lens,
+                                const float* lse, int32_t fresh, float* mass, int64_t mass_stride, void* ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* What a token's row in a pool looks like (the formats above). */
+typedef enum {
+  DSA_TOKEN_KEY_FP8 = 0,
+  DSA_TOKEN_KEY_MXFP4 = 1,
+  DSA_TOKEN_LAT_FP8 = 2,
+  DSA_TOKEN_LAT_NVFP4 = 3
+} dsa_token_fmt_t;
+
+/* A pool whose tokens move: layer l's page p is at base + l * layer_stride + p * page_stride. */
+typedef struct {
+  void* base;           /* 16-B aligned */
+  int64_t page_stride;  /* multiples of 16; layers lie side by side in a page's row ... */
+  int64_t layer_stride; /* ... or each layer has num_pages pages of its own */
+  int32_t layers;       /* 1 .. 4096 */
+  int32_t fmt;          /* dsa_token_fmt_t */
+} dsa_token_pool_t;
+
+/* Evicts tokens: every request b with more tokens than budgets[b] (int32 [batch]; a negative entry
+ * leaves the request as it is) is cut to budgets[b] tokens. It keeps its first s = min(sinks, budget)
+ * tokens, its last r = min(recent, budget - s), and of those between the budget - s - r with the
+ * largest mass (a tie goes to the lower token; -0 == +0, a NaN is below everything). What is kept moves together, in its order: the
+ * rows in every pool, and the masses (those past the new length become 0). Pages before the first evicted
+ * token stay as they are; of the others those with one reference are rewritten in place, and for each with more the
+ * request gets a fresh page (references 1; the shared one loses one), so that no other holder sees a
+ * change. The pages past ceil(new / 64) lose a reference each, and their entries become -1. Fresh pages are the free pages with the lowest
+ * numbers, in the order of the requests and of their pages; pages that this call frees are not handed out by it. If they do
+ * not reach, the first request that does not fit and every later one that needs fresh pages
+ * keep their tokens (DSA_DEVERR_NO_PAGES).
+ * Rotary positions are in the latents: later tokens need dsa_latent_frontend's positions.
+ *   sinks, recent >= 0
+ *   mass    fp32 [B, token_stride], as dsa_attention_mass leaves it; not negative, usually
+ *   pools   host array of n_pools (0 .. 64) pools
+ *   kept    int32 [B, token_stride] or NULL: the old index of each token of the new context
+ *           (the first new-length entries of a row are written; of an unchanged request too)
+ *   token_stride >= max_pages_per_req * page_size
+ *   block_table, ctx_lens, page_refs  as the page operations; at most 2^30 pages
+ * A request with ctx_b out of [0, max_pages_per_req * 64] keeps its tokens (DSA_DEVERR_CTX; its kept is not written), and so
+ * does one that is over its budget with an entry out of range (DSA_DEVERR_BLOCK_TABLE) or without references (DSA_DEVERR_PAGES)
+ * among its pages. */
+dsa_status_t dsa_tokens_evict(const dsa_params_t* params, const int32_t* budgets, int32_t sinks, int32_t recent,
+                              float* mass, int64_t token_stride, const dsa_token_pool_t* pools, int32_t n_pools,
+                              int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs, int32_t* kept, void* ws,
+                              size_t ws_bytes, cudaStream_t stream);
 
 /* Element types of dsa_verify_draft's probabilities. */
 typedef enum { DSA_PROB_F32 = 0, DSA_PROB_BF16 = 1, DSA_PROB_F16 = 2 } dsa_prob_t;
