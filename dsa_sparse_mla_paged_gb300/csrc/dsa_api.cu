@@ -376,6 +376,7 @@ dsa_status_t dsa_attention_mass(const dsa_params_t* params, const void* q, const
   if ((s = check_mla_args(q, lat_pool, block_table, ctx_lens, mass)) != DSA_OK) return s;
   if (sinks < 0 || window < 1 || fresh < 0 || !lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return DSA_ERR_INVALID;
   if (mass_stride < int64_t(params->max_pages_per_req) * params->page_size) return DSA_ERR_INVALID;
+  if (int64_t(params->batch) * params->n_q * params->max_pages_per_req > kPfxMaxTiles / 2) return DSA_ERR_UNSUPPORTED;
   WsLayout L;
   if ((s = check_ws(params, ws, ws_bytes, &L)) != DSA_OK) return s;
   return cuda_status(launch_attention_mass(*params, L, static_cast<char*>(ws), q, lat_pool, sinks, window, block_table,

@@ -1,94 +1,572 @@
-// Accumulated attention weight of every cached token: mass[s] += sum over rows and heads of
-// exp(scale q_h . c_s - lse_h). The simple form: a block per page, its latents in fp32 in shared
-// memory, a thread per token and 24 heads.
-#include <cuda_bf16.h>
+// Accumulated attention weight of every cached token: mass[s] += sum over rows t and heads h of
+// exp(scale q_th . c_s - lse_th), for the tokens that the rows see.
+//
+// It is the dense attention's first product without its second, and its sum runs over the heads, not the tokens. So a
+// token is a row of the product here: S = C . Q^T with 128 tokens (two pages) against a query row's 96 heads,
+// one accumulator lane per token; a thread has one token, and its sum over the heads is its own: no shuffle, no
+// atomic, the same bits in any batch. The query is prepared as for the dense attention (FP8 latents: E4M3 + E5M2,
+// multiplied with the latents as TMA brings them; NVFP4 ones: fp16, the latents converted) and stays in
+// shared memory (110 KB) while tiles of tokens stream past it.
+//
+// The tiles of all requests are a line that is cut into equal runs, one per CTA, and a run into chunks of at most 16
+// tiles of one request. A chunk is gone through once per row (its latents come from L2 after the first), its sums
+// wait in shared memory, and are added to the weights once. The next row's query arrives block by block behind the
+// last tile that uses the old one.
+#include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <cstring>
+
 #include "dsa_internal.cuh"
+#include "sm103_ptx.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kPitch = kDQK + 1;
+constexpr int kTok = 128;                     // tokens of a tile
+constexpr int kStage = kTok * 128;            // 16,384 B: a K-block, 128 rows of 128 B
+constexpr int kStages = 6;
+constexpr int kQChunk = kHeads * 16;          // 1,536 B: 16 B of each head
+constexpr int kQBytes = 72 * kQChunk;
+constexpr int kChunk = 16;                    // tiles of a chunk
+constexpr int kDBufs = 4;                     // accumulators of 128 columns
+template <bool kNv>
+constexpr int kBlocks = kNv ? 9 : 5;          // K-blocks of a tile: 64 dims of fp16; 128 of E4M3, the last 64
+constexpr int kConvWarps = 8;
+template <bool kNv>
+constexpr int kThreads = kNv ? 512 : 256;
+// warps: 0..3 sums, 4 products, 5 latents (FP8), 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
+constexpr int kMmaWarp = 4, kTileWarp = 5, kQueryWarp = 6, kHeadWarp = 7;
+constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * kDBufs + 4 + 1;
+constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
+static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables");
+constexpr uint32_t kPolls = 1u << 20;  // 4 s
 
 struct MassArgs {
-  const __nv_bfloat16* q;
+  const uint8_t* q;   // [72][rows * 96] 16-B chunks of the prepared query
+  const float* qs;    // [rows * 96] its scales
+  const float* lse;   // [rows * 96]
   const uint8_t* lat;
   const int32_t* table;
   const int32_t* ctx;
-  const float* lse;
   float* mass;
   int* err;
   int64_t stride, mass_stride;
-  int n_q, max_pages, cap, num_pages, sinks, window, fresh, nv;
-  float scale;
+  int batch, n_q, max_pages, cap, num_pages, sinks, window, fresh;
+  float scale_log2;
 };
 
-__device__ __forceinline__ float e4m3(uint8_t v) { return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3))); }
+__device__ __forceinline__ int pages_of(int n) { return (n + kPage - 1) / kPage; }
 
-__global__ void __launch_bounds__(256) mass_kernel(MassArgs a) {
-  extern __shared__ float lat[];  // [64][kPitch]
-  __shared__ float part[4][kPage];
-  pdl_wait();
-  const int b = blockIdx.y, n = a.ctx[b];
-  if (n < a.n_q || n > a.cap) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, DSA_DEVERR_CTX);
-    return;
+// The pages that some row of a request with n tokens sees: those of its sinks and those from its first row's window on.
+struct Span {
+  int n, n_head, p0, pages;
+  __device__ __forceinline__ Span(const MassArgs& a, int ctx) {
+    n = ctx >= a.n_q && ctx <= a.cap ? ctx : 0;
+    const int first = max(0, n - a.n_q + 1 - a.window), head = first <= a.sinks ? 0 : a.sinks;
+    n_head = pages_of(head);
+    p0 = head == 0 && first <= a.sinks ? 0 : max(first / kPage, n_head);
+    pages = n > 0 ? n_head + pages_of(n) - p0 : 0;
   }
-  const int tok = threadIdx.x & 63, grp = threadIdx.x >> 6;
-  for (int j = blockIdx.x; j * kPage < n; j += gridDim.x) {
-    const int oldest = max(0, n - a.n_q + 1 - a.window);  // first token of the first row's window
-    if (j * kPage >= a.sinks && (j + 1) * kPage <= oldest) continue;
-    const int pg = a.table[size_t(b) * a.max_pages + j];
-    if (pg < 0 || pg >= a.num_pages) {
-      if (threadIdx.x == 0) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
-      continue;
+  __device__ __forceinline__ int tiles() const { return (pages + 1) / 2; }
+  __device__ __forceinline__ int page(int i) const { return i < n_head ? i : p0 + i - n_head; }
+};
+
+// A CTA's run of the line, chunk by chunk, and the rows that a chunk is gone through for.
+struct Walk {
+  int b, t0, nt, left;  // tiles [t0, t0 + nt) of request b
+  int r0, r1;           // rows [r0, r1] of it see some of them
+  __device__ __forceinline__ void set(const MassArgs& a, const Span& s) {
+    nt = min(min(kChunk, left), s.tiles() - t0);
+    const int lo = s.page(2 * t0) * kPage, hi = min(s.n - 1, s.page(min(2 * (t0 + nt), s.pages) - 1) * kPage + kPage - 1);
+    const int base = s.n - a.n_q;  // row t sees base + t + 1 tokens
+    r0 = max(0, lo - base);
+    r1 = lo < a.sinks ? a.n_q - 1 : min(a.n_q - 1, hi + a.window - base - 1);
+    left -= nt;
+  }
+  __device__ __forceinline__ bool start(const MassArgs& a, int b0, int tile, int tiles) {
+    b = b0;
+    t0 = tile;
+    left = tiles;
+    if (left <= 0) return false;
+    set(a, Span(a, a.ctx[b]));
+    return true;
+  }
+  __device__ __forceinline__ bool next(const MassArgs& a) {
+    if (left <= 0) return false;
+    t0 += nt;
+    if (t0 >= Span(a, a.ctx[b]).tiles()) {
+      t0 = 0;
+      do ++b;
+      while (Span(a, a.ctx[b]).tiles() == 0);
+    }
+    set(a, Span(a, a.ctx[b]));
+    return true;
+  }
+};
+
+// Four E4M3 bytes -> four fp16.
+__device__ __forceinline__ void expand_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// 8 E2M1 values times an E4M3 scale (a pair of fp16): 6 significant bits, exact.
+__device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
+  uint32_t o[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A converter thread's half of a token of an NVFP4 tile: 32 dims of each of eight K-blocks, and of the rotary one.
+struct HalfToken {
+  uint4 v[8], s[2], rope[2];
+  __device__ __forceinline__ void load(const uint8_t* row, int half) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (!row) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = zero;
+      s[0] = s[1] = rope[0] = rope[1] = zero;
+      return;
+    }
+    const uint4* p = reinterpret_cast<const uint4*>(row);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __ldg(p + 2 * j + half);
+    s[0] = __ldg(p + 16);
+    s[1] = __ldg(p + 17);
+    rope[0] = __ldg(p + 18 + 2 * half);
+    rope[1] = __ldg(p + 19 + 2 * half);
+  }
+  template <int kJ>
+  __device__ __forceinline__ void store(uint8_t* blk, int tok, int half) const {
+    uint4 o[4];
+    if constexpr (kJ < 8) {
+      const uint4& q = s[kJ / 4];
+      const uint32_t four = kJ % 4 == 0 ? q.x : kJ % 4 == 1 ? q.y : kJ % 4 == 2 ? q.z : q.w;
+      uint32_t two, none;
+      expand_e4m3(half ? four >> 16 : four, two, none);
+      const __half2 h = *reinterpret_cast<const __half2*>(&two);
+      const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+      o[0] = expand_e2m1(v[kJ].x, s0);
+      o[1] = expand_e2m1(v[kJ].y, s0);
+      o[2] = expand_e2m1(v[kJ].z, s1);
+      o[3] = expand_e2m1(v[kJ].w, s1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        expand_e4m3(rope[i].x, o[2 * i].x, o[2 * i].y);
+        expand_e4m3(rope[i].y, o[2 * i].z, o[2 * i].w);
+        expand_e4m3(rope[i].z, o[2 * i + 1].x, o[2 * i + 1].y);
+        expand_e4m3(rope[i].w, o[2 * i + 1].z, o[2 * i + 1].w);
+      }
+    }
+    uint8_t* at = blk + tok * 128;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(at + (((4 * half + c) ^ (tok & 7)) << 4)) = o[c];
+  }
+};
+
+template <bool kNv>
+__global__ void __launch_bounds__(kThreads<kNv>, 1)
+    mass_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
+                const __grid_constant__ MassArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = ring + kStages * kStage;
+  float* acc = reinterpret_cast<float*>(qbuf + kQBytes);   // [kChunk][128]
+  float* heads = acc + kChunk * kTok;                      // [2][2][96] factors and offsets
+  const uint32_t bars = ptx::smem_u32(heads + 2 * 2 * kHeads);
+  const uint32_t full = bars, free = full + 8 * kStages;                // [kStages]
+  const uint32_t q_full = free + 8 * kStages, q_free = q_full + 8 * 9;  // [kBlocks]
+  const uint32_t d_full = q_free + 8 * 9, d_free = d_full + 8 * kDBufs; // [kDBufs]
+  const uint32_t h_full = d_free + 8 * kDBufs, h_free = h_full + 16;    // [2]
+  const uint32_t mma_done = h_free + 16;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_sum[32], s_b, s_tile, s_bad[2];
+  constexpr int kB = kBlocks<kNv>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(full + 8 * i, kNv ? kConvWarps : 1);
+      ptx::mbar_init(free + 8 * i, 1);
+    }
+    for (int i = 0; i < kB; ++i) {
+      ptx::mbar_init(q_full + 8 * i, 1);
+      ptx::mbar_init(q_free + 8 * i, 1);
+    }
+    for (int i = 0; i < kDBufs; ++i) {
+      ptx::mbar_init(d_full + 8 * i, 1);
+      ptx::mbar_init(d_free + 8 * i, 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(h_full + 8 * i, 1);
+      ptx::mbar_init(h_free + 8 * i, 4);
+    }
+    ptx::mbar_init(mma_done, 1);
+    ptx::fence_mbar_init();
+    s_b = s_tile = 0;
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&tmem_slot, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+
+  // ---- this CTA's run of the line
+  auto scan = [&](int n, int& before, int& all) {
+    int v = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
     }
     __syncthreads();
-    const uint8_t* page = a.lat + int64_t(pg) * a.stride;
-    for (int i = threadIdx.x; i < kPage * kDQK; i += 256) {
-      const int s = i / kDQK, d = i - s * kDQK;
-      float v;
-      if (!a.nv) {
-        v = e4m3(page[s * kDQK + d]);
-      } else if (d < kDNope) {
-        const uint8_t* row = page + s * 352;
-        const __half2_raw pair = __nv_cvt_fp4x2_to_halfraw2(row[d / 2], __NV_E2M1);
-        v = __half2float(__half(__half_raw{(d & 1) ? pair.y : pair.x})) * e4m3(row[256 + d / 16]);
-      } else {
-        v = e4m3(page[s * 352 + 288 + d - kDNope]);
-      }
-      lat[s * kPitch + d] = v;
-    }
+    if (lane == 31) s_sum[warp] = v;
     __syncthreads();
-    const int s = j * kPage + tok;
-    float sum = 0.f;
-    bool seen = false;
-    for (int t = 0; t < a.n_q; ++t) {
-      const int L = n - a.n_q + t + 1;
-      const bool sees = s < L && (s < a.sinks || s >= L - a.window);
-      seen |= sees;
-      float w = 0.f;
-      for (int h = grp * 24; h < grp * 24 + 24; ++h) {
-        const size_t hr = size_t(b * a.n_q + t) * kHeads + h;
-        const float lse = a.lse[hr];
-        if (!isfinite(lse)) continue;
-        const __nv_bfloat16* q = a.q + hr * kDQK;
-        float z = 0.f;
-        for (int d = 0; d < kDQK; ++d) z = fmaf(__bfloat162float(q[d]), lat[tok * kPitch + d], z);
-        w += expf(z * a.scale - lse);
+    before = v - n;
+    all = 0;
+    for (int i = 0; i < kThreads<kNv> / 32; ++i) {
+      if (i < warp) before += s_sum[i];
+      all += s_sum[i];
+    }
+  };
+  auto tiles_of = [&](int b) { return b < a.batch ? Span(a, a.ctx[b]).tiles() : 0; };
+  long long line = 0;
+  int before, all;
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads<kNv>) {
+    scan(tiles_of(b0 + int(threadIdx.x)), before, all);
+    line += all;
+  }
+  const long long lo = line * blockIdx.x / gridDim.x, hi = line * (blockIdx.x + 1) / gridDim.x;
+  const int run = int(hi - lo);
+  long long base = 0;
+  for (int b0 = 0; b0 < a.batch && base <= lo; b0 += kThreads<kNv>) {
+    const int b = b0 + int(threadIdx.x), n = tiles_of(b);
+    scan(n, before, all);
+    const long long first = base + before;
+    if (lo >= first && lo < first + n) {
+      s_b = b;
+      s_tile = int(lo - first);
+    }
+    base += all;
+  }
+  __syncthreads();
+  const int b0 = s_b, tile0 = s_tile;
+  bool ok = true;
+  Walk wk;
+
+  if (warp < 4) {
+    // ------------------------------------------------------------ sums
+    const int tok = threadIdx.x;
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    int g = 0, hn = 0;
+#pragma unroll 1
+    for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
+      const Span s(a, a.ctx[wk.b]);
+#pragma unroll 1
+      for (int r = wk.r0; r <= wk.r1 && ok; ++r, ++hn) {
+        const int hb = hn & 1, seen = s.n - a.n_q + r + 1;
+        if (!ptx::mbar_wait(h_full + 8 * hb, uint32_t(hn >> 1) & 1u, kPolls)) { ok = false; break; }
+        const float4* cs = reinterpret_cast<const float4*>(heads + hb * 2 * kHeads);
+        const float4* co = cs + kHeads / 4;
+        const bool bad = s_bad[hb] != 0;
+#pragma unroll 1
+        for (int k = 0; k < wk.nt; ++k, ++g) {
+          // the token, and at the last row what its weight was
+          const int i = 2 * (wk.t0 + k) + (tok >> 6);
+          const int at = i < s.pages ? s.page(i) * kPage + (tok & 63) : s.n;
+          bool put = r == wk.r1 && at < s.n && (at < a.sinks || at + a.window >= s.n - a.n_q + 1);
+          float old = 0.f;
+          float* dst = a.mass + wk.b * a.mass_stride + at;
+          if (put) {
+            const int pg = __ldg(a.table + size_t(wk.b) * a.max_pages + at / kPage);
+            put = pg >= 0 && pg < a.num_pages;
+            if (at < s.n - a.fresh) old = *dst;
+          }
+          const int buf = g % kDBufs;
+          if (!ptx::mbar_wait(d_full + 8 * buf, uint32_t(g / kDBufs) & 1u, kPolls)) { ok = false; break; }
+          ptx::tc_fence_after();
+          float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f;
+          float z[2][32];
+          ptx::tmem_ld32_nowait(tmem + lanes + buf * 128, z[0]);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            float(&x)[32] = z[c & 1];
+            ptx::tmem_ld_wait(x);
+            if (c < 2) ptx::tmem_ld32_nowait(tmem + lanes + buf * 128 + 32 * (c + 1), z[(c + 1) & 1]);
+#pragma unroll
+            for (int h = 0; h < 32; h += 4) {
+              const float4 f = cs[8 * c + h / 4], o = co[8 * c + h / 4];
+              float y[4] = {fmaf(x[h], f.x, o.x), fmaf(x[h + 1], f.y, o.y), fmaf(x[h + 2], f.z, o.z), fmaf(x[h + 3], f.w, o.w)};
+              if (bad) {  // heads without a finite lse, whatever their products are
+                y[0] = o.x == -INFINITY ? o.x : y[0];
+                y[1] = o.y == -INFINITY ? o.y : y[1];
+                y[2] = o.z == -INFINITY ? o.z : y[2];
+                y[3] = o.w == -INFINITY ? o.w : y[3];
+              }
+              ptx::add2(w0, w1, ptx::ex2_approx(y[0]), ptx::ex2_approx(y[1]));
+              ptx::add2(w2, w3, ptx::ex2_approx(y[2]), ptx::ex2_approx(y[3]));
+            }
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(d_free + 8 * buf);
+          const bool sees = at < seen && (at < a.sinks || at >= seen - a.window);
+          float w = sees ? (w0 + w1) + (w2 + w3) : 0.f;
+          if (r > wk.r0) w += acc[k * kTok + tok];
+          if (r < wk.r1) acc[k * kTok + tok] = w;
+          else if (put) *dst = old + w;
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(h_free + 8 * hb);
       }
-      part[grp][tok] = w;
-      __syncthreads();
-      if (sees) sum += part[0][tok] + part[1][tok] + part[2][tok] + part[3][tok];
-      __syncthreads();
     }
-    if (grp == 0 && seen) {
-      float* m = a.mass + b * a.mass_stride + s;
-      *m = s >= n - a.fresh ? sum : *m + sum;
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ S = C . Q^T
+    const uint32_t r0 = ptx::smem_u32(ring), q0 = ptx::smem_u32(qbuf);
+    int g = 0, c = 0, qn = -1, row_in = -1;  // tiles, K-blocks, queries so far; the row in shared memory
+    bool on = wk.start(a, b0, tile0, run);
+#pragma unroll 1
+    while (on && ok) {
+      const int first = wk.b * a.n_q + wk.r0, last = wk.b * a.n_q + wk.r1, nt = wk.nt;
+      on = wk.next(a);
+      const int then = on ? wk.b * a.n_q + wk.r0 : -1;
+#pragma unroll 1
+      for (int row = first; row <= last && ok; ++row) {
+        const bool fresh_q = row != row_in;
+        if (fresh_q) ++qn;
+        row_in = row;
+        const bool leaves = (row < last ? row + 1 : then) != row;
+#pragma unroll 1
+        for (int k = 0; k < nt && ok; ++k, ++g) {
+          const int buf = g % kDBufs;
+          if (g >= kDBufs && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kDBufs - 1) & 1u, kPolls)) { ok = false; break; }
+          const uint32_t d = tmem + buf * 128;
+#pragma unroll 1
+          for (int j = 0; j < kB; ++j, ++c) {
+            const int st = c % kStages;
+            if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
+            if (!ptx::mbar_wait(full + 8 * st, uint32_t(c / kStages) & 1u, kPolls)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t blk = r0 + st * kStage;
+            if (ptx::elect_one()) {
+              if constexpr (kNv) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  ptx::mma_f16(d, ptx::sdesc_sw128(blk + kk * 32), ptx::sdesc_plain(q0 + (8 * j + 2 * kk) * kQChunk, kQChunk, 128),
+                               ptx::idesc(0, 0, kTok, kHeads), (j | kk) ? 1u : 0u);
+              } else {
+                const int steps = j < 4 ? 4 : 2;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)  // the query's E4M3, then its E5M2 part
+#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    if (kk < steps)
+                      ptx::mma_f8f6f4(d, j < 4 ? ptx::sdesc_sw128(blk + kk * 32) : ptx::sdesc_sw64(blk + kk * 32),
+                                      ptx::sdesc_plain(q0 + (36 * part + 8 * j + 2 * kk) * kQChunk, kQChunk, 128),
+                                      ptx::idesc(0, part, kTok, kHeads), (j | kk | part) ? 1u : 0u);
+              }
+              ptx::mma_commit(free + 8 * st);
+              if (k == nt - 1 && leaves) ptx::mma_commit(q_free + 8 * j);
+              if (j == kB - 1) ptx::mma_commit(d_full + 8 * buf);
+            }
+            __syncwarp();
+          }
+        }
+      }
     }
+    // nothing of this warp's left in flight when the tensor memory is released
+    if (ptx::elect_one()) ptx::mma_commit(mma_done);
+    __syncwarp();
+    ptx::mbar_wait(mma_done, 0, kPolls);
+  } else if (warp == kQueryWarp) {
+    // ------------------------------------------------------------ the rows' queries
+    const uint32_t q0 = ptx::smem_u32(qbuf);
+    const int64_t pitch = int64_t(a.batch) * a.n_q * kHeads * 16;  // between chunks
+    int qn = 0, row_in = -1;
+#pragma unroll 1
+    for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
+#pragma unroll 1
+      for (int row = wk.b * a.n_q + wk.r0; row <= wk.b * a.n_q + wk.r1 && ok; ++row) {
+        if (row == row_in) continue;
+        row_in = row;
+        const uint8_t* src = a.q + int64_t(row) * kQChunk;
+#pragma unroll 1
+        for (int j = 0; j < kB; ++j) {
+          if (qn > 0 && !ptx::mbar_wait(q_free + 8 * j, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
+          // chunks 8j .. of the query, or of both of its parts
+          const int per = kNv || j < 4 ? 8 : 4, n = kNv ? per : 2 * per;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(q_full + 8 * j, n * kQChunk);
+          __syncwarp();
+          if (lane < n) {
+            const int ch = 8 * j + (lane < per ? lane : lane - per + 36);
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(q0 + ch * kQChunk),
+                "l"(reinterpret_cast<uint64_t>(src + ch * pitch)), "r"(kQChunk), "r"(q_full + 8 * j)
+                : "memory");
+          }
+          __syncwarp();
+        }
+        ++qn;
+      }
+    }
+    // no copy left in flight
+    if (!ok)
+      for (int i = 0; i < 2 * kB; ++i) ptx::mbar_wait(q_full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+  } else if (warp == kHeadWarp) {
+    // ------------------------------------------------------------ the heads' factors and offsets
+    int hn = 0;
+#pragma unroll 1
+    for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
+#pragma unroll 1
+      for (int r = wk.r0; r <= wk.r1; ++r, ++hn) {
+        const int hb = hn & 1;
+        float f[3], o[3];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int64_t hr = int64_t(wk.b * a.n_q + r) * kHeads + 32 * i + lane;
+          f[i] = a.scale_log2 * __ldg(a.qs + hr);
+          const float lse = __ldg(a.lse + hr);
+          const bool good = lse - lse == 0.f;  // finite
+          o[i] = good ? lse * -1.4426950408889634f : -INFINITY;
+          bad |= !good;
+        }
+        if (hn >= 2 && !ptx::mbar_wait(h_free + 8 * hb, uint32_t(hn / 2 - 1) & 1u, kPolls)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          heads[hb * 2 * kHeads + 32 * i + lane] = f[i];
+          heads[hb * 2 * kHeads + kHeads + 32 * i + lane] = o[i];
+        }
+        const int any = __any_sync(0xffffffffu, bad);
+        if (lane == 0) s_bad[hb] = any;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(h_full + 8 * hb);
+      }
+    }
+  } else if (!kNv && warp == kTileWarp) {
+    // ------------------------------------------------------------ FP8 latents by TMA, page by page
+    const uint32_t r0 = ptx::smem_u32(ring);
+    int c = 0;
+#pragma unroll 1
+    for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
+      const Span s(a, a.ctx[wk.b]);
+      const int i0 = 2 * wk.t0 + lane;  // a chunk's pages: a lane each
+      int mine = -1;
+      if (lane < 2 * wk.nt && i0 < s.pages) {
+        mine = __ldg(a.table + size_t(wk.b) * a.max_pages + s.page(i0));
+        if (mine < 0 || mine >= a.num_pages) {
+          atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+          mine = -1;
+        }
+      }
+#pragma unroll 1
+      for (int r = wk.r0; r <= wk.r1 && ok; ++r) {
+#pragma unroll 1
+        for (int k = 0; k < wk.nt && ok; ++k) {
+          const int p0 = __shfl_sync(0xffffffffu, mine, 2 * k), p1 = __shfl_sync(0xffffffffu, mine, 2 * k + 1);
+#pragma unroll 1
+          for (int j = 0; j < kB; ++j, ++c) {
+            const int st = c % kStages;
+            if (c >= kStages && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kStages - 1) & 1u, kPolls)) { ok = false; break; }
+            if (lane == 0) {
+              const uint32_t dst = r0 + st * kStage, bar = full + 8 * st, half = j < 4 ? kStage / 2 : kStage / 4;
+              // (a page that is missing leaves what lay there: its tokens' sums are not used)
+              const uint32_t bytes = (p0 >= 0 ? half : 0) + (p1 >= 0 ? half : 0);
+              if (bytes) ptx::mbar_arrive_expect_tx(bar, bytes);
+              else ptx::mbar_arrive(bar);
+              const CUtensorMap* m = j < 4 ? &kmap : &rmap;
+              if (p0 >= 0) ptx::tma_load_3d(dst, m, bar, 128 * j, 0, p0);
+              if (p1 >= 0) ptx::tma_load_3d(dst + half, m, bar, 128 * j, 0, p1);
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    if (!ok)
+      for (int i = 0; i < 2 * kStages; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+  } else if (kNv && warp >= 8) {
+    // ------------------------------------------------------------ NVFP4 latents to fp16, two threads a token
+    const int ct = int(threadIdx.x) - 256, tok = ct >> 1, half = ct & 1;
+    int c = 0;
+    // the tiles in order, with the next one's loads in flight
+    bool on = wk.start(a, b0, tile0, run);
+    int r = wk.r0, k = 0;
+    auto fetch = [&](HalfToken& t) {
+      const Span s(a, a.ctx[wk.b]);
+      const int i = 2 * (wk.t0 + k) + (tok >> 6);
+      const uint8_t* row = nullptr;
+      if (i < s.pages) {
+        const int pg = __ldg(a.table + size_t(wk.b) * a.max_pages + s.page(i));
+        if (pg >= 0 && pg < a.num_pages) row = a.lat + int64_t(pg) * a.stride + (tok & 63) * 352;
+        else if ((ct & 127) == 0) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
+      }
+      t.load(row, half);
+      if (++k == wk.nt) {
+        k = 0;
+        if (++r > wk.r1) {
+          on = wk.next(a);
+          r = wk.r0;
+        }
+      }
+    };
+    HalfToken now, next;
+    bool more = on;
+    if (on) fetch(now);
+#pragma unroll 1
+    while (more && ok) {
+      more = on;
+      if (on) fetch(next);
+      auto block = [&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        if (!ok) return;
+        const int st = c % kStages;
+        if (c >= kStages && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kStages - 1) & 1u, kPolls)) {
+          ok = false;
+          return;
+        }
+        now.template store<j>(ring + st * kStage, tok, half);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full + 8 * st);
+        ++c;
+      };
+      block(std::integral_constant<int, 0>{});
+      block(std::integral_constant<int, 1>{});
+      block(std::integral_constant<int, 2>{});
+      block(std::integral_constant<int, 3>{});
+      block(std::integral_constant<int, 4>{});
+      block(std::integral_constant<int, 5>{});
+      block(std::integral_constant<int, 6>{});
+      block(std::integral_constant<int, 7>{});
+      block(std::integral_constant<int, 8>{});
+      now = next;
+    }
+  }
+  if (!ok) atomicOr(a.err, DSA_DEVERR_TIMEOUT);
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -97,13 +575,45 @@ __global__ void __launch_bounds__(256) mass_kernel(MassArgs a) {
 cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const void* lat_pool,
                                   int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens,
                                   const float* lse, int fresh, float* mass, int64_t mass_stride, cudaStream_t st) {
-  MassArgs a = {static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(lat_pool), block_table, ctx_lens, lse, mass,
-                reinterpret_cast<int*>(ws + L.err), p.lat_page_stride, mass_stride, p.n_q, p.max_pages_per_req, L.cap,
-                p.num_pages, sinks, window, fresh, p.lat_fmt == DSA_LAT_NVFP4_352, p.softmax_scale * p.latent_scale};
-  const size_t smem = size_t(kPage) * kPitch * 4;
-  cudaError_t e = cudaFuncSetAttribute(mass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  MassArgs a = {};
+  a.q = reinterpret_cast<const uint8_t*>(ws + L.pfx_q);
+  a.qs = reinterpret_cast<const float*>(ws + L.pfx_qs);
+  a.lse = lse;
+  a.lat = static_cast<const uint8_t*>(lat_pool);
+  a.table = block_table;
+  a.ctx = ctx_lens;
+  a.mass = mass;
+  a.err = reinterpret_cast<int*>(ws + L.err);
+  a.stride = p.lat_page_stride;
+  a.mass_stride = mass_stride;
+  a.batch = p.batch;
+  a.n_q = p.n_q;
+  a.max_pages = p.max_pages_per_req;
+  a.cap = L.cap;
+  a.num_pages = p.num_pages;
+  a.sinks = sinks < L.cap ? sinks : L.cap;
+  a.window = window < L.cap ? window : L.cap;
+  a.fresh = fresh;
+  a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
+  const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
+  CUtensorMap kmap, rmap;
+  std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
+  std::memset(&rmap, 0, sizeof(rmap));
+  if (!nv) {
+    // [num_pages][64][576] bytes: 128 dims of a page's rows at a time, and the 64 rope dims
+    const uint64_t dims[3] = {uint64_t(kDQK), uint64_t(kPage), uint64_t(p.num_pages)};
+    const uint64_t strides[2] = {uint64_t(kDQK), uint64_t(p.lat_page_stride)};
+    const uint32_t box[3] = {128, kPage, 1}, rbox[3] = {64, kPage, 1};
+    if (!encode_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, 0, st);
   if (e != cudaSuccess) return e;
-  return launch_pdl(mass_kernel, dim3(p.max_pages_per_req < 1024 ? p.max_pages_per_req : 1024, p.batch), dim3(256), smem, st, a);
+  auto kern = nv ? mass_kernel<true> : mass_kernel<false>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(sm_count()), dim3(nv ? kThreads<true> : kThreads<false>), kSmem, st, kmap, rmap, a);
 }
 
 }  // namespace dsa

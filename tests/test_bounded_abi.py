@@ -82,6 +82,7 @@ def test_window_calls_limits(lib):
     assert _call("dsa_attention_mass", p, MASS, fresh=top, bytes=dsa.workspace_size(p) - 1) == WORKSPACE
     big = _params(batch=1, n_q=65535, max_pages_per_req=1 << 22, topk=1)
     assert _call("dsa_window_mla_decode", big, WINDOW) == UNSUPPORTED
+    assert _call("dsa_attention_mass", big, MASS, stride=1 << 28) == UNSUPPORTED
 
 
 EVICT = dict(budgets=FAKE, sinks=4, recent=8, mass=FAKE, stride=640, pools=None, n=0, table=FAKE, ctx=FAKE, refs=FAKE, kept=None)
