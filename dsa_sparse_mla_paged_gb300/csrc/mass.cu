@@ -5,8 +5,10 @@
 // token is a row of the product here: S = C . Q^T with 128 tokens (two pages) against a query row's 96 heads,
 // one accumulator lane per token; a thread has one token, and its sum over the heads is its own: no shuffle, no
 // atomic, the same bits in any batch. The query is prepared as for the dense attention (FP8 latents: E4M3 + E5M2,
-// multiplied with the latents as TMA brings them; NVFP4 ones: fp16, the latents converted) and stays in
-// shared memory (110 KB) while tiles of tokens stream past it.
+// multiplied with the latents as TMA brings them; NVFP4 ones: fp16) and stays in
+// shared memory (110 KB) while tiles of tokens stream past it. NVFP4 latents are converted to fp16 and multiplied from tensor
+// memory: through shared memory, which the products read 28 KB of per K-block, their 16 KB took 226 us for the
+// case below.
 //
 // The tiles of all requests are a line that is cut into equal runs, one per CTA, and a run into chunks of at most 16
 // tiles of one request. A chunk is gone through once per row (its latents come from L2 after the first), its sums
@@ -27,19 +29,28 @@ namespace {
 
 constexpr int kTok = 128;                     // tokens of a tile
 constexpr int kStage = kTok * 128;            // 16,384 B: a K-block, 128 rows of 128 B
-constexpr int kStages = 6;
+constexpr int kStages = 6;                    // (NVFP4: of the rows as they lie, three to a tile)
 constexpr int kQChunk = kHeads * 16;          // 1,536 B: 16 B of each head
 constexpr int kQBytes = 72 * kQChunk;
 constexpr int kChunk = 16;                    // tiles of a chunk
-constexpr int kDBufs = 4;                     // accumulators of 128 columns
 template <bool kNv>
 constexpr int kBlocks = kNv ? 9 : 5;          // K-blocks of a tile: 64 dims of fp16; 128 of E4M3, the last 64
-constexpr int kConvWarps = 8;
+template <bool kNv>
+constexpr int kLoads = kNv ? 3 : 5;           // stages that a tile's rows take
+// tensor memory: FP8 four accumulators of 96 columns; NVFP4 two, and ten K-blocks of 32
+template <bool kNv>
+constexpr int kDBufs = kNv ? 2 : 4;
+template <bool kNv>
+constexpr int kDCols = kNv ? 96 : 128;
+constexpr int kABufs = 10, kACol = 192;
+static_assert(kACol + kABufs * 32 == 512, "tensor memory");
+// NVFP4: the order of the K-blocks, which two groups of converters make in turn (the first: 0..3 and the rotary one)
+__host__ __device__ constexpr int block_at(int i) { return i == 8 ? 8 : (i & 1) * 4 + i / 2; }
 template <bool kNv>
 constexpr int kThreads = kNv ? 512 : 256;
 // warps: 0..3 sums, 4 products, 5 latents (FP8), 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
 constexpr int kMmaWarp = 4, kTileWarp = 5, kQueryWarp = 6, kHeadWarp = 7;
-constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * kDBufs + 4 + 1;
+constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * 4 + 4 + 2 * kABufs + 1;
 constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
 static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables");
 constexpr uint32_t kPolls = 1u << 20;  // 4 s
@@ -129,54 +140,6 @@ __device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A converter thread's half of a token of an NVFP4 tile: 32 dims of each of eight K-blocks, and of the rotary one.
-struct HalfToken {
-  uint4 v[8], s[2], rope[2];
-  __device__ __forceinline__ void load(const uint8_t* row, int half) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    if (!row) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = zero;
-      s[0] = s[1] = rope[0] = rope[1] = zero;
-      return;
-    }
-    const uint4* p = reinterpret_cast<const uint4*>(row);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __ldg(p + 2 * j + half);
-    s[0] = __ldg(p + 16);
-    s[1] = __ldg(p + 17);
-    rope[0] = __ldg(p + 18 + 2 * half);
-    rope[1] = __ldg(p + 19 + 2 * half);
-  }
-  template <int kJ>
-  __device__ __forceinline__ void store(uint8_t* blk, int tok, int half) const {
-    uint4 o[4];
-    if constexpr (kJ < 8) {
-      const uint4& q = s[kJ / 4];
-      const uint32_t four = kJ % 4 == 0 ? q.x : kJ % 4 == 1 ? q.y : kJ % 4 == 2 ? q.z : q.w;
-      uint32_t two, none;
-      expand_e4m3(half ? four >> 16 : four, two, none);
-      const __half2 h = *reinterpret_cast<const __half2*>(&two);
-      const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-      o[0] = expand_e2m1(v[kJ].x, s0);
-      o[1] = expand_e2m1(v[kJ].y, s0);
-      o[2] = expand_e2m1(v[kJ].z, s1);
-      o[3] = expand_e2m1(v[kJ].w, s1);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        expand_e4m3(rope[i].x, o[2 * i].x, o[2 * i].y);
-        expand_e4m3(rope[i].y, o[2 * i].z, o[2 * i].w);
-        expand_e4m3(rope[i].z, o[2 * i + 1].x, o[2 * i + 1].y);
-        expand_e4m3(rope[i].w, o[2 * i + 1].z, o[2 * i + 1].w);
-      }
-    }
-    uint8_t* at = blk + tok * 128;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(at + (((4 * half + c) ^ (tok & 7)) << 4)) = o[c];
-  }
-};
-
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads<kNv>, 1)
     mass_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
@@ -189,24 +152,30 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   const uint32_t bars = ptx::smem_u32(heads + 2 * 2 * kHeads);
   const uint32_t full = bars, free = full + 8 * kStages;                // [kStages]
   const uint32_t q_full = free + 8 * kStages, q_free = q_full + 8 * 9;  // [kBlocks]
-  const uint32_t d_full = q_free + 8 * 9, d_free = d_full + 8 * kDBufs; // [kDBufs]
-  const uint32_t h_full = d_free + 8 * kDBufs, h_free = h_full + 16;    // [2]
-  const uint32_t mma_done = h_free + 16;
+  const uint32_t d_full = q_free + 8 * 9, d_free = d_full + 8 * 4;      // [kDBufs]
+  const uint32_t h_full = d_free + 8 * 4, h_free = h_full + 16;         // [2]
+  const uint32_t a_full = h_free + 16, a_free = a_full + 8 * kABufs;    // [kABufs] NVFP4: K-blocks in tensor memory
+  const uint32_t mma_done = a_free + 8 * kABufs;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_sum[32], s_b, s_tile, s_bad[2];
-  constexpr int kB = kBlocks<kNv>;
+  constexpr int kB = kBlocks<kNv>, kD = kDBufs<kNv>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(full + 8 * i, kNv ? kConvWarps : 1);
-      ptx::mbar_init(free + 8 * i, 1);
+      ptx::mbar_init(full + 8 * i, 1);
+      // (NVFP4: scales and rotary values are for both groups of converters, the others for one)
+      ptx::mbar_init(free + 8 * i, !kNv ? 1 : i % 3 == 0 ? 8 : 4);
+    }
+    for (int i = 0; i < kABufs; ++i) {
+      ptx::mbar_init(a_full + 8 * i, 4);
+      ptx::mbar_init(a_free + 8 * i, 1);
     }
     for (int i = 0; i < kB; ++i) {
       ptx::mbar_init(q_full + 8 * i, 1);
       ptx::mbar_init(q_free + 8 * i, 1);
     }
-    for (int i = 0; i < kDBufs; ++i) {
+    for (int i = 0; i < kDBufs<kNv>; ++i) {
       ptx::mbar_init(d_full + 8 * i, 1);
       ptx::mbar_init(d_free + 8 * i, 4);
     }
@@ -299,17 +268,17 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
             put = pg >= 0 && pg < a.num_pages;
             if (at < s.n - a.fresh) old = *dst;
           }
-          const int buf = g % kDBufs;
-          if (!ptx::mbar_wait(d_full + 8 * buf, uint32_t(g / kDBufs) & 1u, kPolls)) { ok = false; break; }
+          const int buf = g % kD;
+          if (!ptx::mbar_wait(d_full + 8 * buf, uint32_t(g / kD) & 1u, kPolls)) { ok = false; break; }
           ptx::tc_fence_after();
           float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f;
           float z[2][32];
-          ptx::tmem_ld32_nowait(tmem + lanes + buf * 128, z[0]);
+          ptx::tmem_ld32_nowait(tmem + lanes + buf * kDCols<kNv>, z[0]);
 #pragma unroll
           for (int c = 0; c < 3; ++c) {
             float(&x)[32] = z[c & 1];
             ptx::tmem_ld_wait(x);
-            if (c < 2) ptx::tmem_ld32_nowait(tmem + lanes + buf * 128 + 32 * (c + 1), z[(c + 1) & 1]);
+            if (c < 2) ptx::tmem_ld32_nowait(tmem + lanes + buf * kDCols<kNv> + 32 * (c + 1), z[(c + 1) & 1]);
 #pragma unroll
             for (int h = 0; h < 32; h += 4) {
               const float4 f = cs[8 * c + h / 4], o = co[8 * c + h / 4];
@@ -355,22 +324,24 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         const bool leaves = (row < last ? row + 1 : then) != row;
 #pragma unroll 1
         for (int k = 0; k < nt && ok; ++k, ++g) {
-          const int buf = g % kDBufs;
-          if (g >= kDBufs && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kDBufs - 1) & 1u, kPolls)) { ok = false; break; }
-          const uint32_t d = tmem + buf * 128;
+          const int buf = g % kD;
+          if (g >= kD && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kD - 1) & 1u, kPolls)) { ok = false; break; }
+          const uint32_t d = tmem + buf * kDCols<kNv>;
 #pragma unroll 1
-          for (int j = 0; j < kB; ++j, ++c) {
-            const int st = c % kStages;
+          for (int i = 0; i < kB; ++i, ++c) {
+            constexpr int kRing = kNv ? kABufs : kStages;
+            const int st = c % kRing, j = kNv ? block_at(i) : i;
             if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
-            if (!ptx::mbar_wait(full + 8 * st, uint32_t(c / kStages) & 1u, kPolls)) { ok = false; break; }
+            if (!ptx::mbar_wait((kNv ? a_full : full) + 8 * st, uint32_t(c / kRing) & 1u, kPolls)) { ok = false; break; }
             ptx::tc_fence_after();
             const uint32_t blk = r0 + st * kStage;
             if (ptx::elect_one()) {
               if constexpr (kNv) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  ptx::mma_f16(d, ptx::sdesc_sw128(blk + kk * 32), ptx::sdesc_plain(q0 + (8 * j + 2 * kk) * kQChunk, kQChunk, 128),
-                               ptx::idesc(0, 0, kTok, kHeads), (j | kk) ? 1u : 0u);
+                  ptx::mma_f16_tmem_a(d, tmem + kACol + st * 32 + kk * 8,
+                                      ptx::sdesc_plain(q0 + (8 * j + 2 * kk) * kQChunk, kQChunk, 128),
+                                      ptx::idesc(0, 0, kTok, kHeads), (i | kk) ? 1u : 0u);
               } else {
                 const int steps = j < 4 ? 4 : 2;
 #pragma unroll
@@ -382,9 +353,9 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
                                       ptx::sdesc_plain(q0 + (36 * part + 8 * j + 2 * kk) * kQChunk, kQChunk, 128),
                                       ptx::idesc(0, part, kTok, kHeads), (j | kk | part) ? 1u : 0u);
               }
-              ptx::mma_commit(free + 8 * st);
+              ptx::mma_commit((kNv ? a_free : free) + 8 * st);
               if (k == nt - 1 && leaves) ptx::mma_commit(q_free + 8 * j);
-              if (j == kB - 1) ptx::mma_commit(d_full + 8 * buf);
+              if (i == kB - 1) ptx::mma_commit(d_full + 8 * buf);
             }
             __syncwarp();
           }
@@ -408,7 +379,8 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         row_in = row;
         const uint8_t* src = a.q + int64_t(row) * kQChunk;
 #pragma unroll 1
-        for (int j = 0; j < kB; ++j) {
+        for (int i = 0; i < kB; ++i) {
+          const int j = kNv ? block_at(i) : i;
           if (qn > 0 && !ptx::mbar_wait(q_free + 8 * j, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
           // chunks 8j .. of the query, or of both of its parts
           const int per = kNv || j < 4 ? 8 : 4, n = kNv ? per : 2 * per;
@@ -460,8 +432,8 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         if (lane == 0) ptx::mbar_arrive(h_full + 8 * hb);
       }
     }
-  } else if (!kNv && warp == kTileWarp) {
-    // ------------------------------------------------------------ FP8 latents by TMA, page by page
+  } else if (warp == kTileWarp) {
+    // ------------------------------------------------------------ latents by TMA, page by page
     const uint32_t r0 = ptx::smem_u32(ring);
     int c = 0;
 #pragma unroll 1
@@ -482,18 +454,19 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         for (int k = 0; k < wk.nt && ok; ++k) {
           const int p0 = __shfl_sync(0xffffffffu, mine, 2 * k), p1 = __shfl_sync(0xffffffffu, mine, 2 * k + 1);
 #pragma unroll 1
-          for (int j = 0; j < kB; ++j, ++c) {
-            const int st = c % kStages;
+          for (int i = 0; i < kLoads<kNv>; ++i, ++c) {
+            const int st = c % kStages, j = kNv ? (i + 2) % 3 : i;  // (NVFP4: 128 B of the rows, the last ones first)
             if (c >= kStages && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kStages - 1) & 1u, kPolls)) { ok = false; break; }
             if (lane == 0) {
-              const uint32_t dst = r0 + st * kStage, bar = full + 8 * st, half = j < 4 ? kStage / 2 : kStage / 4;
+              const uint32_t dst = r0 + st * kStage, bar = full + 8 * st, half = kNv || j < 4 ? kStage / 2 : kStage / 4;
               // (a page that is missing leaves what lay there: its tokens' sums are not used)
               const uint32_t bytes = (p0 >= 0 ? half : 0) + (p1 >= 0 ? half : 0);
               if (bytes) ptx::mbar_arrive_expect_tx(bar, bytes);
               else ptx::mbar_arrive(bar);
-              const CUtensorMap* m = j < 4 ? &kmap : &rmap;
-              if (p0 >= 0) ptx::tma_load_3d(dst, m, bar, 128 * j, 0, p0);
-              if (p1 >= 0) ptx::tma_load_3d(dst + half, m, bar, 128 * j, 0, p1);
+              const CUtensorMap* m = kNv || j < 4 ? &kmap : &rmap;
+              const int x = kNv ? 32 * j : 128 * j;
+              if (p0 >= 0) ptx::tma_load_3d(dst, m, bar, x, 0, p0);
+              if (p1 >= 0) ptx::tma_load_3d(dst + half, m, bar, x, 0, p1);
             }
             __syncwarp();
           }
@@ -503,61 +476,77 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
     if (!ok)
       for (int i = 0; i < 2 * kStages; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
   } else if (kNv && warp >= 8) {
-    // ------------------------------------------------------------ NVFP4 latents to fp16, two threads a token
-    const int ct = int(threadIdx.x) - 256, tok = ct >> 1, half = ct & 1;
-    int c = 0;
-    // the tiles in order, with the next one's loads in flight
-    bool on = wk.start(a, b0, tile0, run);
-    int r = wk.r0, k = 0;
-    auto fetch = [&](HalfToken& t) {
-      const Span s(a, a.ctx[wk.b]);
-      const int i = 2 * (wk.t0 + k) + (tok >> 6);
-      const uint8_t* row = nullptr;
-      if (i < s.pages) {
-        const int pg = __ldg(a.table + size_t(wk.b) * a.max_pages + s.page(i));
-        if (pg >= 0 && pg < a.num_pages) row = a.lat + int64_t(pg) * a.stride + (tok & 63) * 352;
-        else if ((ct & 127) == 0) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
-      }
-      t.load(row, half);
-      if (++k == wk.nt) {
-        k = 0;
-        if (++r > wk.r1) {
-          on = wk.next(a);
-          r = wk.r0;
-        }
-      }
+    // ------------------------------------------------------------ NVFP4 latents to fp16, a thread a token: its rows' 64
+    // values of a K-block are 32 columns of its lane of tensor memory, so they cost shared memory nothing
+    const int group = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + kACol;
+    const uint8_t* mine = ring + tok * 128;
+    auto piece = [&](int slot, int i) {  // 16 B of the token's 128 in a stage (128-B swizzle)
+      return *reinterpret_cast<const uint4*>(mine + slot * kStage + ((i ^ (tok & 7)) << 4));
     };
-    HalfToken now, next;
-    bool more = on;
-    if (on) fetch(now);
+    int g = 0;
 #pragma unroll 1
-    while (more && ok) {
-      more = on;
-      if (on) fetch(next);
-      auto block = [&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        if (!ok) return;
-        const int st = c % kStages;
-        if (c >= kStages && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kStages - 1) & 1u, kPolls)) {
-          ok = false;
-          return;
+    for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
+#pragma unroll 1
+      for (int n = wk.nt * (wk.r1 - wk.r0 + 1); n > 0 && ok; --n, ++g) {
+        const int s0 = g % 2 * 3, s1 = s0 + 1 + group;
+        const uint32_t par = uint32_t(g / 2) & 1u;
+        if (!ptx::mbar_wait(full + 8 * s0, par, kPolls)) { ok = false; break; }
+        const uint4 sc = piece(s0, group);  // 16 scales: of this group's 256 values
+        uint4 rope[4];
+        if (group == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rope[i] = piece(s0, 2 + i);
         }
-        now.template store<j>(ring + st * kStage, tok, half);
-        ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(full + 8 * st);
-        ++c;
-      };
-      block(std::integral_constant<int, 0>{});
-      block(std::integral_constant<int, 1>{});
-      block(std::integral_constant<int, 2>{});
-      block(std::integral_constant<int, 3>{});
-      block(std::integral_constant<int, 4>{});
-      block(std::integral_constant<int, 5>{});
-      block(std::integral_constant<int, 6>{});
-      block(std::integral_constant<int, 7>{});
-      block(std::integral_constant<int, 8>{});
-      now = next;
+        if (lane == 0) ptx::mbar_arrive(free + 8 * s0);
+        if (!ptx::mbar_wait(full + 8 * s1, par, kPolls)) { ok = false; break; }
+        const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v[2] = {piece(s1, 2 * i), piece(s1, 2 * i + 1)};
+          if (i == 3) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(free + 8 * s1);
+          }
+          uint32_t f[32], two[2];
+          expand_e4m3(scales[i], two[0], two[1]);
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            const __half2 h = *reinterpret_cast<const __half2*>(&two[d]);
+            const uint32_t w[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 o = expand_e2m1(w[e], e < 2 ? __low2half2(h) : __high2half2(h));
+              f[16 * d + 4 * e] = o.x; f[16 * d + 4 * e + 1] = o.y; f[16 * d + 4 * e + 2] = o.z; f[16 * d + 4 * e + 3] = o.w;
+            }
+          }
+          const int c = 9 * g + 2 * i + group, st = c % kABufs;
+          if (c >= kABufs && !ptx::mbar_wait(a_free + 8 * st, uint32_t(c / kABufs - 1) & 1u, kPolls)) { ok = false; break; }
+          ptx::tc_fence_after();
+          ptx::tmem_st32_u(lanes + st * 32, f);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
+        }
+        if (group == 0 && ok) {
+          uint32_t f[32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            expand_e4m3(rope[i].x, f[8 * i], f[8 * i + 1]);
+            expand_e4m3(rope[i].y, f[8 * i + 2], f[8 * i + 3]);
+            expand_e4m3(rope[i].z, f[8 * i + 4], f[8 * i + 5]);
+            expand_e4m3(rope[i].w, f[8 * i + 6], f[8 * i + 7]);
+          }
+          const int c = 9 * g + 8, st = c % kABufs;
+          if (c >= kABufs && !ptx::mbar_wait(a_free + 8 * st, uint32_t(c / kABufs - 1) & 1u, kPolls)) { ok = false; break; }
+          ptx::tc_fence_after();
+          ptx::tmem_st32_u(lanes + st * 32, f);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
+        }
+      }
     }
   }
   if (!ok) atomicOr(a.err, DSA_DEVERR_TIMEOUT);
@@ -597,9 +586,15 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
   CUtensorMap kmap, rmap;
-  std::memset(&kmap, 0, sizeof(kmap));  // NVFP4 rows go through the converters
   std::memset(&rmap, 0, sizeof(rmap));
-  if (!nv) {
+  if (nv) {
+    // [num_pages][64][88] words, 32 of them at a time (the last 8 of 96 are past the row, and read as 0)
+    const uint64_t dims[3] = {88, uint64_t(kPage), uint64_t(p.num_pages)};
+    const uint64_t strides[2] = {352, uint64_t(p.lat_page_stride)};
+    const uint32_t box[3] = {32, kPage, 1};
+    if (!encode_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, lat_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  } else {
     // [num_pages][64][576] bytes: 128 dims of a page's rows at a time, and the 64 rope dims
     const uint64_t dims[3] = {uint64_t(kDQK), uint64_t(kPage), uint64_t(p.num_pages)};
     const uint64_t strides[2] = {uint64_t(kDQK), uint64_t(p.lat_page_stride)};
