@@ -356,9 +356,9 @@ cudaError_t launch_window_mla(const dsa_params_t& p, const WsLayout& L, char* ws
                               int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
                               float* lse, cudaStream_t st);
 // The query as the dense attention's tensor cores take it (pfx_q, pfx_qs) and each row's visible tokens past
-// `prefix` (pfx_len).
+// `prefix` (pfx_len). head_major: [rows * 96][1,152 B] instead of pfx_q's chunks.
 cudaError_t launch_prefix_query(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const int32_t* ctx_lens,
-                                int prefix, cudaStream_t st);
+                                int prefix, bool head_major, cudaStream_t st);
 cudaError_t launch_pages_resize(const dsa_params_t& p, const WsLayout& L, char* ws, const int32_t* new_lens,
                                 const dsa_page_pool_t* pools, int n_pools, int32_t* block_table, int32_t* ctx_lens,
                                 int32_t* page_refs, cudaStream_t st);

@@ -30,8 +30,8 @@ namespace {
 constexpr int kTok = 128;                     // tokens of a tile
 constexpr int kStage = kTok * 128;            // 16,384 B: a K-block, 128 rows of 128 B
 constexpr int kStages = 6;                    // (NVFP4: of the rows as they lie, three to a tile)
-constexpr int kQChunk = kHeads * 16;          // 1,536 B: 16 B of each head
-constexpr int kQBytes = 72 * kQChunk;
+constexpr int kQBlk = kHeads * 128;           // 12,288 B: 128 B of each head
+constexpr int kQBytes = 9 * kQBlk;
 constexpr int kChunk = 16;                    // tiles of a chunk
 template <bool kNv>
 constexpr int kBlocks = kNv ? 9 : 5;          // K-blocks of a tile: 64 dims of fp16; 128 of E4M3, the last 64
@@ -56,7 +56,6 @@ static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables")
 constexpr uint32_t kPolls = 1u << 20;  // 4 s
 
 struct MassArgs {
-  const uint8_t* q;   // [72][rows * 96] 16-B chunks of the prepared query
   const float* qs;    // [rows * 96] its scales
   const float* lse;   // [rows * 96]
   const uint8_t* lat;
@@ -143,7 +142,7 @@ __device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads<kNv>, 1)
     mass_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
-                const __grid_constant__ MassArgs a) {
+                const __grid_constant__ CUtensorMap qmap, const __grid_constant__ MassArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = ring + kStages * kStage;
@@ -309,7 +308,8 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ S = C . Q^T
     const uint32_t r0 = ptx::smem_u32(ring), q0 = ptx::smem_u32(qbuf);
-    int g = 0, c = 0, qn = -1, row_in = -1;  // tiles, K-blocks, queries so far; the row in shared memory
+    int g = 0, st = 0, qn = -1, row_in = -1;  // tiles, the K-block's place in its ring, queries so far; the row in shared memory
+    uint32_t par = 0;
     bool on = wk.start(a, b0, tile0, run);
 #pragma unroll 1
     while (on && ok) {
@@ -326,21 +326,22 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         for (int k = 0; k < nt && ok; ++k, ++g) {
           const int buf = g % kD;
           if (g >= kD && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kD - 1) & 1u, kPolls)) { ok = false; break; }
+          ptx::tc_fence_after();
           const uint32_t d = tmem + buf * kDCols<kNv>;
-#pragma unroll 1
-          for (int i = 0; i < kB; ++i, ++c) {
+#pragma unroll
+          for (int i = 0; i < kB; ++i) {
             constexpr int kRing = kNv ? kABufs : kStages;
-            const int st = c % kRing, j = kNv ? block_at(i) : i;
+            const int j = kNv ? block_at(i) : i;
             if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
-            if (!ptx::mbar_wait((kNv ? a_full : full) + 8 * st, uint32_t(c / kRing) & 1u, kPolls)) { ok = false; break; }
-            ptx::tc_fence_after();
+            if (!ptx::mbar_wait((kNv ? a_full : full) + 8 * st, par, kPolls)) { ok = false; break; }
+            // (TMA's writes need no fence; the converters' in tensor memory do)
+            if (kNv) ptx::tc_fence_after();
             const uint32_t blk = r0 + st * kStage;
             if (ptx::elect_one()) {
               if constexpr (kNv) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  ptx::mma_f16_tmem_a(d, tmem + kACol + st * 32 + kk * 8,
-                                      ptx::sdesc_plain(q0 + (8 * j + 2 * kk) * kQChunk, kQChunk, 128),
+                  ptx::mma_f16_tmem_a(d, tmem + kACol + st * 32 + kk * 8, ptx::sdesc_sw128(q0 + j * kQBlk + kk * 32),
                                       ptx::idesc(0, 0, kTok, kHeads), (i | kk) ? 1u : 0u);
               } else {
                 const int steps = j < 4 ? 4 : 2;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
                   for (int kk = 0; kk < 4; ++kk)
                     if (kk < steps)
                       ptx::mma_f8f6f4(d, j < 4 ? ptx::sdesc_sw128(blk + kk * 32) : ptx::sdesc_sw64(blk + kk * 32),
-                                      ptx::sdesc_plain(q0 + (36 * part + 8 * j + 2 * kk) * kQChunk, kQChunk, 128),
+                                      ptx::sdesc_sw128(q0 + (j < 4 ? (4 * part + j) * kQBlk : 8 * kQBlk + part * 64) + kk * 32),
                                       ptx::idesc(0, part, kTok, kHeads), (j | kk | part) ? 1u : 0u);
               }
               ptx::mma_commit((kNv ? a_free : free) + 8 * st);
@@ -358,6 +359,10 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
               if (i == kB - 1) ptx::mma_commit(d_full + 8 * buf);
             }
             __syncwarp();
+            if (++st == kRing) {
+              st = 0;
+              par ^= 1;
+            }
           }
         }
       }
@@ -369,7 +374,6 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   } else if (warp == kQueryWarp) {
     // ------------------------------------------------------------ the rows' queries
     const uint32_t q0 = ptx::smem_u32(qbuf);
-    const int64_t pitch = int64_t(a.batch) * a.n_q * kHeads * 16;  // between chunks
     int qn = 0, row_in = -1;
 #pragma unroll 1
     for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
@@ -377,21 +381,17 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
       for (int row = wk.b * a.n_q + wk.r0; row <= wk.b * a.n_q + wk.r1 && ok; ++row) {
         if (row == row_in) continue;
         row_in = row;
-        const uint8_t* src = a.q + int64_t(row) * kQChunk;
 #pragma unroll 1
         for (int i = 0; i < kB; ++i) {
           const int j = kNv ? block_at(i) : i;
           if (qn > 0 && !ptx::mbar_wait(q_free + 8 * j, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
-          // chunks 8j .. of the query, or of both of its parts
-          const int per = kNv || j < 4 ? 8 : 4, n = kNv ? per : 2 * per;
-          if (lane == 0) ptx::mbar_arrive_expect_tx(q_full + 8 * j, n * kQChunk);
-          __syncwarp();
-          if (lane < n) {
-            const int ch = 8 * j + (lane < per ? lane : lane - per + 36);
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(q0 + ch * kQChunk),
-                "l"(reinterpret_cast<uint64_t>(src + ch * pitch)), "r"(kQChunk), "r"(q_full + 8 * j)
-                : "memory");
+          if (lane == 0) {  // (FP8: both parts of the K-block)
+            const bool two = !kNv && j < 4;
+            const uint32_t bar = q_full + 8 * j;
+            const int at = kNv || j < 4 ? j : 8;
+            ptx::mbar_arrive_expect_tx(bar, two ? 2 * kQBlk : kQBlk);
+            ptx::tma_load_3d(q0 + at * kQBlk, &qmap, bar, 128 * at, 0, row);
+            if (two) ptx::tma_load_3d(q0 + (4 + at) * kQBlk, &qmap, bar, 128 * (4 + at), 0, row);
           }
           __syncwarp();
         }
@@ -565,7 +565,6 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
                                   int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens,
                                   const float* lse, int fresh, float* mass, int64_t mass_stride, cudaStream_t st) {
   MassArgs a = {};
-  a.q = reinterpret_cast<const uint8_t*>(ws + L.pfx_q);
   a.qs = reinterpret_cast<const float*>(ws + L.pfx_qs);
   a.lse = lse;
   a.lat = static_cast<const uint8_t*>(lat_pool);
@@ -603,12 +602,20 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
         !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, 0, st);
+  CUtensorMap qmap;
+  {
+    const uint64_t dims[3] = {1152, uint64_t(kHeads), uint64_t(L.rows)}, strides[2] = {1152, uint64_t(1152) * kHeads};
+    const uint32_t box[3] = {128, kHeads, 1};
+    if (!encode_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + L.pfx_q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, 0, true, st);
   if (e != cudaSuccess) return e;
   auto kern = nv ? mass_kernel<true> : mass_kernel<false>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(sm_count()), dim3(nv ? kThreads<true> : kThreads<false>), kSmem, st, kmap, rmap, a);
+  return launch_pdl(kern, dim3(sm_count()), dim3(nv ? kThreads<true> : kThreads<false>), kSmem, st, kmap, rmap,
+                    qmap, a);
 }
 
 }  // namespace dsa

@@ -1101,7 +1101,9 @@ __device__ __forceinline__ void split_query(float a, float b, uint32_t& hi, uint
       : "f"(a), "f"(b));
 }
 
-template <bool kNv>
+// kHeadMajor: for dsa_attention_mass, whose heads are the products' second operand, a head's 1,152 bytes
+// together: nine 128-byte pieces, FP8: four of each part's first 512 dims, then the last 64 dims of both.
+template <bool kNv, bool kHeadMajor>
 __global__ void __launch_bounds__(32 * kQueryWarps)
     prefix_query_kernel(const uint32_t* __restrict__ q, int heads, uint32_t* __restrict__ prepared, float* __restrict__ qs,
                         const int32_t* __restrict__ ctx, int32_t* __restrict__ lens, int n_q, int prefix, int cap,
@@ -1159,6 +1161,15 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
   }
   if (lane == 0) qs[hr] = scalbnf(1.f, e);
   __syncthreads();
+  if constexpr (kHeadMajor) {
+    for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
+      const int h = i / kChunks, at = i % kChunks;
+      const int chunk = kNv || at < 32 || at >= 68 ? at : at < 64 ? at + 4 : at - 32;
+      reinterpret_cast<uint4*>(prepared)[size_t(blockIdx.x * kQueryWarps) * kChunks + i] =
+          *reinterpret_cast<const uint4*>(s_out + chunk * kPitch + h * 4);
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
     const int chunk = i / kQueryWarps, h = i % kQueryWarps;
     reinterpret_cast<uint4*>(prepared)[size_t(chunk) * heads + blockIdx.x * kQueryWarps + h] =
@@ -1269,10 +1280,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
 }  // namespace
 
 cudaError_t launch_prefix_query(const dsa_params_t& p, const WsLayout& L, char* ws, const void* q, const int32_t* ctx_lens,
-                                int prefix, cudaStream_t st) {
+                                int prefix, bool head_major, cudaStream_t st) {
   const int heads = L.rows * kHeads;
-  return launch_pdl(p.lat_fmt == DSA_LAT_NVFP4_352 ? prefix_query_kernel<true> : prefix_query_kernel<false>,
-                    dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0, st,
+  const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
+  auto kern = head_major ? (nv ? prefix_query_kernel<true, true> : prefix_query_kernel<false, true>)
+                         : (nv ? prefix_query_kernel<true, false> : prefix_query_kernel<false, false>);
+  return launch_pdl(kern, dim3((heads + kQueryWarps - 1) / kQueryWarps), dim3(32 * kQueryWarps), 0, st,
                     static_cast<const uint32_t*>(q), heads, reinterpret_cast<uint32_t*>(ws + L.pfx_q),
                     reinterpret_cast<float*>(ws + L.pfx_qs), ctx_lens, reinterpret_cast<int32_t*>(ws + L.pfx_len), int(p.n_q),
                     prefix, L.cap, reinterpret_cast<int*>(ws + L.err));
@@ -1313,7 +1326,7 @@ static cudaError_t launch_dense(const dsa_params_t& p, const WsLayout& L, char* 
         !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, a.prefix, st);
+  cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, a.prefix, false, st);
   if (e != cudaSuccess) return e;
   const size_t smem = nv ? kSmem<true> : kSmem<false>;
   auto kern = nv ? prefix_mla_kernel<true, kWin> : prefix_mla_kernel<false, kWin>;
