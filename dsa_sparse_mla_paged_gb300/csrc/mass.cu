@@ -37,20 +37,19 @@ template <bool kNv>
 constexpr int kBlocks = kNv ? 9 : 5;          // K-blocks of a tile: 64 dims of fp16; 128 of E4M3, the last 64
 template <bool kNv>
 constexpr int kLoads = kNv ? 3 : 5;           // stages that a tile's rows take
-// tensor memory: FP8 four accumulators of 96 columns; NVFP4 two, and ten K-blocks of 32
+// tensor memory: FP8 four accumulators of 96 columns; NVFP4 two, and a tile's values in three stages of 96 columns (192 dims:
+// with a stage for each of the nine K-blocks the wait and the fence of every four products took 116 us for the case below)
 template <bool kNv>
 constexpr int kDBufs = kNv ? 2 : 4;
 template <bool kNv>
 constexpr int kDCols = kNv ? 96 : 128;
-constexpr int kABufs = 10, kACol = 192;
-static_assert(kACol + kABufs * 32 == 512, "tensor memory");
-// NVFP4: the order of the K-blocks, which two groups of converters make in turn (the first: 0..3 and the rotary one)
-__host__ __device__ constexpr int block_at(int i) { return i == 8 ? 8 : (i & 1) * 4 + i / 2; }
+constexpr int kAStages = 3, kABlocks = 3, kACol = 192;
+static_assert(kAStages * kABlocks == 9 && kACol + 9 * 32 <= 512, "tensor memory");
 template <bool kNv>
 constexpr int kThreads = kNv ? 512 : 256;
 // warps: 0..3 sums, 4 products, 5 latents (FP8), 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
 constexpr int kMmaWarp = 4, kTileWarp = 5, kQueryWarp = 6, kHeadWarp = 7;
-constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * 4 + 4 + 2 * kABufs + 1;
+constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * 4 + 4 + 2 * kAStages + 1;
 constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
 static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables");
 constexpr uint32_t kPolls = 1u << 20;  // 4 s
@@ -153,8 +152,8 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   const uint32_t q_full = free + 8 * kStages, q_free = q_full + 8 * 9;  // [kBlocks]
   const uint32_t d_full = q_free + 8 * 9, d_free = d_full + 8 * 4;      // [kDBufs]
   const uint32_t h_full = d_free + 8 * 4, h_free = h_full + 16;         // [2]
-  const uint32_t a_full = h_free + 16, a_free = a_full + 8 * kABufs;    // [kABufs] NVFP4: K-blocks in tensor memory
-  const uint32_t mma_done = a_free + 8 * kABufs;
+  const uint32_t a_full = h_free + 16, a_free = a_full + 8 * kAStages;  // [kAStages] NVFP4: values in tensor memory
+  const uint32_t mma_done = a_free + 8 * kAStages;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_sum[32], s_b, s_tile, s_bad[2];
   constexpr int kB = kBlocks<kNv>, kD = kDBufs<kNv>;
@@ -163,11 +162,10 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
-      // (NVFP4: scales and rotary values are for both groups of converters, the others for one)
-      ptx::mbar_init(free + 8 * i, !kNv ? 1 : i % 3 == 0 ? 8 : 4);
+      ptx::mbar_init(free + 8 * i, kNv ? 8 : 1);
     }
-    for (int i = 0; i < kABufs; ++i) {
-      ptx::mbar_init(a_full + 8 * i, 4);
+    for (int i = 0; i < kAStages; ++i) {
+      ptx::mbar_init(a_full + 8 * i, 8);
       ptx::mbar_init(a_free + 8 * i, 1);
     }
     for (int i = 0; i < kB; ++i) {
@@ -328,22 +326,34 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
           if (g >= kD && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kD - 1) & 1u, kPolls)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t d = tmem + buf * kDCols<kNv>;
+          if constexpr (kNv) {
 #pragma unroll
-          for (int i = 0; i < kB; ++i) {
-            constexpr int kRing = kNv ? kABufs : kStages;
-            const int j = kNv ? block_at(i) : i;
-            if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
-            if (!ptx::mbar_wait((kNv ? a_full : full) + 8 * st, par, kPolls)) { ok = false; break; }
-            // (TMA's writes need no fence; the converters' in tensor memory do)
-            if (kNv) ptx::tc_fence_after();
-            const uint32_t blk = r0 + st * kStage;
-            if (ptx::elect_one()) {
-              if constexpr (kNv) {
+            for (int i = 0; i < kAStages; ++i) {
+              if (fresh_q && k == 0)
+                for (int j = 0; j < kABlocks && ok; ++j) ok = ptx::mbar_wait(q_full + 8 * (kABlocks * i + j), uint32_t(qn) & 1u, kPolls);
+              if (!ok || !ptx::mbar_wait(a_full + 8 * i, uint32_t(g) & 1u, kPolls)) { ok = false; break; }
+              ptx::tc_fence_after();
+              if (ptx::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  ptx::mma_f16_tmem_a(d, tmem + kACol + st * 32 + kk * 8, ptx::sdesc_sw128(q0 + j * kQBlk + kk * 32),
-                                      ptx::idesc(0, 0, kTok, kHeads), (i | kk) ? 1u : 0u);
-              } else {
+                for (int kk = 0; kk < 4 * kABlocks; ++kk) {
+                  const int n = 4 * kABlocks * i + kk;  // of the tile's 36 products
+                  ptx::mma_f16_tmem_a(d, tmem + kACol + n * 8, ptx::sdesc_sw128(q0 + n / 4 * kQBlk + n % 4 * 32),
+                                      ptx::idesc(0, 0, kTok, kHeads), n ? 1u : 0u);
+                }
+                ptx::mma_commit(a_free + 8 * i);
+                if (k == nt - 1 && leaves)
+                  for (int j = 0; j < kABlocks; ++j) ptx::mma_commit(q_free + 8 * (kABlocks * i + j));
+                if (i == kAStages - 1) ptx::mma_commit(d_full + 8 * buf);
+              }
+              __syncwarp();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+              if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
+              if (!ptx::mbar_wait(full + 8 * st, par, kPolls)) { ok = false; break; }
+              const uint32_t blk = r0 + st * kStage;  // (TMA's writes need no fence)
+              if (ptx::elect_one()) {
                 const int steps = j < 4 ? 4 : 2;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)  // the query's E4M3, then its E5M2 part
@@ -353,15 +363,15 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
                       ptx::mma_f8f6f4(d, j < 4 ? ptx::sdesc_sw128(blk + kk * 32) : ptx::sdesc_sw64(blk + kk * 32),
                                       ptx::sdesc_sw128(q0 + (j < 4 ? (4 * part + j) * kQBlk : 8 * kQBlk + part * 64) + kk * 32),
                                       ptx::idesc(0, part, kTok, kHeads), (j | kk | part) ? 1u : 0u);
+                ptx::mma_commit(free + 8 * st);
+                if (k == nt - 1 && leaves) ptx::mma_commit(q_free + 8 * j);
+                if (j == kB - 1) ptx::mma_commit(d_full + 8 * buf);
               }
-              ptx::mma_commit((kNv ? a_free : free) + 8 * st);
-              if (k == nt - 1 && leaves) ptx::mma_commit(q_free + 8 * j);
-              if (i == kB - 1) ptx::mma_commit(d_full + 8 * buf);
-            }
-            __syncwarp();
-            if (++st == kRing) {
-              st = 0;
-              par ^= 1;
+              __syncwarp();
+              if (++st == kStages) {
+                st = 0;
+                par ^= 1;
+              }
             }
           }
         }
@@ -382,8 +392,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         if (row == row_in) continue;
         row_in = row;
 #pragma unroll 1
-        for (int i = 0; i < kB; ++i) {
-          const int j = kNv ? block_at(i) : i;
+        for (int j = 0; j < kB; ++j) {
           if (qn > 0 && !ptx::mbar_wait(q_free + 8 * j, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
           if (lane == 0) {  // (FP8: both parts of the K-block)
             const bool two = !kNv && j < 4;
@@ -476,8 +485,8 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
     if (!ok)
       for (int i = 0; i < 2 * kStages; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
   } else if (kNv && warp >= 8) {
-    // ------------------------------------------------------------ NVFP4 latents to fp16, a thread a token: its rows' 64
-    // values of a K-block are 32 columns of its lane of tensor memory, so they cost shared memory nothing
+    // ------------------------------------------------------------ NVFP4 latents to fp16, two threads a token (a warp of
+    // each group): 32 values are 16 columns of the token's lane of tensor memory, so they cost shared memory nothing
     const int group = (warp - 8) >> 2, tok = (warp & 3) * 32 + lane;
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + kACol;
     const uint8_t* mine = ring + tok * 128;
@@ -489,62 +498,68 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
     for (bool on = wk.start(a, b0, tile0, run); on && ok; on = wk.next(a)) {
 #pragma unroll 1
       for (int n = wk.nt * (wk.r1 - wk.r0 + 1); n > 0 && ok; --n, ++g) {
-        const int s0 = g % 2 * 3, s1 = s0 + 1 + group;
+        const int s0 = g % 2 * 3;
         const uint32_t par = uint32_t(g / 2) & 1u;
+        auto take = [&](int slot) {  // a stage has been read
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(free + 8 * (s0 + slot));
+        };
         if (!ptx::mbar_wait(full + 8 * s0, par, kPolls)) { ok = false; break; }
-        const uint4 sc = piece(s0, group);  // 16 scales: of this group's 256 values
+        const uint4 sc[2] = {piece(s0, 0), piece(s0, 1)};
         uint4 rope[4];
-        if (group == 0) {
+        if (group == 1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) rope[i] = piece(s0, 2 + i);
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(free + 8 * s0);
-        if (!ptx::mbar_wait(full + 8 * s1, par, kPolls)) { ok = false; break; }
-        const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+        take(0);
+        if (!ptx::mbar_wait(full + 8 * (s0 + 1), par, kPolls)) { ok = false; break; }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v[2] = {piece(s1, 2 * i), piece(s1, 2 * i + 1)};
-          if (i == 3) {
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(free + 8 * s1);
-          }
-          uint32_t f[32], two[2];
-          expand_e4m3(scales[i], two[0], two[1]);
+        for (int i = 0; i < kAStages; ++i) {
+          // the group's three of the tile's 18 pieces of 32 dims, of which the last two are rotary
+          if (i == 1 && !ptx::mbar_wait(full + 8 * (s0 + 2), par, kPolls)) ok = false;
+          uint32_t f[3][16];
+          auto convert = [&](int p, uint32_t (&o)[16]) {
+            if (p < 16) {
+              const uint4 v = piece(s0 + 1 + p / 8, p % 8);
+              const uint4& q = sc[p / 8];
+              const uint32_t four = p / 2 % 4 == 0 ? q.x : p / 2 % 4 == 1 ? q.y : p / 2 % 4 == 2 ? q.z : q.w;
+              uint32_t two, none;
+              expand_e4m3(p % 2 ? four >> 16 : four, two, none);
+              const __half2 h = *reinterpret_cast<const __half2*>(&two);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
-            const __half2 h = *reinterpret_cast<const __half2*>(&two[d]);
-            const uint32_t w[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
+              for (int e = 0; e < 4; ++e) {
+                const uint4 x = expand_e2m1(w[e], e < 2 ? __low2half2(h) : __high2half2(h));
+                o[4 * e] = x.x; o[4 * e + 1] = x.y; o[4 * e + 2] = x.z; o[4 * e + 3] = x.w;
+              }
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 o = expand_e2m1(w[e], e < 2 ? __low2half2(h) : __high2half2(h));
-              f[16 * d + 4 * e] = o.x; f[16 * d + 4 * e + 1] = o.y; f[16 * d + 4 * e + 2] = o.z; f[16 * d + 4 * e + 3] = o.w;
+              for (int e = 0; e < 2; ++e) {
+                const uint4& x = rope[2 * (p - 16) + e];
+                expand_e4m3(x.x, o[8 * e], o[8 * e + 1]);
+                expand_e4m3(x.y, o[8 * e + 2], o[8 * e + 3]);
+                expand_e4m3(x.z, o[8 * e + 4], o[8 * e + 5]);
+                expand_e4m3(x.w, o[8 * e + 6], o[8 * e + 7]);
+              }
             }
-          }
-          const int c = 9 * g + 2 * i + group, st = c % kABufs;
-          if (c >= kABufs && !ptx::mbar_wait(a_free + 8 * st, uint32_t(c / kABufs - 1) & 1u, kPolls)) { ok = false; break; }
-          ptx::tc_fence_after();
-          ptx::tmem_st32_u(lanes + st * 32, f);
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
-        }
-        if (group == 0 && ok) {
-          uint32_t f[32];
+          };
+          if (group == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            expand_e4m3(rope[i].x, f[8 * i], f[8 * i + 1]);
-            expand_e4m3(rope[i].y, f[8 * i + 2], f[8 * i + 3]);
-            expand_e4m3(rope[i].z, f[8 * i + 4], f[8 * i + 5]);
-            expand_e4m3(rope[i].w, f[8 * i + 6], f[8 * i + 7]);
+            for (int e = 0; e < 3; ++e) convert(6 * i + e, f[e]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) convert(6 * i + 3 + e, f[e]);
           }
-          const int c = 9 * g + 8, st = c % kABufs;
-          if (c >= kABufs && !ptx::mbar_wait(a_free + 8 * st, uint32_t(c / kABufs - 1) & 1u, kPolls)) { ok = false; break; }
+          if (i == 1) take(1);
+          if (i == 2) take(2);
+          if (!ok || (g > 0 && !ptx::mbar_wait(a_free + 8 * i, uint32_t(g - 1) & 1u, kPolls))) { ok = false; break; }
           ptx::tc_fence_after();
-          ptx::tmem_st32_u(lanes + st * 32, f);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) ptx::tmem_st16_nowait(lanes + 96 * i + 48 * group + 16 * e, f[e]);
+          ptx::tmem_st_wait();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(a_full + 8 * st);
+          if (lane == 0) ptx::mbar_arrive(a_full + 8 * i);
         }
       }
     }
