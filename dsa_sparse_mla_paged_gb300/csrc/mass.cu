@@ -28,29 +28,33 @@ namespace dsa {
 namespace {
 
 constexpr int kTok = 128;                     // tokens of a tile
-constexpr int kStage = kTok * 128;            // 16,384 B: a K-block, 128 rows of 128 B
-constexpr int kStages = 6;                    // (NVFP4: of the rows as they lie, three to a tile)
+// A tile comes in three parts. FP8: 192 dims of its rows, 128 rows of 128 B and 128 of 64 B, in four stages. NVFP4: 128 B of its
+// rows as they lie, in six. (The issuing warp's wait for a part costs some 95 cycles behind its products, which it blocks on:
+// parts of 128 dims took 62.7 us for the first case below.)
+constexpr int kParts = 3;
+template <bool kNv>
+constexpr int kStage = kNv ? kTok * 128 : kTok * 192;  // 16,384 or 24,576 B
+template <bool kNv>
+constexpr int kStages = kNv ? 6 : 4;
+constexpr int kRingBytes = 6 * 16384;
+static_assert(kStage<true> * kStages<true> == kRingBytes && kStage<false> * kStages<false> == kRingBytes, "either ring");
 constexpr int kQBlk = kHeads * 128;           // 12,288 B: 128 B of each head
-constexpr int kQBytes = 9 * kQBlk;
+constexpr int kQBytes = 9 * kQBlk;            // of a row's heads: pieces of the dims (FP8: [part][4] and both rotary pieces)
 constexpr int kChunk = 16;                    // tiles of a chunk
-template <bool kNv>
-constexpr int kBlocks = kNv ? 9 : 5;          // K-blocks of a tile: 64 dims of fp16; 128 of E4M3, the last 64
-template <bool kNv>
-constexpr int kLoads = kNv ? 3 : 5;           // stages that a tile's rows take
 // tensor memory: FP8 four accumulators of 96 columns; NVFP4 two, and a tile's values in three stages of 96 columns (192 dims:
 // with a stage for each of the nine K-blocks the wait and the fence of every four products took 116 us for the case below)
 template <bool kNv>
 constexpr int kDBufs = kNv ? 2 : 4;
 template <bool kNv>
 constexpr int kDCols = kNv ? 96 : 128;
-constexpr int kAStages = 3, kABlocks = 3, kACol = 192;
-static_assert(kAStages * kABlocks == 9 && kACol + 9 * 32 <= 512, "tensor memory");
+constexpr int kACol = 192;
+static_assert(kACol + kDQK / 2 <= 512, "tensor memory");
 template <bool kNv>
 constexpr int kThreads = kNv ? 512 : 256;
 // warps: 0..3 sums, 4 products, 5 latents (FP8), 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
 constexpr int kMmaWarp = 4, kTileWarp = 5, kQueryWarp = 6, kHeadWarp = 7;
-constexpr int kNumBars = 2 * kStages + 2 * 9 + 2 * 4 + 4 + 2 * kAStages + 1;
-constexpr size_t kSmem = 1024 + size_t(kStages) * kStage + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
+constexpr int kNumBars = 2 * 6 + 2 * kParts + 2 * 4 + 4 + 2 * kParts + 1;
+constexpr size_t kSmem = 1024 + kRingBytes + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
 static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables");
 constexpr uint32_t kPolls = 1u << 20;  // 4 s
 
@@ -144,31 +148,29 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
                 const __grid_constant__ CUtensorMap qmap, const __grid_constant__ MassArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qbuf = ring + kStages * kStage;
+  uint8_t* qbuf = ring + kRingBytes;
   float* acc = reinterpret_cast<float*>(qbuf + kQBytes);   // [kChunk][128]
   float* heads = acc + kChunk * kTok;                      // [2][2][96] factors and offsets
   const uint32_t bars = ptx::smem_u32(heads + 2 * 2 * kHeads);
-  const uint32_t full = bars, free = full + 8 * kStages;                // [kStages]
-  const uint32_t q_full = free + 8 * kStages, q_free = q_full + 8 * 9;  // [kBlocks]
-  const uint32_t d_full = q_free + 8 * 9, d_free = d_full + 8 * 4;      // [kDBufs]
-  const uint32_t h_full = d_free + 8 * 4, h_free = h_full + 16;         // [2]
-  const uint32_t a_full = h_free + 16, a_free = a_full + 8 * kAStages;  // [kAStages] NVFP4: values in tensor memory
-  const uint32_t mma_done = a_free + 8 * kAStages;
+  const uint32_t full = bars, free = full + 8 * 6;                        // [kStages]
+  const uint32_t q_full = free + 8 * 6, q_free = q_full + 8 * kParts;     // the query's blocks that a part needs first
+  const uint32_t d_full = q_free + 8 * kParts, d_free = d_full + 8 * 4;   // [kDBufs]
+  const uint32_t h_full = d_free + 8 * 4, h_free = h_full + 16;           // [2]
+  const uint32_t a_full = h_free + 16, a_free = a_full + 8 * kParts;      // NVFP4: a part's values in tensor memory
+  const uint32_t mma_done = a_free + 8 * kParts;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_sum[32], s_b, s_tile, s_bad[2];
-  constexpr int kB = kBlocks<kNv>, kD = kDBufs<kNv>;
+  constexpr int kD = kDBufs<kNv>, kSt = kStages<kNv>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kSt; ++i) {
       ptx::mbar_init(full + 8 * i, 1);
       ptx::mbar_init(free + 8 * i, kNv ? 8 : 1);
     }
-    for (int i = 0; i < kAStages; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       ptx::mbar_init(a_full + 8 * i, 8);
       ptx::mbar_init(a_free + 8 * i, 1);
-    }
-    for (int i = 0; i < kB; ++i) {
       ptx::mbar_init(q_full + 8 * i, 1);
       ptx::mbar_init(q_free + 8 * i, 1);
     }
@@ -326,52 +328,47 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
           if (g >= kD && !ptx::mbar_wait(d_free + 8 * buf, uint32_t(g / kD - 1) & 1u, kPolls)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t d = tmem + buf * kDCols<kNv>;
-          if constexpr (kNv) {
 #pragma unroll
-            for (int i = 0; i < kAStages; ++i) {
-              if (fresh_q && k == 0)
-                for (int j = 0; j < kABlocks && ok; ++j) ok = ptx::mbar_wait(q_full + 8 * (kABlocks * i + j), uint32_t(qn) & 1u, kPolls);
-              if (!ok || !ptx::mbar_wait(a_full + 8 * i, uint32_t(g) & 1u, kPolls)) { ok = false; break; }
-              ptx::tc_fence_after();
-              if (ptx::elect_one()) {
+          for (int i = 0; i < kParts; ++i) {
+            if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * i, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
+            if (!ptx::mbar_wait(kNv ? a_full + 8 * i : full + 8 * st, kNv ? uint32_t(g) & 1u : par, kPolls)) { ok = false; break; }
+            // (TMA's writes need no fence; the converters' in tensor memory do)
+            if (kNv) ptx::tc_fence_after();
+            const uint32_t in = r0 + st * kStage<kNv>;
+            if (ptx::elect_one()) {
+              if constexpr (kNv) {
 #pragma unroll
-                for (int kk = 0; kk < 4 * kABlocks; ++kk) {
-                  const int n = 4 * kABlocks * i + kk;  // of the tile's 36 products
+                for (int kk = 0; kk < 12; ++kk) {
+                  const int n = 12 * i + kk;  // 16 dims of the tile's 576
                   ptx::mma_f16_tmem_a(d, tmem + kACol + n * 8, ptx::sdesc_sw128(q0 + n / 4 * kQBlk + n % 4 * 32),
                                       ptx::idesc(0, 0, kTok, kHeads), n ? 1u : 0u);
                 }
                 ptx::mma_commit(a_free + 8 * i);
-                if (k == nt - 1 && leaves)
-                  for (int j = 0; j < kABlocks; ++j) ptx::mma_commit(q_free + 8 * (kABlocks * i + j));
-                if (i == kAStages - 1) ptx::mma_commit(d_full + 8 * buf);
-              }
-              __syncwarp();
-            }
-          } else {
+              } else {
 #pragma unroll
-            for (int j = 0; j < kB; ++j) {
-              if (fresh_q && k == 0 && !ptx::mbar_wait(q_full + 8 * j, uint32_t(qn) & 1u, kPolls)) { ok = false; break; }
-              if (!ptx::mbar_wait(full + 8 * st, par, kPolls)) { ok = false; break; }
-              const uint32_t blk = r0 + st * kStage;  // (TMA's writes need no fence)
-              if (ptx::elect_one()) {
-                const int steps = j < 4 ? 4 : 2;
+                for (int half = 0; half < 2; ++half)  // the query's E4M3, then its E5M2 part
 #pragma unroll
-                for (int part = 0; part < 2; ++part)  // the query's E4M3, then its E5M2 part
-#pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
-                    if (kk < steps)
-                      ptx::mma_f8f6f4(d, j < 4 ? ptx::sdesc_sw128(blk + kk * 32) : ptx::sdesc_sw64(blk + kk * 32),
-                                      ptx::sdesc_sw128(q0 + (j < 4 ? (4 * part + j) * kQBlk : 8 * kQBlk + part * 64) + kk * 32),
-                                      ptx::idesc(0, part, kTok, kHeads), (j | kk | part) ? 1u : 0u);
+                  for (int kk = 0; kk < 6; ++kk) {
+                    const int n = 6 * i + kk;         // 32 dims of the tile's 576
+                    const uint32_t q = n < 16 ? (4 * half + n / 4) * kQBlk + n % 4 * 32 : 8 * kQBlk + half * 64 + n % 2 * 32;
+                    ptx::mma_f8f6f4(d, kk < 4 ? ptx::sdesc_sw128(in + kk * 32) : ptx::sdesc_sw64(in + kTok * 128 + (kk - 4) * 32),
+                                    ptx::sdesc_sw128(q0 + q), ptx::idesc(0, half, kTok, kHeads), (i | half | kk) ? 1u : 0u);
+                  }
                 ptx::mma_commit(free + 8 * st);
-                if (k == nt - 1 && leaves) ptx::mma_commit(q_free + 8 * j);
-                if (j == kB - 1) ptx::mma_commit(d_full + 8 * buf);
               }
-              __syncwarp();
-              if (++st == kStages) {
-                st = 0;
-                par ^= 1;
+              if (k == nt - 1 && leaves) {  // (FP8: the first part's blocks are used by the second, too)
+                if (kNv || i == 2) ptx::mma_commit(q_free + 8 * i);
+                if (!kNv && i == 1) {
+                  ptx::mma_commit(q_free);
+                  ptx::mma_commit(q_free + 8);
+                }
               }
+              if (i == kParts - 1) ptx::mma_commit(d_full + 8 * buf);
+            }
+            __syncwarp();
+            if (!kNv && ++st == kSt) {
+              st = 0;
+              par ^= 1;
             }
           }
         }
@@ -392,15 +389,15 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         if (row == row_in) continue;
         row_in = row;
 #pragma unroll 1
-        for (int j = 0; j < kB; ++j) {
-          if (qn > 0 && !ptx::mbar_wait(q_free + 8 * j, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
-          if (lane == 0) {  // (FP8: both parts of the K-block)
-            const bool two = !kNv && j < 4;
-            const uint32_t bar = q_full + 8 * j;
-            const int at = kNv || j < 4 ? j : 8;
-            ptx::mbar_arrive_expect_tx(bar, two ? 2 * kQBlk : kQBlk);
-            ptx::tma_load_3d(q0 + at * kQBlk, &qmap, bar, 128 * at, 0, row);
-            if (two) ptx::tma_load_3d(q0 + (4 + at) * kQBlk, &qmap, bar, 128 * (4 + at), 0, row);
+        for (int i = 0; i < kParts; ++i) {
+          if (qn > 0 && !ptx::mbar_wait(q_free + 8 * i, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
+          if (lane == 0) {
+            // NVFP4: blocks 3i ..; FP8: 0, 1 of both parts, 2 of both, 3 of both and the rotary block
+            const uint32_t bar = q_full + 8 * i, blocks = kNv ? 7u << (3 * i) : i == 0 ? 0x33u : i == 1 ? 0x44u : 0x188u;
+            ptx::mbar_arrive_expect_tx(bar, __popc(blocks) * kQBlk);
+#pragma unroll
+            for (int j = 0; j < 9; ++j)
+              if (blocks >> j & 1) ptx::tma_load_3d(q0 + j * kQBlk, &qmap, bar, 128 * j, 0, row);
           }
           __syncwarp();
         }
@@ -409,7 +406,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
     }
     // no copy left in flight
     if (!ok)
-      for (int i = 0; i < 2 * kB; ++i) ptx::mbar_wait(q_full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+      for (int i = 0; i < 2 * kParts; ++i) ptx::mbar_wait(q_full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
   } else if (warp == kHeadWarp) {
     // ------------------------------------------------------------ the heads' factors and offsets
     int hn = 0;
@@ -463,19 +460,22 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         for (int k = 0; k < wk.nt && ok; ++k) {
           const int p0 = __shfl_sync(0xffffffffu, mine, 2 * k), p1 = __shfl_sync(0xffffffffu, mine, 2 * k + 1);
 #pragma unroll 1
-          for (int i = 0; i < kLoads<kNv>; ++i, ++c) {
-            const int st = c % kStages, j = kNv ? (i + 2) % 3 : i;  // (NVFP4: 128 B of the rows, the last ones first)
-            if (c >= kStages && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kStages - 1) & 1u, kPolls)) { ok = false; break; }
+          for (int i = 0; i < kParts; ++i, ++c) {
+            const int st = c % kSt, j = kNv ? (i + 2) % 3 : i;  // (NVFP4: the last 128 B, with the scales, first)
+            if (c >= kSt && !ptx::mbar_wait(free + 8 * st, uint32_t(c / kSt - 1) & 1u, kPolls)) { ok = false; break; }
             if (lane == 0) {
-              const uint32_t dst = r0 + st * kStage, bar = full + 8 * st, half = kNv || j < 4 ? kStage / 2 : kStage / 4;
+              const uint32_t dst = r0 + st * kStage<kNv>, bar = full + 8 * st;
               // (a page that is missing leaves what lay there: its tokens' sums are not used)
-              const uint32_t bytes = (p0 >= 0 ? half : 0) + (p1 >= 0 ? half : 0);
+              const uint32_t bytes = ((p0 >= 0) + (p1 >= 0)) * (kStage<kNv> / 2);
               if (bytes) ptx::mbar_arrive_expect_tx(bar, bytes);
               else ptx::mbar_arrive(bar);
-              const CUtensorMap* m = kNv || j < 4 ? &kmap : &rmap;
-              const int x = kNv ? 32 * j : 128 * j;
-              if (p0 >= 0) ptx::tma_load_3d(dst, m, bar, x, 0, p0);
-              if (p1 >= 0) ptx::tma_load_3d(dst + half, m, bar, x, 0, p1);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int pg = h ? p1 : p0;
+                if (pg < 0) continue;
+                ptx::tma_load_3d(dst + h * 8192, &kmap, bar, kNv ? 32 * j : 192 * j, 0, pg);
+                if (!kNv) ptx::tma_load_3d(dst + kTok * 128 + h * 4096, &rmap, bar, 192 * j + 128, 0, pg);
+              }
             }
             __syncwarp();
           }
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
       }
     }
     if (!ok)
-      for (int i = 0; i < 2 * kStages; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+      for (int i = 0; i < 2 * kSt; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
   } else if (kNv && warp >= 8) {
     // ------------------------------------------------------------ NVFP4 latents to fp16, two threads a token (a warp of
     // each group): 32 values are 16 columns of the token's lane of tensor memory, so they cost shared memory nothing
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + kACol;
     const uint8_t* mine = ring + tok * 128;
     auto piece = [&](int slot, int i) {  // 16 B of the token's 128 in a stage (128-B swizzle)
-      return *reinterpret_cast<const uint4*>(mine + slot * kStage + ((i ^ (tok & 7)) << 4));
+      return *reinterpret_cast<const uint4*>(mine + slot * kStage<kNv> + ((i ^ (tok & 7)) << 4));
     };
     int g = 0;
 #pragma unroll 1
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         take(0);
         if (!ptx::mbar_wait(full + 8 * (s0 + 1), par, kPolls)) { ok = false; break; }
 #pragma unroll
-        for (int i = 0; i < kAStages; ++i) {
+        for (int i = 0; i < kParts; ++i) {
           // the group's three of the tile's 18 pieces of 32 dims, of which the last two are rotary
           if (i == 1 && !ptx::mbar_wait(full + 8 * (s0 + 2), par, kPolls)) ok = false;
           uint32_t f[3][16];
@@ -609,7 +609,7 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
     if (!encode_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, lat_pool, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   } else {
-    // [num_pages][64][576] bytes: 128 dims of a page's rows at a time, and the 64 rope dims
+    // [num_pages][64][576] bytes: 128 dims of a page's rows at a time, and 64
     const uint64_t dims[3] = {uint64_t(kDQK), uint64_t(kPage), uint64_t(p.num_pages)};
     const uint64_t strides[2] = {uint64_t(kDQK), uint64_t(p.lat_page_stride)};
     const uint32_t box[3] = {128, kPage, 1}, rbox[3] = {64, kPage, 1};
