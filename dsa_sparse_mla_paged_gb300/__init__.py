@@ -385,27 +385,32 @@ def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_len
         _ptr(n_accepted), _ptr(out_tokens), _ptr(new_lens), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
-def _strided(fn, name, t, rows, heads, width):
-    """(address, elements between rows, elements between heads) of a bf16 tensor of `rows` rows (of `heads` heads, 0: none) of
-    `width` values each; its leading dimensions are the rows. None and addresses pass as they are (dense)."""
-    import torch
+_BF16 = _F32 = _I32 = None  # (torch is imported with the first call)
 
-    if t is None or isinstance(t, int):
-        return t, width * max(heads, 1), width
-    inner = (heads, width) if heads else (width,)
-    lead, strides = t.shape[:t.dim() - len(inner)], t.stride()
-    if t.dtype is not torch.bfloat16 or tuple(t.shape[t.dim() - len(inner):]) != inner or strides[-1] != 1:
-        raise ValueError(f"{fn}: {name} is not a bfloat16 tensor of rows of {' x '.join(map(str, inner))} values")
-    n, row = 1, None
-    for size, d in zip(reversed(lead), reversed(strides[:len(lead)])):
-        if size > 1:
-            if row is not None and d != row * n:
-                raise ValueError(f"{fn}: {name} is not {rows} equally spaced rows")
-            row = d if row is None else row
-            n *= size
-    if n != rows:
-        raise ValueError(f"{fn}: {name} has {n} rows, not {rows}")
-    return t.data_ptr(), row or width * max(heads, 1), strides[-2] if heads else 0
+
+def _strided(fn, name, t, rows, heads, width):
+    """(address, elements between rows, elements between heads) of a bf16 tensor of `rows` rows of `width` values, or of `heads`
+    times that; its leading dimensions are the rows. Addresses pass as they are (dense)."""
+    if isinstance(t, int):
+        return t, (heads or 1) * width, width
+    shape, strides, n = t.shape, t.stride(), 2 if heads else 1
+    if t.dtype is not _BF16 or len(shape) < n or shape[-1] != width or strides[-1] != 1 or (heads and shape[-2] != heads):
+        raise ValueError(f"{fn}: {name} is not a bfloat16 tensor of rows of {f'{heads} x ' if heads else ''}{width} values")
+    count, row = 1, (heads or 1) * width
+    if len(shape) == n + 1:
+        count = shape[0]
+        if count > 1:
+            row = strides[0]
+    else:
+        for size, d in zip(reversed(shape[:-n]), reversed(strides[:-n])):
+            if size > 1:
+                if count > 1 and d != row * count:
+                    raise ValueError(f"{fn}: {name} is not {rows} equally spaced rows")
+                row = d if count == 1 else row
+                count *= size
+    if count != rows:
+        raise ValueError(f"{fn}: {name} has {count} rows, not {rows}")
+    return t.data_ptr(), row, strides[-2] if heads else 0
 
 
 def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv_freq, positions, lat_pool, block_table,
@@ -413,22 +418,31 @@ def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv
     """Norms, rotation, the query [rows, 96, 576] and the new tokens' latents written into lat_pool. `q_nope`
     [rows, 96, 512], `q_rope` [rows, 96, 64], `c_kv` [rows, 512] and `k_rope` [rows, 64] may be strided (slices of the
     projections' outputs); `gamma_q` None: no norm of the query; `q_out` None: the cache alone; `c_kv` None: the query alone."""
-    import torch
+    global _BF16, _F32, _I32
+    if _BF16 is None:
+        import torch
 
+        _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
     fn, rows = "latent_frontend", params.batch * params.n_q
-    dims = LatentDims(eps=eps, interleaved=int(bool(interleaved)))
+    qn = qh = rn = rh = cr = kr = 0
     if q_out is not None:
-        q_nope, dims.q_nope_row, dims.q_nope_head = _strided(fn, "q_nope", q_nope, rows, 96, 512)
-        q_rope, dims.q_rope_row, dims.q_rope_head = _strided(fn, "q_rope", q_rope, rows, 96, 64)
-        q_out, gamma_q = _array(fn, "q_out", q_out, torch.bfloat16, rows * 96 * 576), _array(fn, "gamma_q", gamma_q, torch.bfloat16, 512)
+        q_nope, qn, qh = _strided(fn, "q_nope", q_nope, rows, 96, 512)
+        q_rope, rn, rh = _strided(fn, "q_rope", q_rope, rows, 96, 64)
+        q_out = _array(fn, "q_out", q_out, _BF16, rows * 55296)
+        gamma_q = _array(fn, "gamma_q", gamma_q, _BF16, 512)
+    else:
+        q_nope = q_rope = gamma_q = None
     if c_kv is not None:
-        c_kv, dims.c_kv_row, _ = _strided(fn, "c_kv", c_kv, rows, 0, 512)
-        k_rope, dims.k_rope_row, _ = _strided(fn, "k_rope", k_rope, rows, 0, 64)
-        gamma_kv = _array(fn, "gamma_kv", gamma_kv, torch.bfloat16, 512)
+        c_kv, cr, _ = _strided(fn, "c_kv", c_kv, rows, 0, 512)
+        k_rope, kr, _ = _strided(fn, "k_rope", k_rope, rows, 0, 64)
+        gamma_kv, lat_pool, block_table = _array(fn, "gamma_kv", gamma_kv, _BF16, 512), _ptr(lat_pool), _ptr(block_table)
+    else:
+        k_rope = gamma_kv = lat_pool = block_table = None
+    dims = LatentDims(qn, qh, rn, rh, cr, kr, eps, bool(interleaved))
     _check("dsa_latent_frontend", load().dsa_latent_frontend(
-        ctypes.byref(params), ctypes.byref(dims), _ptr(q_nope), _ptr(q_rope), gamma_q, c_kv, _ptr(k_rope), gamma_kv,
-        _array(fn, "inv_freq", inv_freq, torch.float32, 32), _array(fn, "positions", positions, torch.int32, rows), _ptr(lat_pool),
-        _ptr(block_table), _ptr(ctx_lens), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(params), ctypes.byref(dims), q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv,
+        _array(fn, "inv_freq", inv_freq, _F32, 32), _array(fn, "positions", positions, _I32, rows), lat_pool, block_table,
+        _ptr(ctx_lens), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def window_mla_decode(params, q, lat_pool, sinks, window, block_table, ctx_lens, out, lse, ws, stream=None):

@@ -1,9 +1,9 @@
 // Eviction of cached tokens by accumulated attention weight: choose the tokens that stay, plan the pages,
 // move the rows together.
 //
-// select: a cluster of 8 CTAs per request finds the k-th largest weight exactly, by three passes of histograms (11, 11
+// select: a cluster per request finds the k-th largest weight exactly, by three passes of histograms (11, 11
 //   and 10 bits of the order key) over its slices of the weights, summed through distributed shared memory; then
-//   one pass writes the kept tokens in order. The weights are read five times, from L2 after the first.
+//   one pass writes the kept tokens in order. The weights are read once, their keys stay in shared memory.
 // plan: one cluster ranks the free pages (if a shared page has to be replaced) and gives every request its fresh pages
 //   and its place in the list of moves.
 // apply: the moves, then tables, counts, lengths and weights. A page is rewritten in place where nobody else holds
@@ -22,7 +22,10 @@ namespace dsa {
 
 namespace {
 
-constexpr int kCtas = 8;        // of a cluster
+constexpr int kCtas = 8;        // of the plan's cluster
+constexpr int kMaxCl = 16;      // of the choice's: at most (16 KB of weights are then a CTA's up to 65,536 tokens, 48 K keys fit)
+constexpr int kClTokens = 16384;  // tokens a CTA is to have, until the cluster is full
+constexpr int kMaxKeys = 49152;   // keys that fit a CTA
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
 
@@ -97,15 +100,21 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
 __device__ __forceinline__ uint32_t mass_key(float f) { return f != f ? 0u : score_order_key(f); }
 
 // ---------------------------------------------------------------- select
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) evict_select_kernel(EvictArgs a) {
+// A cluster per request, of as many CTAs as its tokens need (1 to 16). A CTA has a slice of the tokens, whose keys
+// stay in shared memory (`room` of them; what is behind is read again), a warp a stretch of the slice, so that the order within it
+// takes ballots and no barrier.
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int room) {
   namespace cg = cooperative_groups;
+  extern __shared__ uint32_t keys[];
   __shared__ uint32_t hist[3][kBins];
-  __shared__ uint32_t sums[32];
-  __shared__ uint32_t s_bin, s_left, s_gt[kCtas], s_eq[kCtas], s_first[kCtas], s_mine;
+  __shared__ uint32_t sums[32], s_gt[32], s_eq[32];
+  __shared__ uint32_t s_bin, s_left, s_all[kMaxCl][3], s_shared[kMaxCl], s_mine;
   pdl_wait();
-  const int b = blockIdx.x / kCtas, n = a.ctx[b], budget = a.budgets[b];
+  cg::cluster_group cl = cg::this_cluster();
+  const int ctas = int(cl.num_blocks()), me = int(cl.block_rank()), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / ctas, n = a.ctx[b], budget = a.budgets[b];
   if (budget < 0 || n < 0 || n > a.cap || n <= budget) {  // (the same for the whole cluster)
-    if (blockIdx.x % kCtas == 0 && threadIdx.x == 0) {
+    if (me == 0 && tid == 0) {
       a.plan[kPlanNew * a.batch + b] = -1;
       a.plan[kPlanOld * a.batch + b] = n < 0 || n > a.cap ? 0 : n;
       a.plan[kPlanNeed * a.batch + b] = 0;
@@ -114,132 +123,182 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) evict_
     return;
   }
   ptx::cluster_arrive();
-  cg::cluster_group cl = cg::this_cluster();
-  const int me = int(cl.block_rank()), tid = threadIdx.x;
   const int head = min(a.sinks, budget), tail = min(a.recent, budget - head);
   const int mid = n - head - tail;                  // tokens to choose from
-  const int per = (mid + kCtas - 1) / kCtas, i0 = min(mid, me * per), i1 = min(mid, i0 + per);
-  const float* mass = a.mass + b * a.stride + head;
+  const int per = ((mid + ctas - 1) / ctas + 1023) & ~1023, i0 = min(mid, me * per), len = min(mid, i0 + per) - i0;
+  const int seg = per / 32, w0 = min(len, warp * seg), w1 = min(len, w0 + seg);  // (seg is a multiple of 32)
+  const float* mass = a.mass + b * a.stride + head + i0;
   int32_t* list = a.list + size_t(b) * a.cap;
+  auto key = [&](int i) { return i < room ? keys[i] : mass_key(mass[i]); };
   // the ends
-  for (int i = me * kThreads + tid; i < head; i += kCtas * kThreads) list[i] = i;
-  for (int i = me * kThreads + tid; i < tail; i += kCtas * kThreads) list[budget - tail + i] = n - tail + i;
+  for (int i = me * kThreads + tid; i < head; i += ctas * kThreads) list[i] = i;
+  for (int i = me * kThreads + tid; i < tail; i += ctas * kThreads) list[budget - tail + i] = n - tail + i;
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   if (tid == 0) s_mine = 0x7FFFFFFF;
   __syncthreads();
+  // Many weights may be alike (those of tokens that nothing looked at): one addition for a warp of them.
+  auto count = [&](uint32_t* h, bool in, uint32_t bin) {
+    int same;
+    __match_all_sync(0xffffffffu, in ? bin : ~0u, &same);
+    if (same) {
+      if (in && lane == 0) atomicAdd(h + bin, 32u);
+    } else if (in) {
+      atomicAdd(h + bin, 1u);
+    }
+  };
   const uint32_t k = uint32_t(budget - head - tail);
   uint32_t tau = 0xFFFFFFFFu, left = 0;             // keys above tau stay, and the first `left` that equal it
+  // the first pass also fills shared memory, four loads at a time
+  for (int j = w0; j < w1; j += 128) {
+    float m[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) m[d] = j + 32 * d + lane < w1 ? mass[j + 32 * d + lane] : 0.f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int i = j + 32 * d + lane;
+      const uint32_t x = mass_key(m[d]);
+      if (i < w1 && i < room) keys[i] = x;
+      count(hist[0], i < w1, x >> 21);
+    }
+  }
+  __syncthreads();
+  ptx::cluster_wait();  // every CTA has started: their shared memory can be read
   if (k > 0) {
     tau = 0;
     left = k;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t bins = pass == 2 ? 1024 : kBins;
-      // the bits above this pass's are those of tau
-      const uint64_t above = ~uint64_t(0) << (pass == 0 ? 32 : pass == 1 ? 21 : 10);
-      for (int j0 = i0; j0 < i1; j0 += kThreads) {
-        const int i = j0 + tid;
-        const uint32_t key = i < i1 ? mass_key(mass[i]) : 0;
-        const bool in = i < i1 && ((key ^ tau) & uint32_t(above)) == 0;
-        const uint32_t bin = in ? (key >> shift) & (bins - 1) : ~0u;
-        // many weights alike (those of tokens that nothing looked at): one addition for a warp of them
-        int same;
-        __match_all_sync(0xffffffffu, bin, &same);
-        if (same) {
-          if (in && (tid & 31) == 0) atomicAdd(&hist[pass][bin], 32u);
-        } else if (in) {
-          atomicAdd(&hist[pass][bin], 1u);
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+      if (pass > 0) {
+        const int above = pass == 1 ? 21 : 10;  // the bits from there on are those of tau
+        for (int j = w0; j < w1; j += 32) {
+          const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
+          count(hist[pass], j + lane < w1 && (x ^ tau) >> above == 0, (x >> shift) & (bins - 1));
         }
+        __syncthreads();
       }
-      __syncthreads();
-      if (pass == 0) ptx::cluster_wait();  // every CTA has started: their shared memory can be read
-      cl.sync();
+      if (ctas > 1) cl.sync();
       // thread t: bins from the top, 2t and 2t + 1 below it
       uint32_t c[2] = {0, 0};
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const int bin = int(bins) - 1 - (2 * tid + d);
-        if (bin >= 0)
-          for (int r = 0; r < kCtas; ++r) c[d] += cl.map_shared_rank(&hist[pass][0], r)[bin];
+      const int bin = bins - 2 - 2 * tid;
+      if (bin >= 0) {
+        for (int r = 0; r < ctas; ++r) {
+          const uint2 v = *reinterpret_cast<const uint2*>((ctas > 1 ? cl.map_shared_rank(&hist[pass][0], r) : hist[pass]) + bin);
+          c[0] += v.y;
+          c[1] += v.x;
+        }
       }
       uint32_t total;
       const uint32_t upto = block_scan<uint32_t>(c[0] + c[1], sums, total), before = upto - c[0] - c[1];
       if (before < left && upto >= left) {
         const int second = before + c[0] < left;
-        s_bin = bins - 1 - (2 * tid + second);
+        s_bin = bin + 1 - second;
         s_left = left - before - (second ? c[0] : 0);
       }
       __syncthreads();
       tau |= s_bin << shift;
       left = s_left;
-      __syncthreads();
     }
-  } else {
-    ptx::cluster_wait();
   }
-  // how many of each kind the slices hold
+  // how many of each kind the warps and the CTAs hold, and the first token that goes (equal ones go from `left` on)
   uint32_t gt = 0, eq = 0;
-  for (int i = i0 + tid; i < i1; i += kThreads) {
-    const uint32_t key = mass_key(mass[i]);
-    gt += k > 0 && key > tau;
-    eq += k > 0 && key == tau;
+  for (int j = w0; j < w1; j += 32) {
+    const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > 0 && x > tau));
+    eq += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > 0 && x == tau));
   }
-  uint32_t all_gt, all_eq;
-  block_scan<uint32_t>(gt, sums, all_gt);
-  block_scan<uint32_t>(eq, sums, all_eq);
-  if (tid < kCtas) {
-    *cl.map_shared_rank(s_gt + me, tid) = all_gt;
-    *cl.map_shared_rank(s_eq + me, tid) = all_eq;
+  if (lane == 0) {
+    s_gt[warp] = gt;
+    s_eq[warp] = eq;
   }
-  cl.sync();
+  __syncthreads();
   gt = eq = 0;
-  for (int r = 0; r < me; ++r) {
-    gt += s_gt[r];
-    eq += s_eq[r];
+  uint32_t all_gt = 0, all_eq = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w == warp) {
+      gt = all_gt;
+      eq = all_eq;
+    }
+    all_gt += s_gt[w];
+    all_eq += s_eq[w];
+  }
+  if (ctas > 1) {
+    if (tid < ctas) {
+      uint32_t* to = cl.map_shared_rank(&s_all[me][0], tid);
+      to[0] = all_gt;
+      to[1] = all_eq;
+    }
+    cl.sync();
+    for (int r = 0; r < me; ++r) {
+      gt += s_all[r][0];
+      eq += s_all[r][1];
+    }
   }
   // the kept tokens, in order; a tie's rank decides
-  int first = 0x7FFFFFFF;  // the first that goes
-  for (int j0 = i0; j0 < i1; j0 += kThreads) {
-    const int i = j0 + tid;
-    const uint32_t key = i < i1 ? mass_key(mass[i]) : 0;
-    const bool is_gt = i < i1 && k > 0 && key > tau, is_eq = i < i1 && k > 0 && key == tau;
-    uint32_t total;
-    const uint32_t up = block_scan<uint32_t>(uint32_t(is_gt) | uint32_t(is_eq) << 16, sums, total);
-    const uint32_t g = gt + (up & 0xFFFF) - is_gt, e = eq + (up >> 16) - is_eq;  // before this one
-    gt += total & 0xFFFF;
-    eq += total >> 16;
-    if (is_gt || (is_eq && e < left)) list[head + g + min(e, left)] = head + i;
-    else if (i < i1) first = min(first, head + i);
+  const uint32_t below = (1u << lane) - 1;
+  int first = 0x7FFFFFFF;
+  for (int j = w0; j < w1; j += 32) {
+    const int i = j + lane;
+    const uint32_t x = i < w1 ? key(i) : 0;
+    const bool is_gt = i < w1 && k > 0 && x > tau, is_eq = i < w1 && k > 0 && x == tau;
+    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me2 = __ballot_sync(0xffffffffu, is_eq);
+    const uint32_t g = gt + __popc(mg & below), e = eq + __popc(me2 & below);
+    if (is_gt || (is_eq && e < left)) list[head + g + min(e, left)] = head + i0 + i;
+    else if (i < w1) first = min(first, head + i0 + i);
+    gt += __popc(mg);
+    eq += __popc(me2);
   }
-  if (first != 0x7FFFFFFF) atomicMin(&s_mine, uint32_t(first));
+  first = __reduce_min_sync(0xffffffffu, first);
+  if (lane == 0 && first != 0x7FFFFFFF) atomicMin(&s_mine, uint32_t(first));
   __syncthreads();
-  if (tid == 0) *cl.map_shared_rank(s_first + me, 0) = s_mine;
-  cl.sync();  // (also: the list is complete)
-  if (me != 0) return;
-  // the request's pages
-  first = 0x7FFFFFFF;
-  for (int r = 0; r < kCtas; ++r) first = min(first, int(s_first[r]));
+  first = int(s_mine);
+  if (ctas > 1) {
+    if (tid < ctas) cl.map_shared_rank(&s_all[me][0], tid)[2] = uint32_t(first);
+    cl.sync();
+    for (int r = 0; r < ctas; ++r) first = min(first, int(s_all[r][2]));
+  }
+  // the request's pages, a range of them each
   const int used = pages_of(n), want = pages_of(budget), from = first < budget ? first / kPage : want;
+  const int per_page = (used + ctas - 1) / ctas, p0 = min(used, me * per_page), p1 = min(used, p0 + per_page);
   const int32_t* row = a.table + size_t(b) * a.max_pages;
+  int32_t* fresh = a.fresh + size_t(b) * a.max_pages;
   uint32_t bad = 0, need = 0;
-  for (int j0 = 0; j0 < used; j0 += kThreads) {
+  for (int j0 = p0; j0 < p1; j0 += kThreads) {
     const int j = j0 + tid;
-    uint32_t shared = 0;
-    if (j < used) {
+    int shared = 0;
+    if (j < p1) {
       const int pg = row[j];
-      if (pg < 0 || pg >= a.num_pages) bad |= DSA_DEVERR_BLOCK_TABLE;
-      else if (a.refs[pg] < 1) bad |= DSA_DEVERR_PAGES;
-      else shared = j >= from && j < want && a.refs[pg] > 1;
+      if (pg < 0 || pg >= a.num_pages) {
+        bad |= DSA_DEVERR_BLOCK_TABLE;
+      } else {
+        const int refs = a.refs[pg];
+        if (refs < 1) bad |= DSA_DEVERR_PAGES;
+        else shared = j >= from && j < want && refs > 1;
+      }
     }
-    uint32_t total;
-    const uint32_t up = block_scan<uint32_t>(shared, sums, total);
-    if (j < used) a.fresh[size_t(b) * a.max_pages + j] = shared ? int(need + up - 1) : -1;
+    uint32_t total = 0, up = 0;
+    if (__syncthreads_or(shared)) up = block_scan<uint32_t>(shared, sums, total);
+    if (j < p1) fresh[j] = shared ? int(need + up - 1) : -1;
     need += total;
   }
   bad = uint32_t(__syncthreads_or(int(bad & DSA_DEVERR_BLOCK_TABLE)) ? DSA_DEVERR_BLOCK_TABLE : 0) |
         uint32_t(__syncthreads_or(int(bad & DSA_DEVERR_PAGES)) ? DSA_DEVERR_PAGES : 0);
-  if (tid == 0) {
+  if (ctas > 1) {
+    if (tid < ctas) *cl.map_shared_rank(s_shared + me, tid) = need | bad << 24;  // (at most 2^22 pages, bits 0 and 4)
+    cl.sync();
+    uint32_t before = 0, all = 0;
+    for (int r = 0; r < ctas; ++r) {
+      const uint32_t v = s_shared[r];
+      bad |= v >> 24;
+      if (r < me) before += v & 0xFFFFFF;
+      all += v & 0xFFFFFF;
+    }
+    if (before > 0 && need > 0)
+      for (int j = p0 + tid; j < p1; j += kThreads)
+        if (fresh[j] >= 0) fresh[j] += int(before);
+    need = all;
+  }
+  if (me == 0 && tid == 0) {
     if (bad) atomicOr(a.err, int(bad));
     a.plan[kPlanNew * a.batch + b] = bad ? -1 : budget;
     a.plan[kPlanOld * a.batch + b] = n;
@@ -323,12 +382,17 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) evict_
 }
 
 // ---------------------------------------------------------------- apply
-// What a warp needs to write a gathered unit.
+// A unit in hand: what to gather (lane i has the addresses of rows i and i + 32; of words, that of the first
+// weight's place in the list), and where it goes.
 struct Unit {
-  char* dst;    // rows, whole 16 B each (null: none)
-  char* words;  // index keys' scales, or weights (null: none)
-  int bytes, n_words, words_at;  // where in the slot the words begin
+  const char* src[2];
+  const char* scale[2];  // index keys: the tokens' scales
+  const int32_t* list;   // weights: which
+  char* dst;             // rows, whole 16 B each (null: none)
+  char* words;           // index keys' scales, or weights (null: none)
+  int n, fmt, width;     // tokens; bytes of a row
 };
+constexpr int kFmtMass = 4;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
@@ -337,40 +401,38 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
 }
 
-// Gathers tokens' rows of kChunks 16-B chunks: lane i has the addresses of rows i and i + 32.
-template <int kChunks>
-__device__ __forceinline__ void gather_rows(uint32_t smem, const char* r0, const char* r1, int rows, int lane) {
-  const int n = rows * kChunks;
-#pragma unroll 4
-  for (int c0 = 0; c0 < n; c0 += 32) {  // (whole warps: the shuffles)
-    const int c = c0 + lane, row = c / kChunks, off = c - row * kChunks;
-    const uint64_t lo = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(r0), row & 31);
-    const uint64_t hi = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(r1), row & 31);
-    if (c < n) cp_async16(smem + c * 16, reinterpret_cast<const char*>(row < 32 ? lo : hi) + off * 16);
-  }
-}
+// What a CTA keeps of the requests' plans in shared memory, if there are no more of them.
+constexpr int kKept = 512;
+struct Plans {
+  long long item[kKept];
+  int32_t len[kKept], from[kKept], fresh[kKept];
+};
 
-// Starts the gathering of item `it` by a warp.
-__device__ __forceinline__ Unit gather(const EvictArgs& a, const TokenPools& pools, long long it, uint32_t smem, int lane) {
+// Where item `it` begins and ends. kNear: the plans are in shared memory.
+template <bool kNear>
+__device__ __forceinline__ Unit look_up(const EvictArgs& a, const TokenPools& pools, const Plans& near, long long it, int lane) {
   // the request: the last whose items begin at or before it (those without any share their start with the next)
   int lo = 0, hi = a.batch;
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    if (a.item[m] <= it) lo = m;
+    if ((kNear ? near.item[m] : a.item[m]) <= it) lo = m;
     else hi = m;
   }
-  const int b = lo, len = a.plan[kPlanNew * a.batch + b], from = a.plan[kPlanFirstPage * a.batch + b];
+  const int b = lo, len = kNear ? near.len[b] : a.plan[kPlanNew * a.batch + b];
+  const int from = kNear ? near.from[b] : a.plan[kPlanFirstPage * a.batch + b];
+  const int first_fresh = kNear ? near.fresh[b] : a.plan[kPlanFresh * a.batch + b];
   const int pages = pages_of(len) - from;
-  long long q = it - a.item[b];
+  long long q = it - (kNear ? near.item[b] : a.item[b]);
   const int32_t* list = a.list + size_t(b) * a.cap;
   const int32_t* row = a.table + size_t(b) * a.max_pages;
-  Unit u{nullptr, nullptr, 0, 0, 0};
+  Unit u = {};
   if (q >= (long long)pages * a.units) {  // weights
-    const int i0 = from * kPage + int(q - (long long)pages * a.units) * kMassUnit, n = min(kMassUnit, len - i0);
-    const float* mass = a.mass + b * a.stride;
-    for (int i = lane; i < n; i += 32) cp_async4(smem + i * 4, mass + list[i0 + i]);
+    const int i0 = from * kPage + int(q - (long long)pages * a.units) * kMassUnit;
+    u.fmt = kFmtMass;
+    u.n = min(kMassUnit, len - i0);
+    u.src[0] = reinterpret_cast<const char*>(a.mass + b * a.stride);
+    u.list = list + i0;
     u.words = reinterpret_cast<char*>(a.mass + b * a.stride + i0);
-    u.n_words = n;
     return u;
   }
   // the pool, layer, page and part of it
@@ -381,39 +443,60 @@ __device__ __forceinline__ Unit gather(const EvictArgs& a, const TokenPools& poo
     if (q < size) break;
     q -= size;
   }
-  const int fmt = pools.fmt[pool], layer = int(q / ((long long)pages * per)), r = int(q - (long long)layer * pages * per);
+  u.fmt = pools.fmt[pool];
+  const int layer = int(q / ((long long)pages * per)), r = int(q - (long long)layer * pages * per);
   const int j = from + r / per, tokens = kPage / per, slot0 = (r % per) * tokens, i0 = j * kPage + slot0;
-  const int n = min(tokens, len - i0);
-  if (n <= 0) return u;
+  u.n = max(0, min(tokens, len - i0));
+  if (u.n == 0) return u;
+  u.width = u.fmt == DSA_TOKEN_KEY_FP8 ? 128 : u.fmt == DSA_TOKEN_KEY_MXFP4 ? 64 : u.fmt == DSA_TOKEN_LAT_FP8 ? 576 : 352;
   char* base = pools.base[pool] + layer * pools.layer_stride[pool];
-  const int rank = a.fresh[size_t(b) * a.max_pages + j];
-  const int to = rank < 0 ? row[j] : a.free[a.plan[kPlanFresh * a.batch + b] + rank];
-  char* dst = base + int64_t(to) * pools.page_stride[pool];
-  const int width = fmt == DSA_TOKEN_KEY_FP8 ? 128 : fmt == DSA_TOKEN_KEY_MXFP4 ? 64 : fmt == DSA_TOKEN_LAT_FP8 ? 576 : 352;
-  const char* src[2] = {nullptr, nullptr};
+  const int rank = a.fresh[size_t(b) * a.max_pages + j], here = row[j];
+  int tok[2], pg[2];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) tok[d] = list[i0 + min(32 * d + lane, u.n - 1)];
+#pragma unroll
+  for (int d = 0; d < 2; ++d) pg[d] = row[tok[d] / kPage];
 #pragma unroll
   for (int d = 0; d < 2; ++d) {
-    const int i = 32 * d + lane;
-    if (i < n) {
-      const int tok = list[i0 + i];
-      const char* page = base + int64_t(row[tok / kPage]) * pools.page_stride[pool];
-      src[d] = page + (tok % kPage) * width;
-      if (fmt <= DSA_TOKEN_KEY_MXFP4)  // its scale, behind the rows
-        cp_async4(smem + kPage * width + i * 4, page + kPage * width + (tok % kPage) * 4);
+    const char* page = base + int64_t(pg[d]) * pools.page_stride[pool];
+    u.src[d] = page + (tok[d] % kPage) * u.width;
+    u.scale[d] = page + kPage * u.width + (tok[d] % kPage) * 4;
+  }
+  const int to = rank < 0 ? here : a.free[first_fresh + rank];
+  char* dst = base + int64_t(to) * pools.page_stride[pool];
+  u.dst = dst + slot0 * u.width;
+  if (u.fmt <= DSA_TOKEN_KEY_MXFP4) u.words = dst + kPage * u.width;
+  return u;
+}
+
+// Rows of kChunks 16-B chunks.
+template <int kChunks>
+__device__ __forceinline__ void gather_rows(uint32_t smem, const Unit& u, int lane) {
+  const int n = u.n * kChunks;
+#pragma unroll 4
+  for (int c0 = 0; c0 < n; c0 += 32) {  // (whole warps: the shuffles)
+    const int c = c0 + lane, row = c / kChunks, off = c - row * kChunks;
+    const uint64_t lo = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(u.src[0]), row & 31);
+    const uint64_t hi = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(u.src[1]), row & 31);
+    if (c < n) cp_async16(smem + c * 16, reinterpret_cast<const char*>(row < 32 ? lo : hi) + off * 16);
+  }
+}
+
+__device__ __forceinline__ void gather(const Unit& u, uint32_t smem, int lane) {
+  if (u.n > 0) {
+    if (u.fmt == DSA_TOKEN_LAT_FP8) gather_rows<36>(smem, u, lane);
+    else if (u.fmt == DSA_TOKEN_LAT_NVFP4) gather_rows<22>(smem, u, lane);
+    else if (u.fmt == DSA_TOKEN_KEY_FP8) gather_rows<8>(smem, u, lane);
+    else if (u.fmt == DSA_TOKEN_KEY_MXFP4) gather_rows<4>(smem, u, lane);
+    else
+      for (int i = lane; i < u.n; i += 32) cp_async4(smem + i * 4, u.src[0] + int64_t(u.list[i]) * 4);
+    if (u.fmt <= DSA_TOKEN_KEY_MXFP4) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+        if (32 * d + lane < u.n) cp_async4(smem + kPage * u.width + (32 * d + lane) * 4, u.scale[d]);
     }
   }
-  if (fmt == DSA_TOKEN_LAT_FP8) gather_rows<36>(smem, src[0], src[1], n, lane);
-  else if (fmt == DSA_TOKEN_LAT_NVFP4) gather_rows<22>(smem, src[0], src[1], n, lane);
-  else if (fmt == DSA_TOKEN_KEY_FP8) gather_rows<8>(smem, src[0], src[1], n, lane);
-  else gather_rows<4>(smem, src[0], src[1], n, lane);
-  u.dst = dst + slot0 * width;
-  u.bytes = n * width;
-  if (fmt <= DSA_TOKEN_KEY_MXFP4) {
-    u.words = dst + kPage * width;
-    u.n_words = n;
-    u.words_at = kPage * width;
-  }
-  return u;
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 __device__ __forceinline__ void drop_ref(const EvictArgs& a, int pg) {
@@ -428,20 +511,33 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
                                                                         const __grid_constant__ TokenPools pools) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_ok;
+  __shared__ Plans near;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long items = a.head[kHeadItems], per = (long long)gridDim.x * kMoveWarps;
   const long long batches = (items + per - 1) / per;
   unsigned long long* arrived = reinterpret_cast<unsigned long long*>(a.head + kHeadArrived);
   auto slot = [&](long long k) { return smem + (size_t(k & 1) * kMoveWarps + warp) * kSlot; };
-  auto start = [&](long long k) {
+  auto unit = [&](long long k) {
     const long long it = k * per + (long long)blockIdx.x * kMoveWarps + warp;
-    Unit u{nullptr, nullptr, 0, 0, 0};
-    if (it < items) u = gather(a, pools, it, ptx::smem_u32(slot(k)), lane);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    return u;
+    if (it >= items) return Unit{};
+    return a.batch <= kKept ? look_up<true>(a, pools, near, it, lane) : look_up<false>(a, pools, near, it, lane);
   };
-  Unit now = {};
-  if (batches > 0) now = start(0);
+  if (a.batch <= kKept && batches > 0) {
+    for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
+      near.item[b] = a.item[b];
+      near.len[b] = a.plan[kPlanNew * a.batch + b];
+      near.from[b] = a.plan[kPlanFirstPage * a.batch + b];
+      near.fresh[b] = a.plan[kPlanFresh * a.batch + b];
+    }
+    __syncthreads();
+  }
+  // A unit's addresses take a chain of loads, so they are looked up a batch ahead, while rows are under way.
+  Unit now = {}, next = {};
+  if (batches > 0) {
+    now = unit(0);
+    gather(now, ptx::smem_u32(slot(0)), lane);
+    next = unit(1);
+  }
   for (long long k = 0; k < batches; ++k) {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();  // this CTA has read what it needs of batches up to k
@@ -449,23 +545,18 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
       __threadfence();
       atomicAdd(arrived, 1ull);
     }
-    Unit next = {};
     if (k + 1 < batches) {
       if (lane == 0) ptx::bulk_wait_read();  // the other half was written out from
       __syncwarp();
-      next = start(k + 1);
+      gather(next, ptx::smem_u32(slot(k + 1)), lane);
     }
     if (threadIdx.x == 0) {
       const unsigned long long goal = (unsigned long long)(k + 1) * gridDim.x;
       int ok = 0;
-      for (uint32_t i = 0; i < kBarrierPolls; ++i) {
+      for (uint32_t i = 0; i < kBarrierPolls && !ok; ++i) {
         unsigned long long v;
         asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(arrived) : "memory");
-        if (v >= goal) {
-          ok = 1;
-          break;
-        }
-        __nanosleep(64);
+        ok = v >= goal;
       }
       s_ok = ok;
     }
@@ -477,25 +568,30 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
       return;
     }
     const uint8_t* from = slot(k);
-    for (int i = lane; i < now.n_words; i += 32)
-      reinterpret_cast<uint32_t*>(now.words)[i] = reinterpret_cast<const uint32_t*>(from + now.words_at)[i];
+    if (now.words) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(from + (now.dst ? kPage * now.width : 0));
+      for (int i = lane; i < now.n; i += 32) reinterpret_cast<uint32_t*>(now.words)[i] = w[i];
+    }
     ptx::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (now.dst) ptx::bulk_store(now.dst, from, uint32_t(now.bytes));
+      if (now.dst) ptx::bulk_store(now.dst, from, uint32_t(now.n * now.width));
       ptx::bulk_commit();
     }
     __syncwarp();
     now = next;
+    next = unit(k + 2);
   }
   if (lane == 0) ptx::bulk_wait_read();
-  // Every row has been read: tables, counts and lengths, a CTA a request ...
-  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
-    const int len = a.plan[kPlanNew * a.batch + b];
+  // Every row has been read: tables, counts and lengths ...
+  const int row_pieces = (a.max_pages + int(blockDim.x) - 1) / int(blockDim.x);
+  for (long long q = blockIdx.x; q < (long long)a.batch * row_pieces; q += gridDim.x) {
+    const int b = int(q / row_pieces), piece = int(q - (long long)b * row_pieces), len = a.plan[kPlanNew * a.batch + b];
     if (len < 0) continue;
     int32_t* row = a.table + size_t(b) * a.max_pages;
     const int first = a.plan[kPlanFirstPage * a.batch + b], want = pages_of(len), used = pages_of(a.plan[kPlanOld * a.batch + b]);
-    for (int j = first + int(threadIdx.x); j < used; j += blockDim.x) {
+    const int j = piece * int(blockDim.x) + int(threadIdx.x);
+    if (j >= first && j < used) {
       const int pg = row[j], rank = a.fresh[size_t(b) * a.max_pages + j];
       if (j >= want) {
         row[j] = -1;
@@ -507,7 +603,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
         drop_ref(a, pg);
       }
     }
-    if (threadIdx.x == 0) a.ctx[b] = len;
+    if (piece == 0 && threadIdx.x == 0) a.ctx[b] = len;
   }
   // ... and the old indices of what stays and the weights behind the new ends, in pieces of the requests
   const int piece = 4 * int(blockDim.x), pieces = (a.cap + piece - 1) / piece;
@@ -565,8 +661,30 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   a.sinks = sinks;
   a.recent = recent;
   a.units = q.units;
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(kCtas * p.batch), dim3(kThreads), 0, st, a);
+  int ctas = 1;
+  while (ctas < kMaxCl && L.cap > ctas * kClTokens) ctas *= 2;
+  const int slice = ((L.cap + ctas - 1) / ctas + 1023) & ~1023, room = slice < kMaxKeys ? slice : kMaxKeys;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas * p.batch);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = size_t(room) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, room);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_pdl(evict_plan_kernel, dim3(kCtas), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(evict_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMoveSmem));
