@@ -25,7 +25,7 @@ namespace {
 constexpr int kCtas = 8;        // of the plan's cluster
 constexpr int kMaxCl = 16;      // of the choice's: at most (16 KB of weights are then a CTA's up to 65,536 tokens, 48 K keys fit)
 constexpr int kClTokens = 16384;  // tokens a CTA is to have, until the cluster is full
-constexpr int kMaxKeys = 49152;   // keys that fit a CTA
+constexpr int kMaxKeys = 47104;   // keys that fit a CTA
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
 
@@ -37,10 +37,10 @@ constexpr int kMassUnit = 1024; // weights
 static_assert(kSlot >= kMassUnit * 4, "weights");
 constexpr int kMoveWarps = 12;
 constexpr size_t kMoveSmem = size_t(2) * kMoveWarps * kSlot;
-constexpr uint32_t kBarrierPolls = 1u << 22;  // 0.1 us and more each
+constexpr uint32_t kGridPolls = 1u << 22;  // of a counter in L2, 0.5 us and more each
 
 enum { kPlanNew = 0, kPlanOld = 1, kPlanFirstPage = 2, kPlanNeed = 3, kPlanFresh = 4 };  // int32 [5][batch]
-enum { kHeadItems = 0, kHeadArrived = 1 };                                 // int64 [4]
+enum { kHeadItems = 0, kHeadArrived = 1 };                                 // int64 [8]
 
 struct TokenPools {
   char* base[kMaxPools];
@@ -106,8 +106,8 @@ __device__ __forceinline__ uint32_t mass_key(float f) { return f != f ? 0u : sco
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int room) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[3][kBins];
-  __shared__ uint32_t sums[32], s_gt[32], s_eq[32];
+  __shared__ __align__(8) uint32_t hist[3][kBins], s_total[kBins];
+  __shared__ uint32_t s_part[kThreads], sums[32], s_gt[32], s_eq[32];
   __shared__ uint32_t s_bin, s_left, s_all[kMaxCl][3], s_shared[kMaxCl], s_mine;
   pdl_wait();
   cg::cluster_group cl = cg::this_cluster();
@@ -138,23 +138,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   __syncthreads();
   // Many weights may be alike (those of tokens that nothing looked at): one addition for a warp of them.
   auto count = [&](uint32_t* h, bool in, uint32_t bin) {
-    int same;
-    __match_all_sync(0xffffffffu, in ? bin : ~0u, &same);
-    if (same) {
-      if (in && lane == 0) atomicAdd(h + bin, 32u);
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (m == 0) return;
+    const int lead = __ffs(m) - 1;
+    const uint32_t b0 = __shfl_sync(0xffffffffu, bin, lead);
+    if (__all_sync(0xffffffffu, !in || bin == b0)) {
+      if (lane == lead) atomicAdd(h + bin, uint32_t(__popc(m)));
     } else if (in) {
       atomicAdd(h + bin, 1u);
     }
   };
   const uint32_t k = uint32_t(budget - head - tail);
   uint32_t tau = 0xFFFFFFFFu, left = 0;             // keys above tau stay, and the first `left` that equal it
-  // the first pass also fills shared memory, four loads at a time
-  for (int j = w0; j < w1; j += 128) {
-    float m[4];
+  // the first pass also fills shared memory, eight loads at a time
+  for (int j = w0; j < w1; j += 256) {
+    float m[8];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) m[d] = j + 32 * d + lane < w1 ? mass[j + 32 * d + lane] : 0.f;
+    for (int d = 0; d < 8; ++d) m[d] = j + 32 * d + lane < w1 ? mass[j + 32 * d + lane] : 0.f;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
+    for (int d = 0; d < 8; ++d) {
       const int i = j + 32 * d + lane;
       const uint32_t x = mass_key(m[d]);
       if (i < w1 && i < room) keys[i] = x;
@@ -171,22 +173,34 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
       if (pass > 0) {
         const int above = pass == 1 ? 21 : 10;  // the bits from there on are those of tau
+#pragma unroll 4
         for (int j = w0; j < w1; j += 32) {
           const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
           count(hist[pass], j + lane < w1 && (x ^ tau) >> above == 0, (x >> shift) & (bins - 1));
         }
         __syncthreads();
       }
-      if (ctas > 1) cl.sync();
+      if (ctas > 1) {
+        // every CTA adds up its share of the bins over all of them, and hands the sums out. (Every CTA reading all bins
+        // of all took 13,000 cycles for 16 CTAs.)
+        cl.sync();
+        const int share = bins / ctas, bin = tid % share, step = kThreads / share;
+        uint32_t sum = 0;
+        for (int r = tid / share; r < ctas; r += step) sum += cl.map_shared_rank(&hist[pass][0], (r + me) % ctas)[me * share + bin];
+        if (tid < share) s_part[tid] = 0;
+        __syncthreads();
+        if (sum) atomicAdd(&s_part[bin], sum);
+        __syncthreads();
+        for (int r = tid / share; r < ctas; r += step) cl.map_shared_rank(s_total, r)[me * share + bin] = s_part[bin];
+        cl.sync();
+      }
       // thread t: bins from the top, 2t and 2t + 1 below it
       uint32_t c[2] = {0, 0};
       const int bin = bins - 2 - 2 * tid;
       if (bin >= 0) {
-        for (int r = 0; r < ctas; ++r) {
-          const uint2 v = *reinterpret_cast<const uint2*>((ctas > 1 ? cl.map_shared_rank(&hist[pass][0], r) : hist[pass]) + bin);
-          c[0] += v.y;
-          c[1] += v.x;
-        }
+        const uint2 v = *reinterpret_cast<const uint2*>((ctas > 1 ? s_total : hist[pass]) + bin);
+        c[0] = v.y;
+        c[1] = v.x;
       }
       uint32_t total;
       const uint32_t upto = block_scan<uint32_t>(c[0] + c[1], sums, total), before = upto - c[0] - c[1];
@@ -202,6 +216,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   }
   // how many of each kind the warps and the CTAs hold, and the first token that goes (equal ones go from `left` on)
   uint32_t gt = 0, eq = 0;
+#pragma unroll 4
   for (int j = w0; j < w1; j += 32) {
     const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
     gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > 0 && x > tau));
@@ -212,16 +227,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     s_eq[warp] = eq;
   }
   __syncthreads();
-  gt = eq = 0;
-  uint32_t all_gt = 0, all_eq = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w == warp) {
-      gt = all_gt;
-      eq = all_eq;
+  // (every warp scans the warps' counts)
+  uint32_t up_gt = s_gt[lane], up_eq = s_eq[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, up_gt, o), y = __shfl_up_sync(0xffffffffu, up_eq, o);
+    if (lane >= o) {
+      up_gt += x;
+      up_eq += y;
     }
-    all_gt += s_gt[w];
-    all_eq += s_eq[w];
   }
+  const uint32_t all_gt = __shfl_sync(0xffffffffu, up_gt, 31), all_eq = __shfl_sync(0xffffffffu, up_eq, 31);
+  gt = __shfl_sync(0xffffffffu, up_gt, warp) - gt;
+  eq = __shfl_sync(0xffffffffu, up_eq, warp) - eq;
   if (ctas > 1) {
     if (tid < ctas) {
       uint32_t* to = cl.map_shared_rank(&s_all[me][0], tid);
@@ -237,6 +255,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   // the kept tokens, in order; a tie's rank decides
   const uint32_t below = (1u << lane) - 1;
   int first = 0x7FFFFFFF;
+#pragma unroll 4
   for (int j = w0; j < w1; j += 32) {
     const int i = j + lane;
     const uint32_t x = i < w1 ? key(i) : 0;
@@ -553,7 +572,7 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
     if (threadIdx.x == 0) {
       const unsigned long long goal = (unsigned long long)(k + 1) * gridDim.x;
       int ok = 0;
-      for (uint32_t i = 0; i < kBarrierPolls && !ok; ++i) {
+      for (uint32_t i = 0; i < kGridPolls && !ok; ++i) {
         unsigned long long v;
         asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(arrived) : "memory");
         ok = v >= goal;
@@ -664,9 +683,10 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   int ctas = 1;
   while (ctas < kMaxCl && L.cap > ctas * kClTokens) ctas *= 2;
   const int slice = ((L.cap + ctas - 1) / ctas + 1023) & ~1023, room = slice < kMaxKeys ? slice : kMaxKeys;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
+  static std::atomic<uint64_t> keys_set{0}, cluster_set{0}, slots_set{0};
+  cudaError_t e = set_once(keys_set, evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  e = set_once(cluster_set, evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   {
     cudaLaunchConfig_t cfg = {};
@@ -687,7 +707,7 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   }
   e = launch_pdl(evict_plan_kernel, dim3(kCtas), dim3(kThreads), 0, st, a);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(evict_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMoveSmem));
+  e = set_once(slots_set, evict_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMoveSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sm_count());

@@ -4,8 +4,7 @@
 // A row moves 220 KB of query through (96 heads of 576 bf16 values, read once and written once) for
 // about 120,000 multiplications: bytes bound it, and a small call its launch. One warp has a head: 64
 // 16-B chunks of the normed part, two a lane, so that the sum of squares is 16 values a lane and five
-// shuffles; four heads at a time where there are many rows, whose 4 x 8 chunks of the rotary part are then
-// one a lane. The angles of a row are worked out once per block, in fp64 (a product of a 31-bit position
+// shuffles; two heads at a time, whose 2 x 8 chunks of the rotary part are then one for every other lane. The angles of a row are worked out once per block, in fp64 (a product of a 31-bit position
 // and a 24-bit frequency does not fit fp32), 32 lanes a frequency each.
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
@@ -19,6 +18,11 @@ namespace dsa {
 namespace {
 
 constexpr int kWarps = 8;
+// Heads of a warp at a time, and how often; blocks a row. (With normalised heads, 1, 64, 384 and 8,194 rows: 4.8, 7.6, 18.1 and
+// 298 us; one block a row 7.3, 7.6, 18.5, 300; four heads at a time in three blocks 4.9, 8.5, 21.3, 371 at two blocks an SM and
+// 4.7, 8.3, 18.8, 312 at three; twelve blocks of a head a warp 4.8, 8.6, 26.2, 506.)
+constexpr int kPer = 2, kLoops = 3, kSplits = 2;
+static_assert(kWarps * kPer * kLoops * kSplits == kHeads, "a row's heads");
 
 // cos and sin of p * f, each rounded once from fp64 (in all but about one in 2^13): the angle reduced to
 // [-pi/4, pi/4] by whole quarter turns (pi/2 as the sum of two doubles, Cody and Waite's reduction), then the
@@ -94,13 +98,11 @@ __device__ __forceinline__ int row_position(const LatentIn& in, int row, int b, 
   return in.positions ? in.positions[row] : in.ctx_lens[b] - n_q + (row - b * n_q);
 }
 
-// Blocks [0, lat_blocks): a warp per row's latent. The others: kPer heads a warp at a time, `loops` times; `splits`
-// blocks a row.
-template <bool kInterleaved, bool kNv, int kPer>
-__global__ void __launch_bounds__(32 * kWarps) latent_frontend_kernel(const __grid_constant__ LatentIn in, int rows, int n_q,
-                                                                     int max_pages, int cap, int num_pages, int64_t stride,
-                                                                     float inv_scale, int lat_blocks, int splits, int loops,
-                                                                     int* err) {
+// Blocks [0, lat_blocks): a warp per row's latent. The others: kSplits a row, a warp has kPer heads at a time, kLoops times.
+template <bool kInterleaved, bool kNv>
+__global__ void __launch_bounds__(32 * kWarps, 4)
+    latent_frontend_kernel(const __grid_constant__ LatentIn in, int rows, int n_q, int max_pages, int cap, int num_pages,
+                           int64_t stride, float inv_scale, int lat_blocks, int* err) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (int(blockIdx.x) < lat_blocks) {
@@ -200,12 +202,12 @@ __global__ void __launch_bounds__(32 * kWarps) latent_frontend_kernel(const __gr
   }
   // -------------------------------------------------------------- query heads
   __shared__ float2 s_cs[32];
-  const int item = int(blockIdx.x) - lat_blocks, row = item / splits, part = item - row * splits;
+  const int item = int(blockIdx.x) - lat_blocks, row = item / kSplits, part = item - row * kSplits;
   const int b = row / n_q;
   const __nv_bfloat16* nope = static_cast<const __nv_bfloat16*>(in.q_nope) + row * in.q_nope_row;
   const __nv_bfloat16* rope = static_cast<const __nv_bfloat16*>(in.q_rope) + row * in.q_rope_row;
   uint4* out = static_cast<uint4*>(in.q_out) + size_t(row) * kHeads * (kDQK / 8);
-  const int h0 = (part * kWarps + warp) * kPer * loops;
+  const int h0 = (part * kWarps + warp) * kPer * kLoops;
   const int rh = lane >> 3, rj = lane & 7;  // the rotary chunk of this lane
   uint4 w[kPer][2], rw;
   auto load = [&](int h) {
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_frontend_kernel(const __gr
   }
   __syncthreads();
 #pragma unroll 1
-  for (int l = 0; l < loops; ++l) {
+  for (int l = 0; l < kLoops; ++l) {
     const int h = h0 + l * kPer;
     if (norm) {
       float x[8], sum[kPer];
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_frontend_kernel(const __gr
       o[32 + lane] = w[i][1];
     }
     if (rh < kPer) out[(h + rh) * (kDQK / 8) + kDNope / 8 + rj] = pack8(y);
-    if (l + 1 < loops) load(h + kPer);
+    if (l + 1 < kLoops) load(h + kPer);
   }
 }
 
@@ -282,20 +284,12 @@ __global__ void __launch_bounds__(32 * kWarps) latent_frontend_kernel(const __gr
 cudaError_t launch_latent_frontend(const dsa_params_t& p, int* err, const LatentIn& in, bool interleaved, cudaStream_t st) {
   const int rows = p.batch * p.n_q, cap = p.max_pages_per_req * p.page_size;
   const int lat_blocks = in.c_kv ? (rows + kWarps - 1) / kWarps : 0;
-  const bool few = rows <= 2 * sm_count() / 3;
-  const int splits = few ? kHeads / kWarps : 1, loops = few ? 1 : kHeads / kWarps / 4;
-  const int blocks = lat_blocks + (in.q_out ? rows * splits : 0);
+  const int blocks = lat_blocks + (in.q_out ? rows * kSplits : 0);
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(blocks), dim3(32 * kWarps), 0, st, in, rows, int(p.n_q), int(p.max_pages_per_req), cap,
-                      int(p.num_pages), int64_t(p.lat_page_stride), 1.f / p.latent_scale, lat_blocks, splits, loops, err);
-  };
-  if (interleaved) {
-    if (nv) return few ? go(latent_frontend_kernel<true, true, 1>) : go(latent_frontend_kernel<true, true, 4>);
-    return few ? go(latent_frontend_kernel<true, false, 1>) : go(latent_frontend_kernel<true, false, 4>);
-  }
-  if (nv) return few ? go(latent_frontend_kernel<false, true, 1>) : go(latent_frontend_kernel<false, true, 4>);
-  return few ? go(latent_frontend_kernel<false, false, 1>) : go(latent_frontend_kernel<false, false, 4>);
+  auto kern = interleaved ? (nv ? latent_frontend_kernel<true, true> : latent_frontend_kernel<true, false>)
+                          : (nv ? latent_frontend_kernel<false, true> : latent_frontend_kernel<false, false>);
+  return launch_pdl(kern, dim3(blocks), dim3(32 * kWarps), 0, st, in, rows, int(p.n_q), int(p.max_pages_per_req), cap,
+                    int(p.num_pages), int64_t(p.lat_page_stride), 1.f / p.latent_scale, lat_blocks, err);
 }
 
 }  // namespace dsa

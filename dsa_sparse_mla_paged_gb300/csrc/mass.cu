@@ -627,7 +627,8 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
   cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, 0, true, st);
   if (e != cudaSuccess) return e;
   auto kern = nv ? mass_kernel<true> : mass_kernel<false>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  static std::atomic<uint64_t> smem_set[2];
+  e = set_once(smem_set[nv], kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(sm_count()), dim3(nv ? kThreads<true> : kThreads<false>), kSmem, st, kmap, rmap,
                     qmap, a);
