@@ -88,6 +88,8 @@ dsa_status_t check_token_pools(const dsa_params_t* p, const dsa_token_pool_t* po
   if (n_pools > kMaxPools) return DSA_ERR_UNSUPPORTED;
   for (int i = 0; i < n_pools; ++i) {
     const dsa_token_pool_t& q = pools[i];
+    for (int j = 0; j < i; ++j)  // a pool's tokens move once
+      if (pools[j].base == q.base) return DSA_ERR_INVALID;
     if (!q.base || !aligned16(q.base) || q.fmt < DSA_TOKEN_KEY_FP8 || q.fmt > DSA_TOKEN_LAT_NVFP4 || q.layers < 1)
       return DSA_ERR_INVALID;
     if (q.layers > 4096) return DSA_ERR_UNSUPPORTED;
@@ -373,7 +375,8 @@ dsa_status_t dsa_attention_mass(const dsa_params_t* params, const void* q, const
                                 size_t ws_bytes, cudaStream_t stream) {
   dsa_status_t s = check_params(params);
   if (s != DSA_OK) return s;
-  if ((s = check_mla_args(q, lat_pool, block_table, ctx_lens, mass)) != DSA_OK) return s;
+  if (!q || !lat_pool || !block_table || !ctx_lens || !mass) return DSA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(lat_pool) || (reinterpret_cast<uintptr_t>(mass) & 3)) return DSA_ERR_INVALID;
   if (sinks < 0 || window < 1 || fresh < 0 || !lse || (reinterpret_cast<uintptr_t>(lse) & 3)) return DSA_ERR_INVALID;
   if (mass_stride < int64_t(params->max_pages_per_req) * params->page_size) return DSA_ERR_INVALID;
   if (int64_t(params->batch) * params->n_q * params->max_pages_per_req > kPfxMaxTiles / 2) return DSA_ERR_UNSUPPORTED;

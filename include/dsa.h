@@ -426,7 +426,7 @@ dsa_status_t dsa_pages_compact(const dsa_params_t* params, const dsa_page_pool_t
                                int32_t* block_table, const int32_t* ctx_lens, int32_t* page_refs, int32_t* page_map,
                                int32_t* live, void* ws, size_t ws_bytes, cudaStream_t stream);
 
-/* Strides of the front end's inputs, in elements (multiples of 8). */
+/* Strides of the front end's inputs, in elements (multiples of 8, at least the values of a head or row). */
 typedef struct {
   int64_t q_nope_row, q_nope_head; /* between rows, and between a row's heads, of q_nope */
   int64_t q_rope_row, q_rope_head; /* of q_rope */
@@ -489,6 +489,7 @@ dsa_status_t dsa_window_mla_decode(const dsa_params_t* params, const void* q, co
  * a token whose latent holds a NaN gets NaN.
  *   fresh  >= 0: the last `fresh` tokens of each context (new ones, whose entries hold what an
  *          earlier token left there) are set instead of added to
+ *   lse    fp32 [B, n_q, heads]
  *   mass   fp32 [B, mass_stride], mass_stride >= max_pages_per_req * page_size
  * Errors: a request with an invalid ctx_b changes nothing (DSA_DEVERR_CTX); the tokens of a bad page
  * change nothing (DSA_DEVERR_BLOCK_TABLE). */
@@ -528,7 +529,7 @@ typedef struct {
  * Rotary positions are in the latents: later tokens need dsa_latent_frontend's positions.
  *   sinks, recent >= 0
  *   mass    fp32 [B, token_stride], as dsa_attention_mass leaves it; not negative, usually
- *   pools   host array of n_pools (0 .. 64) pools
+ *   pools   host array of n_pools (0 .. 64) pools, each in memory of its own
  *   kept    int32 [B, token_stride] or NULL: the old index of each token of the new context
  *           (the first new-length entries of a row are written; of an unchanged request too)
  *   token_stride >= max_pages_per_req * page_size

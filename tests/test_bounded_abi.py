@@ -77,7 +77,7 @@ def test_window_calls_limits(lib):
     assert _call("dsa_window_mla_decode", p, WINDOW, out=None) == INVALID
     assert _call("dsa_window_mla_decode", p, WINDOW, out=FAKE + 8) == INVALID
     assert _call("dsa_window_mla_decode", p, WINDOW, sinks=top, window=top, bytes=0) == WORKSPACE
-    for change in (dict(lse=None), dict(fresh=-1), dict(mass=None), dict(mass=FAKE + 4), dict(stride=639)):
+    for change in (dict(lse=None), dict(fresh=-1), dict(mass=None), dict(mass=FAKE + 2), dict(stride=639)):
         assert _call("dsa_attention_mass", p, MASS, **change) == INVALID, change
     assert _call("dsa_attention_mass", p, MASS, fresh=top, bytes=dsa.workspace_size(p) - 1) == WORKSPACE
     big = _params(batch=1, n_q=65535, max_pages_per_req=1 << 22, topk=1)
@@ -104,16 +104,18 @@ def test_evict_pools(lib):
 
     good = (FAKE, V, 1, 0, 36864)
     assert status(good, bytes=0) == WORKSPACE
-    assert status((FAKE, V, 3, 36864, 3 * 36864), (FAKE, K, 2, 20 * 8448, 8448), bytes=0) == WORKSPACE
+    assert status((FAKE, V, 3, 36864, 3 * 36864), (2 * FAKE, K, 2, 20 * 8448, 8448), bytes=0) == WORKSPACE
+    assert status(good, (2 * FAKE, V, 1, 0, 36864), good) == INVALID  # its tokens would move twice
     for bad in ((None, V, 1, 0, 36864), (FAKE + 8, V, 1, 0, 36864), (FAKE, 4, 1, 0, 36864), (FAKE, -1, 1, 0, 36864),
                 (FAKE, V, 0, 0, 36864), (FAKE, V, 1, 0, 36848), (FAKE, V, 1, 0, 36872), (FAKE, K, 1, 0, 8432),
                 (FAKE, V, 2, 36864, 36864), (FAKE, V, 2, 36848, 1 << 20), (FAKE, V, 2, 36872, 1 << 20),
                 (FAKE, V, 3, 36864, 3 * 36864 - 16), (FAKE, K, 2, 20 * 8448 - 16, 8448)):
-        assert status(good, bad) == INVALID, bad
+        assert status((4 * FAKE, V, 1, 0, 36864), bad) == INVALID, bad
     assert status((FAKE, V, 4097, 36864, 1 << 30)) == UNSUPPORTED
     assert status((FAKE, V, 1, 0, 1 << 41)) == UNSUPPORTED
-    assert status(*[good] * 65) == UNSUPPORTED
-    assert status(*[good] * 64, bytes=0) == WORKSPACE
+    many = [(FAKE * (i + 1), V, 1, 0, 36864) for i in range(65)]
+    assert status(*many) == UNSUPPORTED
+    assert status(*many[:64], bytes=0) == WORKSPACE
     p = _params(num_pages=(1 << 30) + 1)
     assert status(good) == UNSUPPORTED
 
