@@ -10,6 +10,12 @@
 // borders; each segment leaves an unnormalised partial output with its softmax
 // reference and sum, and the merge kernel adds up the segments of a row's two jobs.
 //
+// With kWin the same kernel attends with a sliding window and sinks: there is no shared prefix, and a job is 128 heads of a
+// request's rows (row * 96 + head, so rows pack without padding: 333 rows take 250 jobs) against the pages of the sinks and
+// then those of the rows' windows. In the few tiles that not all of its rows see alike each row masks its own tokens; values
+// there that are NaN count as 0, so that they do not reach a row that does not see them (one that does has a NaN score
+// for the token, and with it a NaN result).
+//
 // Both products take FP8 latents as they lie in the cache, by TMA, and their other operand
 // as the sum of two FP8 parts, which costs what one product in fp16 does: the query as
 // E4M3 + E5M2, which holds a bf16 value's 8 bits, and a softmax weight as E4M3 + E5M2 too,
@@ -149,27 +155,42 @@ struct PfxArgs {
   int prefix, n_q, rows, max_pages, num_pages, tiles;  // tiles: prefix jobs
   float scale_log2, lat_scale;
   int sinks, window;  // (kWin)
+  int jobs, per_req;  // jobs after the prefix ones; kWin: of a request
 };
 
-// What a row of `len` visible tokens sees through a sliding window: its tokens [0, head) and [first, len), in tiles that
+// What the rows of a job see through their sliding windows: the tokens [0, head) and [first, len), in tiles that
 // are the pages of the first part and then those of the second. (A page that both parts end in is two tiles. Where
-// the parts meet, head is 0 and the second is everything.)
+// the parts meet, head is 0 and the second is everything.) The rows see lo .. len tokens before their ends.
 struct Window {
-  int head, first, n_head, n;
-  __device__ __forceinline__ Window(const PfxArgs& a, int len) {
-    first = max(0, len - a.window);
+  int head, first, n_head, n, lo, len;
+  __device__ __forceinline__ Window(const PfxArgs& a, int job) {
+    const int b = job / a.per_req, h0 = (job - b * a.per_req) * kPfxTileRows;
+    lo = a.lens[b * a.n_q + h0 / kHeads];
+    len = a.lens[b * a.n_q + min(a.n_q - 1, (h0 + kPfxTileRows - 1) / kHeads)];
+    first = max(0, lo - a.window);
     head = a.sinks;
     if (first <= head) first = head = 0;
     n_head = (head + kNT - 1) / kNT;
     n = len > 0 ? n_head + (len + kNT - 1) / kNT - first / kNT : 0;
   }
   __device__ __forceinline__ int page(int k) const { return k < n_head ? k : first / kNT + k - n_head; }
+  // whether some of the tokens that tile k has for the job are hidden from one of its rows
+  __device__ __forceinline__ bool mixed(const PfxArgs& a, int k) const {
+    const int at = page(k) * kNT;
+    return lo < len && k >= n_head && !(at + kNT <= lo && (at >= len - a.window || at + kNT <= a.sinks));
+  }
 };
+// The request's first head, and behind it the job's (kWin).
+__device__ __forceinline__ int first_head(const PfxArgs& a, int job, int& in_req) {
+  const int b = job / a.per_req;
+  in_req = (job - b * a.per_req) * kPfxTileRows;
+  return b * a.n_q * kHeads;
+}
 
-// kWin: a sliding window and sinks instead of a shared prefix (every job is a row's).
+// kWin: a sliding window and sinks instead of a shared prefix.
 template <bool kWin>
 __device__ __forceinline__ int job_tiles(const PfxArgs& a, int job) {
-  if constexpr (kWin) return Window(a, a.lens[job]).n;
+  if constexpr (kWin) return Window(a, job).n;
   return job < a.tiles ? a.prefix / kNT : (a.lens[job - a.tiles] + kNT - 1) / kNT;
 }
 
@@ -195,7 +216,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const PfxArgs& a) {
 #pragma unroll 1
-    while (left > 0 && ++job < a.tiles + a.rows)
+    while (left > 0 && ++job < a.tiles + a.jobs)
       if (take(a, 0)) return true;
     return false;
   }
@@ -248,7 +269,7 @@ struct TileRegs {
   uint4 v[2][4];
   uint32_t s[2][4];
   uint4 rope[2];
-  __device__ __forceinline__ void load(const uint8_t* page, int from, int valid, int w, int lane) {
+  __device__ __forceinline__ void load(const uint8_t* page, int from, int valid, int w, int lane, bool clean) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     auto in = [&](int tok) { return tok >= from && tok < valid; };
 #pragma unroll
@@ -259,6 +280,7 @@ struct TileRegs {
         const uint8_t* row = page + tok * 352;
         v[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
         s[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
+        if (clean) s[b][u] &= ~((((s[b][u] & 0x7F7Fu) + 0x0101u & 0x8080u) >> 7) * 0xFFu);  // NaN scales count as 0
       }
     if constexpr (kRope) {
 #pragma unroll
@@ -317,17 +339,23 @@ __device__ __forceinline__ void split_large(uint32_t a, uint32_t b, uint32_t& e5
       : "r"(a), "r"(b));
 }
 
+// The bits below bit n of a word.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; }
+
 // 2^x of a whole number, exactly; 0 below 2^-126.
 __device__ __forceinline__ float pow2_whole(float x) { return __int_as_float((min(max(int(x), -127), 127) + 127) << 23); }
 
 // What the warps of a CTA need to know of a tile, in a ring that one warp fills.
 struct Tile {
-  int page, valid;  // physical page, and how many of its tokens the job sees (0 for a bad page); kWin: 256 times
-                    // the first of them added
+  int page, valid;  // physical page, and how many of its tokens the job sees (0 for a bad page); kWin: plus 256 times
+                    // the first of them, and kMixed if they are not alike for all of its rows
   template <bool kWin>
-  __device__ __forceinline__ int from() const { return kWin ? valid >> 8 : 0; }
+  __device__ __forceinline__ int from() const { return kWin ? valid >> 8 & 255 : 0; }
   template <bool kWin>
   __device__ __forceinline__ int to() const { return kWin ? valid & 255 : valid; }
+  template <bool kWin>
+  __device__ __forceinline__ bool mixed() const { return kWin && (valid & kMixed); }
+  static constexpr int kMixed = 1 << 16;
 };
 constexpr int kRing = 8;
 
@@ -335,19 +363,21 @@ constexpr int kRing = 8;
 // each(g, tile): what else it does for a tile (lane 0 has just published it).
 template <bool kWin, typename Each>
 __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int unit, int units, int lane, bool report,
-                                     Tile* ring, uint32_t full, uint32_t free, Each each) {
+                                     Tile* ring, int* place, uint32_t full, uint32_t free, Each each) {
   Walk<kWin> wk;
   int g = 0;
 #pragma unroll 1
   for (bool on = gtot > 0 && wk.start(a, job0, unit, units); on; on = wk.next(a)) {
     const int32_t* list = a.prefix_pages;
     int len = a.prefix;
-    if (kWin || wk.job >= a.tiles) {
+    if constexpr (kWin) {
+      list = a.table + size_t(wk.job / a.per_req) * a.max_pages;
+    } else if (wk.job >= a.tiles) {
       const int r = wk.job - a.tiles;
       list = a.table + size_t(r / a.n_q) * a.max_pages + a.prefix / kNT;
       len = a.lens[r];
     }
-    const Window win(a, len);
+    const Window win(a, kWin ? wk.job : 0);
     int mine = 0;
 #pragma unroll 1
     for (int k = wk.k0; k < wk.k1; ++k, ++g) {
@@ -358,7 +388,8 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
       int valid = min(kNT, len - k * kNT);
       if constexpr (kWin) {
         const int at = win.page(k) * kNT;
-        valid = k < win.n_head ? min(kNT, win.head - at) : min(kNT, len - at) | max(0, win.first - at) << 8;
+        valid = k < win.n_head ? min(kNT, win.head - at) : min(kNT, win.len - at) | max(0, win.first - at) << 8;
+        if (win.mixed(a, k)) valid |= Tile::kMixed;
       }
       const Tile t{good ? pg : 0, good ? valid : 0};
       const int slot = g % kRing;
@@ -366,6 +397,7 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
       if (lane == 0) {
         if (!good && report) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
         ring[slot] = t;
+        if constexpr (kWin) place[slot] = win.page(k) * kNT;
         ptx::mbar_arrive(full + 8 * slot);
       }
       if (!each(g, t)) return false;
@@ -390,7 +422,8 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
     const Tile tile = ring[slot];
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
-    t.load(a.lat + int64_t(tile.page) * a.stride, tile.from<kWin>(), tile.to<kWin>(), w, lane);
+    t.load(a.lat + int64_t(tile.page) * a.stride, tile.from<kWin>(), tile.to<kWin>(), w, lane,
+           !kKeys && tile.mixed<kWin>());
     return true;
   };
   if (group < gtot && !load(group)) return false;
@@ -465,6 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* PB = sm + 2 * kVBuf;
   uint8_t* side = PB + kPBufs<kNv> * kPBuf;  // [kPBufs] factors and flags
   __shared__ long long s_sum[kThreads / 32];
+  __shared__ int s_place[kRing];  // kWin: the tile's first token
   __shared__ int s_job, s_unit, s_tiles, s_ask;  // s_ask: the tile that wants O rescaled, -1 at a job's end
 
   const int half = int(ptx::cluster_ctarank());
@@ -519,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int units, gtot;
   {
     auto row_units = [&](int r) {
-      const int n = r < a.rows ? job_tiles<kWin>(a, a.tiles + r) : 0;
+      const int n = r < a.jobs ? job_tiles<kWin>(a, a.tiles + r) : 0;
       return n > 0 ? (long long)(n + kJobCost) : 0ll;
     };
     auto warp_scan = [&](long long v) {
@@ -543,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     long long n = row_units(threadIdx.x), before, all;
     chunk_scan(n, before, all);
     int64_t line = all;
-    for (int r0 = kThreads; r0 < a.rows; r0 += kThreads) {
+    for (int r0 = kThreads; r0 < a.jobs; r0 += kThreads) {
       long long b, more;
       __syncthreads();
       chunk_scan(row_units(r0 + int(threadIdx.x)), b, more);
@@ -585,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       base += all;
       r0 += kThreads;
-      if (r0 >= a.rows || hi <= base) break;
+      if (r0 >= a.jobs || hi <= base) break;
       n = row_units(r0 + int(threadIdx.x));
       __syncthreads();
       chunk_scan(n, before, all);
@@ -639,7 +673,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // (four dims of all rows together, so that a warp's stores are whole lines)
       float4* dst = reinterpret_cast<float4*>(a.part) + size_t(wk.job + clu) * kPfxTileRows * (kDNope / 4) + row;
-      const bool real = wk.job < a.tiles ? wk.job * kPfxTileRows + row < a.rows * kHeads : row < kHeads;
+      int in_req;
+      const bool real = kWin ? (first_head(a, wk.job, in_req), in_req + row < a.n_q * kHeads)
+                             : wk.job < a.tiles ? wk.job * kPfxTileRows + row < a.rows * kHeads : row < kHeads;
 #pragma unroll 1
       for (int c = c0; c < c1; c += 32) {
         float o[32];
@@ -667,11 +703,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // CTA 0: 32 heads of a job's query, `blocks` times 32 columns from block kb0, to tensor memory
   auto query_blocks = [&](int job, int kb0, auto blocks, uint32_t bar, auto until) {
     const int row = (warp & 3) * 32 + lane;
-    const int hr = (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
+    int in_req = 0;
+    const int hr = kWin ? first_head(a, job, in_req) + in_req + row
+                        : (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
     const int heads = a.rows * kHeads;
     // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too. Not for NVFP4, whose
     // converters have no registers to spare: 214.7 for 212.8 us)
-    const bool in = kNv || job < a.tiles ? hr < heads : row < kHeads;
+    const bool in = kWin ? in_req + row < a.n_q * kHeads : kNv || job < a.tiles ? hr < heads : row < kHeads;
     auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -773,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = half == 0 ? kKBuf8 : kVBuf8;
       constexpr int kBufs = 4;
       static_assert(kNv || (kKBufs<kNv> == kBufs && kVBufs<kNv> == kBufs), "FP8 buffers");
-      ok = feed<kWin>(a, gtot, job0, unit0, units, lane, half == 0, ring, ring_full, ring_free, [&](int g, const Tile& t) {
+      ok = feed<kWin>(a, gtot, job0, unit0, units, lane, half == 0, ring, s_place, ring_full, ring_free, [&](int g, const Tile& t) {
         if (kNv) return true;
         const int buf = g % kBufs;
         if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
@@ -874,6 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int slot = g % kRing, buf = g % kVBufs<kNv>;
             if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) { ok = false; break; }
             const int from = ring[slot].template from<kWin>(), valid = ring[slot].template to<kWin>();
+            const bool mixed = ring[slot].template mixed<kWin>();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
             if (!ptx::mbar_wait(v_full + 8 * buf, uint32_t(g / kVBufs<kNv>) & 1u)) { ok = false; break; }
@@ -881,6 +920,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int t = 0; t < from; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
             if (valid < kNT) {
               for (int t = valid; t < kNT; ++t) *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(0, 0, 0, 0);
+            }
+            if (mixed) {  // NaN values (0x7F and 0xFF) count as 0
+#pragma unroll 4
+              for (int t = from; t < valid; ++t) {
+                const uint4 x = *reinterpret_cast<const uint4*>(v + t * 128);
+                auto nan = [](uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; };
+                auto clean = [&](uint32_t w) { return w & ~((nan(w) >> 7) * 0xFFu); };
+                if (nan(x.x) | nan(x.y) | nan(x.z) | nan(x.w))
+                  *reinterpret_cast<uint4*>(v + t * 128) = make_uint4(clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+              }
             }
           }
           const uint4 flags = *reinterpret_cast<const uint4*>(side + pb * kPSide + 512);
@@ -956,8 +1005,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int g0 = 0;  // the segment's first tile
 #pragma unroll 1
     for (bool on = gtot > 0 && wk.start(a, job0, unit0, units); on && ok; on = wk.next(a)) {
-      const int hr = (wk.job < a.tiles ? wk.job * kPfxTileRows : (wk.job - a.tiles) * kHeads) + row;
-      const float cs = fmaxf(hr < a.rows * kHeads ? a.scale_log2 * a.qs[hr] : 1.f, 1.1754944e-38f);
+      int hr = (wk.job < a.tiles ? wk.job * kPfxTileRows : (wk.job - a.tiles) * kHeads) + row, seen = 0;
+      bool in = hr < a.rows * kHeads;
+      if constexpr (kWin) {
+        int in_req;
+        hr = first_head(a, wk.job, in_req) + in_req + row;
+        in = in_req + row < a.n_q * kHeads;
+        seen = a.lens[(in ? hr : hr - row) / kHeads];  // (a padded row sees what the job's first one does)
+      }
+      const float cs = fmaxf(in ? a.scale_log2 * a.qs[hr] : 1.f, 1.1754944e-38f);
       if (g0 == 0) first_query(wk.job);
       float m_mine = -INFINITY, l = 0.f;  // the reference that l is relative to
       const int g1 = g0 + wk.k1 - wk.k0;
@@ -971,18 +1027,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32_nowait(tmem + lane_base + kSCol + sb * kNT + 32, *reinterpret_cast<float(*)[32]>(&sv[32]));
         if (!ptx::mbar_wait(ring_full + 8 * (g % kRing), uint32_t(g / kRing) & 1u)) ok = false;
         const int from = ring[g % kRing].template from<kWin>(), valid = ring[g % kRing].template to<kWin>();
+        const bool mixed = ring[g % kRing].template mixed<kWin>();
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[0]));
         ptx::tmem_ld_wait(*reinterpret_cast<float(*)[32]>(&sv[32]));
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive(s_free + 8 * (g % (2 * kSBufs)));
-          ptx::mbar_arrive(ring_free + 8 * (g % kRing));
+          if (!kWin) ptx::mbar_arrive(ring_free + 8 * (g % kRing));
         }
         if (!ok) break;
-        if (valid < kNT || from > 0) {
+        if (!kWin && valid < kNT) {
 #pragma unroll
-          for (int i = 0; i < kNT; ++i) sv[i] = i >= from && i < valid ? sv[i] : -INFINITY;
+          for (int i = 0; i < kNT; ++i) sv[i] = i < valid ? sv[i] : -INFINITY;
+        }
+        if (kWin && (valid < kNT || from > 0 || mixed)) {
+          // the row sees [lo, hi) of the tile, and [from, stay) of the sinks
+          int lo = from, hi = valid, stay = 0;
+          if (mixed) {
+            const int place = s_place[g % kRing];
+            lo = max(from, seen - a.window - place);
+            hi = min(valid, seen - place);
+            stay = min(hi, a.sinks - place);
+          }
+          const uint32_t m0 = bits_below(hi) & ~bits_below(lo) | bits_below(stay) & ~bits_below(from);
+          const uint32_t m1 = bits_below(hi - 32) & ~bits_below(lo - 32) | bits_below(stay - 32) & ~bits_below(from - 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            sv[i] = m0 >> i & 1u ? sv[i] : -INFINITY;
+            sv[i + 32] = m1 >> i & 1u ? sv[i + 32] : -INFINITY;
+          }
+        }
+        if constexpr (kWin) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(ring_free + 8 * (g % kRing));
         }
         float t0 = fmaxf(sv[0], sv[1]), t1 = fmaxf(sv[2], sv[3]);
 #pragma unroll
@@ -1188,7 +1266,7 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
-template <int kSplit>
+template <int kSplit, bool kWin>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs a, __nv_bfloat16* __restrict__ out,
                                                                        float* __restrict__ lse) {
   constexpr int kParts = kMergeWarps / kSplit;  // warps with dims of their own
@@ -1200,7 +1278,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
   const int r = blockIdx.x, h = blockIdx.y * 32 + lane, c0 = blockIdx.z * kChunks + warp / kSplit * 4;
-  const int hr = r * kHeads + h, job0 = hr / kPfxTileRows, job1 = a.tiles + r;
+  const int hr = r * kHeads + h, job0 = hr / kPfxTileRows;
+  const int in_req = kWin ? (r % a.n_q) * kHeads + h : h;  // (32 heads are of one job)
+  const int job1 = kWin ? r / a.n_q * a.per_req + in_req / kPfxTileRows : a.tiles + r;
   float4 acc[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1214,7 +1294,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(PfxArgs 
     const int f1 = a.plan[2 * job1], n1 = a.plan[2 * job1 + 1] - f1 + 1;
     // segment i's slot and row
     auto slot = [&](int i) { return i < n0 ? job0 + f0 + i : job1 + f1 + i - n0; };
-    auto row = [&](int i) { return i < n0 ? hr % kPfxTileRows : h; };
+    auto row = [&](int i) { return i < n0 ? hr % kPfxTileRows : in_req % kPfxTileRows; };
 #pragma unroll 2
     for (int i = part; i < n0 + n1; i += kSplit) {
       const float* ml = a.ml + size_t(slot(i)) * 512 + row(i);
@@ -1311,6 +1391,8 @@ static cudaError_t launch_dense(const dsa_params_t& p, const WsLayout& L, char* 
   a.max_pages = p.max_pages_per_req;
   a.num_pages = p.num_pages;
   a.tiles = a.prefix > 0 ? L.pfx_tiles : 0;
+  a.per_req = (p.n_q * kHeads + kPfxTileRows - 1) / kPfxTileRows;
+  a.jobs = kWin ? p.batch * a.per_req : L.rows;
   a.scale_log2 = p.softmax_scale * p.latent_scale * 1.4426950408889634f;
   const bool nv = p.lat_fmt == DSA_LAT_NVFP4_352;
   a.lat_scale = p.latent_scale;
@@ -1338,7 +1420,7 @@ static cudaError_t launch_dense(const dsa_params_t& p, const WsLayout& L, char* 
   // a row has a little more than clusters / rows segments (one row of 65: 20.5 us shared by
   // eight warps, 26.5 not; 24 rows of five: 42.3 and 39.7)
   const bool split = L.rows * 4 <= clusters;
-  return launch_pdl(split ? prefix_merge_kernel<kMergeWarps> : prefix_merge_kernel<1>,
+  return launch_pdl(split ? prefix_merge_kernel<kMergeWarps, kWin> : prefix_merge_kernel<1, kWin>,
                     dim3(L.rows, kHeads / 32, kDNope / 4 / (split ? 4 : 4 * kMergeWarps)), dim3(32 * kMergeWarps), 0, st,
                     a, static_cast<__nv_bfloat16*>(out), lse);
 }
