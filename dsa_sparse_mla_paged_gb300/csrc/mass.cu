@@ -4,8 +4,9 @@
 // It is the dense attention's first product without its second, and its sum runs over the heads, not the tokens. So a
 // token is a row of the product here: S = C . Q^T with 128 tokens (two pages) against a query row's 96 heads,
 // one accumulator lane per token; a thread has one token, and its sum over the heads is its own: no shuffle, no
-// atomic, the same bits in any batch. The query is prepared as for the dense attention (FP8 latents: E4M3 + E5M2,
-// multiplied with the latents as TMA brings them; NVFP4 ones: fp16) and stays in
+// atomic, the same bits in any batch. The query is prepared as for the dense attention (FP8 latents: two FP8 parts, here both
+// E4M3, the second times 2^5, multiplied with the latents as TMA brings them in one product of 192 columns, so that the latents
+// are read from shared memory once: with a product for each part 59.3 us for the first case below; NVFP4 ones: fp16) and stays in
 // shared memory (110 KB) while tiles of tokens stream past it. NVFP4 latents are converted to fp16 and multiplied from tensor
 // memory: through shared memory, which the products read 28 KB of per K-block, their 16 KB took 226 us for the
 // case below.
@@ -39,14 +40,14 @@ constexpr int kStages = kNv ? 6 : 4;
 constexpr int kRingBytes = 6 * 16384;
 static_assert(kStage<true> * kStages<true> == kRingBytes && kStage<false> * kStages<false> == kRingBytes, "either ring");
 constexpr int kQBlk = kHeads * 128;           // 12,288 B: 128 B of each head
-constexpr int kQBytes = 9 * kQBlk;            // of a row's heads: pieces of the dims (FP8: [part][4] and both rotary pieces)
+constexpr int kQBytes = 9 * kQBlk;            // of a row's heads: pieces of the dims (FP8: [4][part], and [part] of 64 rotary bytes)
 constexpr int kChunk = 16;                    // tiles of a chunk
-// tensor memory: FP8 four accumulators of 96 columns; NVFP4 two, and a tile's values in three stages of 96 columns (192 dims:
-// with a stage for each of the nine K-blocks the wait and the fence of every four products took 116 us for the case below)
+// tensor memory: two accumulators of 96 columns, FP8: of 192, for the two parts of the query; NVFP4: and a tile's values in three
+// stages of 96 columns (192 dims: with a stage for each of the nine K-blocks the wait and the fence of every four products took
+// 116 us for the case below)
+constexpr int kDBufs = 2;
 template <bool kNv>
-constexpr int kDBufs = kNv ? 2 : 4;
-template <bool kNv>
-constexpr int kDCols = kNv ? 96 : 128;
+constexpr int kDCols = kNv ? 96 : 192;
 constexpr int kACol = 192;
 static_assert(kACol + kDQK / 2 <= 512, "tensor memory");
 template <bool kNv>
@@ -145,7 +146,8 @@ __device__ __forceinline__ uint4 expand_e2m1(uint32_t w, __half2 s) {
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads<kNv>, 1)
     mass_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap rmap,
-                const __grid_constant__ CUtensorMap qmap, const __grid_constant__ MassArgs a) {
+                const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap qrmap,
+                const __grid_constant__ MassArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = ring + kRingBytes;
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
   const uint32_t mma_done = a_free + 8 * kParts;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_sum[32], s_b, s_tile, s_bad[2];
-  constexpr int kD = kDBufs<kNv>, kSt = kStages<kNv>;
+  constexpr int kD = kDBufs, kSt = kStages<kNv>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
       ptx::mbar_init(q_full + 8 * i, 1);
       ptx::mbar_init(q_free + 8 * i, 1);
     }
-    for (int i = 0; i < kDBufs<kNv>; ++i) {
+    for (int i = 0; i < kDBufs; ++i) {
       ptx::mbar_init(d_full + 8 * i, 1);
       ptx::mbar_init(d_free + 8 * i, 4);
     }
@@ -271,13 +273,22 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
           if (!ptx::mbar_wait(d_full + 8 * buf, uint32_t(g / kD) & 1u, kPolls)) { ok = false; break; }
           ptx::tc_fence_after();
           float w0 = 0.f, w1 = 0.f, w2 = 0.f, w3 = 0.f;
-          float z[2][32];
-          ptx::tmem_ld32_nowait(tmem + lanes + buf * kDCols<kNv>, z[0]);
+          float z[2][32];  // NVFP4: a piece of 32 heads and the next; FP8: both parts of one
+          const uint32_t d = tmem + lanes + buf * kDCols<kNv>;
+          ptx::tmem_ld32_nowait(d, z[0]);
 #pragma unroll
           for (int c = 0; c < 3; ++c) {
-            float(&x)[32] = z[c & 1];
-            ptx::tmem_ld_wait(x);
-            if (c < 2) ptx::tmem_ld32_nowait(tmem + lanes + buf * kDCols<kNv> + 32 * (c + 1), z[(c + 1) & 1]);
+            float(&x)[32] = z[kNv ? c & 1 : 0];
+            if constexpr (kNv) {
+              ptx::tmem_ld_wait(x);
+              if (c < 2) ptx::tmem_ld32_nowait(d + 32 * (c + 1), z[(c + 1) & 1]);
+            } else {
+              ptx::tmem_ld32_nowait(d + kHeads + 32 * c, z[1]);
+              ptx::tmem_ld_wait(x);
+              ptx::tmem_ld_wait(z[1]);
+#pragma unroll
+              for (int h = 0; h < 32; ++h) x[h] = fmaf(z[1][h], 0.03125f, x[h]);  // 2^-5
+            }
 #pragma unroll
             for (int h = 0; h < 32; h += 4) {
               const float4 f = cs[8 * c + h / 4], o = co[8 * c + h / 4];
@@ -291,6 +302,7 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
               ptx::add2(w0, w1, ptx::ex2_approx(y[0]), ptx::ex2_approx(y[1]));
               ptx::add2(w2, w3, ptx::ex2_approx(y[2]), ptx::ex2_approx(y[3]));
             }
+            if (!kNv && c < 2) ptx::tmem_ld32_nowait(d + 32 * (c + 1), z[0]);
           }
           ptx::tc_fence_before();
           __syncwarp();
@@ -346,14 +358,12 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
                 ptx::mma_commit(a_free + 8 * i);
               } else {
 #pragma unroll
-                for (int half = 0; half < 2; ++half)  // the query's E4M3, then its E5M2 part
-#pragma unroll
-                  for (int kk = 0; kk < 6; ++kk) {
-                    const int n = 6 * i + kk;         // 32 dims of the tile's 576
-                    const uint32_t q = n < 16 ? (4 * half + n / 4) * kQBlk + n % 4 * 32 : 8 * kQBlk + half * 64 + n % 2 * 32;
-                    ptx::mma_f8f6f4(d, kk < 4 ? ptx::sdesc_sw128(in + kk * 32) : ptx::sdesc_sw64(in + kTok * 128 + (kk - 4) * 32),
-                                    ptx::sdesc_sw128(q0 + q), ptx::idesc(0, half, kTok, kHeads), (i | half | kk) ? 1u : 0u);
-                  }
+                for (int kk = 0; kk < 6; ++kk) {
+                  const int n = 6 * i + kk;  // 32 dims of the tile's 576, against both parts of the query
+                  ptx::mma_f8f6f4(d, kk < 4 ? ptx::sdesc_sw128(in + kk * 32) : ptx::sdesc_sw64(in + kTok * 128 + (kk - 4) * 32),
+                                  n < 16 ? ptx::sdesc_sw128(q0 + n / 4 * 2 * kQBlk + n % 4 * 32) : ptx::sdesc_sw64(q0 + 8 * kQBlk + n % 2 * 32),
+                                  ptx::idesc(0, 0, kTok, 2 * kHeads), n ? 1u : 0u);
+                }
                 ptx::mma_commit(free + 8 * st);
               }
               if (k == nt - 1 && leaves) {  // (FP8: the first part's blocks are used by the second, too)
@@ -392,12 +402,19 @@ __global__ void __launch_bounds__(kThreads<kNv>, 1)
         for (int i = 0; i < kParts; ++i) {
           if (qn > 0 && !ptx::mbar_wait(q_free + 8 * i, uint32_t(qn - 1) & 1u, kPolls)) { ok = false; break; }
           if (lane == 0) {
-            // NVFP4: blocks 3i ..; FP8: 0, 1 of both parts, 2 of both, 3 of both and the rotary block
-            const uint32_t bar = q_full + 8 * i, blocks = kNv ? 7u << (3 * i) : i == 0 ? 0x33u : i == 1 ? 0x44u : 0x188u;
-            ptx::mbar_arrive_expect_tx(bar, __popc(blocks) * kQBlk);
-#pragma unroll
-            for (int j = 0; j < 9; ++j)
-              if (blocks >> j & 1) ptx::tma_load_3d(q0 + j * kQBlk, &qmap, bar, 128 * j, 0, row);
+            const uint32_t bar = q_full + 8 * i;
+            auto block = [&](int at, int piece) { ptx::tma_load_3d(q0 + at * kQBlk, &qmap, bar, 128 * piece, 0, row); };
+            if constexpr (kNv) {
+              ptx::mbar_arrive_expect_tx(bar, 3 * kQBlk);
+              for (int j = 3 * i; j < 3 * i + 3; ++j) block(j, j);
+            } else {  // both parts of 128-dim pieces: 0 and 1, 2, 3 and the rotary dims
+              ptx::mbar_arrive_expect_tx(bar, (i == 0 ? 4 : i == 1 ? 2 : 3) * kQBlk);
+              for (int j = i == 0 ? 0 : i + 1; j < i + 2; ++j)
+                for (int part = 0; part < 2; ++part) block(2 * j + part, 4 * part + j);
+              if (i == 2)
+                for (int part = 0; part < 2; ++part)
+                  ptx::tma_load_3d(q0 + 8 * kQBlk + part * kQBlk / 2, &qrmap, bar, 1024 + 64 * part, 0, row);
+            }
           }
           __syncwarp();
         }
@@ -617,11 +634,14 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
         !encode_map(&rmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, lat_pool, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
-  CUtensorMap qmap;
+  CUtensorMap qmap, qrmap;
+  std::memset(&qrmap, 0, sizeof(qrmap));
   {
     const uint64_t dims[3] = {1152, uint64_t(kHeads), uint64_t(L.rows)}, strides[2] = {1152, uint64_t(1152) * kHeads};
-    const uint32_t box[3] = {128, kHeads, 1};
+    const uint32_t box[3] = {128, kHeads, 1}, rbox[3] = {64, kHeads, 1};
     if (!encode_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + L.pfx_q, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    if (!nv && !encode_map(&qrmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + L.pfx_q, 3, dims, strides, rbox, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
   cudaError_t e = launch_prefix_query(p, L, ws, q, ctx_lens, 0, true, st);
@@ -631,7 +651,7 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
   e = set_once(smem_set[nv], kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(sm_count()), dim3(nv ? kThreads<true> : kThreads<false>), kSmem, st, kmap, rmap,
-                    qmap, a);
+                    qmap, qrmap, a);
 }
 
 }  // namespace dsa

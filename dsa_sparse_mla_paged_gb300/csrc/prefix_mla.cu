@@ -1181,6 +1181,18 @@ __device__ __forceinline__ void split_query(float a, float b, uint32_t& hi, uint
 
 // kHeadMajor: for dsa_attention_mass, whose heads are the products' second operand, a head's 1,152 bytes
 // together: nine 128-byte pieces, FP8: four of each part's first 512 dims, then the last 64 dims of both.
+// For that the rest is E4M3, too, times 2^5, as both parts are multiplied in one product there: it is at most 8, and in units of
+// 2^-14 (four bits of it), which is finer than above.
+__device__ __forceinline__ void split_query_e4m3(float a, float b, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l, p, q;\n\t.reg .b32 u;\n\t.reg .f32 x, y;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %3, %2;\n\tcvt.rn.f16x2.e4m3x2 u, h;\n\tmov.b32 {p, q}, u;\n\t"
+      "cvt.f32.f16 x, p;\n\tcvt.f32.f16 y, q;\n\tsub.rn.f32 x, %2, x;\n\tsub.rn.f32 y, %3, y;\n\t"
+      "mul.rn.f32 x, x, 0f42000000;\n\tmul.rn.f32 y, y, 0f42000000;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, y, x;\n\tcvt.u32.u16 %0, h;\n\tcvt.u32.u16 %1, l;\n}\n"
+      : "=&r"(hi), "=r"(lo)
+      : "f"(a), "f"(b));
+}
+
 template <bool kNv, bool kHeadMajor>
 __global__ void __launch_bounds__(32 * kQueryWarps)
     prefix_query_kernel(const uint32_t* __restrict__ q, int heads, uint32_t* __restrict__ prepared, float* __restrict__ qs,
@@ -1229,9 +1241,11 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
       if (word(i) >= kWords) continue;
       uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int d = 0; d < 2; ++d)
-        split_query(__uint_as_float(w[i + d] << 16) * f0 * f1, __uint_as_float(w[i + d] & 0xFFFF0000u) * f0 * f1, hi[d],
-                    lo[d]);
+      for (int d = 0; d < 2; ++d) {
+        const float x = __uint_as_float(w[i + d] << 16) * f0 * f1, y = __uint_as_float(w[i + d] & 0xFFFF0000u) * f0 * f1;
+        if constexpr (kHeadMajor) split_query_e4m3(x, y, hi[d], lo[d]);
+        else split_query(x, y, hi[d], lo[d]);
+      }
       const int out = word(i) >> 1;  // the word of four dims: 16 dims a chunk
       put(0, out, hi[0] | hi[1] << 16);
       put(kChunks / 2, out, lo[0] | lo[1] << 16);
