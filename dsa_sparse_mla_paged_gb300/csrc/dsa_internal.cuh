@@ -86,7 +86,7 @@ struct WsLayout {
   size_t pfx_part;  // float [pfx_slots][512 / 4][128][4] partial outputs
   size_t ev_list;   // int32 [batch][cap] eviction: the tokens that stay (in the room of scores)
   size_t ev_head;   // int64 [8] its totals and its barrier
-  size_t ev_req;    // int64 [batch] first item of a request's moves; then int32 [5][batch] its plan
+  size_t ev_req;    // int64 [2][batch] first item of a request's moves and of what follows; int32 [5][batch] its plan
   size_t ev_page;   // int32 [batch][max_pages] rank of a page's fresh page among the request's, -1: rewritten in place
   size_t ev_free;   // int32 [num_pages] free pages by rank
   size_t total;
@@ -167,7 +167,7 @@ inline WsLayout ws_layout(const dsa_params_t& p) {
   group([&](size_t at) {
     const size_t from = at;
     L.ev_head = at; at = align256(at + 64);
-    L.ev_req = at; at = align256(at + size_t(28) * p.batch);
+    L.ev_req = at; at = align256(at + size_t(36) * p.batch);
     L.ev_page = at; at = align256(at + size_t(p.batch) * p.max_pages_per_req * 4);
     L.ev_free = at; at = align256(at + size_t(p.num_pages) * 4);
     return at - from;

@@ -23,9 +23,10 @@ namespace dsa {
 namespace {
 
 constexpr int kCtas = 8;        // of the plan's cluster
-constexpr int kMaxCl = 16;      // of the choice's: at most (16 KB of weights are then a CTA's up to 65,536 tokens, 48 K keys fit)
-constexpr int kClTokens = 16384;  // tokens a CTA is to have, until the cluster is full
+constexpr int kMaxCl = 16;        // of the choice's, at most
+constexpr int kClTokens = 16384;  // tokens of a CTA's slice, at most, while the GPU has CTAs to give
 constexpr int kMaxKeys = 47104;   // keys that fit a CTA
+constexpr int kPieceTokens = 1536;  // what a CTA finishes at once: tables, weights behind the end, kept tokens
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
 
@@ -40,7 +41,7 @@ constexpr size_t kMoveSmem = size_t(2) * kMoveWarps * kSlot;
 constexpr uint32_t kGridPolls = 1u << 22;  // of a counter in L2, 0.5 us and more each
 
 enum { kPlanNew = 0, kPlanOld = 1, kPlanFirstPage = 2, kPlanNeed = 3, kPlanFresh = 4 };  // int32 [5][batch]
-enum { kHeadItems = 0, kHeadArrived = 1 };                                 // int64 [8]
+enum { kHeadItems = 0, kHeadArrived = 1, kHeadPieces = 2 };                // int64 [8]
 
 struct TokenPools {
   char* base[kMaxPools];
@@ -58,7 +59,8 @@ struct EvictArgs {
   int32_t* kept;
   int32_t* list;   // [batch][cap]
   long long* head;
-  long long* item; // [batch] first item of a request's moves
+  long long* item;   // [batch] first item of a request's moves
+  long long* piece;  // [batch] and its first piece of what is finished behind them
   int32_t* plan;   // [5][batch]: new length (-1: the request stays as it is) and old one, first page that changes, fresh
                    // pages, rank of the first of them
   int32_t* fresh;  // [batch][max_pages] rank of a page's fresh page among its request's, -1: in place
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) evict_
     }
   }
   if (me != 0) return;
-  long long pages = 0, items = 0;
+  long long pages = 0, items = 0, pieces = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + tid;
     int need = 0, len = -1;
@@ -389,13 +391,18 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCtas, 1, 1) evict_
     const long long mine = len >= 0 ? items_of(a.plan[kPlanFirstPage * a.batch + b], len, a.units) : 0;
     const long long end = items + block_scan<long long>(mine, sums64, total);
     items += total;
+    const long long rest = b < a.batch && (len >= 0 || a.kept) ? (a.plan[kPlanOld * a.batch + b] + kPieceTokens - 1) / kPieceTokens : 0;
+    const long long last = pieces + block_scan<long long>(rest, sums64, total);
+    pieces += total;
     if (b < a.batch) {
       a.plan[kPlanFresh * a.batch + b] = int(upto - need);
       a.item[b] = end - mine;
+      a.piece[b] = last - rest;
     }
   }
   if (tid == 0) {
     a.head[kHeadItems] = items;
+    a.head[kHeadPieces] = pieces;
     a.head[kHeadArrived] = 0;
   }
 }
@@ -421,23 +428,27 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 // What a CTA keeps of the requests' plans in shared memory, if there are no more of them.
-constexpr int kKept = 512;
+constexpr int kKept = 256;
 struct Plans {
-  long long item[kKept];
-  int32_t len[kKept], from[kKept], fresh[kKept];
+  long long item[kKept], piece[kKept];
+  int32_t len[kKept], from[kKept], fresh[kKept], old[kKept];
 };
+
+// The last request whose first item (or piece) is at or before `at`: those without any share their start with the next.
+__device__ __forceinline__ int request_of(const long long* first, int batch, long long at) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (first[m] <= at) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
 
 // Where item `it` begins and ends. kNear: the plans are in shared memory.
 template <bool kNear>
 __device__ __forceinline__ Unit look_up(const EvictArgs& a, const TokenPools& pools, const Plans& near, long long it, int lane) {
-  // the request: the last whose items begin at or before it (those without any share their start with the next)
-  int lo = 0, hi = a.batch;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) >> 1;
-    if ((kNear ? near.item[m] : a.item[m]) <= it) lo = m;
-    else hi = m;
-  }
-  const int b = lo, len = kNear ? near.len[b] : a.plan[kPlanNew * a.batch + b];
+  const int b = request_of(kNear ? near.item : a.item, a.batch, it), len = kNear ? near.len[b] : a.plan[kPlanNew * a.batch + b];
   const int from = kNear ? near.from[b] : a.plan[kPlanFirstPage * a.batch + b];
   const int first_fresh = kNear ? near.fresh[b] : a.plan[kPlanFresh * a.batch + b];
   const int pages = pages_of(len) - from;
@@ -541,12 +552,14 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
     if (it >= items) return Unit{};
     return a.batch <= kKept ? look_up<true>(a, pools, near, it, lane) : look_up<false>(a, pools, near, it, lane);
   };
-  if (a.batch <= kKept && batches > 0) {
+  if (a.batch <= kKept) {
     for (int b = threadIdx.x; b < a.batch; b += blockDim.x) {
       near.item[b] = a.item[b];
       near.len[b] = a.plan[kPlanNew * a.batch + b];
       near.from[b] = a.plan[kPlanFirstPage * a.batch + b];
       near.fresh[b] = a.plan[kPlanFresh * a.batch + b];
+      near.old[b] = a.plan[kPlanOld * a.batch + b];
+      near.piece[b] = a.piece[b];
     }
     __syncthreads();
   }
@@ -602,43 +615,36 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
     next = unit(k + 2);
   }
   if (lane == 0) ptx::bulk_wait_read();
-  // Every row has been read: tables, counts and lengths ...
-  const int row_pieces = (a.max_pages + int(blockDim.x) - 1) / int(blockDim.x);
-  for (long long q = blockIdx.x; q < (long long)a.batch * row_pieces; q += gridDim.x) {
-    const int b = int(q / row_pieces), piece = int(q - (long long)b * row_pieces), len = a.plan[kPlanNew * a.batch + b];
+  // Every row has been read: tables, counts, lengths, the old indices of what stays, the weights behind the new ends.
+  const long long pieces = a.head[kHeadPieces];
+  const bool is_near = a.batch <= kKept;
+  for (long long q = blockIdx.x; q < pieces; q += gridDim.x) {
+    const int b = request_of(is_near ? near.piece : a.piece, a.batch, q);
+    const int i0 = int(q - (is_near ? near.piece[b] : a.piece[b])) * kPieceTokens;
+    const int len = is_near ? near.len[b] : a.plan[kPlanNew * a.batch + b], old = is_near ? near.old[b] : a.plan[kPlanOld * a.batch + b];
+    const int end = min(i0 + kPieceTokens, old);
+    const int32_t* list = a.list + size_t(b) * a.cap;
+    for (int i = i0 + int(threadIdx.x); i < end; i += blockDim.x) {
+      if (len < 0) a.kept[b * a.stride + i] = i;
+      else if (i >= len) a.mass[b * a.stride + i] = 0.f;
+      else if (a.kept) a.kept[b * a.stride + i] = list[i];
+    }
     if (len < 0) continue;
-    int32_t* row = a.table + size_t(b) * a.max_pages;
-    const int first = a.plan[kPlanFirstPage * a.batch + b], want = pages_of(len), used = pages_of(a.plan[kPlanOld * a.batch + b]);
-    const int j = piece * int(blockDim.x) + int(threadIdx.x);
-    if (j >= first && j < used) {
+    const int from = is_near ? near.from[b] : a.plan[kPlanFirstPage * a.batch + b], j = i0 / kPage + int(threadIdx.x);
+    if (j >= from && j < pages_of(end)) {
+      int32_t* row = a.table + size_t(b) * a.max_pages;
       const int pg = row[j], rank = a.fresh[size_t(b) * a.max_pages + j];
-      if (j >= want) {
+      if (j >= pages_of(len)) {
         row[j] = -1;
         drop_ref(a, pg);
       } else if (rank >= 0) {
-        const int to = a.free[a.plan[kPlanFresh * a.batch + b] + rank];
+        const int to = a.free[(is_near ? near.fresh[b] : a.plan[kPlanFresh * a.batch + b]) + rank];
         row[j] = to;
         a.refs[to] = 1;
         drop_ref(a, pg);
       }
     }
-    if (piece == 0 && threadIdx.x == 0) a.ctx[b] = len;
-  }
-  // ... and the old indices of what stays and the weights behind the new ends, in pieces of the requests
-  const int piece = 4 * int(blockDim.x), pieces = (a.cap + piece - 1) / piece;
-  for (long long q = blockIdx.x; q < (long long)a.batch * pieces; q += gridDim.x) {
-    const int b = int(q / pieces), i0 = int(q - (long long)b * pieces) * piece;
-    const int len = a.plan[kPlanNew * a.batch + b], old = a.plan[kPlanOld * a.batch + b];
-    const int32_t* list = a.list + size_t(b) * a.cap;
-    for (int i = i0 + int(threadIdx.x); i < min(i0 + piece, old); i += blockDim.x) {
-      if (len < 0) {
-        if (a.kept) a.kept[b * a.stride + i] = i;
-      } else if (i >= len) {
-        a.mass[b * a.stride + i] = 0.f;
-      } else if (a.kept) {
-        a.kept[b * a.stride + i] = list[i];
-      }
-    }
+    if (i0 == 0 && threadIdx.x == 0) a.ctx[b] = len;
   }
 }
 
@@ -668,7 +674,8 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   a.list = reinterpret_cast<int32_t*>(ws + L.ev_list);
   a.head = reinterpret_cast<long long*>(ws + L.ev_head);
   a.item = reinterpret_cast<long long*>(ws + L.ev_req);
-  a.plan = reinterpret_cast<int32_t*>(ws + L.ev_req + size_t(8) * p.batch);
+  a.piece = a.item + p.batch;
+  a.plan = reinterpret_cast<int32_t*>(a.piece + p.batch);
   a.fresh = reinterpret_cast<int32_t*>(ws + L.ev_page);
   a.free = reinterpret_cast<int32_t*>(ws + L.ev_free);
   a.err = reinterpret_cast<int*>(ws + L.err);
@@ -681,7 +688,9 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   a.recent = recent;
   a.units = q.units;
   int ctas = 1;
-  while (ctas < kMaxCl && L.cap > ctas * kClTokens) ctas *= 2;
+  // (a table may be far wider than its contexts: with 16 CTAs for each of 64 requests of 4,096 tokens in one of 1,048,576
+  // a call took 178 us)
+  while (ctas < kMaxCl && L.cap > ctas * kClTokens && p.batch * ctas * 2 <= sm_count()) ctas *= 2;
   const int slice = ((L.cap + ctas - 1) / ctas + 1023) & ~1023, room = slice < kMaxKeys ? slice : kMaxKeys;
   static std::atomic<uint64_t> keys_set{0}, cluster_set{0}, slots_set{0};
   cudaError_t e = set_once(keys_set, evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);

@@ -160,6 +160,14 @@ def test_many_requests():
     State(lens, ("key_mxfp4",), seed=8).check(budgets, 2, 5)
 
 
+@pytest.mark.parametrize("batch,width", [(3, 5000), (40, 3000), (300, 700)])
+def test_a_table_far_wider_than_its_contexts(batch, width):
+    rng = np.random.default_rng(16)
+    lens = rng.integers(1, 400, batch).tolist()
+    lens[0] = 2500
+    State(lens, ("key_mxfp4",), seed=16, width=width).check([n - 1 - n // 3 for n in lens], 3, 9)
+
+
 def test_many_batches_of_moves():
     """More units than all CTAs gather at once, several times over, for one request and for several."""
     State([150000], seed=9).check([110000], 0, 100)
