@@ -25,7 +25,9 @@ namespace {
 constexpr int kCtas = 8;        // of the plan's cluster
 constexpr int kMaxCl = 16;        // of the choice's, at most
 constexpr int kClTokens = 16384;  // tokens of a CTA's slice, at most, while the GPU has CTAs to give
-constexpr int kMaxKeys = 47104;   // keys that fit a CTA
+constexpr int kRound = 4096;      // a slice is a multiple of: 128 tokens a warp
+constexpr int kMaxKeys = 45056;   // keys that fit a CTA
+static_assert(kMaxKeys % kRound == 0, "whole slices");
 constexpr int kPieceTokens = 1536;  // what a CTA finishes at once: tables, weights behind the end, kept tokens
 constexpr int kThreads = 1024;
 constexpr int kBins = 2048;
@@ -104,10 +106,10 @@ __device__ __forceinline__ uint32_t mass_key(float f) { return f != f ? 0u : sco
 // ---------------------------------------------------------------- select
 // A cluster per request, of as many CTAs as its tokens need (1 to 16). A CTA has a slice of the tokens, whose keys
 // stay in shared memory (`room` of them; what is behind is read again), a warp a stretch of the slice, so that the order within it
-// takes ballots and no barrier.
+// takes shuffles and no barrier. A lane has four consecutive keys at a time.
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int room) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(8) uint32_t hist[3][kBins], s_total[kBins];
   __shared__ uint32_t s_part[kThreads], sums[32], s_gt[32], s_eq[32];
   __shared__ uint32_t s_bin, s_left, s_all[kMaxCl][3], s_shared[kMaxCl], s_mine;
@@ -127,11 +129,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   ptx::cluster_arrive();
   const int head = min(a.sinks, budget), tail = min(a.recent, budget - head);
   const int mid = n - head - tail;                  // tokens to choose from
-  const int per = ((mid + ctas - 1) / ctas + 1023) & ~1023, i0 = min(mid, me * per), len = min(mid, i0 + per) - i0;
-  const int seg = per / 32, w0 = min(len, warp * seg), w1 = min(len, w0 + seg);  // (seg is a multiple of 32)
+  const int per = ((mid + ctas - 1) / ctas + kRound - 1) / kRound * kRound, i0 = min(mid, me * per), len = min(mid, i0 + per) - i0;
+  const int seg = per / 32, w0 = min(len, warp * seg), w1 = min(len, w0 + seg);  // (whole 128s before the last)
   const float* mass = a.mass + b * a.stride + head + i0;
   int32_t* list = a.list + size_t(b) * a.cap;
-  auto key = [&](int i) { return i < room ? keys[i] : mass_key(mass[i]); };
+  auto keys4 = [&](int i, uint32_t (&x)[4]) {  // those at and past w1 are anything
+    if (i + 3 < room) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = i + e < w1 ? mass_key(mass[i + e]) : 0;
+    }
+  };
   // the ends
   for (int i = me * kThreads + tid; i < head; i += ctas * kThreads) list[i] = i;
   for (int i = me * kThreads + tid; i < tail; i += ctas * kThreads) list[budget - tail + i] = n - tail + i;
@@ -175,10 +185,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
       if (pass > 0) {
         const int above = pass == 1 ? 21 : 10;  // the bits from there on are those of tau
-#pragma unroll 4
-        for (int j = w0; j < w1; j += 32) {
-          const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
-          count(hist[pass], j + lane < w1 && (x ^ tau) >> above == 0, (x >> shift) & (bins - 1));
+#pragma unroll 2
+        for (int j = w0; j < w1; j += 128) {
+          const int i = j + 4 * lane;
+          uint32_t x[4];
+          bool in[4];
+          keys4(i, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) in[e] = i + e < w1 && (x[e] ^ tau) >> above == 0;
+          if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) count(hist[pass], in[e], (x[e] >> shift) & (bins - 1));
         }
         __syncthreads();
       }
@@ -218,12 +235,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   }
   // how many of each kind the warps and the CTAs hold, and the first token that goes (equal ones go from `left` on)
   uint32_t gt = 0, eq = 0;
-#pragma unroll 4
-  for (int j = w0; j < w1; j += 32) {
-    const uint32_t x = j + lane < w1 ? key(j + lane) : 0;
-    gt += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > 0 && x > tau));
-    eq += __popc(__ballot_sync(0xffffffffu, j + lane < w1 && k > 0 && x == tau));
+#pragma unroll 2
+  for (int j = w0; j < w1; j += 128) {
+    const int i = j + 4 * lane;
+    uint32_t x[4];
+    keys4(i, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += i + e < w1 && k > 0 && x[e] > tau;
+      eq += i + e < w1 && k > 0 && x[e] == tau;
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
@@ -255,19 +279,36 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     }
   }
   // the kept tokens, in order; a tie's rank decides
-  const uint32_t below = (1u << lane) - 1;
   int first = 0x7FFFFFFF;
-#pragma unroll 4
-  for (int j = w0; j < w1; j += 32) {
-    const int i = j + lane;
-    const uint32_t x = i < w1 ? key(i) : 0;
-    const bool is_gt = i < w1 && k > 0 && x > tau, is_eq = i < w1 && k > 0 && x == tau;
-    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me2 = __ballot_sync(0xffffffffu, is_eq);
-    const uint32_t g = gt + __popc(mg & below), e = eq + __popc(me2 & below);
-    if (is_gt || (is_eq && e < left)) list[head + g + min(e, left)] = head + i0 + i;
-    else if (i < w1) first = min(first, head + i0 + i);
-    gt += __popc(mg);
-    eq += __popc(me2);
+#pragma unroll 2
+  for (int j = w0; j < w1; j += 128) {
+    const int i = j + 4 * lane;
+    uint32_t x[4];
+    keys4(i, x);
+    uint32_t mine = 0;  // counts of both kinds, the ties' above bit 16
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      mine += i + e < w1 && k > 0 ? uint32_t(x[e] > tau) | uint32_t(x[e] == tau) << 16 : 0;
+    uint32_t up = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, up, 31);
+    uint32_t g = gt + ((up - mine) & 0xFFFF), q = eq + ((up - mine) >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool is_gt = k > 0 && x[e] > tau, is_eq = k > 0 && x[e] == tau;
+      if (i + e < w1) {
+        if (is_gt || (is_eq && q < left)) list[head + g + min(q, left)] = head + i0 + i + e;
+        else first = min(first, head + i0 + i + e);
+      }
+      g += is_gt;
+      q += is_eq;
+    }
+    gt += all & 0xFFFF;
+    eq += all >> 16;
   }
   first = __reduce_min_sync(0xffffffffu, first);
   if (lane == 0 && first != 0x7FFFFFFF) atomicMin(&s_mine, uint32_t(first));
@@ -691,7 +732,7 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   // (a table may be far wider than its contexts: with 16 CTAs for each of 64 requests of 4,096 tokens in one of 1,048,576
   // a call took 178 us)
   while (ctas < kMaxCl && L.cap > ctas * kClTokens && p.batch * ctas * 2 <= sm_count()) ctas *= 2;
-  const int slice = ((L.cap + ctas - 1) / ctas + 1023) & ~1023, room = slice < kMaxKeys ? slice : kMaxKeys;
+  const int slice = ((L.cap + ctas - 1) / ctas + kRound - 1) / kRound * kRound, room = slice < kMaxKeys ? slice : kMaxKeys;
   static std::atomic<uint64_t> keys_set{0}, cluster_set{0}, slots_set{0};
   cudaError_t e = set_once(keys_set, evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeys * 4);
   if (e != cudaSuccess) return e;

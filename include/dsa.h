@@ -125,7 +125,8 @@ typedef struct {
  * the split-KV partial outputs and (for dsa_decode) the fp32 scores of every
  * row over max_pages_per_req * page_size tokens. The scratch of dsa_prefix_mla_decode
  * and of the page operations shares the room of the partial outputs where it fits (0.6 MB a
- * row and 21 MB; 12 B a page). */
+ * row and 21 MB; 12 B a page), and so does that of dsa_window_mla_decode, dsa_attention_mass and
+ * dsa_tokens_evict (the scores' room for its list). */
 dsa_status_t dsa_workspace_size(const dsa_params_t* params, size_t* bytes);
 
 /* Stage 1, the lightning indexer ("K3.1 Pro 中的稀疏注意力"), with the FP8 query
