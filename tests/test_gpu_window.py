@@ -97,6 +97,29 @@ def test_long_contexts_and_many_rows():
     check(inp, 70, 500, rows={0, 1, 64, 101, 178, 179})
 
 
+@pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
+@pytest.mark.parametrize("lens,n_q", [([200 + i for i in range(76)], 1), ([300] * 100, 1), ([900] * 24, 4), ([130] * 200, 3), ([64, 5000], 2)])
+def test_many_jobs(lat_fmt, lens, n_q):
+    """As many jobs as CTA pairs, or several times as many, or one that dwarfs the other, with empty requests and bad pages among
+    them; the same call gives the same bits."""
+    import torch
+
+    inp = make(lens, n_q, 70, 120, seed=30 + n_q, lat_fmt=lat_fmt, release=False)
+    inp.ctx = inp.ctx.copy()
+    rows = {r for b in (1, len(lens) // 2, len(lens) - 1) for r in range(b * n_q, (b + 1) * n_q)}
+    bits = 0
+    if len(lens) > 2:
+        inp.ctx[0] = 0  # no job
+        inp.block_table[len(lens) - 1, 0] = -1
+        bits = dsa.DSA_DEVERR_CTX | dsa.DSA_DEVERR_BLOCK_TABLE
+    d, out, lse = check(inp, 70, 120, rows=rows, bits=bits)
+    if len(lens) > 2:
+        assert (out[:n_q] == 0).all() and (lse[:n_q] == -np.inf).all()
+    again, _ = launch(d, 70, 120, lse=False)
+    assert (again.view(torch.int16) == out.view(torch.int16)).all()
+    assert dsa.get_device_error(d.ws) == bits
+
+
 def test_a_wide_window_is_the_dense_call():
     """The same bits for single rows (rows of a request share jobs here, and not there)."""
     import torch
