@@ -13,6 +13,11 @@
 //   order: every CTA gathers its units of batch k into shared memory, all CTAs meet, and the units are written, while
 //   those of batch k + 1 (which read behind all that batches up to k write) are already on their way into the other half of
 //   shared memory. The bytes moved bound it, read once and written once.
+//
+// Measured (one GB300, in a graph, all three): 48 requests of 12,000 tokens to 8,192, FP8 latents and index keys of four layers,
+// 258 us (1.15 GB; the moves at 5 TB/s, in lock step with a barrier a batch); one of 524,289 tokens to 131,072 96 us, some 40 of
+// them the choice by 16 CTAs; 4 of 4,096 to 2,048 24 us, the latency of the passes and barriers. (The choice with its keys in
+// global memory and the move's addresses looked up a batch at a time: 324, 218 and 38 us.)
 #include <cooperative_groups.h>
 
 #include "dsa_internal.cuh"

@@ -6,15 +6,19 @@
 // one accumulator lane per token; a thread has one token, and its sum over the heads is its own: no shuffle, no
 // atomic, the same bits in any batch. The query is prepared as for the dense attention (FP8 latents: two FP8 parts, here both
 // E4M3, the second times 2^5, multiplied with the latents as TMA brings them in one product of 192 columns, so that the latents
-// are read from shared memory once: with a product for each part 59.3 us for the first case below; NVFP4 ones: fp16) and stays in
+// are read from shared memory once: with a product for each part 60.8 us for 40 requests; NVFP4 ones: fp16) and stays in
 // shared memory (110 KB) while tiles of tokens stream past it. NVFP4 latents are converted to fp16 and multiplied from tensor
-// memory: through shared memory, which the products read 28 KB of per K-block, their 16 KB took 226 us for the
-// case below.
+// memory: through shared memory, which the products read 28 KB of per K-block, their 16 KB took 226 us for the 48 rows.
 //
 // The tiles of all requests are a line that is cut into equal runs, one per CTA, and a run into chunks of at most 16
 // tiles of one request. A chunk is gone through once per row (its latents come from L2 after the first), its sums
 // wait in shared memory, and are added to the weights once. The next row's query arrives block by block behind the
 // last tile that uses the old one.
+//
+// Measured (one GB300; these are "the 40 requests" and "the 48 rows" of this file): 40 requests of up to 16,384 FP8 tokens 57.5 us in
+// a graph, of which the query's preparation and the start are some 8 (292 MB of latents and weights, 5.1 TB/s; 15.8 ms with plain
+// loops), bound by the bytes, then by the issue of the products; 6 requests of 8 rows on 20,001 NVFP4 tokens 92.5 us (1.11 PFLOP/s),
+// bound by the converters, which go through a tile once per row, and by shared memory; one row on 4,100 tokens 8.6 us.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
@@ -31,7 +35,7 @@ namespace {
 constexpr int kTok = 128;                     // tokens of a tile
 // A tile comes in three parts. FP8: 192 dims of its rows, 128 rows of 128 B and 128 of 64 B, in four stages. NVFP4: 128 B of its
 // rows as they lie, in six. (The issuing warp's wait for a part costs some 95 cycles behind its products, which it blocks on:
-// parts of 128 dims took 62.7 us for the first case below.)
+// parts of 128 dims took 62.6 us for the 40 requests, these 60.8.)
 constexpr int kParts = 3;
 template <bool kNv>
 constexpr int kStage = kNv ? kTok * 128 : kTok * 192;  // 16,384 or 24,576 B
@@ -40,11 +44,12 @@ constexpr int kStages = kNv ? 6 : 4;
 constexpr int kRingBytes = 6 * 16384;
 static_assert(kStage<true> * kStages<true> == kRingBytes && kStage<false> * kStages<false> == kRingBytes, "either ring");
 constexpr int kQBlk = kHeads * 128;           // 12,288 B: 128 B of each head
-constexpr int kQBytes = 9 * kQBlk;            // of a row's heads: pieces of the dims (FP8: [4][part], and [part] of 64 rotary bytes)
+// of a row's heads: pieces of the dims (FP8: [4][part], and [part] of 64 rotary bytes)
+constexpr int kQBytes = 9 * kQBlk;
 constexpr int kChunk = 16;                    // tiles of a chunk
 // tensor memory: two accumulators of 96 columns, FP8: of 192, for the two parts of the query; NVFP4: and a tile's values in three
 // stages of 96 columns (192 dims: with a stage for each of the nine K-blocks the wait and the fence of every four products took
-// 116 us for the case below)
+// 116 us for the 48 rows, this 102)
 constexpr int kDBufs = 2;
 template <bool kNv>
 constexpr int kDCols = kNv ? 96 : 192;
@@ -52,7 +57,7 @@ constexpr int kACol = 192;
 static_assert(kACol + kDQK / 2 <= 512, "tensor memory");
 template <bool kNv>
 constexpr int kThreads = kNv ? 512 : 256;
-// warps: 0..3 sums, 4 products, 5 latents (FP8), 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
+// warps: 0..3 sums, 4 products, 5 latents, 6 query, 7 the heads' constants, 8..15 converters (NVFP4)
 constexpr int kMmaWarp = 4, kTileWarp = 5, kQueryWarp = 6, kHeadWarp = 7;
 constexpr int kNumBars = 2 * 6 + 2 * kParts + 2 * 4 + 4 + 2 * kParts + 1;
 constexpr size_t kSmem = 1024 + kRingBytes + kQBytes + kChunk * kTok * 4 + 2 * 2 * kHeads * 4 + kNumBars * 8 + 64;
@@ -60,7 +65,7 @@ static_assert(kSmem <= 232448 - 512, "shared memory, with the static variables")
 constexpr uint32_t kPolls = 1u << 20;  // 4 s
 
 struct MassArgs {
-  const float* qs;    // [rows * 96] its scales
+  const float* qs;    // [rows * 96] the prepared query's scales
   const float* lse;   // [rows * 96]
   const uint8_t* lat;
   const int32_t* table;

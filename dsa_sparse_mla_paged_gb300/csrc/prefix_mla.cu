@@ -32,7 +32,8 @@
 // on 262,144 shared tokens 990 to 1,090 us by the card (1.44 to 1.31 PFLOP/s; 882 us with pauses between
 // calls), 64 rows on 32,768 and 1,900 of their own 297 to 317 us (1.52 to 1.43 PFLOP/s; 282 with pauses),
 // 24 rows on 8,111 of their own 41.5 us, one row on 4,096 20.4 us; NVFP4, 8 x 6 rows on 16,384 and 700
-// of their own 212 us (0.79 PFLOP/s). An FP8 tile takes about
+// of their own 212 us (0.79 PFLOP/s). With kWin 64 rows that see 64 + 4,096 tokens 72.4 us, 3 requests of 333 rows that see 5 + 2,049
+// NVFP4 ones 666 us (835 with a job a row), one row on 4 + 1,024 19.9 us. An FP8 tile takes about
 // 1,430 cycles; the scores' products, at 1,165, bound it, and an NVFP4 tile about 2,600: its
 // K-blocks' stores and products share CTA 0's shared memory (without the stores 152 us,
 // without the arithmetic of the conversion 206). Registers are at their limit of 96: the NVFP4 kernel

@@ -519,14 +519,15 @@ typedef struct {
 /* Evicts tokens: every request b with more tokens than budgets[b] (int32 [batch]; a negative entry
  * leaves the request as it is) is cut to budgets[b] tokens. It keeps its first s = min(sinks, budget)
  * tokens, its last r = min(recent, budget - s), and of those between the budget - s - r with the
- * largest mass (a tie goes to the lower token; -0 == +0, a NaN is below everything). What is kept moves together, in its order: the
- * rows in every pool, and the masses (those past the new length become 0). Pages before the first evicted
- * token stay as they are; of the others those with one reference are rewritten in place, and for each with more the
- * request gets a fresh page (references 1; the shared one loses one), so that no other holder sees a
- * change. The pages past ceil(new / 64) lose a reference each, and their entries become -1. Fresh pages are the free pages with the lowest
- * numbers, in the order of the requests and of their pages; pages that this call frees are not handed out by it. If they do
- * not reach, the first request that does not fit and every later one that needs fresh pages
- * keep their tokens (DSA_DEVERR_NO_PAGES).
+ * largest mass (a tie goes to the lower token; -0 == +0, a NaN is below everything). What is kept moves
+ * together, in its order: the rows in every pool, and the masses (those past the new length become 0).
+ * Pages before the first evicted token stay as they are; of the others those with one reference are
+ * rewritten in place, and for each with more the request gets a fresh page (references 1; the shared one
+ * loses one), so that no other holder sees a change. The pages past ceil(new / 64) lose a reference each,
+ * and their entries become -1. Fresh pages are the free pages with the lowest numbers, in the order of the
+ * requests and of their pages; pages that this call frees are not handed out by it. If they do not reach,
+ * the first request that does not fit and every later one that needs fresh pages keep their tokens
+ * (DSA_DEVERR_NO_PAGES).
  * Rotary positions are in the latents: later tokens need dsa_latent_frontend's positions.
  *   sinks, recent >= 0
  *   mass    fp32 [B, token_stride], as dsa_attention_mass leaves it; not negative, usually
