@@ -1,4 +1,5 @@
 // libdsa C ABI: host-side validation, workspace carving and stage launches.
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
@@ -95,7 +96,9 @@ dsa_status_t check_token_pools(const dsa_params_t* p, const dsa_token_pool_t* po
     if (q.layers > 4096) return DSA_ERR_UNSUPPORTED;
     const int64_t page = kTokenPage[q.fmt];
     if (q.page_stride < page || (q.page_stride & 15)) return DSA_ERR_INVALID;
-    if (q.page_stride > (int64_t(1) << 40) || q.layer_stride > (int64_t(1) << 50)) return DSA_ERR_UNSUPPORTED;
+    // (2^50 B: what the sums below, and the kernels' offsets, hold)
+    if (q.page_stride > std::min(int64_t(1) << 40, (int64_t(1) << 50) / p->num_pages) || q.layer_stride > (int64_t(1) << 50))
+      return DSA_ERR_UNSUPPORTED;
     if (q.layers == 1) continue;
     if (q.layer_stride < page || (q.layer_stride & 15)) return DSA_ERR_INVALID;
     // layers inside a page's row, or pages inside a layer

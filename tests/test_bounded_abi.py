@@ -113,6 +113,9 @@ def test_evict_pools(lib):
         assert status((4 * FAKE, V, 1, 0, 36864), bad) == INVALID, bad
     assert status((FAKE, V, 4097, 36864, 1 << 30)) == UNSUPPORTED
     assert status((FAKE, V, 1, 0, 1 << 41)) == UNSUPPORTED
+    far = _params(num_pages=1 << 30)  # pages at products past 63 bits
+    q, n = dsa.make_token_pools([(FAKE, V, 2, 36864, 1 << 34)])
+    assert _call("dsa_tokens_evict", far, EVICT, pools=q, n=n, bytes=0) == UNSUPPORTED
     many = [(FAKE * (i + 1), V, 1, 0, 36864) for i in range(65)]
     assert status(*many) == UNSUPPORTED
     assert status(*many[:64], bytes=0) == WORKSPACE
