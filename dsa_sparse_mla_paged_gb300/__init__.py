@@ -7,7 +7,8 @@ exceptions. There is no fallback: if libdsa.so is missing, ``load()`` raises.
 Entry points mirror include/dsa.h: ``workspace_size``, ``indexer_scores``,
 ``indexer_frontend``, ``indexer_prefill_scores``, ``topk``, ``topk_noalloc``, ``dcp_topk_merge``, ``lse_combine``, ``sparse_mla_decode``,
 ``decode``, ``prefix_mla_decode``, ``pages_resize``, ``pages_fork``, ``pages_compact``, ``verify_draft``,
-``latent_frontend``, ``window_mla_decode``, ``attention_mass``, ``tokens_evict``, ``get_device_error``, ``selftest_wait_timeout``, ``status_string``.
+``latent_frontend``, ``window_mla_decode``, ``attention_mass``, ``tokens_evict``, ``get_device_error``,
+``selftest_wait_timeout``, ``status_string``.
 """
 from __future__ import annotations
 
@@ -445,11 +446,19 @@ def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv
         _ptr(ctx_lens), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
+def _int32(fn, name, v):
+    """A count that the C call takes in 32 bits (ctypes would cut it off)."""
+    if not -1 << 31 <= v < 1 << 31:
+        raise ValueError(f"{fn}: {name} = {v} is not a 32-bit integer")
+    return int(v)
+
+
 def window_mla_decode(params, q, lat_pool, sinks, window, block_table, ctx_lens, out, lse, ws, stream=None):
     """Attention to each row's last `window` tokens and the request's first `sinks`."""
+    fn = "window_mla_decode"
     _check("dsa_window_mla_decode", load().dsa_window_mla_decode(
-        ctypes.byref(params), _ptr(q), _ptr(lat_pool), int(sinks), int(window), _ptr(block_table), _ptr(ctx_lens), _ptr(out),
-        _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _int32(fn, "sinks", sinks), _int32(fn, "window", window), _ptr(block_table),
+        _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def _per_token(fn, name, t, dtype, batch):
@@ -464,19 +473,20 @@ def attention_mass(params, q, lat_pool, sinks, window, block_table, ctx_lens, ls
     last `fresh` tokens of each context are set instead."""
     import torch
 
-    at, stride, width = _per_token("attention_mass", "mass", mass, torch.float32, params.batch)
+    fn = "attention_mass"
+    at, stride, width = _per_token(fn, "mass", mass, torch.float32, params.batch)
     if width < params.max_pages_per_req * params.page_size:
         raise ValueError("attention_mass: mass has fewer tokens than the block table's pages")
     _check("dsa_attention_mass", load().dsa_attention_mass(
-        ctypes.byref(params), _ptr(q), _ptr(lat_pool), int(sinks), int(window), _ptr(block_table), _ptr(ctx_lens),
-        _array("attention_mass", "lse", lse, torch.float32, params.batch * params.n_q * 96), int(fresh), at, stride, _ptr(ws),
-        _nbytes(ws), _stream(stream)))
+        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _int32(fn, "sinks", sinks), _int32(fn, "window", window), _ptr(block_table),
+        _ptr(ctx_lens), _array(fn, "lse", lse, torch.float32, params.batch * params.n_q * 96), _int32(fn, "fresh", fresh), at, stride,
+        _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def make_token_pools(pools):
     """tokens_evict's pool list from (tensor or address, DSA_TOKEN_*, layers, layer_stride, page_stride) tuples (bytes)."""
     pools = list(pools)
-    return (TokenPool * max(len(pools), 1))(*[TokenPool(_ptr(t), int(page), int(layer), int(n), int(fmt))
+    return (TokenPool * max(len(pools), 1))(*[TokenPool(_ptr(t), int(page), int(layer), _int32("make_token_pools", "layers", n), int(fmt))
                                               for t, fmt, n, layer, page in pools]), len(pools)
 
 
@@ -494,8 +504,9 @@ def tokens_evict(params, budgets, sinks, recent, mass, pools, block_table, ctx_l
         if (kept_stride, kept_width) != (stride, width):
             raise ValueError("tokens_evict: kept and mass differ in shape or strides")
     _check("dsa_tokens_evict", load().dsa_tokens_evict(
-        ctypes.byref(params), _array(fn, "budgets", budgets, torch.int32, params.batch), int(sinks), int(recent), at, stride,
-        pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs), kept, _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(params), _array(fn, "budgets", budgets, torch.int32, params.batch), _int32(fn, "sinks", sinks),
+        _int32(fn, "recent", recent), at, stride, pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs), kept, _ptr(ws),
+        _nbytes(ws), _stream(stream)))
 
 
 def get_device_error(ws, stream=None) -> int:

@@ -163,7 +163,20 @@ def test_binding_checks():
         a = {"lse": lse, "mass": mass, name: bad}
         with pytest.raises(ValueError, match=name):
             dsa.attention_mass(p, FAKE, FAKE, 0, 640, FAKE, FAKE, a["lse"], 0, a["mass"], z(256, dtype=torch.uint8), 0)
-    pools, budgets = dsa.make_token_pools([]), z(2, dtype=i32)
+    pools, budgets, ws = dsa.make_token_pools([]), z(2, dtype=i32), z(256, dtype=torch.uint8)
+    for v in (1 << 31, (1 << 32) + 5, 1 << 40, -(1 << 32) + 1):  # the C call would see their low 32 bits
+        for name, call in (
+                ("sinks", lambda: dsa.window_mla_decode(p, FAKE, FAKE, v, 4, FAKE, FAKE, FAKE, None, ws, 0)),
+                ("window", lambda: dsa.window_mla_decode(p, FAKE, FAKE, 0, v, FAKE, FAKE, FAKE, None, ws, 0)),
+                ("sinks", lambda: dsa.attention_mass(p, FAKE, FAKE, v, 4, FAKE, FAKE, lse, 0, mass, ws, 0)),
+                ("window", lambda: dsa.attention_mass(p, FAKE, FAKE, 0, v, FAKE, FAKE, lse, 0, mass, ws, 0)),
+                ("fresh", lambda: dsa.attention_mass(p, FAKE, FAKE, 0, 4, FAKE, FAKE, lse, v, mass, ws, 0)),
+                ("sinks", lambda: dsa.tokens_evict(p, budgets, v, 0, mass, pools, FAKE, FAKE, FAKE, None, ws, 0)),
+                ("recent", lambda: dsa.tokens_evict(p, budgets, 0, v, mass, pools, FAKE, FAKE, FAKE, None, ws, 0))):
+            with pytest.raises(ValueError, match=name):
+                call()
+        with pytest.raises(ValueError, match="layers"):
+            dsa.make_token_pools([(FAKE, 0, v, 0, 8448)])
     for name, bad in (("mass", z(2, 600, dtype=f32)), ("kept", z(2, 640, dtype=torch.int64)), ("kept", z(2, 641, dtype=i32)),
                       ("budgets", z(1, dtype=i32)), ("budgets", z(2, dtype=torch.int64))):
         a = {"mass": mass, "kept": None, "budgets": budgets, name: bad}
