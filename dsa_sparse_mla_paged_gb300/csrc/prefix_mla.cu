@@ -1453,8 +1453,8 @@ cudaError_t launch_window_mla(const dsa_params_t& p, const WsLayout& L, char* ws
                               int sinks, int window, const int32_t* block_table, const int32_t* ctx_lens, void* out,
                               float* lse, cudaStream_t st) {
   PfxArgs a = {};
-  a.sinks = sinks;
-  a.window = window;
+  a.sinks = std::min(sinks, L.cap);  // (all there are, and sums that stay in 31 bits)
+  a.window = std::min(window, L.cap);
   return launch_dense<true>(p, L, ws, a, q, lat_pool, block_table, ctx_lens, out, lse, st);
 }
 

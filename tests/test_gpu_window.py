@@ -86,6 +86,13 @@ def test_matches_oracle(lat_fmt, lens, n_q, sinks, window):
     check(make(lens, n_q, sinks, window, seed=len(lens) + n_q, lat_fmt=lat_fmt), sinks, window)
 
 
+@pytest.mark.parametrize("sinks,window", [(0, 2 ** 31 - 1), (2 ** 31 - 1, 1), (2 ** 31 - 1, 2 ** 31 - 1)])
+def test_the_largest_counts(sinks, window):
+    """More than there can be, in tiles that lie behind a job's first rows: all tokens up to the row's own."""
+    inp = make([200, 331], 150, sinks, window, seed=8)
+    check(inp, sinks, window, rows={0, 1, 70, 149, 150, 223, 299})
+
+
 @pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
 def test_a_prompt_chunk(lat_fmt):
     inp = make([900, 150], 140, 10, 200, seed=3, lat_fmt=lat_fmt)
