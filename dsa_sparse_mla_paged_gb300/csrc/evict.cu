@@ -15,7 +15,7 @@
 //   shared memory. The bytes moved bound it, read once and written once.
 //
 // Measured (one GB300, in a graph, all three): 48 requests of 12,000 tokens to 8,192, FP8 latents and index keys of four layers,
-// 258 us (1.15 GB; the moves at 5 TB/s, in lock step with a barrier a batch); one of 524,289 tokens to 131,072 96 us, some 40 of
+// 250 us (1.15 GB; the moves take some 215, and 195 without their barriers); one of 524,289 tokens to 131,072 89 us, some 35 of
 // them the choice by 16 CTAs; 4 of 4,096 to 2,048 24 us, the latency of the passes and barriers. (The choice with its keys in
 // global memory and the move's addresses looked up a batch at a time: 324, 218 and 38 us.)
 #include <cooperative_groups.h>
@@ -43,7 +43,10 @@ constexpr int kSlot = kLatUnit * kLatRowFp8;
 static_assert(kSlot >= kPage * (kIdxDim + 4), "a page of index keys is a unit, too");
 constexpr int kMassUnit = 1024; // weights
 static_assert(kSlot >= kMassUnit * 4, "weights");
-constexpr int kMoveWarps = 12;
+// Warps of a CTA, two CTAs an SM. (One of twelve warps: 256 and 91.9 us in a graph for the first two cases above, two of six 249 and
+// 88.5; three or four places a warp in the same room, so that rows are gathered two or three batches ahead: 296 and 345 for 264 call by
+// call, as a batch has some 2 us whatever it moves; the moves cut into two parts whose batches do not wait for each other 248.5.)
+constexpr int kMoveWarps = 6;
 constexpr size_t kMoveSmem = size_t(2) * kMoveWarps * kSlot;
 constexpr uint32_t kGridPolls = 1u << 22;  // of a counter in L2, 0.5 us and more each
 
@@ -153,31 +156,50 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   if (tid == 0) s_mine = 0x7FFFFFFF;
   __syncthreads();
-  // Many weights may be alike (those of tokens that nothing looked at): one addition for a warp of them.
-  auto count = [&](uint32_t* h, bool in, uint32_t bin) {
-    const uint32_t m = __ballot_sync(0xffffffffu, in);
+  // Many weights may be alike (those of tokens that nothing looked at): one addition for a warp's four each, if they are.
+  auto count = [&](uint32_t* h, const bool (&in)[4], const uint32_t (&bin)[4]) {
+    uint32_t one = 0xFFFFFFFFu, n = 0;
+#pragma unroll
+    for (int e = 3; e >= 0; --e) {
+      one = in[e] ? bin[e] : one;
+      n += in[e];
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, n > 0);
     if (m == 0) return;
-    const int lead = __ffs(m) - 1;
-    const uint32_t b0 = __shfl_sync(0xffffffffu, bin, lead);
-    if (__all_sync(0xffffffffu, !in || bin == b0)) {
-      if (lane == lead) atomicAdd(h + bin, uint32_t(__popc(m)));
-    } else if (in) {
-      atomicAdd(h + bin, 1u);
+    const uint32_t b0 = __shfl_sync(0xffffffffu, one, __ffs(m) - 1);
+    bool same = true;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) same &= !in[e] || bin[e] == b0;
+    if (__all_sync(0xffffffffu, same)) {
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) atomicAdd(h + b0, n);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in[e]) atomicAdd(h + bin[e], 1u);
     }
   };
   const uint32_t k = uint32_t(budget - head - tail);
-  uint32_t tau = 0xFFFFFFFFu, left = 0;             // keys above tau stay, and the first `left` that equal it
+  // keys above tau stay, and the first `left` that equal it (no key is 0xFFFFFFFF: a NaN's is 0)
+  uint32_t tau = 0xFFFFFFFFu, left = 0;
   // the first pass also fills shared memory, eight loads at a time
   for (int j = w0; j < w1; j += 256) {
     float m[8];
 #pragma unroll
     for (int d = 0; d < 8; ++d) m[d] = j + 32 * d + lane < w1 ? mass[j + 32 * d + lane] : 0.f;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-      const int i = j + 32 * d + lane;
-      const uint32_t x = mass_key(m[d]);
-      if (i < w1 && i < room) keys[i] = x;
-      count(hist[0], i < w1, x >> 21);
+    for (int d = 0; d < 8; d += 4) {
+      bool in[4];
+      uint32_t bin[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = j + 32 * (d + e) + lane;
+        const uint32_t x = mass_key(m[d + e]);
+        if (i < w1 && i < room) keys[i] = x;
+        in[e] = i < w1;
+        bin[e] = x >> 21;
+      }
+      count(hist[0], in, bin);
     }
   }
   __syncthreads();
@@ -197,10 +219,11 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
           bool in[4];
           keys4(i, x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) in[e] = i + e < w1 && (x[e] ^ tau) >> above == 0;
-          if (!__any_sync(0xffffffffu, in[0] | in[1] | in[2] | in[3])) continue;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) count(hist[pass], in[e], (x[e] >> shift) & (bins - 1));
+          for (int e = 0; e < 4; ++e) {
+            in[e] = i + e < w1 && (x[e] ^ tau) >> above == 0;
+            x[e] = (x[e] >> shift) & (bins - 1);
+          }
+          count(hist[pass], in, x);
         }
         __syncthreads();
       }
@@ -247,8 +270,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     keys4(i, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      gt += i + e < w1 && k > 0 && x[e] > tau;
-      eq += i + e < w1 && k > 0 && x[e] == tau;
+      gt += i + e < w1 && x[e] > tau;
+      eq += i + e < w1 && x[e] == tau;
     }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
@@ -285,35 +308,30 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   }
   // the kept tokens, in order; a tie's rank decides
   int first = 0x7FFFFFFF;
-#pragma unroll 2
+  uint32_t at = head + gt + min(eq, left);
+  const uint32_t below = (1u << lane) - 1;
+#pragma unroll 1
   for (int j = w0; j < w1; j += 128) {
-    const int i = j + 4 * lane;
     uint32_t x[4];
-    keys4(i, x);
-    uint32_t mine = 0;  // counts of both kinds, the ties' above bit 16
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      mine += i + e < w1 && k > 0 ? uint32_t(x[e] > tau) | uint32_t(x[e] == tau) << 16 : 0;
-    uint32_t up = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, up, o);
-      if (lane >= o) up += y;
-    }
-    const uint32_t all = __shfl_sync(0xffffffffu, up, 31);
-    uint32_t g = gt + ((up - mine) & 0xFFFF), q = eq + ((up - mine) >> 16);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool is_gt = k > 0 && x[e] > tau, is_eq = k > 0 && x[e] == tau;
-      if (i + e < w1) {
-        if (is_gt || (is_eq && q < left)) list[head + g + min(q, left)] = head + i0 + i + e;
-        else first = min(first, head + i0 + i + e);
-      }
-      g += is_gt;
-      q += is_eq;
+      const int i = j + 32 * e + lane;  // (128 tokens are on one side of `room`)
+      x[e] = j < room ? keys[i] : i < w1 ? mass_key(mass[i]) : 0;
     }
-    gt += all & 0xFFFF;
-    eq += all >> 16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = j + 32 * e + lane;
+      bool keep = i < w1 && x[e] > tau;
+      const uint32_t ties = __ballot_sync(0xffffffffu, i < w1 && x[e] == tau);
+      if (ties) {
+        keep |= (ties >> lane & 1) && eq + __popc(ties & below) < left;
+        eq += __popc(ties);
+      }
+      const uint32_t kept = __ballot_sync(0xffffffffu, keep);
+      if (keep) list[at + __popc(kept & below)] = head + i0 + i;
+      else if (i < w1) first = min(first, head + i0 + i);
+      at += __popc(kept);
+    }
   }
   first = __reduce_min_sync(0xffffffffu, first);
   if (lane == 0 && first != 0x7FFFFFFF) atomicMin(&s_mine, uint32_t(first));
@@ -474,13 +492,14 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 
 // What a CTA keeps of the requests' plans in shared memory, if there are no more of them.
-constexpr int kKept = 256;
+constexpr int kKept = 192;
 struct Plans {
-  long long item[kKept], piece[kKept];
-  int32_t len[kKept], from[kKept], fresh[kKept], old[kKept];
+  long long item[kKept];
+  int32_t len[kKept], from[kKept], fresh[kKept];
 };
+static_assert(kMoveSmem + sizeof(Plans) + 1024 + 64 <= 233472 / 2, "two CTAs an SM");
 
-// The last request whose first item (or piece) is at or before `at`: those without any share their start with the next.
+// The last request whose first item (or piece of what follows) is at or before `at`: those without any share their start with the next.
 __device__ __forceinline__ int request_of(const long long* first, int batch, long long at) {
   int lo = 0, hi = batch;
   while (hi - lo > 1) {
@@ -583,7 +602,7 @@ __device__ __forceinline__ void drop_ref(const EvictArgs& a, int pg) {
 }
 
 // A cooperative launch (its CTAs meet).
-__global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const __grid_constant__ EvictArgs a,
+__global__ void __launch_bounds__(32 * kMoveWarps, 2) evict_apply_kernel(const __grid_constant__ EvictArgs a,
                                                                         const __grid_constant__ TokenPools pools) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_ok;
@@ -604,8 +623,6 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
       near.len[b] = a.plan[kPlanNew * a.batch + b];
       near.from[b] = a.plan[kPlanFirstPage * a.batch + b];
       near.fresh[b] = a.plan[kPlanFresh * a.batch + b];
-      near.old[b] = a.plan[kPlanOld * a.batch + b];
-      near.piece[b] = a.piece[b];
     }
     __syncthreads();
   }
@@ -665,9 +682,9 @@ __global__ void __launch_bounds__(32 * kMoveWarps, 1) evict_apply_kernel(const _
   const long long pieces = a.head[kHeadPieces];
   const bool is_near = a.batch <= kKept;
   for (long long q = blockIdx.x; q < pieces; q += gridDim.x) {
-    const int b = request_of(is_near ? near.piece : a.piece, a.batch, q);
-    const int i0 = int(q - (is_near ? near.piece[b] : a.piece[b])) * kPieceTokens;
-    const int len = is_near ? near.len[b] : a.plan[kPlanNew * a.batch + b], old = is_near ? near.old[b] : a.plan[kPlanOld * a.batch + b];
+    const int b = request_of(a.piece, a.batch, q);
+    const int i0 = int(q - a.piece[b]) * kPieceTokens;
+    const int len = is_near ? near.len[b] : a.plan[kPlanNew * a.batch + b], old = a.plan[kPlanOld * a.batch + b];
     const int end = min(i0 + kPieceTokens, old);
     const int32_t* list = a.list + size_t(b) * a.cap;
     for (int i = i0 + int(threadIdx.x); i < end; i += blockDim.x) {
@@ -765,7 +782,7 @@ cudaError_t launch_tokens_evict(const dsa_params_t& p, const WsLayout& L, char* 
   e = set_once(slots_set, evict_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMoveSmem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sm_count());
+  cfg.gridDim = dim3(2 * sm_count());
   cfg.blockDim = dim3(32 * kMoveWarps);
   cfg.dynamicSmemBytes = kMoveSmem;
   cfg.stream = st;
