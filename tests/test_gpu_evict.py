@@ -129,6 +129,15 @@ def test_fresh_pages_run_out():
     assert s.ctx.tolist() == [100, 320, 310, 90]
 
 
+@pytest.mark.parametrize("spare", [0, 5, 40, 2000, 70001])
+def test_fresh_pages_from_pools_of_any_size(spare):
+    """The lowest free pages, wherever they lie, and none handed out twice."""
+    s = State([700 + 3 * i for i in range(30)], ("key_mxfp4",), shared=9, sharers=20, seed=17, spare=spare)
+    s.check([400 + i for i in range(30)], 3, 9, bits=0 if spare > 150 else dsa.DSA_DEVERR_NO_PAGES)
+    live = np.concatenate([s.table[b, :-(-int(n) // 64)] for b, n in enumerate(s.ctx)])
+    assert (np.bincount(live, minlength=s.num_pages) == s.refs).all()
+
+
 def test_bad_requests_are_left_alone():
     s = State([300, 320, 310, 200, 100], seed=6, width=6)
     s.table[0, 2], s.refs[s.table[1, 4]] = s.num_pages, 0
