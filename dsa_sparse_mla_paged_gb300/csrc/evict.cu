@@ -114,7 +114,8 @@ __device__ __forceinline__ uint32_t mass_key(float f) { return f != f ? 0u : sco
 // ---------------------------------------------------------------- select
 // A cluster per request, of as many CTAs as its tokens need (1 to 16). A CTA has a slice of the tokens, whose keys
 // stay in shared memory (`room` of them; what is behind is read again), a warp a stretch of the slice, so that the order within it
-// takes shuffles and no barrier. A lane has four consecutive keys at a time.
+// takes shuffles and no barrier. A lane has four consecutive keys at a time. (Loops are not unrolled: a phase's first
+// instructions come slower than its keys.)
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int room) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint32_t keys[];
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
       if (pass > 0) {
         const int above = pass == 1 ? 21 : 10;  // the bits from there on are those of tau
-#pragma unroll 2
+#pragma unroll 1
         for (int j = w0; j < w1; j += 128) {
           const int i = j + 4 * lane;
           uint32_t x[4];
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
   }
   // how many of each kind the warps and the CTAs hold, and the first token that goes (equal ones go from `left` on)
   uint32_t gt = 0, eq = 0;
-#pragma unroll 2
+#pragma unroll 1
   for (int j = w0; j < w1; j += 128) {
     const int i = j + 4 * lane;
     uint32_t x[4];

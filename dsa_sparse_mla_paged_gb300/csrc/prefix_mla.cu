@@ -1254,19 +1254,17 @@ __global__ void __launch_bounds__(32 * kQueryWarps)
   }
   if (lane == 0) qs[hr] = scalbnf(1.f, e);
   __syncthreads();
-  if constexpr (kHeadMajor) {
-    for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
+  for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
+    if constexpr (kHeadMajor) {
       const int h = i / kChunks, at = i % kChunks;
       const int chunk = kNv || at < 32 || at >= 68 ? at : at < 64 ? at + 4 : at - 32;
       reinterpret_cast<uint4*>(prepared)[size_t(blockIdx.x * kQueryWarps) * kChunks + i] =
           *reinterpret_cast<const uint4*>(s_out + chunk * kPitch + h * 4);
+    } else {
+      const int chunk = i / kQueryWarps, h = i % kQueryWarps;
+      reinterpret_cast<uint4*>(prepared)[size_t(chunk) * heads + blockIdx.x * kQueryWarps + h] =
+          *reinterpret_cast<const uint4*>(s_out + chunk * kPitch + h * 4);
     }
-    return;
-  }
-  for (int i = threadIdx.x; i < kChunks * kQueryWarps; i += 32 * kQueryWarps) {
-    const int chunk = i / kQueryWarps, h = i % kQueryWarps;
-    reinterpret_cast<uint4*>(prepared)[size_t(chunk) * heads + blockIdx.x * kQueryWarps + h] =
-        *reinterpret_cast<const uint4*>(s_out + chunk * kPitch + h * 4);
   }
 }
 
