@@ -29,15 +29,17 @@
 // adds up over the thousands of them. Sums are fp32 throughout.
 //
 // Measured (one GB300, call after call, where the clock falls under the power limit): 13 x 2 rows
-// on 262,144 shared tokens 990 to 1,090 us by the card (1.44 to 1.31 PFLOP/s; 882 us with pauses between
-// calls), 64 rows on 32,768 and 1,900 of their own 297 to 317 us (1.52 to 1.43 PFLOP/s; 282 with pauses),
-// 24 rows on 8,111 of their own 41.5 us, one row on 4,096 20.4 us; NVFP4, 8 x 6 rows on 16,384 and 700
-// of their own 212 us (0.79 PFLOP/s). With kWin 64 rows that see 64 + 4,096 tokens 72.4 us, 3 requests of 333 rows that see 5 + 2,049
-// NVFP4 ones 666 us (835 with a job a row), one row on 4 + 1,024 19.9 us. An FP8 tile takes about
-// 1,430 cycles; the scores' products, at 1,165, bound it, and an NVFP4 tile about 2,600: its
-// K-blocks' stores and products share CTA 0's shared memory (without the stores 152 us,
-// without the arithmetic of the conversion 206). Registers are at their limit of 96: the NVFP4 kernel
-// spills 80 bytes a thread, the FP8 one 8.
+// on 262,144 shared tokens 960 to 1,090 us by the card (1.48 to 1.31 PFLOP/s; 882 us with pauses between
+// calls), 64 rows on 32,768 and 1,900 of their own 272 to 310 us, 24 rows on 8,111 of their own 50 us,
+// one row on 4,096 19.7 us; NVFP4, 8 x 6 rows on 16,384 and 700 of their own 165 us (1.01 PFLOP/s). With kWin 64 rows
+// that see 64 + 4,096 tokens 71.3 us, 3 requests of 333 rows that see 5 + 2,049 NVFP4 ones 536 us, one row on 4 + 1,024
+// 19.5 us. An FP8 tile takes about 1,430 cycles; the scores' products, at 1,165, bound it.
+//
+// Beside the products, how much code the SM goes through per tile decides: its warps share the instruction cache, and what
+// is unrolled is fetched again for every tile. NVFP4, 3 requests of 333 rows, all else alike: conversion by unrolled loops
+// from registers that loads had filled a tile ahead 666 us, unrolled from pages in shared memory 772, a loop over 16 tokens
+// 622, with the K-blocks in two parts 572 (unrolled by two 593, the products unrolled 6% more), its last inner loops rolled
+// 537; but two passes for a thread's 32 values 570. FP8: the two parts of the query by one loop, 73.3 to 71.3 us for 64 rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -65,9 +67,10 @@ namespace {
 //   CTA 0: warps 0..3, 4..7  softmax of the even and of the odd tiles: one query head
 //                            per thread; the two groups hand the reference on
 //          warps 8..15       at a new job Q to tensor memory; NVFP4: two groups of
-//                            converters, the page's 64 rows to fp16 (nine K-blocks)
+//                            converters, the page's 64 rows to fp16 (nine K-blocks, the even
+//                            ones first, which are multiplied while the others are written)
 //          warp  16          MMA of the even tiles: Q from tensor memory (288 columns), S in 3 x 64 columns
-//          warp  17          the tiles' pages for the others; FP8: the rows by TMA, as they are
+//          warp  17          the tiles' pages for the others; the rows by TMA, as they are
 //          warp  18          MMA of the odd tiles
 //   CTA 1: warps 0..15       rescale O where the reference has moved, write O at a job's end.
 //                            NVFP4: warps 0..3; and 4..15 three groups of converters: the
@@ -75,7 +78,6 @@ namespace {
 //          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
 //                            pages, FP8: and their 512 value dims by TMA; what the MMA of a
 //                            tile waits for
-// A converter group issues the loads of its next tile right after it has stored one.
 // ---------------------------------------------------------------------------
 constexpr int kNT = 64;                      // tokens per tile: one page
 constexpr int kBlk = kNT * 128;              // 8,192 B: a K-block, 64 rows of 64 fp16
@@ -91,7 +93,7 @@ constexpr int kKBufs = kNv ? 2 : 4;
 template <bool kNv>
 constexpr int kVBufs = kNv ? 2 : 4;
 template <bool kNv>
-constexpr int kPBufs = kNv ? 3 : 4;          // (NVFP4: 4 leave the converters' loads less L1: 225 for 199 us)
+constexpr int kPBufs = kNv ? 3 : 4;          // (NVFP4: 3, the pages need the room)
 static_assert(2 * kKBuf == 4 * kKBuf8 && 2 * kVBuf == 4 * kVBuf8, "either kind of buffers");
 // P: 8 chunks, of 8 tokens in fp16 or of 16 tokens of the E5M2 (0..3) or the E4M3 part
 // (4..7), each 16 B per row in row order (the unswizzled core
@@ -103,10 +105,14 @@ constexpr uint32_t kPBytes = kPBuf + kPSide;
 constexpr int kThreads = 640;                // five warpgroups; the last holds the warps below and an idle one
 constexpr int kMmaWarp = 16, kFeedWarp = 17, kMmaWarp2 = 18, kReadyWarp = 18;
 constexpr uint32_t kSCol = 288;              // S after Q's 9 x 32 columns
-constexpr int kNumBars = 77;
+// NVFP4: pages as they lie, ahead of the converters, at the end of either CTA's buffers
+constexpr int kRaw = kNT * 352;              // 22,528 B
+constexpr int kRaws0 = 3, kRaws1 = 2;        // in CTA 0, in CTA 1
+constexpr int kRawAt0 = 2 * kKBuf + 1024, kRawAt1 = (2 * kVBuf + kPBufs<true> * (kPBuf + kPSide) + 127) / 128 * 128;
+constexpr int kNumBars = 83;
 template <bool kNv>
-constexpr size_t kData = 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
-static_assert(kData<true> >= 2 * kKBuf + 1024 && kData<false> >= 2 * kKBuf + 1024, "CTA 0's buffers");
+constexpr size_t kData = kNv ? kRawAt1 + kRaws1 * kRaw : 2 * kVBuf + kPBufs<kNv> * (kPBuf + kPSide);  // of CTA 1; CTA 0 needs less
+static_assert(kData<true> >= kRawAt0 + kRaws0 * kRaw && kData<false> >= 2 * kKBuf + 1024, "CTA 0's buffers");
 template <bool kNv>
 constexpr size_t kSmem = 1024 + kData<kNv> + kNumBars * 8 + 64 + 16;
 static_assert(kSmem<true> + 256 <= 232448 && kSmem<false> + 256 <= 232448, "shared memory, with the static variables");
@@ -261,60 +267,36 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
   *reinterpret_cast<uint4*>(row + (((c + 1) ^ (tok & 7)) << 4)) = hi;
 }
 
-// A converter thread's share of an NVFP4 tile; warp w of 4 has nope K-blocks 2w and 2w + 1:
-// eight 16-B units (32 values, two scales), and for keys (kRope) two 16-B pieces of the
-// rope dims. Tokens at or past `valid`, or before `from`, are zeros: their weights are 0, but their
-// bytes could be NaN.
-template <bool kRope>
-struct TileRegs {
-  uint4 v[2][4];
-  uint32_t s[2][4];
-  uint4 rope[2];
-  __device__ __forceinline__ void load(const uint8_t* page, int from, int valid, int w, int lane, bool clean) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    auto in = [&](int tok) { return tok >= from && tok < valid; };
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int tok = u * 16 + (lane >> 1), unit = 4 * w + 2 * b + (lane & 1);
-        const uint8_t* row = page + tok * 352;
-        v[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint4*>(row + 16 * unit)) : zero;
-        s[b][u] = in(tok) ? __ldg(reinterpret_cast<const uint16_t*>(row + 256 + 2 * unit)) : 0;
-        if (clean) s[b][u] &= ~((((s[b][u] & 0x7F7Fu) + 0x0101u & 0x8080u) >> 7) * 0xFFu);  // NaN scales count as 0
-      }
-    if constexpr (kRope) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ct = b * 128 + w * 32 + lane, tok = ct >> 2;
-        rope[b] = in(tok) ? __ldg(reinterpret_cast<const uint4*>(page + tok * 352 + 288 + 16 * (ct & 3))) : zero;
-      }
-    }
+// A converter thread's share of 16 tokens (16 step and up) of one nope K-block of an NVFP4 tile, from the page in shared
+// memory: a 16-B unit (32 values, two scales). Tokens at or past `valid`, or before `from`, get zero scales: their weights are 0,
+// but their bytes could be NaN. clean: NaN scales count as 0.
+__device__ __forceinline__ void convert_step(uint32_t page, uint8_t* buf, int step, int block, int from, int valid, int lane,
+                                             bool clean) {
+  const int tok = 16 * step + (lane >> 1), c0 = (lane & 1) * 4;
+  const uint32_t row = page + tok * 352;
+  // (the block's four scales: a half of them is this thread's)
+  uint32_t s = ptx::ld_shared_u32(row + 256 + 4 * block) >> (16 * (lane & 1)) & 0xFFFFu, pair, none;
+  const uint4 v = ptx::ld_shared_v4(row + 32 * block + 16 * (lane & 1));
+  if (tok < from || tok >= valid) s = 0;
+  if (clean) s &= ~((((s & 0x7F7Fu) + 0x0101u & 0x8080u) >> 7) * 0xFFu);
+  expand_e4m3(s, pair, none);
+  const __half2 h = *reinterpret_cast<const __half2*>(&pair);
+  const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+  uint8_t* blk = buf + block * kBlk;
+  put2(blk, tok, c0, expand_e2m1(v.x, s0), expand_e2m1(v.y, s0));
+  put2(blk, tok, c0 + 2, expand_e2m1(v.z, s1), expand_e2m1(v.w, s1));
+}
+// Its two 16-B pieces of the tile's rotary dims.
+__device__ __forceinline__ void convert_rope(uint32_t page, uint8_t* buf, int from, int valid, int w, int lane) {
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    const int ct = b * 128 + w * 32 + lane, tok = ct >> 2;
+    uint4 x = ptx::ld_shared_v4(page + tok * 352 + 288 + 16 * (ct & 3)), lo, hi;
+    if (tok < from || tok >= valid) x = make_uint4(0, 0, 0, 0);
+    expand16(x, lo, hi);
+    put2(buf + 8 * kBlk, tok, (ct & 3) * 2, lo, hi);
   }
-  // 16 of the tokens, 16 step and up
-  __device__ __forceinline__ void store(int step, uint8_t* buf, int w, int lane) const {
-    const int tok = 16 * step + (lane >> 1), c0 = (lane & 1) * 4;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint8_t* blk = buf + (2 * w + b) * kBlk;
-      uint32_t two, none;
-      expand_e4m3(s[b][step], two, none);
-      const __half2 h = *reinterpret_cast<const __half2*>(&two);
-      const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-      put2(blk, tok, c0, expand_e2m1(v[b][step].x, s0), expand_e2m1(v[b][step].y, s0));
-      put2(blk, tok, c0 + 2, expand_e2m1(v[b][step].z, s1), expand_e2m1(v[b][step].w, s1));
-    }
-  }
-  __device__ __forceinline__ void store_rope(uint8_t* buf, int w, int lane) const {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint4 lo, hi;
-      const int ct = b * 128 + w * 32 + lane;
-      expand16(rope[b], lo, hi);
-      put2(buf + 8 * kBlk, ct >> 2, (ct & 3) * 2, lo, hi);
-    }
-  }
-};
+}
 
 // Four weights as fp16 -> their E4M3 part and the E5M2 part of the rest, for weights up to 2^kLarge. E4M3 is off by half
 // of its step, 2^-4 of the weight, which needs three bits, or by 2^-10 of weights under 2^-6: the two parts
@@ -361,10 +343,10 @@ struct Tile {
 constexpr int kRing = 8;
 
 // The ring's producer (one warp): 32 page numbers of the walk's job at a time.
-// each(g, tile): what else it does for a tile (lane 0 has just published it).
-template <bool kWin, typename Each>
+// before(g): what it waits for first; each(g, tile): what else it does for a tile (lane 0 has just published it).
+template <bool kWin, typename Before, typename Each>
 __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int unit, int units, int lane, bool report,
-                                     Tile* ring, int* place, uint32_t full, uint32_t free, Each each) {
+                                     Tile* ring, int* place, uint32_t full, uint32_t free, Before before, Each each) {
   Walk<kWin> wk;
   int g = 0;
 #pragma unroll 1
@@ -395,6 +377,7 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
       const Tile t{good ? pg : 0, good ? valid : 0};
       const int slot = g % kRing;
       if (g >= kRing && !ptx::mbar_wait(free + 8 * slot, uint32_t(g / kRing - 1) & 1u)) return false;
+      if (!before(g)) return false;
       if (lane == 0) {
         if (!good && report) atomicOr(a.err, DSA_DEVERR_BLOCK_TABLE);
         ring[slot] = t;
@@ -408,55 +391,61 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
 }
 
 // One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (NVFP4).
-// kKeys (CTA 0): all 576 dims, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
+// kKeys (CTA 0): all 576 dims, in two parts of K-blocks, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
 // its barriers as in feed; full / free: the buffers' (or halves') barriers; turn: the groups take buffers in the order of their
 // tiles (a group that came early could take a buffer's barrier for one a round older,
-// which has the same parity); after(g): called once tile g is stored.
+// which has the same parity); raw, raw_full, raw_free: the pages that the feeding warp fetches ahead, and their barriers;
+// after(g): called once tile g is stored.
 template <bool kWin, bool kKeys, int kGroups, typename After>
 __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
                                         uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
-                                        uint32_t free, uint32_t turn, After after) {
-  TileRegs<kKeys> t;
-  auto load = [&](int g) {
-    const int slot = g % kRing;
-    if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) return false;
-    const Tile tile = ring[slot];
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
-    t.load(a.lat + int64_t(tile.page) * a.stride, tile.from<kWin>(), tile.to<kWin>(), w, lane,
-           !kKeys && tile.mixed<kWin>());
-    return true;
-  };
-  if (group < gtot && !load(group)) return false;
+                                        uint32_t free, uint32_t turn, uint32_t raw, uint32_t raw_full, uint32_t raw_free,
+                                        After after) {
+  constexpr int kRaws = kKeys ? kRaws0 : kRaws1;
 #pragma unroll 1
   for (int g = group; g < gtot; g += kGroups) {
+    const int slot = g % kRing, at = g % kRaws;
+    if (!ptx::mbar_wait(ring_full + 8 * slot, uint32_t(g / kRing) & 1u)) return false;
+    const Tile tile = ring[slot];
+    const int from = tile.from<kWin>(), valid = tile.to<kWin>();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ring_free + 8 * slot);
+    const uint32_t page = raw + at * kRaw;
     if constexpr (kKeys) {
       constexpr int kBufs = kKBufs<true>;
       const int buf = g % kBufs;
-      if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
+      if (!ptx::mbar_wait(raw_full + 8 * at, uint32_t(g / kRaws) & 1u)) return false;
       uint8_t* dst = bufs + buf * kKBuf;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t.store(i, dst, w, lane);
-      t.store_rope(dst, w, lane);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(full + 8 * buf);
-    } else {
-      const int buf = g % kVBufs<true>;
-      if (g > 0 && !ptx::mbar_wait(turn + 8 * ((g - 1) % kGroups), uint32_t((g - 1) / kGroups) & 1u)) return false;
-#pragma unroll
+      // a warp's two K-blocks one after the other: the even blocks are multiplied while the odd ones are written
+#pragma unroll 1
       for (int i = 0; i < 2; ++i) {
-        if (g >= kVBufs<true> && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kVBufs<true> - 1) & 1u)) return false;
-        if (i == 1 && lane == 0) ptx::mbar_arrive(turn + 8 * group);
-        t.store(2 * i, bufs + buf * kVBuf, w, lane);
-        t.store(2 * i + 1, bufs + buf * kVBuf, w, lane);
+        if (g >= kBufs && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kBufs - 1) & 1u)) return false;
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) convert_step(page, dst, u, 2 * w + i, from, valid, lane, false);
+        if (i) convert_rope(page, dst, from, valid, w, lane);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(full + 8 * (2 * buf + i));
       }
+    } else {
+      const int buf = g % kVBufs<true>;
+      if (g > 0 && !ptx::mbar_wait(turn + 8 * ((g - 1) % kGroups), uint32_t((g - 1) / kGroups) & 1u)) return false;
+      if (!ptx::mbar_wait(raw_full + 8 * at, uint32_t(g / kRaws) & 1u)) return false;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        if (i % 2 == 0 && g >= kVBufs<true> && !ptx::mbar_wait(free + 8 * (2 * buf + i / 2), uint32_t(g / kVBufs<true> - 1) & 1u))
+          return false;
+        if (i == 2 && lane == 0) ptx::mbar_arrive(turn + 8 * group);
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) convert_step(page, bufs + buf * kVBuf, i, 2 * w + b, from, valid, lane, tile.mixed<kWin>());
+        if (i % 2 == 0) continue;
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full + 8 * (2 * buf + i / 2));
+      }
     }
+    if (lane == 0) ptx::mbar_arrive(raw_free + 8 * at);  // (behind a __syncwarp)
     if (!after(g)) return false;
-    if (g + kGroups < gtot && !load(g + kGroups)) return false;
   }
   return true;
 }
@@ -473,8 +462,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t q_full = bars + 1 * 8;      // a later job's query is there
   const uint32_t q_first = bars + 76 * 8;    // the first job's
   const uint32_t q_free = bars + 2 * 8;      // every product with the job's query is done
-  const uint32_t k_full = bars + 3 * 8;      // [kKBufs]
-  const uint32_t k_free = bars + 7 * 8;      // [kKBufs]  S of the buffer's tile is done
+  const uint32_t k_full = bars + 3 * 8;      // [4] NVFP4: by even and odd K-blocks of a buffer
+  const uint32_t k_free = bars + 7 * 8;      // [4]  their products are done
   const uint32_t s_full = bars + 11 * 8;     // [kSBufs]
   const uint32_t s_free = bars + 70 * 8;     // [2 kSBufs]  the softmax has read S of a tile (modulo 6)
   const uint32_t turn = bars + 17 * 8;       // [4]  by softmax warp: the tile's reference is decided
@@ -488,6 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t v_turn = bars + 60 * 8;     // [3]  by group: the tile's buffer is the group's
   const uint32_t ask = bars + 67 * 8;        // O is to be rescaled, or written
   const uint32_t o_ok = bars + 68 * 8;       // and it is
+  const uint32_t raw_full = bars + 77 * 8;   // [3] NVFP4: a page has come
+  const uint32_t raw_free = bars + 80 * 8;   // [3]  and has been converted
   Tile* ring = reinterpret_cast<Tile*>(sm + kData<kNv> + kNumBars * 8);  // [8]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring + kRing);
   // CTA 0
@@ -513,6 +504,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::mbar_init(q_first, 16);
     ptx::mbar_init(q_free, 2);
     ptx::mbar_init(ask, 1);
+    for (int i = 0; i < 3; ++i) {
+      ptx::mbar_init(raw_full + 8 * i, 1);
+      ptx::mbar_init(raw_free + 8 * i, 4);
+    }
     for (int i = 0; i < 3; ++i) ptx::mbar_init(v_turn + 8 * i, 4);
     ptx::mbar_init(o_ok, kNv ? 4 : 16);
     for (int i = 0; i < kPBufs<kNv>; ++i) {
@@ -698,7 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // CTA 1, NVFP4, warps 4..15
   auto values = [&]() {
     return convert<kWin, false, 3>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
-                             [](int) { return true; });
+                                   ptx::smem_u32(sm) + kRawAt1, raw_full, raw_free, [](int) { return true; });
   };
 
   // CTA 0: 32 heads of a job's query, `blocks` times 32 columns from block kb0, to tensor memory
@@ -708,9 +703,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int hr = kWin ? first_head(a, job, in_req) + in_req + row
                         : (job < a.tiles ? job * kPfxTileRows : (job - a.tiles) * kHeads) + row;
     const int heads = a.rows * kHeads;
-    // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too. Not for NVFP4, whose
-    // converters have no registers to spare: 214.7 for 212.8 us)
-    const bool in = kWin ? in_req + row < a.n_q * kHeads : kNv || job < a.tiles ? hr < heads : row < kHeads;
+    // (a private job's last 32 rows are zeros: the next row's heads would ask for rescales, too)
+    const bool in = kWin ? in_req + row < a.n_q * kHeads : job < a.tiles ? hr < heads : row < kHeads;
     auto load = [&](int kb, uint32_t (&v)[32]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -719,7 +713,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     };
     // blocks are loaded ahead, the first before the old query is let go: one at a time
-    // after that took 4.3 us a job. (NVFP4: one ahead, as the converters' registers allow.)
+    // after that took 4.3 us a job. (NVFP4: one ahead, less code: 536 us, 541 with two.)
     constexpr int kBlocks = decltype(blocks)::value, kAhead = kNv ? 1 : 2;
     uint32_t v[kAhead][32];
 #pragma unroll
@@ -763,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int k = wk.k0; k < wk.k1; ++k, ++g) {
           if ((g & 1) != (warp == kMmaWarp2)) continue;
           const int buf = g % kKBufs<kNv>, sb = g % kSBufs;
-          if (!ptx::mbar_wait(k_full + 8 * buf, uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
+          if (!ptx::mbar_wait(k_full + 8 * (kNv ? 2 * buf : buf), uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
           // S of the tile three before has been read. (It has a barrier that only tiles of its
           // own kind, odd or even, use: they are read in order, so the barrier is at most a
           // round back. One for all tiles in this place could be two rounds back, which
@@ -774,17 +768,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           ptx::tc_fence_after();
           const uint32_t kb = kb0 + buf * (kNv ? kKBuf : kKBuf8), s = tmem + kSCol + sb * kNT;
-          if (ptx::elect_one()) {
-            if constexpr (kNv) {
-              const uint32_t id = ptx::idesc(0, 0, 128, kNT);
+          if constexpr (kNv) {
+            const uint32_t id = ptx::idesc(0, 0, 128, kNT);
 #pragma unroll 1
-              for (int j = 0; j < kKBlks; ++j)
+            for (int i = 0; i < 2; ++i) {  // the even K-blocks, and the odd and the rotary ones
+              if (i) {
+                if (!ptx::mbar_wait(k_full + 8 * (2 * buf + 1), uint32_t(g / kKBufs<kNv>) & 1u)) { ok = false; break; }
+                ptx::tc_fence_after();
+              }
+              if (ptx::elect_one()) {
+#pragma unroll 1
+                for (int j = i; j < kKBlks; j += i && j == kKBlks - 2 ? 1 : 2) {
+                  if (!i && j == kKBlks - 1) break;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  ptx::mma_f16_tmem_a(s, tmem + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id,
-                                      (j | kk) ? 1u : 0u);
-            } else {
-#pragma unroll
+                  for (int kk = 0; kk < 4; ++kk)
+                    ptx::mma_f16_tmem_a(s, tmem + j * 32 + kk * 8, ptx::sdesc_sw128(kb + j * kBlk + kk * 32), id, (j | kk) ? 1u : 0u);
+                }
+                if (i) ptx::mma_commit(s_full + 8 * sb);
+                ptx::mma_commit(k_free + 8 * (2 * buf + i));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+          } else {
+            if (ptx::elect_one()) {
+#pragma unroll 1
               for (int part = 0; part < 2; ++part) {  // the query's E4M3, then its E5M2 part
                 const uint32_t id = ptx::idesc(part, 0, 128, kNT), q = tmem + part * 144;
 #pragma unroll
@@ -797,23 +805,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int kk = 0; kk < 2; ++kk)
                   ptx::mma_f8_tmem_a(s, q + 128 + kk * 8, ptx::sdesc_sw64(kb + 4 * kBlk + kk * 32), id, 1u);
               }
+              ptx::mma_commit(s_full + 8 * sb);
+              ptx::mma_commit(k_free + 8 * buf);
             }
-            ptx::mma_commit(s_full + 8 * sb);
-            ptx::mma_commit(k_free + 8 * buf);
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (ok && ptx::elect_one()) ptx::mma_commit(q_free);
         __syncwarp();
       }
     } else if (warp == kFeedWarp) {
-      // ---------------------------------------------------------- tiles; FP8 rows by TMA
+      // ---------------------------------------------------------- tiles; their rows by TMA, NVFP4: as pages
       const uint32_t dst0 = ptx::smem_u32(sm), full = half == 0 ? k_full : v_full, free = half == 0 ? k_free : v_free;
       const uint32_t bytes = half == 0 ? kKBuf8 : kVBuf8;
       constexpr int kBufs = 4;
       static_assert(kNv || (kKBufs<kNv> == kBufs && kVBufs<kNv> == kBufs), "FP8 buffers");
-      ok = feed<kWin>(a, gtot, job0, unit0, units, lane, half == 0, ring, s_place, ring_full, ring_free, [&](int g, const Tile& t) {
-        if (kNv) return true;
+      const int raws = half == 0 ? kRaws0 : kRaws1;
+      // (Whoever finds tile g published knows that the page before it in its place has come and gone: the place's barrier
+      // is at most a phase back.)
+      auto before = [&](int g) {
+        return !kNv || g < raws || ptx::mbar_wait(raw_free + 8 * (g % raws), uint32_t(g / raws - 1) & 1u);
+      };
+      ok = feed<kWin>(a, gtot, job0, unit0, units, lane, half == 0, ring, s_place, ring_full, ring_free, before,
+                      [&](int g, const Tile& t) {
+        if constexpr (kNv) {
+          const int at = g % raws;
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(raw_full + 8 * at, kRaw);
+            ptx::bulk_load(dst0 + (half == 0 ? kRawAt0 : kRawAt1) + at * kRaw, a.lat + int64_t(t.page) * a.stride, kRaw,
+                           raw_full + 8 * at);
+          }
+          __syncwarp();
+          return true;
+        }
         const int buf = g % kBufs;
         if (g >= kBufs && !ptx::mbar_wait(free + 8 * buf, uint32_t(g / kBufs - 1) & 1u)) return false;
         if (lane == 0) {
@@ -827,8 +851,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return true;
       });
       // no copy left in flight
-      if (!ok && !kNv)
-        for (int i = 0; i < 2 * kBufs; ++i) ptx::mbar_wait(full + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
+      if (!ok)
+        for (int i = 0; i < 2 * (kNv ? 3 : kBufs); ++i) ptx::mbar_wait((kNv ? raw_full : full) + 8 * (i >> 1), uint32_t(i & 1), 1 << 8);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- O += P . V
       const uint32_t vb0 = ptx::smem_u32(VB), pb0 = ptx::smem_u32(PB);
@@ -865,7 +889,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after();
             const uint32_t vb = vb0 + buf * kVBuf8;
             if (ptx::elect_one()) {
-#pragma unroll
+#pragma unroll 1
               for (int part = 0; part < 2; ++part)  // the weights' E5M2, then their E4M3 part
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
@@ -983,7 +1007,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           return true;
         };
         ok = queries(-2) && convert<kWin, true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
-                                                   queries);
+                                                           ptx::smem_u32(sm) + kRawAt0, raw_full, raw_free, queries);
       } else {
 #pragma unroll 1
         for (; on && ok; on = wk.next(a)) ok = load_q(wk.job);
