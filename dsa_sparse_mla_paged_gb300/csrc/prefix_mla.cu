@@ -31,15 +31,16 @@
 // Measured (one GB300, call after call, where the clock falls under the power limit): 13 x 2 rows
 // on 262,144 shared tokens 960 to 1,090 us by the card (1.48 to 1.31 PFLOP/s; 882 us with pauses between
 // calls), 64 rows on 32,768 and 1,900 of their own 272 to 310 us, 24 rows on 8,111 of their own 50 us,
-// one row on 4,096 19.7 us; NVFP4, 8 x 6 rows on 16,384 and 700 of their own 165 us (1.01 PFLOP/s). With kWin 64 rows
-// that see 64 + 4,096 tokens 71.3 us, 3 requests of 333 rows that see 5 + 2,049 NVFP4 ones 536 us, one row on 4 + 1,024
+// one row on 4,096 19.7 us; NVFP4, 8 x 6 rows on 16,384 and 700 of their own 153 us (1.11 PFLOP/s). With kWin 64 rows
+// that see 64 + 4,096 tokens 71.3 us, 3 requests of 333 rows that see 5 + 2,049 NVFP4 ones 512 us, one row on 4 + 1,024
 // 19.5 us. An FP8 tile takes about 1,430 cycles; the scores' products, at 1,165, bound it.
 //
 // Beside the products, how much code the SM goes through per tile decides: its warps share the instruction cache, and what
 // is unrolled is fetched again for every tile. NVFP4, 3 requests of 333 rows, all else alike: conversion by unrolled loops
 // from registers that loads had filled a tile ahead 666 us, unrolled from pages in shared memory 772, a loop over 16 tokens
 // 622, with the K-blocks in two parts 572 (unrolled by two 593, the products unrolled 6% more), its last inner loops rolled
-// 537; but two passes for a thread's 32 values 570. FP8: the two parts of the query by one loop, 73.3 to 71.3 us for 64 rows.
+// 537; but two passes for a thread's 32 values 570. Then 525 with two groups of converters in CTA 1 instead of three and keys
+// loaded a step ahead, 512 with the third group's warps for the output. FP8: the two parts of the query by one loop, 73.3 to 71.3 us for 64 rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -73,10 +74,10 @@ namespace {
 //          warp  17          the tiles' pages for the others; the rows by TMA, as they are
 //          warp  18          MMA of the odd tiles
 //   CTA 1: warps 0..15       rescale O where the reference has moved, write O at a job's end.
-//                            NVFP4: warps 0..3; and 4..15 three groups of converters: the
+//                            NVFP4: warps 0..3 and 12..15; and 4..11 two groups of converters: the
 //                            512 value dims to fp16 (eight K-blocks of 64 dims, read MN-major)
 //          warps 16..18      MMA: O in all 512 columns, P from shared memory; the tiles'
-//                            pages, FP8: and their 512 value dims by TMA; what the MMA of a
+//                            pages, and their 512 value dims (NVFP4: whole rows) by TMA; what the MMA of a
 //                            tile waits for
 // ---------------------------------------------------------------------------
 constexpr int kNT = 64;                      // tokens per tile: one page
@@ -267,26 +268,32 @@ __device__ __forceinline__ void put2(uint8_t* blk, int tok, int c, const uint4& 
   *reinterpret_cast<uint4*>(row + (((c + 1) ^ (tok & 7)) << 4)) = hi;
 }
 
-// A converter thread's share of 16 tokens (16 step and up) of one nope K-block of an NVFP4 tile, from the page in shared
-// memory: a 16-B unit (32 values, two scales). Tokens at or past `valid`, or before `from`, get zero scales: their weights are 0,
-// but their bytes could be NaN. clean: NaN scales count as 0.
-__device__ __forceinline__ void convert_step(uint32_t page, uint8_t* buf, int step, int block, int from, int valid, int lane,
-                                             bool clean) {
-  const int tok = 16 * step + (lane >> 1), c0 = (lane & 1) * 4;
-  const uint32_t row = page + tok * 352;
-  // (the block's four scales: a half of them is this thread's)
-  uint32_t s = ptx::ld_shared_u32(row + 256 + 4 * block) >> (16 * (lane & 1)) & 0xFFFFu, pair, none;
-  const uint4 v = ptx::ld_shared_v4(row + 32 * block + 16 * (lane & 1));
-  if (tok < from || tok >= valid) s = 0;
-  if (clean) s &= ~((((s & 0x7F7Fu) + 0x0101u & 0x8080u) >> 7) * 0xFFu);
-  expand_e4m3(s, pair, none);
-  const __half2 h = *reinterpret_cast<const __half2*>(&pair);
-  const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
-  uint8_t* blk = buf + block * kBlk;
-  put2(blk, tok, c0, expand_e2m1(v.x, s0), expand_e2m1(v.y, s0));
-  put2(blk, tok, c0 + 2, expand_e2m1(v.z, s1), expand_e2m1(v.w, s1));
-}
-// Its two 16-B pieces of the tile's rotary dims.
+// A converter thread's share of 16 tokens (16 step and up) of one nope K-block of an NVFP4 tile: a 16-B unit (32 values, two
+// scales) of the page in shared memory. Tokens at or past `valid`, or before `from`, get zero scales: their weights are 0, but
+// their bytes could be NaN. clean: NaN scales count as 0.
+struct Step {
+  uint4 v;
+  uint32_t s;
+  __device__ __forceinline__ void load(uint32_t page, int step, int block, int lane) {
+    const uint32_t row = page + (16 * step + (lane >> 1)) * 352;
+    // (the block's four scales: a half of them is this thread's)
+    s = ptx::ld_shared_u32(row + 256 + 4 * block) >> (16 * (lane & 1)) & 0xFFFFu;
+    v = ptx::ld_shared_v4(row + 32 * block + 16 * (lane & 1));
+  }
+  __device__ __forceinline__ void store(uint8_t* buf, int step, int block, int from, int valid, int lane, bool clean) {
+    const int tok = 16 * step + (lane >> 1), c0 = (lane & 1) * 4;
+    if (tok < from || tok >= valid) s = 0;
+    if (clean) s &= ~((((s & 0x7F7Fu) + 0x0101u & 0x8080u) >> 7) * 0xFFu);
+    uint32_t pair, none;
+    expand_e4m3(s, pair, none);
+    const __half2 h = *reinterpret_cast<const __half2*>(&pair);
+    const __half2 s0 = __low2half2(h), s1 = __high2half2(h);
+    uint8_t* blk = buf + block * kBlk;
+    put2(blk, tok, c0, expand_e2m1(v.x, s0), expand_e2m1(v.y, s0));
+    put2(blk, tok, c0 + 2, expand_e2m1(v.z, s1), expand_e2m1(v.w, s1));
+  }
+};
+// A thread's two 16-B pieces of the tile's rotary dims.
 __device__ __forceinline__ void convert_rope(uint32_t page, uint8_t* buf, int from, int valid, int w, int lane) {
 #pragma unroll 1
   for (int b = 0; b < 2; ++b) {
@@ -390,16 +397,16 @@ __device__ __forceinline__ bool feed(const PfxArgs& a, int gtot, int job0, int u
   return true;
 }
 
-// One of the kGroups converter groups (4 warps; tiles in turn) of either CTA (NVFP4).
+// One of the two converter groups (4 warps; tiles in turn, a buffer each) of either CTA (NVFP4).
 // kKeys (CTA 0): all 576 dims, in two parts of K-blocks, else (CTA 1) the 512 values, in two halves of 32 tokens. ring and
-// its barriers as in feed; full / free: the buffers' (or halves') barriers; turn: the groups take buffers in the order of their
-// tiles (a group that came early could take a buffer's barrier for one a round older,
-// which has the same parity); raw, raw_full, raw_free: the pages that the feeding warp fetches ahead, and their barriers;
-// after(g): called once tile g is stored.
-template <bool kWin, bool kKeys, int kGroups, typename After>
+// its barriers as in feed; full / free: the buffers' halves' barriers; raw, raw_full, raw_free: the pages that the feeding
+// warp fetches ahead, and their barriers; after(g): called once tile g is stored.
+constexpr int kGroups = 2;
+static_assert(kKBufs<true> == kGroups && kVBufs<true> == kGroups, "a buffer's barriers are one group's: never two phases back");
+template <bool kWin, bool kKeys, typename After>
 __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, int w, int lane, const Tile* ring,
                                         uint32_t ring_full, uint32_t ring_free, uint8_t* bufs, uint32_t full,
-                                        uint32_t free, uint32_t turn, uint32_t raw, uint32_t raw_full, uint32_t raw_free,
+                                        uint32_t free, uint32_t raw, uint32_t raw_full, uint32_t raw_free,
                                         After after) {
   constexpr int kRaws = kKeys ? kRaws0 : kRaws1;
 #pragma unroll 1
@@ -420,8 +427,14 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         if (g >= kBufs && !ptx::mbar_wait(free + 8 * (2 * buf + i), uint32_t(g / kBufs - 1) & 1u)) return false;
+        Step next;
+        next.load(page, 0, 2 * w + i, lane);
 #pragma unroll 1
-        for (int u = 0; u < 4; ++u) convert_step(page, dst, u, 2 * w + i, from, valid, lane, false);
+        for (int u = 0; u < 4; ++u) {
+          Step now = next;
+          if (u < 3) next.load(page, u + 1, 2 * w + i, lane);
+          now.store(dst, u, 2 * w + i, from, valid, lane, false);
+        }
         if (i) convert_rope(page, dst, from, valid, w, lane);
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -429,15 +442,17 @@ __device__ __forceinline__ bool convert(const PfxArgs& a, int gtot, int group, i
       }
     } else {
       const int buf = g % kVBufs<true>;
-      if (g > 0 && !ptx::mbar_wait(turn + 8 * ((g - 1) % kGroups), uint32_t((g - 1) / kGroups) & 1u)) return false;
       if (!ptx::mbar_wait(raw_full + 8 * at, uint32_t(g / kRaws) & 1u)) return false;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         if (i % 2 == 0 && g >= kVBufs<true> && !ptx::mbar_wait(free + 8 * (2 * buf + i / 2), uint32_t(g / kVBufs<true> - 1) & 1u))
           return false;
-        if (i == 2 && lane == 0) ptx::mbar_arrive(turn + 8 * group);
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) convert_step(page, bufs + buf * kVBuf, i, 2 * w + b, from, valid, lane, tile.mixed<kWin>());
+        for (int b = 0; b < 2; ++b) {
+          Step now;
+          now.load(page, i, 2 * w + b, lane);
+          now.store(bufs + buf * kVBuf, i, 2 * w + b, from, valid, lane, tile.mixed<kWin>());
+        }
         if (i % 2 == 0) continue;
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -474,7 +489,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t go = bars + 45 * 8;         // [kPBufs]  P and O are ready for P . V
   const uint32_t v_full = bars + 49 * 8;     // [4] NVFP4: by half tile
   const uint32_t v_free = bars + 54 * 8;     // [4]  its P . V is done
-  const uint32_t v_turn = bars + 60 * 8;     // [3]  by group: the tile's buffer is the group's
   const uint32_t ask = bars + 67 * 8;        // O is to be rescaled, or written
   const uint32_t o_ok = bars + 68 * 8;       // and it is
   const uint32_t raw_full = bars + 77 * 8;   // [3] NVFP4: a page has come
@@ -508,8 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(raw_full + 8 * i, 1);
       ptx::mbar_init(raw_free + 8 * i, 4);
     }
-    for (int i = 0; i < 3; ++i) ptx::mbar_init(v_turn + 8 * i, 4);
-    ptx::mbar_init(o_ok, kNv ? 4 : 16);
+    ptx::mbar_init(o_ok, kNv ? 8 : 16);
     for (int i = 0; i < kPBufs<kNv>; ++i) {
       ptx::mbar_init(p_free + 8 * i, 1);
       ptx::mbar_init(p_full + 8 * i, 1);
@@ -690,10 +703,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // CTA 1, NVFP4, warps 4..15
+  // CTA 1, NVFP4, warps 4..11
   auto values = [&]() {
-    return convert<kWin, false, 3>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free, v_turn,
-                                   ptx::smem_u32(sm) + kRawAt1, raw_full, raw_free, [](int) { return true; });
+    return convert<kWin, false>(a, gtot, (warp >> 2) - 1, warp & 3, lane, ring, ring_full, ring_free, VB, v_full, v_free,
+                                ptx::smem_u32(sm) + kRawAt1, raw_full, raw_free, [](int) { return true; });
   };
 
   // CTA 0: 32 heads of a job's query, `blocks` times 32 columns from block kb0, to tensor memory
@@ -1006,15 +1019,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           return true;
         };
-        ok = queries(-2) && convert<kWin, true, 2>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free, 0,
-                                                           ptx::smem_u32(sm) + kRawAt0, raw_full, raw_free, queries);
+        ok = queries(-2) && convert<kWin, true>(a, gtot, group, w, lane, ring, ring_full, ring_free, KB, k_full, k_free,
+                                                  ptx::smem_u32(sm) + kRawAt0, raw_full, raw_free, queries);
       } else {
 #pragma unroll 1
         for (; on && ok; on = wk.next(a)) ok = load_q(wk.job);
       }
     } else {
       if constexpr (kNv)
-        ok = values();
+        ok = warp >= 12 ? output(kDNope / 2, kDNope) : values();
       else
         ok = output((warp >> 2) * 128, (warp >> 2) * 128 + 128);
     }
@@ -1163,7 +1176,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if constexpr (kNv)
-      ok = warp >= 4 ? values() : output(0, kDNope);
+      ok = warp >= 4 ? values() : output(0, kDNope / 2);
     else
       ok = output((warp >> 2) * 128, (warp >> 2) * 128 + 128);
   }
