@@ -40,7 +40,8 @@
 // from registers that loads had filled a tile ahead 666 us, unrolled from pages in shared memory 772, a loop over 16 tokens
 // 622, with the K-blocks in two parts 572 (unrolled by two 593, the products unrolled 6% more), its last inner loops rolled
 // 537; but two passes for a thread's 32 values 570. Then 525 with two groups of converters in CTA 1 instead of three and keys
-// loaded a step ahead, 512 with the third group's warps for the output. FP8: the two parts of the query by one loop, 73.3 to 71.3 us for 64 rows.
+// loaded a step ahead, 512 with the third group's warps for the output. FP8: the two parts of the query by one loop, 73.3 to
+// 71.3 us for 64 rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
