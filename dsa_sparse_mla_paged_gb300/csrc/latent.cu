@@ -98,8 +98,9 @@ __device__ __forceinline__ void rotate8(float (&x)[8], int j, CosSin cs) {
   }
 }
 
+// (a length may be anything: without positions it is checked, and the sum of a bad one wraps)
 __device__ __forceinline__ int row_position(const LatentIn& in, int row, int b, int n_q) {
-  return in.positions ? in.positions[row] : in.ctx_lens[b] - n_q + (row - b * n_q);
+  return in.positions ? in.positions[row] : int(uint32_t(in.ctx_lens[b]) - uint32_t(n_q) + uint32_t(row - b * n_q));
 }
 
 // Blocks [0, lat_blocks): a warp per row's latent. The others: kSplits a row, a warp has kPer heads at a time, kLoops times.
@@ -122,11 +123,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
       rw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(in.k_rope) + row * in.k_rope_row) + lane);
     float co, si;
     cos_sin(row_position(in, row, b, n_q), __ldg(in.inv_freq + lane), co, si);
-    const int slot = ctx - n_q + t;
-    int page = -1;
+    int page = -1, slot = 0;
     if (ctx < n_q || ctx > cap) {
       if (lane == 0) atomicOr(err, DSA_DEVERR_CTX);
     } else {
+      slot = ctx - n_q + t;
       page = in.block_table[size_t(b) * max_pages + slot / kPage];
       if (page < 0 || page >= num_pages) {
         if (lane == 0) atomicOr(err, DSA_DEVERR_BLOCK_TABLE);
@@ -229,6 +230,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4)
     float c, s;
     cos_sin(row_position(in, row, b, n_q), __ldg(in.inv_freq + lane), c, s);
     s_cs[lane] = make_float2(c, s);
+    if (lat_blocks == 0 && !in.positions && part == 0 && lane == 0) {  // no latent's warp looks at the length
+      const int ctx = in.ctx_lens[b];
+      if (ctx < n_q || ctx > cap) atomicOr(err, DSA_DEVERR_CTX);
+    }
   }
   float gm[2][8];
   const bool norm = in.gamma_q != nullptr;

@@ -457,7 +457,8 @@ typedef struct {
  * q_out NULL: the cache alone (the query's pointers are not used); c_kv NULL: the query alone.
  * All of them 16-B aligned but positions (4). ws: any workspace of at least 256 bytes (its error word).
  * A row with an invalid ctx_b or block-table entry writes no latent and sets DSA_DEVERR_CTX /
- * DSA_DEVERR_BLOCK_TABLE. */
+ * DSA_DEVERR_BLOCK_TABLE. The query alone sets DSA_DEVERR_CTX too (its row is rotated by whatever position follows), but with
+ * positions it does not look at ctx_lens. */
 dsa_status_t dsa_latent_frontend(const dsa_params_t* params, const dsa_latent_dims_t* dims, const void* q_nope,
                                  const void* q_rope, const void* gamma_q, const void* c_kv, const void* k_rope,
                                  const void* gamma_kv, const float* inv_freq, const int32_t* positions,
