@@ -389,6 +389,16 @@ def verify_draft(params, target, draft, draft_tokens, n_draft, uniforms, ctx_len
 _BF16 = _F32 = _I32 = None  # (torch is imported with the first call)
 
 
+def _types():
+    """The element types that the checks compare with; the callers look at the last of them. (An import statement in each call is
+    not free.)"""
+    global _BF16, _F32, _I32
+    import torch
+
+    _F32, _I32 = torch.float32, torch.int32
+    _BF16 = torch.bfloat16
+
+
 def _strided(fn, name, t, rows, heads, width):
     """(address, elements between rows, elements between heads) of a bf16 tensor of `rows` rows of `width` values, or of `heads`
     times that; its leading dimensions are the rows. Addresses pass as they are (dense)."""
@@ -419,11 +429,8 @@ def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv
     """Norms, rotation, the query [rows, 96, 576] and the new tokens' latents written into lat_pool. `q_nope`
     [rows, 96, 512], `q_rope` [rows, 96, 64], `c_kv` [rows, 512] and `k_rope` [rows, 64] may be strided (slices of the
     projections' outputs); `gamma_q` None: no norm of the query; `q_out` None: the cache alone; `c_kv` None: the query alone."""
-    global _BF16, _F32, _I32
     if _BF16 is None:
-        import torch
-
-        _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+        _types()
     fn, rows = "latent_frontend", params.batch * params.n_q
     qn = qh = rn = rh = cr = kr = 0
     if q_out is not None:
@@ -436,14 +443,15 @@ def latent_frontend(params, q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv, inv
     if c_kv is not None:
         c_kv, cr, _ = _strided(fn, "c_kv", c_kv, rows, 0, 512)
         k_rope, kr, _ = _strided(fn, "k_rope", k_rope, rows, 0, 64)
-        gamma_kv, lat_pool, block_table = _array(fn, "gamma_kv", gamma_kv, _BF16, 512), _ptr(lat_pool), _ptr(block_table)
+        gamma_kv, lat_pool = _array(fn, "gamma_kv", gamma_kv, _BF16, 512), _ptr(lat_pool)
+        block_table = _array(fn, "block_table", block_table, _I32, params.batch * params.max_pages_per_req)
     else:
         k_rope = gamma_kv = lat_pool = block_table = None
     dims = LatentDims(qn, qh, rn, rh, cr, kr, eps, bool(interleaved))
     _check("dsa_latent_frontend", load().dsa_latent_frontend(
         ctypes.byref(params), ctypes.byref(dims), q_nope, q_rope, gamma_q, c_kv, k_rope, gamma_kv,
         _array(fn, "inv_freq", inv_freq, _F32, 32), _array(fn, "positions", positions, _I32, rows), lat_pool, block_table,
-        _ptr(ctx_lens), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
+        _array(fn, "ctx_lens", ctx_lens, _I32, params.batch), q_out, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def _int32(fn, name, v):
@@ -455,10 +463,15 @@ def _int32(fn, name, v):
 
 def window_mla_decode(params, q, lat_pool, sinks, window, block_table, ctx_lens, out, lse, ws, stream=None):
     """Attention to each row's last `window` tokens and the request's first `sinks`."""
-    fn = "window_mla_decode"
+    if _BF16 is None:
+        _types()
+    fn, batch = "window_mla_decode", params.batch
+    rows = batch * params.n_q
     _check("dsa_window_mla_decode", load().dsa_window_mla_decode(
-        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _int32(fn, "sinks", sinks), _int32(fn, "window", window), _ptr(block_table),
-        _ptr(ctx_lens), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(params), _array(fn, "q", q, _BF16, rows * 55296), _ptr(lat_pool), _int32(fn, "sinks", sinks),
+        _int32(fn, "window", window), _array(fn, "block_table", block_table, _I32, batch * params.max_pages_per_req),
+        _array(fn, "ctx_lens", ctx_lens, _I32, batch), _array(fn, "out", out, _BF16, rows * 49152),
+        _array(fn, "lse", lse, _F32, rows * 96), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def _per_token(fn, name, t, dtype, batch):
@@ -471,15 +484,17 @@ def _per_token(fn, name, t, dtype, batch):
 def attention_mass(params, q, lat_pool, sinks, window, block_table, ctx_lens, lse, fresh, mass, ws, stream=None):
     """Add the weight that the step's rows give every token to `mass` [B, tokens]; `lse` is the attention's. The
     last `fresh` tokens of each context are set instead."""
-    import torch
-
-    fn = "attention_mass"
-    at, stride, width = _per_token(fn, "mass", mass, torch.float32, params.batch)
-    if width < params.max_pages_per_req * params.page_size:
+    if _BF16 is None:
+        _types()
+    fn, batch, pages = "attention_mass", params.batch, params.max_pages_per_req
+    rows = batch * params.n_q
+    at, stride, width = _per_token(fn, "mass", mass, _F32, batch)
+    if width < pages * params.page_size:
         raise ValueError("attention_mass: mass has fewer tokens than the block table's pages")
     _check("dsa_attention_mass", load().dsa_attention_mass(
-        ctypes.byref(params), _ptr(q), _ptr(lat_pool), _int32(fn, "sinks", sinks), _int32(fn, "window", window), _ptr(block_table),
-        _ptr(ctx_lens), _array(fn, "lse", lse, torch.float32, params.batch * params.n_q * 96), _int32(fn, "fresh", fresh), at, stride,
+        ctypes.byref(params), _array(fn, "q", q, _BF16, rows * 55296), _ptr(lat_pool), _int32(fn, "sinks", sinks),
+        _int32(fn, "window", window), _array(fn, "block_table", block_table, _I32, batch * pages),
+        _array(fn, "ctx_lens", ctx_lens, _I32, batch), _array(fn, "lse", lse, _F32, rows * 96), _int32(fn, "fresh", fresh), at, stride,
         _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
@@ -493,19 +508,20 @@ def make_token_pools(pools):
 def tokens_evict(params, budgets, sinks, recent, mass, pools, block_table, ctx_lens, page_refs, kept, ws, stream=None):
     """Cut every request with more than budgets[b] tokens (negative: as it is) to its first `sinks`, its last `recent` and those
     of the largest `mass` [B, tokens] between; `pools` from make_token_pools, `kept` int32 [B, tokens] like mass, or None."""
-    import torch
-
-    fn = "tokens_evict"
-    at, stride, width = _per_token(fn, "mass", mass, torch.float32, params.batch)
-    if width < params.max_pages_per_req * params.page_size:
+    if _BF16 is None:
+        _types()
+    fn, batch, pages = "tokens_evict", params.batch, params.max_pages_per_req
+    at, stride, width = _per_token(fn, "mass", mass, _F32, batch)
+    if width < pages * params.page_size:
         raise ValueError("tokens_evict: mass has fewer tokens than the block table's pages")
     if kept is not None:
-        kept, kept_stride, kept_width = _per_token(fn, "kept", kept, torch.int32, params.batch)
+        kept, kept_stride, kept_width = _per_token(fn, "kept", kept, _I32, batch)
         if (kept_stride, kept_width) != (stride, width):
             raise ValueError("tokens_evict: kept and mass differ in shape or strides")
     _check("dsa_tokens_evict", load().dsa_tokens_evict(
-        ctypes.byref(params), _array(fn, "budgets", budgets, torch.int32, params.batch), _int32(fn, "sinks", sinks),
-        _int32(fn, "recent", recent), at, stride, pools[0], pools[1], _ptr(block_table), _ptr(ctx_lens), _ptr(page_refs), kept, _ptr(ws),
+        ctypes.byref(params), _array(fn, "budgets", budgets, _I32, batch), _int32(fn, "sinks", sinks), _int32(fn, "recent", recent), at,
+        stride, pools[0], pools[1], _array(fn, "block_table", block_table, _I32, batch * pages),
+        _array(fn, "ctx_lens", ctx_lens, _I32, batch), _array(fn, "page_refs", page_refs, _I32, params.num_pages), kept, _ptr(ws),
         _nbytes(ws), _stream(stream)))
 
 
