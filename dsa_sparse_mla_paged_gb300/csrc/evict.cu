@@ -3,7 +3,8 @@
 //
 // select: a cluster per request finds the k-th largest weight exactly, by three passes of histograms (11, 11
 //   and 10 bits of the order key) over its slices of the weights, summed through distributed shared memory; then
-//   one pass writes the kept tokens in order. The weights are read once, their keys stay in shared memory.
+//   one pass writes the kept tokens in order. The weights are read once, their keys stay in shared memory; of a slice of more than
+//   45,056 tokens a CTA (long contexts in large batches, one of more than 720,896) what lies behind is read in all five passes.
 // plan: one cluster ranks the free pages (if a shared page has to be replaced) and gives every request its fresh pages
 //   and its place in the list of moves.
 // apply: the moves, then tables, counts, lengths and weights. A page is rewritten in place where nobody else holds

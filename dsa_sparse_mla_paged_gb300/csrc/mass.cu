@@ -67,12 +67,11 @@ constexpr uint32_t kPolls = 1u << 20;  // 4 s
 struct MassArgs {
   const float* qs;    // [rows * 96] the prepared query's scales
   const float* lse;   // [rows * 96]
-  const uint8_t* lat;
   const int32_t* table;
   const int32_t* ctx;
   float* mass;
   int* err;
-  int64_t stride, mass_stride;
+  int64_t mass_stride;
   int batch, n_q, max_pages, cap, num_pages, sinks, window, fresh;
   float scale_log2;
 };
@@ -604,12 +603,10 @@ cudaError_t launch_attention_mass(const dsa_params_t& p, const WsLayout& L, char
   MassArgs a = {};
   a.qs = reinterpret_cast<const float*>(ws + L.pfx_qs);
   a.lse = lse;
-  a.lat = static_cast<const uint8_t*>(lat_pool);
   a.table = block_table;
   a.ctx = ctx_lens;
   a.mass = mass;
   a.err = reinterpret_cast<int*>(ws + L.err);
-  a.stride = p.lat_page_stride;
   a.mass_stride = mass_stride;
   a.batch = p.batch;
   a.n_q = p.n_q;
