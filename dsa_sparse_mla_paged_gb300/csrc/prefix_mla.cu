@@ -29,11 +29,12 @@
 // adds up over the thousands of them. Sums are fp32 throughout.
 //
 // Measured (one GB300, call after call, where the clock falls under the power limit): 13 x 2 rows
-// on 262,144 shared tokens 960 to 1,090 us by the card (1.48 to 1.31 PFLOP/s; 882 us with pauses between
-// calls), 64 rows on 32,768 and 1,900 of their own 272 to 310 us, 24 rows on 8,111 of their own 50 us,
-// one row on 4,096 19.7 us; NVFP4, 8 x 6 rows on 16,384 and 700 of their own 153 us (1.11 PFLOP/s). With kWin 64 rows
+// on 262,144 shared tokens 880 to 1,090 us by the card (1.61 to 1.31 PFLOP/s; 882 us with pauses between
+// calls), 64 rows on 32,768 and 1,900 of their own 272 to 310 us, 24 rows on 8,111 of their own 40.4 us (41 to 52 right behind the 13 x 2
+// rows, whose power lowers the clock), one row on 4,096 20 us; NVFP4, 8 x 6 rows on 16,384 and 700 of their own 153 us (1.11 PFLOP/s). With kWin 64 rows
 // that see 64 + 4,096 tokens 71.3 us, 3 requests of 333 rows that see 5 + 2,049 NVFP4 ones 512 us, one row on 4 + 1,024
-// 19.5 us. An FP8 tile takes about 1,430 cycles; the scores' products, at 1,165, bound it.
+// 19.5 us. An FP8 tile takes about 1,430 cycles; the scores' products, at 1,165, bound it. (64 single rows through windows of 1,024 to 8,192
+// tokens: 0.78 us a tile of a pair, NVFP4 1.0, and some 28 us, NVFP4 30, that do not depend on the tokens.)
 //
 // Beside the products, how much code the SM goes through per tile decides: its warps share the instruction cache, and what
 // is unrolled is fetched again for every tile. NVFP4, 3 requests of 333 rows, all else alike: conversion by unrolled loops

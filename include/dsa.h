@@ -439,7 +439,7 @@ typedef struct {
 /* The attention's front end: norms, rotation, the query as the attention takes it, and the new
  * tokens' latents written into the cache (the index keys are dsa_indexer_frontend's). For row
  * (b, t), with position p (positions[row], or the token's slot ctx_b - n_q + t without positions)
- * and angles a_i = p * inv_freq[i], i < 32 (in fp64, so that far positions keep them):
+ * and angles a_i = p * inv_freq[i], i < 32 (in fp64, so that far positions keep them; below 2^50 in size):
  *   norm(x) = x * r, r = 1 / sqrt(mean(x^2) + eps) over 512 values; rot(x): each pair (x0, x1) of the
  *             64 rotary values becomes (x0 cos a_i - x1 sin a_i, x1 cos a_i + x0 sin a_i)
  *   latent:   v = norm(c_kv) * gamma_kv * (1 / latent_scale) and rot(k_rope) * (1 / latent_scale), in
@@ -484,13 +484,15 @@ dsa_status_t dsa_window_mla_decode(const dsa_params_t* params, const void* q, co
 /* Accumulated attention weight of every cached token, for eviction (dsa_tokens_evict):
  *   mass[b][s] += sum over rows t that see s, and heads h, of exp(softmax_scale * q_h . c_s - lse[b,t,h])
  * where row (b, t) sees what dsa_window_mla_decode lets it see (window >= max_pages_per_req *
- * page_size: all of its tokens, as dsa_prefix_mla_decode does) and lse is that call's result. The products
- * are those of that call; the sums are fp32, over the heads and then the rows, in an order that depends
+ * page_size: all of its tokens, as dsa_prefix_mla_decode does) and lse is that call's result. (A row's lse of
+ * dsa_sparse_mla_decode or dsa_decode is over its top-k alone: with it, tokens that the row did not select would be credited, too.)
+ * The products are those of that call; the sums are fp32, over the heads and then the rows, in an order that depends
  * on nothing but the row (the same bits in any batch).
- * Entries of tokens that no row sees are left as they are. A head whose lse is not finite adds nothing;
+ * Entries of tokens that no row sees are left as they are, whatever `fresh` says. A head whose lse is not finite adds nothing;
  * a token whose latent holds a NaN gets NaN.
  *   fresh  >= 0: the last `fresh` tokens of each context (new ones, whose entries hold what an
- *          earlier token left there) are set instead of added to
+ *          earlier token left there) are set instead of added to, as far as some row sees them: where a
+ *          prompt's tokens come without rows that judge them, the caller clears the slot's mass first
  *   lse    fp32 [B, n_q, heads]
  *   mass   fp32 [B, mass_stride], mass_stride >= max_pages_per_req * page_size
  * Errors: a request with an invalid ctx_b changes nothing (DSA_DEVERR_CTX); the tokens of a bad page
