@@ -79,6 +79,40 @@ def test_two_evictions_at_once():
         s.same()
 
 
+def test_an_eviction_beside_other_streams_attention():
+    """Its CTAs meet although another stream's kernels keep the SMs busy; each call on a workspace of its own."""
+    import torch
+
+    inp = make([9000 + 100 * i for i in range(40)], 2, 10, 6000, seed=36)
+    d = Dev(inp)
+    ref, ref_lse = launch(d, 10, 6000)
+    s = State([30000, 17000, 500], ("key_fp8", "lat_fp8"), seed=37)
+    s.to_device()
+    cuts = [[20000, 16999, 100], [12000, 8000, 99], [700, 7999, 0]]
+    budgets = [torch.tensor(c, dtype=torch.int32, device="cuda") for c in cuts]
+    start = torch.rand(inp.batch, inp.max_pages * 64, device="cuda")
+    masses, ws = start.clone(), torch.zeros_like(d.ws)
+    a, b, c = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(12):
+        with torch.cuda.stream(a):
+            outs.append(launch(d, 10, 6000)[0])
+        dsa.attention_mass(d.p, d.q, d.lat_pool, 10, 6000, d.block_table, d.ctx, ref_lse, 0, masses, ws, c)
+        if i % 4 == 1:
+            s.call(budgets[i // 4], 4, 60, stream=b)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    for w in (s.ws, d.ws, ws):
+        assert dsa.get_device_error(w) == 0
+    for _ in range(12):
+        dsa.attention_mass(d.p, d.q, d.lat_pool, 10, 6000, d.block_table, d.ctx, ref_lse, 0, start, ws)
+    assert torch.equal(masses, start)
+    for cut in cuts:
+        assert B.tokens_evict(s.table, s.ctx, s.refs, s.mass, cut, 4, 60, s.pools(), s.kept) == 0
+    s.same()
+
+
 @pytest.mark.parametrize("lat_fmt", ["fp8", "nvfp4"])
 def test_two_sums_of_weights_at_once(lat_fmt):
     import torch
